@@ -365,6 +365,80 @@ int ar_wire_pack(const void *src, void *wire, size_t nelem, int dst_dtype, int w
 int ar_reduce_host_noalloc(const void *const *h_srcs, void *const *h_dsts, int n_dsts, size_t nelem,
                            int dst_dtype, int wire_dtype, cudaStream_t stream);
 
+/* ---- training operators ---------------------------------------------------
+ * What a tensor-parallel training step does directly behind and before the
+ * reduction: dropout on the reduced sum, and the loss over a vocabulary that
+ * is split into pieces, whose gradient is again a set of partials.  They
+ * have no counterpart in the pages.  The conventions above hold for them too:
+ * ar_init first, work is only enqueued, nothing is allocated (calls that need
+ * scratch memory take a workspace from the caller and say how large it has to
+ * be), AR_Q_LAST_VARIANT is left alone, and calls can be captured in a graph.
+ */
+
+/*
+ * Dropout whose mask is a function of its arguments and is never stored.
+ * Element (row, col) owns word col % 4 of Philox4x32-10 (Salmon, Moraes, Dror
+ * and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) under the key
+ * (seed low, seed high) and the counter (col / 4, row, offset low, offset
+ * high).  It is kept when that word is at least floor(p * 2^32), and a kept
+ * element is multiplied by 1 / (1 - p) in float; p = 1 keeps nothing.  Strides, variants and
+ * grids do not enter, so the backward pass sees the forward pass's mask.  Two
+ * calls have independent masks when their offsets (or seeds) differ.
+ */
+typedef struct {
+    uint64_t seed;
+    uint64_t offset;  /* which call of the step and which step: the counter's upper half */
+    float p;          /* probability that an element is dropped, 0 <= p <= 1 */
+    const void *bias; /* NULL, or one row of ne0 T_dst elements added to the sum before dropout */
+} ar_dropout;
+
+/*
+ * ar_reduce_dropout -- ar_reduce_ex with bias and dropout between the rank
+ * fold and the residual:
+ *   a = fold_r wire(src[r][row][i]);  a = a + bias[i];
+ *   a = keep(row, i) ? a * scale : 0;  a = a + residual[row][i];
+ *   dst[d][row][i] = T_dst(a)
+ * each step rounded to float.  A dropped element is 0 whatever the sum holds
+ * (infinities and NaN included).  Layout, in-place and overlap rules as for
+ * ar_reduce_ex (a residual row broadcast with stride 0 is allowed); bias may
+ * not overlap a destination.  ne1 must fit 32 bits and ne0 34 bits
+ * (AR_ERR_TOO_LARGE).  Every layout and alignment gives the same bits.
+ */
+int ar_reduce_dropout(const void *const *srcs, void *const *dsts, int n_dsts, const ar_layout *layout,
+                      const ar_dropout *dropout, int dst_dtype, int wire_dtype, cudaStream_t stream);
+
+/* Host-only validation of an ar_reduce_dropout call (no CUDA call). */
+int ar_check_dropout(int R, const void *const *srcs, void *const *dsts, int n_dsts, const ar_layout *layout,
+                     const ar_dropout *dropout, size_t max_elems, int dst_dtype, int wire_dtype);
+
+/*
+ * ar_reduce_dropout_grad -- the backward pass of ar_reduce_dropout:
+ *   dx[d][row][i]  = T_dst(keep(row, i) ? dy[row][i] * scale : 0)   d = 0 .. n_dxs-1
+ *   dbias[i]       = sum over rows of the same, in float, unrounded
+ *   dresidual[i]   = sum over rows of dy[row][i], in float
+ * Rounding through the wire type is differentiated as the identity, so every
+ * active rank's partial has the same gradient; the gradient of a full
+ * residual is dy itself.
+ *   dy         T_dst, ne1 rows at layout->src_row_bytes[0] (NULL: packed).
+ *   dxs        n_dxs destinations, 1..16, at layout->dst_row_bytes; one may be
+ *              exactly dy (same stride).
+ *   layout     ne0, ne1 and the strides; residual must be NULL and
+ *              inactive_mask 0.
+ *   dropout    as in the forward call; its bias is not read and may be NULL.
+ *   dbias, dresidual  NULL, or ne0 floats.  dresidual is the gradient of a
+ *              residual row broadcast with stride 0.
+ *   workspace  16-byte aligned device memory of ar_reduce_dropout_grad_workspace
+ *              bytes (NULL where that is 0); its contents do not matter.
+ * Sums are taken in a fixed order: the same call gives the same bits.
+ */
+int ar_reduce_dropout_grad(const void *dy, void *const *dxs, int n_dxs, const ar_layout *layout,
+                           const ar_dropout *dropout, float *dbias, float *dresidual, void *workspace,
+                           size_t workspace_bytes, int dst_dtype, cudaStream_t stream);
+
+/* Workspace of an ar_reduce_dropout_grad call with n_sums (0..2) of dbias and
+ * dresidual given (host only, needs no context). */
+int ar_reduce_dropout_grad_workspace(const ar_layout *layout, int n_sums, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,4 +11,6 @@ from .ar import (  # noqa: F401
     ar_query, ar_reduce, ar_reduce_host, ar_reduce_variant, ar_set_option,
     ar_status_string, library_path, ArLayout, make_layout, ar_reduce_ex, ar_check_layout, ar_wire_pack,
     ar_reduce_host_noalloc, AR_NOALLOC_SCRATCH_BYTES, PreparedReduce,
+    ArDropout, make_dropout, ar_reduce_dropout, ar_check_dropout, ar_reduce_dropout_grad,
+    ar_reduce_dropout_grad_workspace,
 )

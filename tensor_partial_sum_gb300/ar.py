@@ -37,6 +37,12 @@ class ArLayout(ctypes.Structure):
                 ("inactive_mask", ctypes.c_uint32)]
 
 
+class ArDropout(ctypes.Structure):
+    """ar_dropout of include/ar.h."""
+    _fields_ = [("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("p", ctypes.c_float),
+                ("bias", ctypes.c_void_p)]
+
+
 class ARError(RuntimeError):
     def __init__(self, status: int, call: str):
         self.status = status
@@ -84,6 +90,15 @@ def lib() -> ctypes.CDLL:
         L.ar_wire_pack.restype = i
         L.ar_reduce_host_noalloc.argtypes = [pp, pp, i, sz, i, i, vp]
         L.ar_reduce_host_noalloc.restype = i
+        dp, szp = ctypes.POINTER(ArDropout), ctypes.POINTER(sz)
+        L.ar_reduce_dropout.argtypes = [pp, pp, i, lp, dp, i, i, vp]
+        L.ar_reduce_dropout.restype = i
+        L.ar_check_dropout.argtypes = [i, pp, pp, i, lp, dp, sz, i, i]
+        L.ar_check_dropout.restype = i
+        L.ar_reduce_dropout_grad.argtypes = [vp, pp, i, lp, dp, vp, vp, vp, sz, i, vp]
+        L.ar_reduce_dropout_grad.restype = i
+        L.ar_reduce_dropout_grad_workspace.argtypes = [lp, i, szp]
+        L.ar_reduce_dropout_grad_workspace.restype = i
         _lib = L
     return _lib
 
@@ -324,27 +339,34 @@ def make_layout(ne0, ne1, src_row_bytes=None, dst_row_bytes=None, residual=None,
     return L
 
 
+def _check_reach(srcs, dsts, layout, dst_dtype, call):
+    """The rows of every CUDA tensor of an ar_layout call lie inside its storage."""
+    es = ESIZE[_dtype_code(dst_dtype)]
+    ne0, ne1 = layout.ne0, layout.ne1
+    if ne0 * ne1 == 0:
+        return
+
+    def need(stride):
+        return (ne1 - 1) * stride + ne0 * es
+    for kind, xs, rows in (("source", srcs, layout.src_row_bytes), ("destination", dsts, layout.dst_row_bytes)):
+        for k, x in enumerate(xs):
+            reach = _reach(x)
+            n = need(rows[k] if rows else ne0 * es)
+            if reach is not None and reach < n:
+                raise ValueError(f"{call}: {kind} {k} reaches {reach} bytes, its rows span {n}")
+    res = getattr(layout, "_residual_obj", None)
+    reach = _reach(res)
+    if reach is not None:
+        n = ne0 * es if layout.residual_row_bytes == 0 else need(layout.residual_row_bytes)
+        if reach < n:
+            raise ValueError(f"{call}: the residual reaches {reach} bytes, its rows span {n}")
+
+
 def ar_reduce_ex(srcs, dsts, layout: ArLayout, dst_dtype, wire_dtype="bf16", stream=None) -> None:
     """Reduction over an ar_layout (row strides, inactive ranks as None
     sources, residual or bias).  The rows of each CUDA tensor must lie inside
     its storage."""
-    es = ESIZE[_dtype_code(dst_dtype)]
-    ne0, ne1 = layout.ne0, layout.ne1
-    if ne0 * ne1:
-        def need(stride):
-            return (ne1 - 1) * stride + ne0 * es
-        for kind, xs, rows in (("source", srcs, layout.src_row_bytes), ("destination", dsts, layout.dst_row_bytes)):
-            for k, x in enumerate(xs):
-                reach = _reach(x)
-                n = need(rows[k] if rows else ne0 * es)
-                if reach is not None and reach < n:
-                    raise ValueError(f"ar_reduce_ex: {kind} {k} reaches {reach} bytes, its rows span {n}")
-        res = getattr(layout, "_residual_obj", None)
-        reach = _reach(res)
-        if reach is not None:
-            n = ne0 * es if layout.residual_row_bytes == 0 else need(layout.residual_row_bytes)
-            if reach < n:
-                raise ValueError(f"ar_reduce_ex: the residual reaches {reach} bytes, its rows span {n}")
+    _check_reach(srcs, dsts, layout, dst_dtype, "ar_reduce_ex")
     _check(lib().ar_reduce_ex(_ptrs(srcs), _ptrs(dsts), len(dsts), ctypes.byref(layout), _dtype_code(dst_dtype),
                               _dtype_code(wire_dtype), _stream(stream)), "ar_reduce_ex")
 
@@ -381,3 +403,91 @@ def ar_reduce_host_noalloc(h_srcs, h_dsts, nelem=None, dst_dtype=None, wire_dtyp
     _checked(h_dsts, nelem, dcode, "host", "ar_reduce_host_noalloc")
     _check(lib().ar_reduce_host_noalloc(_ptrs(h_srcs), _ptrs(h_dsts), len(h_dsts), nelem, dcode,
                                         _dtype_code(wire_dtype), _stream(stream)), "ar_reduce_host_noalloc")
+
+
+# ---- training operators ------------------------------------------------------
+
+def _typed_row(x, n, dtype, name, call):
+    """A device row (tensor or address) of at least n elements of a torch dtype."""
+    if x is None or isinstance(x, int):
+        return
+    import torch
+    want = {AR_F32: torch.float32, AR_F16: torch.float16, AR_BF16: torch.bfloat16}[dtype]
+    if x.device.type != "cuda":
+        raise TypeError(f"{call}: {name} is a {x.device.type} tensor, a device buffer is needed")
+    if x.dtype != want or not x.is_contiguous() or x.numel() < n:
+        raise ValueError(f"{call}: {name} needs {n} contiguous elements of {want}")
+
+
+def _workspace(need, given, stream, call):
+    """(tensor or address, bytes) of a call's workspace: the caller's, or one
+    from torch's allocator on the stream that will use it."""
+    if need == 0:
+        return None, 0
+    if given is not None:
+        if isinstance(given, int):
+            return given, need
+        if given.device.type != "cuda" or not given.is_contiguous():
+            raise TypeError(f"{call}: the workspace has to be a contiguous device tensor")
+        return given, given.numel() * given.element_size()
+    import torch
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device="cuda"), need
+    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):
+        return torch.empty(need, dtype=torch.uint8, device="cuda"), need
+
+
+def make_dropout(p, seed, offset=0, bias=None) -> ArDropout:
+    """An ar_dropout: probability ``p`` of dropping an element, the 64-bit
+    ``seed``, the 64-bit ``offset`` that tells calls under one seed apart, and
+    an optional bias row added before the dropout."""
+    if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 64:
+        raise ValueError("make_dropout: seed and offset are unsigned 64-bit numbers")
+    d = ArDropout(seed, offset, p, _ptr(bias))
+    d._bias_obj = bias  # kept alive, and for the binding's checks
+    return d
+
+
+def ar_reduce_dropout(srcs, dsts, layout: ArLayout, dropout: ArDropout, dst_dtype, wire_dtype="bf16",
+                      stream=None) -> None:
+    """ar_reduce_ex with bias and dropout between the rank sum and the
+    residual; the mask is a function of the dropout's seed and offset."""
+    _check_reach(srcs, dsts, layout, dst_dtype, "ar_reduce_dropout")
+    dcode = _dtype_code(dst_dtype)
+    _typed_row(getattr(dropout, "_bias_obj", None), layout.ne0, dcode, "the bias", "ar_reduce_dropout")
+    _check(lib().ar_reduce_dropout(_ptrs(srcs), _ptrs(dsts), len(dsts), ctypes.byref(layout), ctypes.byref(dropout),
+                                   dcode, _dtype_code(wire_dtype), _stream(stream)), "ar_reduce_dropout")
+
+
+def ar_check_dropout(R, srcs, dsts, layout: ArLayout, dropout: ArDropout, max_elems, dst_dtype, wire_dtype) -> int:
+    """Host-only validation of an ar_reduce_dropout call; returns the status."""
+    return lib().ar_check_dropout(R, _ptrs(srcs), _ptrs(dsts), len(dsts), ctypes.byref(layout),
+                                  ctypes.byref(dropout), max_elems, _dtype_code(dst_dtype), _dtype_code(wire_dtype))
+
+
+def ar_reduce_dropout_grad_workspace(layout: ArLayout, n_sums: int) -> int:
+    """Workspace bytes of an ar_reduce_dropout_grad call with ``n_sums`` of
+    dbias and dresidual."""
+    n = ctypes.c_size_t(0)
+    _check(lib().ar_reduce_dropout_grad_workspace(ctypes.byref(layout), n_sums, ctypes.byref(n)),
+           "ar_reduce_dropout_grad_workspace")
+    return n.value
+
+
+def ar_reduce_dropout_grad(dy, dxs, layout: ArLayout, dropout: ArDropout, dst_dtype, dbias=None, dresidual=None,
+                           workspace=None, stream=None) -> None:
+    """The backward pass of ar_reduce_dropout: the partials' gradient into
+    every tensor of ``dxs``, and, where asked for, the float32 gradients of
+    the bias row and of a broadcast residual row.  ``workspace`` defaults to
+    one from torch's allocator."""
+    call = "ar_reduce_dropout_grad"
+    _check_reach([dy], dxs, layout, dst_dtype, call)
+    _typed_row(dbias, layout.ne0, AR_F32, "dbias", call)
+    _typed_row(dresidual, layout.ne0, AR_F32, "dresidual", call)
+    n_sums = (dbias is not None) + (dresidual is not None)
+    need = ar_reduce_dropout_grad_workspace(layout, n_sums) if n_sums else 0
+    ws, ws_bytes = _workspace(need, workspace, stream, call)
+    _check(lib().ar_reduce_dropout_grad(_ptr(dy), _ptrs(dxs), len(dxs), ctypes.byref(layout), ctypes.byref(dropout),
+                                        _ptr(dbias), _ptr(dresidual), _ptr(ws), ws_bytes, _dtype_code(dst_dtype),
+                                        _stream(stream)), call)

@@ -19,9 +19,11 @@
 #include <cstring>
 #include <mutex>
 
+#include "ar_context.h"
 #include "ar_dispatch.h"
 
 using tps::ArParams;
+using tps::launch_dependent;
 
 namespace {
 
@@ -216,28 +218,6 @@ const char *variant_name(int v) {
         case AR_VARIANT_TMA: return "tma";
         default: return "auto";
     }
-}
-
-// Launch a kernel that runs griddepcontrol.launch_dependents and
-// griddepcontrol.wait before it loads or stores anything: as a programmatic
-// dependent of the kernel before it on the stream when `pdl`, else plainly.
-template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*fn)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
-                             bool pdl, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    // Not on the default streams: their implicit ordering against other
-    // streams is left exactly as a plain launch has it.
-    const bool default_stream = stream == nullptr || stream == cudaStreamLegacy || stream == cudaStreamPerThread;
-    cfg.numAttrs = (pdl && !default_stream) ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
 int grid_cap(long long want, long long cap) {
@@ -485,6 +465,26 @@ int reduce_host_direct_locked(const void *const *h_srcs, void *const *h_dsts, in
 }
 
 }  // namespace
+
+namespace tps {
+
+std::mutex &context_mutex() { return g_mu; }
+
+bool current_context(CallContext *out) {
+    if (!g_ctx.ready) return false;
+    *out = CallContext{g_ctx.R,        g_ctx.max_elems,         g_ctx.device,    g_ctx.sm_count,
+                       g_ctx.pdl != 0, g_ctx.fault_inject != 0, g_ctx.dev_status};
+    return true;
+}
+
+int check_launch_device(const CallContext &c) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return AR_ERR_CUDA;
+    if (dev != c.device) return AR_ERR_INVALID_ARG;
+    return c.fault_inject ? AR_ERR_CUDA : AR_OK;
+}
+
+}  // namespace tps
 
 extern "C" {
 
