@@ -439,6 +439,68 @@ int ar_reduce_dropout_grad(const void *dy, void *const *dxs, int n_dxs, const ar
  * dresidual given (host only, needs no context). */
 int ar_reduce_dropout_grad_workspace(const ar_layout *layout, int n_sums, size_t *bytes);
 
+/*
+ * Softmax cross entropy against an output matrix whose vocabulary rows are
+ * split into pieces (one per rank), without keeping the logits:
+ *   z[t][v] = sum_i hidden[t][i] * W[v][i]        (W: the pieces one after another)
+ *   lse[t]  = log sum_v exp(z[t][v])
+ *   loss[t] = lse[t] - z[t][targets[t]]
+ * A token whose target is ignore_index has loss 0 and adds nothing to any
+ * gradient, whatever its hidden state holds (infinities and NaN included); a
+ * target that is neither ignore_index nor a row of the vocabulary gives the
+ * loss NaN and no gradient.  Products of 16-bit types are summed in float.
+ */
+typedef struct {
+    size_t rows;                      /* tokens; rows * dim <= max_elems */
+    size_t dim;                       /* elements of a hidden state, >= 1 */
+    const void *hidden;               /* rows x dim of dtype */
+    int64_t hidden_row_bytes;         /* row stride (>= dim elements, whole elements); 0: packed */
+    int n_pieces;                     /* 1..16 */
+    const size_t *piece_rows;         /* n_pieces vocabulary row counts; some may be 0, their sum not */
+    const void *const *weights;       /* n_pieces matrices, piece_rows[r] x dim of dtype */
+    const int64_t *weight_row_bytes;  /* n_pieces row strides, or NULL: packed */
+    const int64_t *targets;           /* device, rows global vocabulary rows (of the pieces in order) */
+    int64_t ignore_index;
+    int dtype;                        /* ar_dtype of hidden, weights and their gradients */
+} ar_vocab;
+
+/*
+ * ar_vocab_loss -- enqueue the loss of every token.
+ *   loss, lse   rows floats each (device); lse is what the gradient call needs.
+ *   workspace   256-byte aligned device memory of at least ar_vocab_workspace
+ *               bytes; its contents do not matter.
+ * Outputs and workspace may overlap neither each other nor an input.
+ */
+int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+
+/*
+ * ar_vocab_loss_grad -- the gradients, the logits computed anew:
+ *   d[t][v]         = dloss[t] * (exp(z[t][v] - lse[t]) - [v == targets[t]])
+ *   dhidden[r]      = d over piece r's columns times weights[r]     rows x dim
+ *   dweights[r]     = (d over piece r's columns)^T times hidden     piece_rows[r] x dim
+ * The dhidden[r] are partials: their sum over r, which ar_reduce takes, is the
+ * gradient of the hidden states.
+ *   lse       as ar_vocab_loss wrote it for the same hidden states and weights.
+ *   dloss     rows floats (device), the gradient of each token's loss.
+ *   dhidden   n_pieces matrices of dtype at dhidden_row_bytes (NULL: packed),
+ *             or NULL: not wanted.
+ *   dweights  n_pieces matrices of dtype at dweight_row_bytes (NULL: packed),
+ *             or NULL: not wanted.
+ * Every output is written whole.  The same call gives the same bits.
+ */
+int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, void *const *dhidden,
+                       const int64_t *dhidden_row_bytes, void *const *dweights, const int64_t *dweight_row_bytes,
+                       void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Host-only checks of an ar_vocab (no CUDA call). */
+int ar_check_vocab(const ar_vocab *v, size_t max_elems);
+
+/* Workspace of ar_vocab_loss (grad = 0) or ar_vocab_loss_grad (grad = 1) for
+ * these arguments (host only; pointers are not read, their alignment and the
+ * strides count). */
+int ar_vocab_workspace(const ar_vocab *v, int grad, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

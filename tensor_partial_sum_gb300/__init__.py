@@ -12,5 +12,6 @@ from .ar import (  # noqa: F401
     ar_status_string, library_path, ArLayout, make_layout, ar_reduce_ex, ar_check_layout, ar_wire_pack,
     ar_reduce_host_noalloc, AR_NOALLOC_SCRATCH_BYTES, PreparedReduce,
     ArDropout, make_dropout, ar_reduce_dropout, ar_check_dropout, ar_reduce_dropout_grad,
-    ar_reduce_dropout_grad_workspace,
+    ar_reduce_dropout_grad_workspace, ArVocab, make_vocab, ar_check_vocab, ar_vocab_workspace, ar_vocab_loss,
+    ar_vocab_loss_grad,
 )

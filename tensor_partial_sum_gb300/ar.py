@@ -43,6 +43,15 @@ class ArDropout(ctypes.Structure):
                 ("bias", ctypes.c_void_p)]
 
 
+class ArVocab(ctypes.Structure):
+    """ar_vocab of include/ar.h."""
+    _fields_ = [("rows", ctypes.c_size_t), ("dim", ctypes.c_size_t), ("hidden", ctypes.c_void_p),
+                ("hidden_row_bytes", ctypes.c_int64), ("n_pieces", ctypes.c_int),
+                ("piece_rows", ctypes.POINTER(ctypes.c_size_t)), ("weights", ctypes.c_char_p),
+                ("weight_row_bytes", ctypes.POINTER(ctypes.c_int64)), ("targets", ctypes.c_void_p),
+                ("ignore_index", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
 class ARError(RuntimeError):
     def __init__(self, status: int, call: str):
         self.status = status
@@ -99,6 +108,15 @@ def lib() -> ctypes.CDLL:
         L.ar_reduce_dropout_grad.restype = i
         L.ar_reduce_dropout_grad_workspace.argtypes = [lp, i, szp]
         L.ar_reduce_dropout_grad_workspace.restype = i
+        vcp, i64p = ctypes.POINTER(ArVocab), ctypes.POINTER(i64)
+        L.ar_vocab_loss.argtypes = [vcp, vp, vp, vp, sz, vp]
+        L.ar_vocab_loss.restype = i
+        L.ar_vocab_loss_grad.argtypes = [vcp, vp, vp, pp, i64p, pp, i64p, vp, sz, vp]
+        L.ar_vocab_loss_grad.restype = i
+        L.ar_check_vocab.argtypes = [vcp, sz]
+        L.ar_check_vocab.restype = i
+        L.ar_vocab_workspace.argtypes = [vcp, i, szp]
+        L.ar_vocab_workspace.restype = i
         _lib = L
     return _lib
 
@@ -491,3 +509,97 @@ def ar_reduce_dropout_grad(dy, dxs, layout: ArLayout, dropout: ArDropout, dst_dt
     _check(lib().ar_reduce_dropout_grad(_ptr(dy), _ptrs(dxs), len(dxs), ctypes.byref(layout), ctypes.byref(dropout),
                                         _ptr(dbias), _ptr(dresidual), _ptr(ws), ws_bytes, _dtype_code(dst_dtype),
                                         _stream(stream)), call)
+
+
+def _matrix(x, rows, dim, dtype, name, call):
+    """Row stride in bytes of a device matrix [rows, dim] with adjacent columns."""
+    if x.device.type != "cuda":
+        raise TypeError(f"{call}: {name} is a {x.device.type} tensor, a device buffer is needed")
+    if x.dtype != dtype:
+        raise TypeError(f"{call}: {name} is {x.dtype}, the hidden states are {dtype}")
+    if x.dim() != 2 or x.shape[0] != rows or x.shape[1] != dim or (dim > 1 and x.stride(1) != 1):
+        raise ValueError(f"{call}: {name} has to be [{rows}, {dim}] with adjacent columns")
+    return x.stride(0) * x.element_size() if rows > 1 else dim * x.element_size()
+
+
+def _vector(x, n, dtype, name, call):
+    if x.device.type != "cuda":
+        raise TypeError(f"{call}: {name} is a {x.device.type} tensor, a device buffer is needed")
+    if x.dtype != dtype or x.dim() != 1 or x.numel() != n or not x.is_contiguous():
+        raise ValueError(f"{call}: {name} has to be {n} contiguous elements of {dtype}")
+
+
+def make_vocab(hidden, weights, targets, ignore_index=-100, call="make_vocab") -> ArVocab:
+    """An ar_vocab of torch tensors: ``hidden`` [tokens, dim], one [rows, dim]
+    matrix per vocabulary piece in ``weights``, and int64 ``targets``
+    [tokens] that count through the pieces in order."""
+    import torch
+    if hidden.dim() != 2:
+        raise ValueError(f"{call}: hidden has to be [tokens, dim]")
+    T, D = hidden.shape
+    if not 1 <= len(weights) <= AR_MAX_RANKS:
+        raise ValueError(f"{call}: {len(weights)} vocabulary pieces, 1 to {AR_MAX_RANKS} are possible")
+    _vector(targets, T, torch.int64, "targets", call)
+    v = ArVocab()
+    v.rows, v.dim, v.hidden = T, D, hidden.data_ptr()
+    v.hidden_row_bytes = _matrix(hidden, T, D, hidden.dtype, "hidden", call)
+    n = v.n_pieces = len(weights)
+    v.weight_row_bytes = (ctypes.c_int64 * n)(*[_matrix(w, w.shape[0], D, hidden.dtype, f"weights[{r}]", call)
+                                                for r, w in enumerate(weights)])
+    v.piece_rows = (ctypes.c_size_t * n)(*[w.shape[0] for w in weights])
+    v._pointers = _ptrs(weights)
+    v.weights = v._pointers
+    v.targets, v.ignore_index = targets.data_ptr(), ignore_index
+    v.dtype = _dtype_code(hidden.dtype)
+    v._keep = (hidden, list(weights), targets)
+    return v
+
+
+def ar_check_vocab(v: ArVocab, max_elems) -> int:
+    """Host-only checks of an ar_vocab; returns the status."""
+    return lib().ar_check_vocab(ctypes.byref(v), max_elems)
+
+
+def ar_vocab_workspace(v: ArVocab, grad: bool) -> int:
+    """Workspace bytes of ar_vocab_loss or (``grad``) ar_vocab_loss_grad."""
+    n = ctypes.c_size_t(0)
+    _check(lib().ar_vocab_workspace(ctypes.byref(v), int(grad), ctypes.byref(n)), "ar_vocab_workspace")
+    return n.value
+
+
+def ar_vocab_loss(hidden, weights, targets, loss, lse, ignore_index=-100, workspace=None, stream=None) -> None:
+    """Softmax cross entropy of every token against a vocabulary split into
+    the ``weights`` pieces, without keeping the logits: float32 ``loss`` and
+    ``lse`` (log-sum-exp) of each token.  ``workspace`` defaults to one from
+    torch's allocator."""
+    import torch
+    call = "ar_vocab_loss"
+    v = make_vocab(hidden, weights, targets, ignore_index, call)
+    _vector(loss, v.rows, torch.float32, "loss", call)
+    _vector(lse, v.rows, torch.float32, "lse", call)
+    ws, ws_bytes = _workspace(ar_vocab_workspace(v, False), workspace, stream, call)
+    _check(lib().ar_vocab_loss(ctypes.byref(v), loss.data_ptr(), lse.data_ptr(), _ptr(ws), ws_bytes, _stream(stream)),
+           call)
+
+
+def ar_vocab_loss_grad(hidden, weights, targets, lse, dloss, dhidden=None, dweights=None, ignore_index=-100,
+                       workspace=None, stream=None) -> None:
+    """The gradients of ar_vocab_loss: one partial gradient of the hidden
+    states per piece into ``dhidden`` (ar_reduce sums them), each piece's
+    weight gradient into ``dweights``; either may be None.  ``lse`` is
+    ar_vocab_loss's, ``dloss`` the float32 gradient of each token's loss."""
+    import torch
+    call = "ar_vocab_loss_grad"
+    v = make_vocab(hidden, weights, targets, ignore_index, call)
+    _vector(lse, v.rows, torch.float32, "lse", call)
+    _vector(dloss, v.rows, torch.float32, "dloss", call)
+    n = v.n_pieces
+    strides = []
+    for name, xs, rows in (("dhidden", dhidden, [v.rows] * n), ("dweights", dweights, [w.shape[0] for w in weights])):
+        if xs is not None and len(xs) != n:
+            raise ValueError(f"{call}: {len(xs)} tensors in {name}, {n} vocabulary pieces")
+        strides.append(None if xs is None else (ctypes.c_int64 * n)(
+            *[_matrix(x, m, v.dim, hidden.dtype, f"{name}[{r}]", call) for r, (x, m) in enumerate(zip(xs, rows))]))
+    ws, ws_bytes = _workspace(ar_vocab_workspace(v, True), workspace, stream, call)
+    _check(lib().ar_vocab_loss_grad(ctypes.byref(v), lse.data_ptr(), dloss.data_ptr(), _ptrs(dhidden), strides[0],
+                                    _ptrs(dweights), strides[1], _ptr(ws), ws_bytes, _stream(stream)), call)
