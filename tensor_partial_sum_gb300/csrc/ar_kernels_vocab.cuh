@@ -1,184 +1,682 @@
 // Device code of ar_vocab_loss and ar_vocab_loss_grad.
+//
+// With logits z = H W^T, lse_t = log sum_v exp z_tv and per-token factors g_t,
+//     loss_t = lse_t - z_t[y_t],     D = g (softmax(z) - onehot(y)),
+//     dH_r = D_r W_r,                dW_r = D_r^T H.
+// Three matrix products with reductions of length dim, vocabulary and tokens.
+// One kernel does all of them, on a pair of CTAs, and differs in what it does
+// with a finished 256x256 tile:
+//   kStats   keeps each row's maximum and sum of exponentials (and the
+//            target's logit): the logits never leave the chip;
+//   kDlogits turns a tile of recomputed logits into a tile of D, held in
+//            16 bits for one chunk of the vocabulary;
+//   kGrads   stores tiles of dH and dW.
+// Small kernels around it list the counted tokens, pack rows that the tiled
+// copies cannot read in place, and join partial results.
+//
+// Float32 inputs go through the same tensor cores: x = x1 + x2 + x3 with three
+// bf16 parts of eight bits each (exact), and the six largest of the nine
+// products; the ones left out are below 2^-21 of the whole, 2^-24 on average.
 #pragma once
 
 #include "ar_kernels.cuh"
+#include "ar_umma.cuh"
 
 namespace tps {
 
-// A matrix read element by element: element (i, j) at base + i * row + j * col (in elements).
-struct VocabMat {
-    const void *base;
-    long long row, col;
-    const unsigned char *live;  // 0: column j counts as zeros, whatever it holds (nullptr: all count)
+enum VocabMode { kStats = 0, kDlogits = 1, kGrads = 2 };
+
+constexpr int kMaxSegs = 16;
+constexpr int kVM = 256;      // rows of a tile, 128 in each CTA
+constexpr int kVN = 256;      // columns of a tile (at most), half of B's rows in each CTA
+constexpr int kVK = 64;       // elements of the reduction per stage: 128 bytes
+constexpr int kVStages = 6;
+constexpr int kVHalf = 128 * kVK * 2;       // bytes of one operand's stage in one CTA
+constexpr int kVStage = 2 * kVHalf;
+constexpr int kVEpilogueWarps = 8;
+constexpr int kVThreads = 128 + 32 * kVEpilogueWarps;
+constexpr unsigned kVTmemCols = 512;        // two accumulators of 256 columns
+constexpr size_t kVSmem = static_cast<size_t>(kVStages) * kVStage + 1024 + 256;
+
+// One counted token of a gradient call, in the order of the list.
+struct VocabRow {
+    float lse, g;   // g: dloss / max |dloss| (times 2^14 for f16)
+    long long y;    // global vocabulary row of the target
 };
 
-constexpr int kVT = 64;  // tile edge of the plain product below
-constexpr int kVK = 16;
+// What the list kernel leaves for the others.
+struct VocabList {
+    int live;      // counted tokens
+    float unscale; // what undoes the scaling of VocabRow::g
+};
 
-// acc[4][4] of a 64x64 tile of A B^T (A [M][K], B [N][K]) for a thread of 256: rows 4 ty.., columns 4 tx..
-template <int Ta, int Tb>
-__device__ __forceinline__ void tile_product(const VocabMat &A, const VocabMat &B, size_t M, size_t N, size_t K, size_t m0,
-                                             size_t n0, float (&acc)[4][4]) {
-    __shared__ float as[kVK][kVT + 1], bs[kVK][kVT + 1];
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    for (size_t k0 = 0; k0 < K; k0 += kVK) {
-        for (int e = threadIdx.x; e < kVT * kVK; e += 256) {
-            const int i = e / kVK, k = e % kVK;
-            as[k][i] = m0 + i < M && k0 + k < K
-                           ? load_elem<Ta, false>(A.base, static_cast<long long>(m0 + i) * A.row + static_cast<long long>(k0 + k) * A.col)
-                           : 0.0f;
-            bs[k][i] = n0 + i < N && k0 + k < K && (!B.live || B.live[k0 + k])
-                           ? load_elem<Tb, false>(B.base, static_cast<long long>(n0 + i) * B.row + static_cast<long long>(k0 + k) * B.col)
-                           : 0.0f;
+// One vocabulary segment of a launch: (part of) a piece.
+struct VocabSeg {
+    long long first;       // global index of its first vocabulary row
+    int rows;
+    int tile0;             // first of its column tiles (kStats, kDlogits), of its dW tiles (kGrads)
+    long long col0;        // its first column of D
+    char *dh;              // kGrads: the piece's dH (nullptr: not now), rows dh_row bytes apart
+    long long dh_row;
+    char *dw;              // kGrads: dW of the segment's first row, nullptr: not wanted
+    long long dw_row;
+};
+
+struct VocabGemmParams {
+    CUtensorMap b_map[kMaxSegs];  // W of each segment: K-major (kStats, kDlogits) or MN-major (kGrads)
+    CUtensorMap a_map;            // H (kStats, kDlogits) or D, K-major
+    CUtensorMap at_map;           // kGrads: D, MN-major
+    CUtensorMap ht_map;           // kGrads: H, MN-major
+    VocabSeg seg[kMaxSegs];
+    int nseg;
+    int rows;                 // tokens
+    int dim;
+    int bn;                   // columns of a tile, <= kVN
+    int pairs;                // products per block of K: 1, or 6 for split float32
+    int tiles;                // column tiles (kStats, kDlogits) or dW tiles (kGrads) of all segments
+    const VocabList *list;    // nullptr: all tokens, in order (kStats)
+    const long long *targets; // kStats
+    float2 *part;             // kStats: [2 * tile + half][rows]
+    float *picked;            // kStats: [rows]
+    const VocabRow *row;      // kDlogits: [live]
+    const int *index;         // kGrads: original token of list entry i
+    unsigned short *d;        // D: [parts][d_rows][d_ld]
+    long long d_ld, d_part;   // elements
+    int slices;               // kGrads: parts of the reduction over a segment's vocabulary
+    int dh_tiles;             // kGrads: column tiles of dH, 0: not wanted
+    float *sum;               // kGrads: [segment][slice][sum_rows][sum_ld] partial dH, nullptr: straight to dh
+    long long sum_rows, sum_ld;
+    int sum_begin;            // the partial sums start here rather than go on
+    unsigned *status;
+};
+
+// Part numbers of A and B in product q of a block of K, largest last so that the small ones are
+// summed while the accumulator is small (float32; the 16-bit types have one part and one product).
+__device__ __forceinline__ void pair_parts(int pairs, int q, int &a, int &b) {
+    // (1,1) (0,2) (2,0) (0,1) (1,0) (0,0)
+    a = pairs == 1 ? 0 : (0x010201 >> (4 * q)) & 0xF;
+    b = pairs == 1 ? 0 : (0x001021 >> (4 * q)) & 0xF;
+}
+
+// A tile: its place, its operands' places and its blocks of K.
+struct VocabTile {
+    int seg;
+    int m, n;        // tile row and column
+    int k0, kn;      // first block of K and their number
+    int slice;
+    bool dw;
+};
+
+// The i-th tile of a pair; false when it has no more.  kStats and kDlogits: row tiles of one column
+// tile next to one another, so that pairs that run together share W and find H in L2.  kGrads: first
+// the dH tiles (long reductions) in turn, then the dW tiles; pairs that got one dH tile fewer take as
+// many more dW tiles as cost the same.
+template <int MODE>
+__device__ __forceinline__ bool vocab_tile(const VocabGemmParams &p, int live, int i, int pair, int npairs, VocabTile &t) {
+    const int mt = (live + kVM - 1) / kVM;
+    t.slice = 0;
+    t.k0 = 0;
+    t.dw = false;
+    if constexpr (MODE != kGrads) {
+        const long long id = pair + static_cast<long long>(i) * npairs;
+        if (mt == 0 || id >= static_cast<long long>(p.tiles) * mt) return false;
+        const int j = static_cast<int>(id / mt);
+        t.m = static_cast<int>(id % mt);
+        t.seg = 0;
+        while (t.seg + 1 < p.nseg && p.seg[t.seg + 1].tile0 <= j) ++t.seg;
+        t.n = j - p.seg[t.seg].tile0;
+        t.kn = (p.dim + kVK - 1) / kVK;
+        return true;
+    } else {
+        const int per_seg = p.slices * p.dh_tiles * mt;
+        const int n_long = p.nseg * per_seg;
+        const int rem = n_long % npairs;
+        const int mine = n_long / npairs + (pair < rem);
+        if (i < mine) {
+            int id = pair + i * npairs;
+            t.seg = id / per_seg;
+            id -= t.seg * per_seg;
+            t.m = id % mt;
+            id /= mt;
+            t.n = id % p.dh_tiles;
+            t.slice = id / p.dh_tiles;
+            const int kb = (p.seg[t.seg].rows + kVK - 1) / kVK, per = (kb + p.slices - 1) / p.slices;
+            t.k0 = t.slice * per;
+            t.kn = max(0, min(per, kb - t.k0));
+            return true;
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kVK; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[k][4 * ty + i], bs[k][4 * tx + j], acc[i][j]);
-        __syncthreads();
+        i -= mine;
+        const int kw = max(1, (live + kVK - 1) / kVK);
+        const int kl = (p.seg[0].rows + kVK * p.slices - 1) / (kVK * p.slices);
+        const int behind = rem ? npairs - rem : 0;
+        int extra = behind ? (kl + kw / 2) / kw : 0;
+        if (static_cast<long long>(extra) * behind > p.tiles) extra = p.tiles / behind;
+        const int first = pair >= rem && rem ? extra : 0;
+        long long id;
+        if (i < first) {
+            id = static_cast<long long>(pair - rem) * extra + i;
+        } else {
+            id = static_cast<long long>(extra) * behind + pair + static_cast<long long>(i - first) * npairs;
+        }
+        if (id >= p.tiles) return false;
+        const int nt = (p.dim + p.bn - 1) / p.bn;
+        const int j = static_cast<int>(id / nt);
+        t.n = static_cast<int>(id % nt);
+        t.seg = 0;
+        while (t.seg + 1 < p.nseg && p.seg[t.seg + 1].tile0 <= j) ++t.seg;
+        t.m = j - p.seg[t.seg].tile0;
+        t.kn = (live + kVK - 1) / kVK;
+        t.dw = true;
+        return true;
     }
 }
 
-struct VocabStatParams {
-    VocabMat h, w;
-    size_t rows, vocab, dim;      // tokens, vocabulary rows of this piece
-    long long first;              // global index of the piece's first row
-    const long long *targets;
-    float2 *part;                 // [tile][rows]: running maximum and sum of exponentials over the tile
-    float *picked;                // [rows]: the target's logit
-    unsigned tile0;               // number of the piece's first tile
-};
-
-// Logits of a tile, reduced to each row's maximum and sum of exp(z - maximum).
+// 32 values of a row to `n` (at most 32) elements of T at `out`: whole vectors where the row allows.
 template <int T>
-__global__ void __launch_bounds__(256) ar_vocab_stat_kernel(const __grid_constant__ VocabStatParams p) {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const size_t m0 = static_cast<size_t>(blockIdx.y) * kVT, n0 = static_cast<size_t>(blockIdx.x) * kVT;
-    float acc[4][4] = {};
-    tile_product<T, T>(p.h, p.w, p.rows, p.vocab, p.dim, m0, n0, acc);
+__device__ __forceinline__ void store_row32(char *out, const float (&v)[32], int n) {
+    constexpr int W = T == kF32 ? 32 : 16;
+    if (n >= 32 && reinterpret_cast<uintptr_t>(out) % 16 == 0) {
+        uint32_t w[W];
+        word_pack<T, W>(v, w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const size_t t = m0 + 4 * ty + i;
-        float m = -INFINITY, s = 0.0f;
+        for (int k = 0; k < W; k += 4)
+            *reinterpret_cast<uint4 *>(out + 4 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+        return;
+    }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (n0 + 4 * tx + j < p.vocab) m = fmaxf(m, acc[i][j]);
-        for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        const float base = fabsf(m) == INFINITY ? 0.0f : m;
+    for (int k = 0; k < 32; ++k)
+        if (k < n) store_elem<T>(out, k, v[k]);
+}
+
+// The three bf16 parts of two floats, eight bits each, packed in pairs.
+__device__ __forceinline__ void split2(float a, float b, uint32_t (&w)[3]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (n0 + 4 * tx + j < p.vocab) s += expf(acc[i][j] - base);
-        for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-        if (t >= p.rows) continue;
-        if (tx == 0) p.part[(p.tile0 + blockIdx.x) * p.rows + t] = make_float2(m, s);
-        const long long at = p.targets[t] - p.first;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (at == static_cast<long long>(n0 + 4 * tx + j) && n0 + 4 * tx + j < p.vocab) p.picked[t] = acc[i][j];
+    for (int q = 0; q < 3; ++q) {
+        const uint32_t ha = __float_as_uint(a) & 0xFFFF0000u, hb = __float_as_uint(b) & 0xFFFF0000u;
+        w[q] = (ha >> 16) | hb;
+        // an infinity or NaN is all in the first part
+        a = fabsf(a) <= 3.402823466e38f ? a - __uint_as_float(ha) : 0.0f;
+        b = fabsf(b) <= 3.402823466e38f ? b - __uint_as_float(hb) : 0.0f;
     }
 }
+
+// ---- the product kernel ---------------------------------------------------------
+//
+// Warps: 0 copies tiles in, 1 issues the products (in the leader), 2 owns the
+// tensor memory, 4..11 turn accumulators into results.  A stage holds 128 rows
+// of A and 128 rows of B for 64 elements of K in each CTA; both CTAs' copies
+// count on the leader's `full` barrier, and a finished product frees the stage
+// in both.  Two accumulators alternate, so the tensor cores work on the next
+// tile while the epilogue reads the last.  Every wait is bounded; one that
+// runs out sets bit 1 of the status word, and the pair winds down.
+template <int MODE, int T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
+    ar_vocab_gemm_kernel(const __grid_constant__ VocabGemmParams p) {
+    extern __shared__ unsigned char raw[];
+    const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
+    // barriers behind the stages
+    const unsigned bars = base + kVStages * kVStage;
+    const unsigned full = bars, empty = bars + 8 * kVStages, tfull = bars + 16 * kVStages, tempty = tfull + 16;
+    const unsigned tmem_slot = tempty + 16, abort_slot = tmem_slot + 4, drain = tmem_slot + 8;
+    volatile unsigned *abort_flag = reinterpret_cast<volatile unsigned *>(raw + (abort_slot - smem_u32(raw)));
+    const unsigned rank = cluster_rank();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
+
+    pdl_launch_dependents();
+    auto init = [](unsigned bar, unsigned count) {
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kVStages; ++s) init(full + 8 * s, 1), init(empty + 8 * s, 1);
+        for (int a = 0; a < 2; ++a) init(tfull + 8 * a, 1), init(tempty + 8 * a, 2 * kVEpilogueWarps);
+        init(drain, 1);
+        *abort_flag = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) tmem_alloc(tmem_slot, kVTmemCols);
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tmem_fence_after();
+    const unsigned tmem = *reinterpret_cast<volatile unsigned *>(raw + (tmem_slot - smem_u32(raw)));
+    pdl_wait();  // the kernel before this one on the stream has finished
+    asm volatile("fence.proxy.async.global;" ::: "memory");  // its plain stores, before this one's copies
+    const int live = p.list ? p.list->live : p.rows;
+
+    auto give_up = [&] {
+        atomicOr(p.status, 2u);
+        *abort_flag = 1u;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- copies: this CTA's half of each operand ----
+            unsigned it = 0;  // stages filled so far
+            bool ok = true;
+            VocabTile t;
+            for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i) {
+                const CUtensorMap *am, *bm;
+                int ay, ax, by, bx;  // first element of this CTA's rows (columns) at block 0 of K
+                const int arow = t.m * kVM + static_cast<int>(rank) * 128;
+                const int brow = t.n * p.bn + static_cast<int>(rank) * (p.bn / 2);
+                const bool a_mn = MODE == kGrads && t.dw, b_mn = MODE == kGrads;
+                if constexpr (MODE != kGrads) {
+                    am = &p.a_map, bm = &p.b_map[t.seg];
+                    ax = 0, ay = arow, bx = 0, by = brow;
+                } else if (t.dw) {
+                    am = &p.at_map, bm = &p.ht_map;
+                    ax = static_cast<int>(p.seg[t.seg].col0) + arow, ay = 0, bx = brow, by = 0;
+                } else {
+                    am = &p.a_map, bm = &p.b_map[t.seg];
+                    ax = static_cast<int>(p.seg[t.seg].col0), ay = arow, bx = brow, by = 0;
+                }
+                const unsigned bytes = 2 * (kVHalf + static_cast<unsigned>(p.bn / 2) * kVK * 2);
+                for (int kq = 0; kq < t.kn * p.pairs; ++kq, ++it) {
+                    const int kb = t.k0 + (p.pairs == 1 ? kq : kq / p.pairs);
+                    int pa, pb;
+                    pair_parts(p.pairs, p.pairs == 1 ? 0 : kq % p.pairs, pa, pb);
+                    const unsigned s = it % kVStages, round = it / kVStages;
+                    if (*abort_flag || (round && !mbar_wait_bounded(empty + 8 * s, (round - 1) & 1))) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    const unsigned bar = leader_addr(full + 8 * s);
+                    if (rank == 0)
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + 8 * s), "r"(bytes)
+                                     : "memory");
+                    const unsigned a = base + s * kVStage, b = a + kVHalf;
+                    const int k = kb * kVK;
+                    if (!a_mn) {
+                        tma_load_3d(a, am, bar, ax + k, ay, pa);
+                    } else {  // two chunks of 64 columns, 64 rows each
+                        tma_load_3d(a, am, bar, ax, ay + k, pa);
+                        tma_load_3d(a + 8192, am, bar, ax + 64, ay + k, pa);
+                    }
+                    if (!b_mn) {
+                        tma_load_3d(b, bm, bar, bx + k, by, pb);
+                    } else {
+                        tma_load_3d(b, bm, bar, bx, by + k, pb);
+                        if (p.bn == 256) tma_load_3d(b + 8192, bm, bar, bx + 64, by + k, pb);
+                    }
+                }
+            }
+            // the products' last arrivals have to find this CTA still here
+            for (unsigned k = it > kVStages ? it - kVStages : 0; ok && k < it; ++k)
+                if (!mbar_wait_bounded(empty + 8 * (k % kVStages), (k / kVStages) & 1)) {
+                    give_up();
+                    ok = false;
+                }
+            if (!ok && rank == 0)  // copies in flight (of both CTAs) land before the pair leaves
+                for (unsigned k = it > kVStages ? it - kVStages : 0; k < it; ++k)
+                    mbar_wait_bounded(full + 8 * (k % kVStages), (k / kVStages) & 1);
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            // ---- products ----
+            unsigned it = 0, acc_it = 0;
+            bool ok = true;
+            VocabTile t;
+            for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i, ++acc_it) {
+                const unsigned acc = acc_it % 2, use = acc_it / 2;
+                if (use && !mbar_wait_bounded(tempty + 8 * acc, (use - 1) & 1)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                const bool a_mn = MODE == kGrads && t.dw, b_mn = MODE == kGrads;
+                const uint32_t idesc = umma_idesc(T != kF16, a_mn, b_mn, static_cast<unsigned>(p.bn));
+                // 16 elements of K: 32 bytes along a K-major row, two groups of eight rows otherwise
+                const unsigned a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
+                for (int kq = 0; kq < t.kn * p.pairs; ++kq, ++it) {
+                    const unsigned s = it % kVStages;
+                    if (*abort_flag || !mbar_wait_bounded(full + 8 * s, (it / kVStages) & 1)) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    tmem_fence_after();
+                    const uint64_t a = umma_desc(base + s * kVStage, 8192), b = umma_desc(base + s * kVStage + kVHalf, 8192);
+#pragma unroll
+                    for (unsigned k = 0; k < kVK / 16; ++k)
+                        umma(tmem + acc * 256, a + k * a_step, b + k * b_step, idesc, kq > 0 || k > 0);
+                    umma_commit(empty + 8 * s);
+                }
+                if (ok) umma_commit(tfull + 8 * acc);
+            }
+            if (!ok) {  // products in flight finish before the tensor memory goes
+                umma_commit(drain);
+                mbar_wait_bounded(drain, 0);
+            }
+        }
+    } else if (warp >= 4) {
+        // ---- results: a warp reads the 32 lanes of its quarter and half of the columns ----
+        const int quarter = warp % 4, half = (warp - 4) / 4;
+        unsigned acc_it = 0;
+        VocabTile t;
+        const float unscale = MODE == kGrads && p.list ? p.list->unscale : 1.0f;
+        for (int i = 0; vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i, ++acc_it) {
+            const unsigned acc = acc_it % 2, use = acc_it / 2;
+            const int r = t.m * kVM + static_cast<int>(rank) * 128 + quarter * 32 + lane;  // row of the product
+            const int c0 = half * (p.bn / 2);                                             // first column in the tile
+            const VocabSeg &seg = p.seg[t.seg];
+            const unsigned src = tmem + acc * 256 + static_cast<unsigned>(c0) + (static_cast<unsigned>(quarter * 32) << 16);
+            long long y = -1;
+            float lse = 0.0f, g = 0.0f;
+            if constexpr (MODE == kStats) {
+                if (r < live) y = p.targets[r];
+            } else if constexpr (MODE == kDlogits) {
+                if (r < live) {
+                    const VocabRow q = p.row[r];
+                    y = q.y, lse = q.lse, g = q.g;
+                }
+            }
+            const bool ok = mbar_wait_bounded(tfull + 8 * acc, use & 1);
+            if (__any_sync(~0u, !ok || *abort_flag)) {
+                if (lane == 0) give_up();
+                break;
+            }
+            tmem_fence_after();
+            const int width = p.bn / 2;
+            if constexpr (MODE == kStats) {
+                const int col = t.n * p.bn + c0;                 // column in the segment
+                const int n = min(width, seg.rows - col);        // columns of this warp that exist
+                const long long at = y - seg.first - col;        // the target's column here, if in [0, n)
+                float m = -INFINITY, s = 0.0f;
+                for (int c = 0; c < width; c += 32) {
+                    float v[32];
+                    tmem_load32(src + c, v);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (c + k < n) top = fmaxf(top, v[k]);
+                    const float to = fmaxf(m, top);
+                    const float ref = fabsf(to) == INFINITY ? 0.0f : to;
+                    s = m == -INFINITY ? s : s * __expf((m == INFINITY ? 0.0f : m) - ref);
+                    m = to;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (c + k < n) s += __expf(v[k] - ref);
+                    if (at >= c && at < c + 32 && at < n && r < live) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (at == c + k) p.picked[r] = v[k];
+                    }
+                }
+                if (r < live) p.part[(2ll * (seg.tile0 + t.n) + half) * p.rows + r] = make_float2(m, s);
+            } else if constexpr (MODE == kDlogits) {
+                const int col = t.n * p.bn + c0;
+                const int n = min(width, seg.rows - col);
+                const long long at = y - seg.first - col;
+                unsigned short *out = p.d + static_cast<long long>(r) * p.d_ld + seg.col0 + col;
+                for (int c = 0; c < width; c += 32) {
+                    float v[32];
+                    tmem_load32(src + c, v);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float q = __expf(v[k] - lse) - (at == c + k ? 1.0f : 0.0f);
+                        v[k] = r < live && c + k < n ? q * g : 0.0f;
+                    }
+                    // rows past the list and columns past the segment hold zeros: whole blocks of K are read
+                    if constexpr (T != kF32) {
+                        uint32_t w[16];
+                        word_pack<T, 16>(v, w);
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4)
+                            *reinterpret_cast<uint4 *>(out + c + 2 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            uint32_t w[4][3];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) split2(v[k + 2 * e], v[k + 2 * e + 1], w[e]);
+#pragma unroll
+                            for (int q = 0; q < 3; ++q)
+                                *reinterpret_cast<uint4 *>(out + q * p.d_part + c + k) =
+                                    make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
+                        }
+                    }
+                }
+            } else {
+                const int col = t.n * p.bn + c0;
+                const int n = min(width, p.dim - col);
+                const bool mine = r < (t.dw ? seg.rows : live);
+                constexpr int es = Elem<T>::bytes;
+                char *out = nullptr;
+                float *sum = nullptr;
+                if (mine && t.dw) {
+                    out = seg.dw + static_cast<long long>(r) * seg.dw_row + static_cast<long long>(col) * es;
+                } else if (mine) {
+                    if (seg.dh) out = seg.dh + static_cast<long long>(p.index[r]) * seg.dh_row + static_cast<long long>(col) * es;
+                    if (p.sum)
+                        sum = p.sum + ((static_cast<long long>(t.seg) * p.slices + t.slice) * p.sum_rows + r) * p.sum_ld + col;
+                }
+                for (int c = 0; c < width; c += 32) {
+                    float v[32];
+                    if (t.kn) {
+                        tmem_load32(src + c, v);
+                    } else {  // nothing to sum over
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = 0.0f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] *= unscale;
+                    if (sum) {
+                        // rows of partial sums are whole groups of eight
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            if (c + k < n) {
+                                float4 *q = reinterpret_cast<float4 *>(sum + c + k);
+                                if (!p.sum_begin) {
+                                    const float4 o = *q;
+                                    v[k] += o.x, v[k + 1] += o.y, v[k + 2] += o.z, v[k + 3] += o.w;
+                                }
+                                if (!out) *q = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                            }
+                    }
+                    if (out && c < n) store_row32<T>(out + c * es, v, min(32, n - c));
+                }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(leader_addr(tempty + 8 * acc));
+        }
+        if constexpr (MODE == kDlogits) asm volatile("fence.proxy.async.global;" ::: "memory");
+    }
+    __syncthreads();
+    __syncwarp();
+    tmem_fence_before();
+    cluster_sync();  // neither CTA leaves or frees its tensor memory while the other may still use it
+    tmem_fence_after();
+    if (warp == 2) tmem_dealloc(tmem, kVTmemCols);
+}
+
+// ---- around the products -----------------------------------------------------------
 
 struct VocabJoinParams {
     const float2 *part;
     const float *picked;
     const long long *targets;
     long long ignore, vocab;  // vocabulary rows of all pieces
-    size_t rows;
-    unsigned tiles;
+    int rows;
+    int parts;
     float *loss, *lse;
 };
 
-// Join the tiles of each row: lse = log sum exp, loss = lse - target's logit.
+// Join the partial statistics of each row: lse = log sum exp, loss = lse - target's logit.  A block
+// takes 32 rows; its warps share the parts, and the first joins the warps.
 static __global__ void __launch_bounds__(256) ar_vocab_join_kernel(const __grid_constant__ VocabJoinParams p) {
+    __shared__ float ms[8][32], ss[8][32];
     pdl_launch_dependents();
     pdl_wait();
-    const size_t t = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (t >= p.rows) return;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const long long t = static_cast<long long>(blockIdx.x) * 32 + lane;
     float m = -INFINITY, s = 0.0f;
-    for (unsigned k = 0; k < p.tiles; ++k) m = fmaxf(m, p.part[k * p.rows + t].x);
-    const float base = fabsf(m) == INFINITY ? 0.0f : m;
-    for (unsigned k = 0; k < p.tiles; ++k) {
-        const float2 q = p.part[k * p.rows + t];
-        if (q.x != -INFINITY) s += q.y * expf((q.x == INFINITY ? 0.0f : q.x) - base);
-    }
-    const float lse = base + logf(s);
+    auto add = [&](float qm, float qs) {
+        if (qm == -INFINITY && !(qs != qs)) return;  // a part without a finite or infinite logit adds nothing
+        const float to = fmaxf(m, qm), ref = fabsf(to) == INFINITY ? 0.0f : to;
+        s = (m == -INFINITY ? s : s * __expf((m == INFINITY ? 0.0f : m) - ref)) +
+            qs * __expf((fabsf(qm) == INFINITY ? 0.0f : qm) - ref);
+        m = to;
+    };
+    if (t < p.rows)
+        for (int k = warp; k < p.parts; k += 8) {
+            const float2 q = p.part[static_cast<long long>(k) * p.rows + t];
+            add(q.x, q.y);
+        }
+    ms[warp][lane] = m;
+    ss[warp][lane] = s;
+    __syncthreads();
+    if (warp || t >= p.rows) return;
+    for (int w = 1; w < 8; ++w) add(ms[w][lane], ss[w][lane]);
+    const float lse = (fabsf(m) == INFINITY ? 0.0f : m) + logf(s);
     p.lse[t] = lse;
     const long long y = p.targets[t];
     p.loss[t] = y == p.ignore ? 0.0f : (y < 0 || y >= p.vocab) ? NAN : lse - p.picked[t];
 }
 
-struct VocabGradParams {
-    VocabMat h, w;
-    size_t rows, vocab, dim;  // tokens, vocabulary rows of this chunk
-    long long first, ignore, total;
+struct VocabListParams {
     const long long *targets;
     const float *lse, *dloss;
-    float *d;                 // [rows][vocab] gradient of the chunk's logits
-    unsigned char *live;      // [rows] 1: the token is counted
+    long long ignore, vocab;
+    int rows;
+    float gain;       // 2^14 for f16, else 1
+    VocabList *list;
+    VocabRow *row;    // [live]
+    int *index;       // [live] original token
+    int *place;       // [rows] list entry, -1: not counted
 };
 
-// d = dloss * (softmax - [target]) of a tile of the chunk's logits, recomputed.
-template <int T>
-__global__ void __launch_bounds__(256) ar_vocab_dlogits_kernel(const __grid_constant__ VocabGradParams p) {
+// List the counted tokens in order, one block.  D is held as (softmax - onehot) dloss / max |dloss|,
+// so that rounding it to 16 bits costs the same whatever the scale of dloss, and costs nothing where
+// all dloss are alike and the probability is small; f16 moves up by 2^14 so that probabilities keep
+// their eleven bits down to 2^-28.
+static __global__ void __launch_bounds__(1024) ar_vocab_list_kernel(const __grid_constant__ VocabListParams p) {
+    __shared__ int counts[32];
+    __shared__ float tops[32];
     pdl_launch_dependents();
     pdl_wait();
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const size_t m0 = static_cast<size_t>(blockIdx.y) * kVT, n0 = static_cast<size_t>(blockIdx.x) * kVT;
-    float acc[4][4] = {};
-    tile_product<T, T>(p.h, p.w, p.rows, p.vocab, p.dim, m0, n0, acc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const size_t t = m0 + 4 * ty + i;
-        if (t >= p.rows) continue;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    auto counted = [&](int t) {
+        if (t >= p.rows) return false;
         const long long y = p.targets[t];
-        const bool live = y != p.ignore && y >= 0 && y < p.total;
-        if (tx == 0 && blockIdx.x == 0) p.live[t] = live;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const size_t v = n0 + 4 * tx + j;
-            if (v >= p.vocab) continue;
-            const float q = expf(acc[i][j] - p.lse[t]) - (y - p.first == static_cast<long long>(v) ? 1.0f : 0.0f);
-            p.d[t * p.vocab + v] = live ? q * p.dloss[t] : 0.0f;
+        return y != p.ignore && y >= 0 && y < p.vocab;
+    };
+    float top = 0.0f;
+    for (int t = threadIdx.x; t < p.rows; t += 1024)
+        if (counted(t)) top = fmaxf(top, fabsf(p.dloss[t]));
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    for (int w = 0; w < 32; ++w) top = fmaxf(top, tops[w]);
+    if (!(top > 0.0f && top <= 3.402823466e38f)) top = 1.0f;
+    int done = 0;
+    for (int t0 = 0; t0 < p.rows; t0 += 1024) {
+        const int t = t0 + static_cast<int>(threadIdx.x);
+        const bool c = counted(t);
+        const unsigned votes = __ballot_sync(~0u, c);
+        if (lane == 0) counts[warp] = __popc(votes);
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int w = 0; w < 32; ++w) {
+            before += w < warp ? counts[w] : 0;
+            all += counts[w];
         }
+        const int at = done + before + __popc(votes & ((1u << lane) - 1u));
+        if (c) {
+            p.row[at] = VocabRow{p.lse[t], p.dloss[t] / top * p.gain, p.targets[t]};
+            p.index[at] = t;
+        }
+        if (t < p.rows) p.place[t] = c ? at : -1;
+        done += all;
+        __syncthreads();
     }
+    if (threadIdx.x == 0) *p.list = VocabList{done, top / p.gain};
 }
 
-struct VocabOutParams {
-    VocabMat a, b;
-    size_t m, n, k;
-    float *sum;       // [m][n] running sum over chunks, nullptr: none
-    int begin;        // the first chunk: the running sum starts here
-    void *out;        // written when not nullptr
-    long long out_row;  // elements
+struct VocabPackParams {
+    const void *src;
+    long long src_row;        // bytes
+    int rows, dim;
+    unsigned short *dst;      // [parts][dst_rows][dst_ld]
+    long long dst_ld, dst_part;
+    const int *place;         // where row t goes (-1: nowhere), nullptr: in order
+    const VocabList *list;    // with place: rows behind the list are zeroed up to a block of K
+    char *dh[kMaxSegs];       // outputs whose row t is zeroed when the token is not counted
+    long long dh_row[kMaxSegs];
+    int n_dh;
 };
 
-// out[m][n] = a b^T (plus the running sum); a is float, b and out T.
+// Copy rows into 16-byte aligned rows of 16-bit elements (float32: three bf16 parts), one row after
+// another per block.
 template <int T>
-__global__ void __launch_bounds__(256) ar_vocab_product_kernel(const __grid_constant__ VocabOutParams p) {
+__global__ void __launch_bounds__(256) ar_vocab_pack_kernel(const __grid_constant__ VocabPackParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const size_t m0 = static_cast<size_t>(blockIdx.y) * kVT, n0 = static_cast<size_t>(blockIdx.x) * kVT;
-    float acc[4][4] = {};
-    tile_product<kF32, T>(p.a, p.b, p.m, p.n, p.k, m0, n0, acc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const size_t r = m0 + 4 * ty + i, c = n0 + 4 * tx + j;
-            if (r >= p.m || c >= p.n) continue;
-            float v = acc[i][j];
-            if (p.sum) {
-                if (!p.begin) v += p.sum[r * p.n + c];
-                p.sum[r * p.n + c] = v;
-            }
-            if (p.out) store_elem<T>(p.out, static_cast<long long>(r) * p.out_row + static_cast<long long>(c), v);
+    auto zero_row = [&](long long at) {
+        for (int q = 0; q < (T == kF32 ? 3 : 1); ++q)
+            for (long long c = threadIdx.x; c < p.dst_ld / 8; c += blockDim.x)
+                reinterpret_cast<uint4 *>(p.dst + q * p.dst_part + at * p.dst_ld)[c] = make_uint4(0, 0, 0, 0);
+    };
+    for (int t = blockIdx.x; t < p.rows; t += gridDim.x) {
+        const int at = p.place ? p.place[t] : t;
+        if (at < 0) {
+            for (int r = 0; r < p.n_dh; ++r)
+                for (int c = threadIdx.x; c < p.dim; c += blockDim.x) store_elem<T>(p.dh[r] + t * p.dh_row[r], c, 0.0f);
+            continue;
         }
+        const char *src = static_cast<const char *>(p.src) + t * p.src_row;
+        for (long long g = threadIdx.x; g < p.dst_ld / 8; g += blockDim.x) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = 8 * g + k < p.dim ? load_elem<T, true>(src, 8 * g + k) : 0.0f;
+            unsigned short *out = p.dst + at * p.dst_ld + 8 * g;
+            if constexpr (T != kF32) {
+                uint32_t w[4];
+                word_pack<T, 4>(v, w);
+                *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                uint32_t w[4][3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split2(v[2 * e], v[2 * e + 1], w[e]);
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+                    *reinterpret_cast<uint4 *>(out + q * p.dst_part) = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
+            }
+        }
+    }
+    if (p.list) {
+        const int live = p.list->live, end = (live + kVK - 1) / kVK * kVK;
+        for (int at = live + blockIdx.x; at < end; at += gridDim.x) zero_row(at);
+    }
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
+struct VocabSumParams {
+    const float *sum;         // [segment][slice][sum_rows][sum_ld]
+    long long sum_rows, sum_ld;
+    int slices, dim;
+    const VocabList *list;
+    const int *index;
+    char *dh[kMaxSegs];       // of each segment's piece
+    long long dh_row[kMaxSegs];
+};
+
+// dH of a piece from its slices, in their order: blockIdx.z picks the segment, blockIdx.y strides over rows.
+template <int T>
+__global__ void __launch_bounds__(256) ar_vocab_sum_kernel(const __grid_constant__ VocabSumParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int live = p.list->live, c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= p.dim) return;
+    for (int r = blockIdx.y; r < live; r += gridDim.y) {
+        float v = 0.0f;
+        for (int s = 0; s < p.slices; ++s)
+            v += p.sum[((static_cast<long long>(blockIdx.z) * p.slices + s) * p.sum_rows + r) * p.sum_ld + c];
+        store_elem<T>(p.dh[blockIdx.z] + static_cast<long long>(p.index[r]) * p.dh_row[blockIdx.z], c, v);
+    }
 }
 
 }  // namespace tps

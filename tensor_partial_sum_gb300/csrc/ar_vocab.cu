@@ -9,14 +9,15 @@
 #include "ar_kernels_vocab.cuh"
 
 using tps::dtype_bytes;
-using tps::VocabMat;
 
 namespace {
 
 // The gradient of the logits is held for one chunk of the vocabulary at a
-// time: as many rows of a piece as fit this many bytes, at least kMinChunk.
+// time, and packed rows likewise: as many rows as fit this many bytes, at
+// least one tile.
 constexpr size_t kChunkBytes = 256ull << 20;
-constexpr size_t kMinChunk = 1024;
+// Partial sums of dH that a split reduction may take.
+constexpr size_t kSliceBytes = 64ull << 20;
 
 struct Carve {  // hands out 256-byte aligned parts of the workspace
     size_t at = 0;
@@ -74,37 +75,167 @@ bool any_overlap(const Span *in, int n_in, const Span *out, int n_out) {
     return false;
 }
 
-size_t tiles_of(size_t rows) { return (rows + tps::kVT - 1) / tps::kVT; }
+
+size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
+size_t tiles_of(size_t n, size_t tile) { return (n + tile - 1) / tile; }
+
+int parts_of(const ar_vocab *v) { return v->dtype == AR_F32 ? 3 : 1; }
+
+// Rows that the tiled copies can read in place: 16-bit, starts and strides on 16-byte boundaries.
+bool in_place(const void *p, size_t stride, const ar_vocab *v) {
+    return v->dtype != AR_F32 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 16 == 0;
+}
+
+bool hidden_in_place(const ar_vocab *v) { return in_place(v->hidden, row_bytes(v->hidden_row_bytes, v), v); }
+
+bool weights_in_place(const ar_vocab *v) {
+    for (int r = 0; r < v->n_pieces; ++r)
+        if (v->piece_rows[r] && !in_place(v->weights[r], weight_stride(v, r), v)) return false;
+    return true;
+}
+
+// Elements between packed rows (of hidden states or weights): 16-byte multiples.
+size_t packed_ld(const ar_vocab *v) { return round_up(v->dim, 8); }
+
+// One launch's vocabulary: whole pieces, or rows [row0, row0 + rows) of one that is larger than a chunk.
+struct Group {
+    int nseg = 0;
+    int piece[tps::kMaxSegs];
+    size_t row0[tps::kMaxSegs], rows[tps::kMaxSegs];
+    size_t padded = 0;  // rows, each segment rounded up to whole tiles
+    bool begins = true, ends = true;  // its pieces' first and last rows are here
+};
+
+// The next group of at most `cap` padded rows from (piece, row); false when the vocabulary is done.
+bool next_group(const ar_vocab *v, size_t cap, int &piece, size_t &row, Group &g) {
+    g = Group{};
+    while (piece < v->n_pieces) {
+        const size_t left = v->piece_rows[piece] - row;
+        if (left == 0) {
+            ++piece, row = 0;
+            continue;
+        }
+        const size_t padded = round_up(left, tps::kVN);
+        if (row || (g.nseg == 0 && padded > cap)) {  // part of a large piece, alone
+            g.piece[0] = piece;
+            g.row0[0] = row;
+            g.rows[0] = left < cap ? left : cap;
+            g.padded = round_up(g.rows[0], tps::kVN);
+            g.nseg = 1;
+            g.begins = row == 0;
+            row += g.rows[0];
+            g.ends = row == v->piece_rows[piece];
+            return true;
+        }
+        if (g.padded + padded > cap) return true;
+        g.piece[g.nseg] = piece;
+        g.row0[g.nseg] = 0;
+        g.rows[g.nseg++] = left;
+        g.padded += padded;
+        ++piece;
+    }
+    return g.nseg > 0;
+}
+
+// Vocabulary rows of a group, a multiple of the tile, when each takes `bytes_per_row`.
+size_t group_cap(size_t bytes_per_row) {
+    const size_t n = kChunkBytes / (bytes_per_row ? bytes_per_row : 1) / tps::kVN * tps::kVN;
+    return n < tps::kVN ? static_cast<size_t>(tps::kVN) : n;
+}
+
+size_t padded_vocab(const ar_vocab *v) {
+    size_t n = 0;
+    for (int r = 0; r < v->n_pieces; ++r) n += round_up(v->piece_rows[r], tps::kVN);
+    return n;
+}
+
+// Columns of a kStats tile.  With one tile row the call is bound by reading W, and pairs that share
+// the column tiles unevenly wait: take the width (a multiple of 16, at least half a tile) that leaves the
+// least to the busiest pair.  With more tile rows the widest tile moves the fewest bytes per product.
+int stats_width(const ar_vocab *v, int pairs) {
+    if (v->rows > tps::kVM) return tps::kVN;
+    size_t best = SIZE_MAX;
+    int bn = tps::kVN;
+    for (int n = tps::kVN; n >= tps::kVN / 2; n -= 16) {
+        size_t tiles = 0;
+        for (int r = 0; r < v->n_pieces; ++r) tiles += tiles_of(v->piece_rows[r], static_cast<size_t>(n));
+        const size_t cost = tiles_of(tiles, static_cast<size_t>(pairs)) * static_cast<size_t>(n);
+        if (cost < best) best = cost, bn = n;
+    }
+    return bn;
+}
 
 struct LossPlan {
-    size_t tiles, part, picked, bytes;
+    size_t cap;  // vocabulary rows of a group
+    size_t part, picked, hidden, weights, bytes;
 };
 
 LossPlan plan_loss(const ar_vocab *v) {
     LossPlan p{};
-    for (int r = 0; r < v->n_pieces; ++r) p.tiles += tiles_of(v->piece_rows[r]);
+    const size_t row = packed_ld(v) * 2 * static_cast<size_t>(parts_of(v));
     Carve c;
-    p.part = c.take(p.tiles * v->rows * sizeof(float2));
+    // statistics for each half tile; the narrowest tile that stats_width may take makes the most of them
+    const size_t narrow = v->rows > tps::kVM ? tps::kVN : tps::kVN / 2;
+    size_t tiles = 0;
+    for (int r = 0; r < v->n_pieces; ++r) tiles += tiles_of(v->piece_rows[r], narrow);
+    p.part = c.take(2 * tiles * v->rows * sizeof(float2));
     p.picked = c.take(v->rows * sizeof(float));
+    p.hidden = c.take(hidden_in_place(v) ? 0 : v->rows * row);
+    const bool pack = !weights_in_place(v);
+    const size_t all = padded_vocab(v);
+    p.cap = pack && group_cap(row) < all ? group_cap(row) : all;
+    p.weights = c.take(pack ? p.cap * row : 0);
     p.bytes = c.at;
     return p;
 }
 
 struct GradPlan {
-    size_t chunk, d, sum, live, bytes;
+    size_t cap;         // vocabulary rows of a group
+    size_t d_rows;      // tokens, whole tiles
+    size_t k_rows;      // tokens, whole blocks of K
+    int slices;         // of dH's reductions
+    bool sums;          // dH goes through partial sums
+    size_t list, row, index, place, hidden, d, weights, sum, bytes;
 };
 
 GradPlan plan_grad(const ar_vocab *v) {
     GradPlan p{};
-    size_t most = 0;
-    for (int r = 0; r < v->n_pieces; ++r) most = v->piece_rows[r] > most ? v->piece_rows[r] : most;
-    p.chunk = v->rows ? kChunkBytes / (v->rows * sizeof(float)) : most;
-    if (p.chunk < kMinChunk) p.chunk = kMinChunk;
-    if (p.chunk > most) p.chunk = most;
+    const size_t parts = static_cast<size_t>(parts_of(v)), row = packed_ld(v) * 2 * parts;
+    p.d_rows = round_up(v->rows, tps::kVM);
+    p.k_rows = round_up(v->rows, tps::kVK);
+    const bool pack = !weights_in_place(v);
+    const size_t all = padded_vocab(v);
+    size_t cap = group_cap(p.d_rows * 2 * parts);
+    if (pack && group_cap(row) < cap) cap = group_cap(row);
+    p.cap = cap < all ? cap : all;
+    // With few tiles of dH their long reductions are cut into slices, so that every pair of SMs gets
+    // some: enough for two rounds of 76 pairs, none shorter than eight blocks of K, and no more partial
+    // sums than kSliceBytes.
+    size_t longest = 0;
+    int segs = 0;
+    for (int r = 0; r < v->n_pieces; ++r) {
+        longest = v->piece_rows[r] > longest ? v->piece_rows[r] : longest;
+        segs += v->piece_rows[r] != 0;
+    }
+    const bool split = round_up(longest, tps::kVN) > p.cap;
+    if (longest > p.cap) longest = p.cap;
+    const size_t tiles = p.d_rows / tps::kVM * tiles_of(v->dim, tps::kVN) * static_cast<size_t>(segs ? segs : 1);
+    const size_t slice = p.d_rows * round_up(v->dim, 8) * sizeof(float);
+    size_t s = tiles ? 152 / tiles : 1;
+    const size_t blocks = tiles_of(longest, tps::kVK);
+    if (s > blocks / 8) s = blocks / 8;
+    if (s > kSliceBytes / (slice * static_cast<size_t>(segs ? segs : 1) + 1)) s = kSliceBytes / (slice * static_cast<size_t>(segs ? segs : 1) + 1);
+    p.slices = s < 2 ? 1 : static_cast<int>(s);
+    p.sums = split || p.slices > 1;
     Carve c;
-    p.d = c.take(p.chunk * v->rows * sizeof(float));
-    p.sum = c.take(v->rows * v->dim * sizeof(float));
-    p.live = c.take(v->rows);
+    p.list = c.take(sizeof(tps::VocabList));
+    p.row = c.take(v->rows * sizeof(tps::VocabRow));
+    p.index = c.take(v->rows * sizeof(int));
+    p.place = c.take(v->rows * sizeof(int));
+    p.hidden = c.take(p.k_rows * row);
+    p.d = c.take(p.d_rows * p.cap * 2 * parts);
+    p.weights = c.take(pack ? p.cap * row : 0);
+    p.sum = c.take(p.sums ? static_cast<size_t>(p.slices) * slice * static_cast<size_t>(p.slices > 1 ? segs : 1) : 0);
     p.bytes = c.at;
     return p;
 }
@@ -123,9 +254,111 @@ Fn<P> by_type(int dtype, Fn<P> f32, Fn<P> f16, Fn<P> bf16) {
     return dtype == AR_F32 ? f32 : dtype == AR_F16 ? f16 : bf16;
 }
 
-dim3 tile_grid(size_t m, size_t n) {
-    return dim3(static_cast<unsigned>(tiles_of(n)), static_cast<unsigned>(tiles_of(m)));
+// cuTensorMapEncodeTiled, through the runtime so that the library loads where there is no driver.
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
 }
+
+// A tensor map over [parts][rows][cols] 16-bit elements, `ld` elements between rows and `part`
+// between parts, copied in boxes of 64 columns by box_rows rows, 128-byte swizzled.
+bool make_map(CUtensorMap *m, bool f16, const void *base, size_t cols, size_t rows, size_t parts, size_t ld, size_t part,
+              unsigned box_rows) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {cols, rows, parts};
+    const cuuint64_t strides[2] = {ld * 2, (parts > 1 ? part : rows * ld) * 2};
+    const cuuint32_t box[3] = {64, box_rows, 1}, step[3] = {1, 1, 1};
+    return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims,
+              strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A call under way: what its launches share.
+struct Call {
+    const ar_vocab *v;
+    tps::CallContext c;
+    cudaStream_t stream;
+    char *ws;
+    size_t parts, ld;     // of packed rows
+    bool f16, pack;       // the weights are packed, group by group
+
+    template <typename P>
+    int launch(Fn<P> fn, dim3 grid, unsigned threads, size_t smem, const P &p) const {
+        return launched(tps::launch_dependent(fn, grid, threads, smem, stream, c.pdl, p));
+    }
+
+    // Rows into packed rows at `dst`, `rows_max` rows apart in parts.
+    tps::VocabPackParams pack_params(const void *src, size_t stride, size_t rows, void *dst, size_t rows_max) const {
+        tps::VocabPackParams p;
+        memset(&p, 0, sizeof p);
+        p.src = src;
+        p.src_row = static_cast<long long>(stride);
+        p.rows = static_cast<int>(rows);
+        p.dim = static_cast<int>(v->dim);
+        p.dst = static_cast<unsigned short *>(dst);
+        p.dst_ld = static_cast<long long>(ld);
+        p.dst_part = static_cast<long long>(rows_max * ld);
+        return p;
+    }
+    int launch_pack(const tps::VocabPackParams &p) const {
+        const int most = c.sm_count * 16;
+        return launch(by_type<tps::VocabPackParams>(v->dtype, tps::ar_vocab_pack_kernel<tps::kF32>,
+                                                    tps::ar_vocab_pack_kernel<tps::kF16>,
+                                                    tps::ar_vocab_pack_kernel<tps::kBF16>),
+                      dim3(static_cast<unsigned>(p.rows < 64 ? 64 : p.rows < most ? p.rows : most)), 256u, 0, p);
+    }
+
+    // The weights of a group: packed at `area` (room for `cap` rows) where they have to be; per segment
+    // the base, rows, row stride in elements and part stride of what the copies read.
+    struct Matrix {
+        const char *base;
+        size_t rows, ld, part;
+    };
+    int group_weights(const Group &g, size_t area, size_t cap, Matrix *out) const {
+        size_t at = 0;
+        for (int s = 0; s < g.nseg; ++s) {
+            const size_t stride = weight_stride(v, g.piece[s]);
+            const char *src = static_cast<const char *>(v->weights[g.piece[s]]) + g.row0[s] * stride;
+            if (!pack) {
+                out[s] = Matrix{src, g.rows[s], stride / 2, 0};
+                continue;
+            }
+            char *dst = ws + area + at * ld * 2;
+            at += g.rows[s];
+            out[s] = Matrix{dst, g.rows[s], ld, cap * ld};
+            const int st = launch_pack(pack_params(src, stride, g.rows[s], dst, cap));
+            if (st != AR_OK) return st;
+        }
+        return AR_OK;
+    }
+
+    template <int MODE>
+    int launch_gemm(const tps::VocabGemmParams &p, size_t tiles) const {
+        const auto fn = by_type<tps::VocabGemmParams>(v->dtype, tps::ar_vocab_gemm_kernel<MODE, tps::kF32>,
+                                                      tps::ar_vocab_gemm_kernel<MODE, tps::kF16>,
+                                                      tps::ar_vocab_gemm_kernel<MODE, tps::kBF16>);
+        if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(tps::kVSmem)) != cudaSuccess) {
+            cudaGetLastError();
+            return AR_ERR_CUDA;
+        }
+        const size_t most = static_cast<size_t>(c.sm_count / 2);
+        const size_t pairs = tiles < 1 ? 1 : tiles < most ? tiles : most;
+        return launch(fn, dim3(static_cast<unsigned>(2 * pairs)), static_cast<unsigned>(tps::kVThreads), tps::kVSmem, p);
+    }
+};
 
 }  // namespace
 
@@ -135,11 +368,11 @@ int ar_check_vocab(const ar_vocab *v, size_t max_elems) {
     if (!v || v->n_pieces < 1 || v->n_pieces > AR_MAX_RANKS || !v->piece_rows || !v->weights || v->dim == 0)
         return AR_ERR_INVALID_ARG;
     if (!dtype_bytes(v->dtype)) return AR_ERR_UNSUPPORTED;
-    // matrix rows and columns are 32-bit coordinates of the copies into shared memory
-    if (v->dim > 0x7FFFFFFFull || v->rows > 65535ull * 64) return AR_ERR_TOO_LARGE;
+    // rows and columns are 32-bit coordinates of the tiled copies
+    if (v->dim > (1ull << 28) || v->rows > (1ull << 28)) return AR_ERR_TOO_LARGE;
     size_t total = 0;
     for (int r = 0; r < v->n_pieces; ++r) {
-        if (v->piece_rows[r] > 0x7FFFFFFFull) return AR_ERR_TOO_LARGE;
+        if (v->piece_rows[r] > (1ull << 28)) return AR_ERR_TOO_LARGE;
         total += v->piece_rows[r];
     }
     if (total == 0) return AR_ERR_INVALID_ARG;
@@ -180,41 +413,64 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
     st = tps::check_launch_device(c);
     if (st != AR_OK) return st;
 
-    const long long es = static_cast<long long>(dtype_bytes(v->dtype));
-    char *base = static_cast<char *>(ws);
-    tps::VocabStatParams p;
-    memset(&p, 0, sizeof p);
-    p.h = VocabMat{v->hidden, static_cast<long long>(row_bytes(v->hidden_row_bytes, v)) / es, 1, nullptr};
-    p.rows = v->rows;
-    p.dim = v->dim;
-    p.targets = reinterpret_cast<const long long *>(v->targets);
-    p.part = reinterpret_cast<float2 *>(base + plan.part);
-    p.picked = reinterpret_cast<float *>(base + plan.picked);
-    for (int r = 0; r < v->n_pieces; ++r) {
-        if (v->piece_rows[r] == 0) continue;
-        p.w = VocabMat{v->weights[r], static_cast<long long>(weight_stride(v, r)) / es, 1, nullptr};
-        p.vocab = v->piece_rows[r];
-        st = launched(tps::launch_dependent(by_type<tps::VocabStatParams>(v->dtype, tps::ar_vocab_stat_kernel<tps::kF32>,
-                                                                          tps::ar_vocab_stat_kernel<tps::kF16>,
-                                                                          tps::ar_vocab_stat_kernel<tps::kBF16>),
-                                            tile_grid(v->rows, p.vocab), 256u, 0, stream, c.pdl, p));
+    Call call{v, c, stream, static_cast<char *>(ws), static_cast<size_t>(parts_of(v)), packed_ld(v), v->dtype == AR_F16,
+              !weights_in_place(v)};
+    const size_t T = v->rows, D = v->dim;
+    // the hidden states as the tiled copies read them
+    Call::Matrix h{static_cast<const char *>(v->hidden), T, row_bytes(v->hidden_row_bytes, v) / 2, 0};
+    if (!hidden_in_place(v)) {
+        h = Call::Matrix{call.ws + plan.hidden, T, call.ld, T * call.ld};
+        st = call.launch_pack(call.pack_params(v->hidden, row_bytes(v->hidden_row_bytes, v), T, call.ws + plan.hidden, T));
         if (st != AR_OK) return st;
-        p.tile0 += static_cast<unsigned>(tiles_of(p.vocab));
-        p.first += static_cast<long long>(p.vocab);
+    }
+    tps::VocabGemmParams p;
+    memset(&p, 0, sizeof p);
+    p.rows = static_cast<int>(T);
+    p.dim = static_cast<int>(D);
+    p.bn = stats_width(v, c.sm_count / 2);
+    p.pairs = call.parts == 1 ? 1 : 6;
+    p.targets = reinterpret_cast<const long long *>(v->targets);
+    p.part = reinterpret_cast<float2 *>(call.ws + plan.part);
+    p.picked = reinterpret_cast<float *>(call.ws + plan.picked);
+    p.status = c.dev_status;
+    if (!make_map(&p.a_map, call.f16, h.base, D, h.rows, call.parts, h.ld, h.part, 128)) return AR_ERR_CUDA;
+    long long first[AR_MAX_RANKS], total = 0;
+    for (int r = 0; r < v->n_pieces; ++r) first[r] = total, total += static_cast<long long>(v->piece_rows[r]);
+    int piece = 0, done = 0;  // column tiles of earlier groups
+    size_t row = 0;
+    Group g;
+    while (next_group(v, plan.cap, piece, row, g)) {
+        Call::Matrix w[tps::kMaxSegs];
+        st = call.group_weights(g, plan.weights, plan.cap, w);
+        if (st != AR_OK) return st;
+        p.nseg = g.nseg;
+        p.tiles = 0;
+        for (int s = 0; s < g.nseg; ++s) {
+            p.seg[s].first = first[g.piece[s]] + static_cast<long long>(g.row0[s]);
+            p.seg[s].rows = static_cast<int>(g.rows[s]);
+            p.seg[s].tile0 = p.tiles;
+            p.tiles += static_cast<int>(tiles_of(g.rows[s], static_cast<size_t>(p.bn)));
+            if (!make_map(&p.b_map[s], call.f16, w[s].base, D, w[s].rows, call.parts, w[s].ld, w[s].part,
+                          static_cast<unsigned>(p.bn / 2)))
+                return AR_ERR_CUDA;
+        }
+        st = call.launch_gemm<tps::kStats>(p, static_cast<size_t>(p.tiles) * tiles_of(T, tps::kVM));
+        if (st != AR_OK) return st;
+        p.part += 2ll * p.tiles * static_cast<long long>(T);
+        done += p.tiles;
     }
     tps::VocabJoinParams j;
     memset(&j, 0, sizeof j);
-    j.part = p.part;
+    j.part = reinterpret_cast<float2 *>(call.ws + plan.part);
     j.picked = p.picked;
     j.targets = p.targets;
     j.ignore = v->ignore_index;
-    j.vocab = p.first;
-    j.rows = v->rows;
-    j.tiles = p.tile0;
+    j.vocab = total;
+    j.rows = p.rows;
+    j.parts = 2 * done;
     j.loss = loss;
     j.lse = lse;
-    return launched(tps::launch_dependent(tps::ar_vocab_join_kernel, dim3(static_cast<unsigned>((v->rows + 255) / 256)),
-                                          256u, 0, stream, c.pdl, j));
+    return call.launch<tps::VocabJoinParams>(tps::ar_vocab_join_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), 256u, 0, j);
 }
 
 int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, void *const *dhidden,
@@ -256,66 +512,142 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
     st = tps::check_launch_device(c);
     if (st != AR_OK) return st;
 
-    char *base = static_cast<char *>(ws);
-    const long long e = static_cast<long long>(es);
-    tps::VocabGradParams p;
+    Call call{v, c, stream, static_cast<char *>(ws), static_cast<size_t>(parts_of(v)), packed_ld(v), v->dtype == AR_F16,
+              !weights_in_place(v)};
+    const size_t T = v->rows, D = v->dim;
+    if (T == 0) {  // no tokens: the weights' gradients are zero
+        for (int r = 0; dweights && r < v->n_pieces; ++r)
+            if (v->piece_rows[r] &&
+                cudaMemset2DAsync(dweights[r], row_bytes(dw_rows ? dw_rows[r] : 0, v), 0, D * es, v->piece_rows[r], stream) !=
+                    cudaSuccess)
+                return launched(cudaErrorUnknown);
+        return AR_OK;
+    }
+    tps::VocabListParams l;
+    memset(&l, 0, sizeof l);
+    l.targets = reinterpret_cast<const long long *>(v->targets);
+    l.lse = lse;
+    l.dloss = dloss;
+    l.ignore = v->ignore_index;
+    l.vocab = static_cast<long long>(total_rows(v));
+    l.rows = static_cast<int>(T);
+    l.gain = call.f16 ? 16384.0f : 1.0f;
+    l.list = reinterpret_cast<tps::VocabList *>(call.ws + plan.list);
+    l.row = reinterpret_cast<tps::VocabRow *>(call.ws + plan.row);
+    l.index = reinterpret_cast<int *>(call.ws + plan.index);
+    l.place = reinterpret_cast<int *>(call.ws + plan.place);
+    st = call.launch<tps::VocabListParams>(tps::ar_vocab_list_kernel, dim3(1), 1024u, 0, l);
+    if (st != AR_OK) return st;
+    tps::VocabPackParams hp =
+        call.pack_params(v->hidden, row_bytes(v->hidden_row_bytes, v), T, call.ws + plan.hidden, plan.k_rows);
+    hp.place = l.place;
+    hp.list = l.list;
+    for (int r = 0; dhidden && r < v->n_pieces; ++r) {
+        hp.dh[r] = static_cast<char *>(dhidden[r]);
+        hp.dh_row[r] = static_cast<long long>(row_bytes(dh_rows ? dh_rows[r] : 0, v));
+        hp.n_dh = r + 1;
+        // a piece without rows has no product that would write its zeros
+        if (v->piece_rows[r] == 0 &&
+            cudaMemset2DAsync(dhidden[r], static_cast<size_t>(hp.dh_row[r]), 0, D * es, T, stream) != cudaSuccess)
+            return launched(cudaErrorUnknown);
+    }
+    st = call.launch_pack(hp);
+    if (st != AR_OK) return st;
+
+    tps::VocabGemmParams p;
     memset(&p, 0, sizeof p);
-    p.h = VocabMat{v->hidden, static_cast<long long>(row_bytes(v->hidden_row_bytes, v)) / e, 1, nullptr};
-    p.rows = v->rows;
-    p.dim = v->dim;
-    p.ignore = v->ignore_index;
-    p.total = static_cast<long long>(total_rows(v));
-    p.targets = reinterpret_cast<const long long *>(v->targets);
-    p.lse = lse;
-    p.dloss = dloss;
-    p.d = reinterpret_cast<float *>(base + plan.d);
-    p.live = reinterpret_cast<unsigned char *>(base + plan.live);
-    const auto product = by_type<tps::VocabOutParams>(v->dtype, tps::ar_vocab_product_kernel<tps::kF32>,
-                                                      tps::ar_vocab_product_kernel<tps::kF16>,
-                                                      tps::ar_vocab_product_kernel<tps::kBF16>);
-    long long first = 0;  // global index of the piece's first row
-    for (int r = 0; r < v->n_pieces; ++r) {
-        const size_t n = v->piece_rows[r], ld = weight_stride(v, r);
-        const size_t hs = row_bytes(dh_rows ? dh_rows[r] : 0, v), wst = row_bytes(dw_rows ? dw_rows[r] : 0, v);
-        for (size_t v0 = 0; v0 == 0 || v0 < n; v0 += plan.chunk) {
-            const size_t rows = n - v0 < plan.chunk ? n - v0 : plan.chunk;
-            p.w = VocabMat{static_cast<const char *>(v->weights[r]) + v0 * ld, static_cast<long long>(ld) / e, 1, nullptr};
-            p.vocab = rows;
-            p.first = first + static_cast<long long>(v0);
-            if (rows && v->rows) {
-                st = launched(tps::launch_dependent(
-                    by_type<tps::VocabGradParams>(v->dtype, tps::ar_vocab_dlogits_kernel<tps::kF32>,
-                                                  tps::ar_vocab_dlogits_kernel<tps::kF16>,
-                                                  tps::ar_vocab_dlogits_kernel<tps::kBF16>),
-                    tile_grid(v->rows, rows), 256u, 0, stream, c.pdl, p));
-                if (st != AR_OK) return st;
-            }
-            tps::VocabOutParams o;
-            memset(&o, 0, sizeof o);
-            if (dhidden && v->rows) {  // a piece without rows still writes its zeros
-                o.a = VocabMat{p.d, static_cast<long long>(rows), 1, nullptr};
-                o.b = VocabMat{p.w.base, 1, p.w.row, nullptr};
-                o.m = v->rows, o.n = v->dim, o.k = rows;
-                o.sum = reinterpret_cast<float *>(base + plan.sum);
-                o.begin = v0 == 0;
-                o.out = v0 + rows >= n ? dhidden[r] : nullptr;
-                o.out_row = static_cast<long long>(hs) / e;
-                st = launched(tps::launch_dependent(product, tile_grid(o.m, o.n), 256u, 0, stream, c.pdl, o));
-                if (st != AR_OK) return st;
-            }
-            if (dweights && rows) {
-                memset(&o, 0, sizeof o);
-                o.a = VocabMat{p.d, 1, static_cast<long long>(rows), nullptr};
-                o.b = VocabMat{v->hidden, 1, p.h.row, p.live};
-                o.m = rows, o.n = v->dim, o.k = v->rows;
-                o.out = static_cast<char *>(dweights[r]) + v0 * wst;
-                o.out_row = static_cast<long long>(wst) / e;
-                st = launched(tps::launch_dependent(product, tile_grid(o.m, o.n), 256u, 0, stream, c.pdl, o));
-                if (st != AR_OK) return st;
-            }
-            if (n == 0) break;
+    p.rows = l.rows;
+    p.dim = static_cast<int>(D);
+    p.pairs = call.parts == 1 ? 1 : 6;
+    p.list = l.list;
+    p.row = l.row;
+    p.index = l.index;
+    p.d = reinterpret_cast<unsigned short *>(call.ws + plan.d);
+    p.status = c.dev_status;
+    const size_t mt = plan.d_rows / tps::kVM;
+    CUtensorMap h_k, h_mn;
+    if (!make_map(&h_k, call.f16, call.ws + plan.hidden, D, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld, 128) ||
+        !make_map(&h_mn, call.f16, call.ws + plan.hidden, D, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld, 64))
+        return AR_ERR_CUDA;
+    long long first[AR_MAX_RANKS], total = 0;
+    for (int r = 0; r < v->n_pieces; ++r) first[r] = total, total += static_cast<long long>(v->piece_rows[r]);
+    int piece = 0;
+    size_t row = 0;
+    Group g;
+    while (next_group(v, plan.cap, piece, row, g)) {
+        Call::Matrix w[tps::kMaxSegs];
+        st = call.group_weights(g, plan.weights, plan.cap, w);
+        if (st != AR_OK) return st;
+        // D of this group's logits
+        p.d_ld = static_cast<long long>(g.padded);
+        p.d_part = p.d_ld * static_cast<long long>(plan.d_rows);
+        p.nseg = g.nseg;
+        p.bn = tps::kVN;
+        p.tiles = 0;
+        p.a_map = h_k;
+        for (int s = 0; s < g.nseg; ++s) {
+            p.seg[s].first = first[g.piece[s]] + static_cast<long long>(g.row0[s]);
+            p.seg[s].rows = static_cast<int>(g.rows[s]);
+            p.seg[s].tile0 = p.tiles;
+            p.seg[s].col0 = static_cast<long long>(p.tiles) * tps::kVN;
+            p.tiles += static_cast<int>(tiles_of(g.rows[s], tps::kVN));
+            if (!make_map(&p.b_map[s], call.f16, w[s].base, D, w[s].rows, call.parts, w[s].ld, w[s].part, tps::kVN / 2))
+                return AR_ERR_CUDA;
         }
-        first += static_cast<long long>(n);
+        st = call.launch_gemm<tps::kDlogits>(p, static_cast<size_t>(p.tiles) * mt);
+        if (st != AR_OK) return st;
+        // dH and dW from it
+        const size_t parts = call.parts, dl = static_cast<size_t>(p.d_ld), dp = static_cast<size_t>(p.d_part);
+        if (!make_map(&p.a_map, call.f16, p.d, dl, plan.d_rows, parts, dl, dp, 128) ||
+            !make_map(&p.at_map, call.f16, p.d, dl, plan.d_rows, parts, dl, dp, 64))
+            return AR_ERR_CUDA;
+        p.ht_map = h_mn;
+        p.bn = D <= tps::kVN / 2 ? tps::kVN / 2 : tps::kVN;
+        p.slices = plan.slices;
+        p.dh_tiles = dhidden ? static_cast<int>(tiles_of(D, static_cast<size_t>(p.bn))) : 0;
+        p.sum_rows = static_cast<long long>(plan.d_rows);
+        p.sum_ld = static_cast<long long>(round_up(D, 8));
+        const bool sums = plan.slices > 1 || !(g.begins && g.ends);
+        p.sum = sums ? reinterpret_cast<float *>(call.ws + plan.sum) : nullptr;
+        p.sum_begin = g.begins;
+        const bool straight = plan.slices == 1 && g.ends;  // this launch finishes dH
+        p.tiles = 0;
+        for (int s = 0; s < g.nseg; ++s) {
+            const int r = g.piece[s];
+            p.seg[s].tile0 = p.tiles;
+            p.seg[s].dh = dhidden && straight ? static_cast<char *>(dhidden[r]) : nullptr;
+            p.seg[s].dh_row = hp.dh_row[r];
+            p.seg[s].dw_row = static_cast<long long>(row_bytes(dw_rows ? dw_rows[r] : 0, v));
+            p.seg[s].dw = dweights ? static_cast<char *>(dweights[r]) + g.row0[s] * static_cast<size_t>(p.seg[s].dw_row) : nullptr;
+            p.tiles += static_cast<int>(tiles_of(g.rows[s], tps::kVM));
+            if (!make_map(&p.b_map[s], call.f16, w[s].base, D, w[s].rows, parts, w[s].ld, w[s].part, 64)) return AR_ERR_CUDA;
+        }
+        p.tiles = dweights ? p.tiles * static_cast<int>(tiles_of(D, static_cast<size_t>(p.bn))) : 0;
+        st = call.launch_gemm<tps::kGrads>(
+            p, static_cast<size_t>(p.tiles) + static_cast<size_t>(g.nseg * p.slices * p.dh_tiles) * mt);
+        if (st != AR_OK) return st;
+        if (dhidden && plan.slices > 1 && g.ends) {
+            tps::VocabSumParams q;
+            memset(&q, 0, sizeof q);
+            q.sum = p.sum;
+            q.sum_rows = p.sum_rows;
+            q.sum_ld = p.sum_ld;
+            q.slices = p.slices;
+            q.dim = p.dim;
+            q.list = l.list;
+            q.index = l.index;
+            for (int s = 0; s < g.nseg; ++s) {
+                q.dh[s] = static_cast<char *>(dhidden[g.piece[s]]);
+                q.dh_row[s] = hp.dh_row[g.piece[s]];
+            }
+            st = call.launch(by_type<tps::VocabSumParams>(v->dtype, tps::ar_vocab_sum_kernel<tps::kF32>,
+                                                          tps::ar_vocab_sum_kernel<tps::kF16>,
+                                                          tps::ar_vocab_sum_kernel<tps::kBF16>),
+                             dim3(static_cast<unsigned>((D + 255) / 256), static_cast<unsigned>(T < 1024 ? T : 1024),
+                                  static_cast<unsigned>(g.nseg)),
+                             256u, 0, q);
+            if (st != AR_OK) return st;
+        }
     }
     return AR_OK;
 }
