@@ -30,13 +30,13 @@ constexpr int kMaxSegs = 16;
 constexpr int kVM = 256;      // rows of a tile, 128 in each CTA
 constexpr int kVN = 256;      // columns of a tile (at most), half of B's rows in each CTA
 constexpr int kVK = 64;       // elements of the reduction per stage: 128 bytes
-constexpr int kVStages = 6;
-constexpr int kVHalf = 128 * kVK * 2;       // bytes of one operand's stage in one CTA
-constexpr int kVStage = 2 * kVHalf;
+constexpr int kVMaxStages = 32;
+constexpr int kVRow = kVK * 2;              // bytes of a row of a stage
+constexpr int kVRing = 6 * 256 * kVRow;     // bytes of the stages: six of full height
 constexpr int kVEpilogueWarps = 8;
 constexpr int kVThreads = 128 + 32 * kVEpilogueWarps;
 constexpr unsigned kVTmemCols = 512;        // two accumulators of 256 columns
-constexpr size_t kVSmem = static_cast<size_t>(kVStages) * kVStage + 1024 + 256;
+constexpr size_t kVSmem = static_cast<size_t>(kVRing) + 1024 + 1024;
 
 // One counted token of a gradient call, in the order of the list.
 struct VocabRow {
@@ -64,7 +64,9 @@ struct VocabSeg {
 
 struct VocabGemmParams {
     CUtensorMap b_map[kMaxSegs];  // W of each segment: K-major (kStats, kDlogits) or MN-major (kGrads)
+    CUtensorMap b_tail[kMaxSegs]; // kStats, kDlogits: W in boxes of half its last tile's width
     CUtensorMap a_map;            // H (kStats, kDlogits) or D, K-major
+    CUtensorMap a_tail_map;       // the same in boxes of a_tail rows
     CUtensorMap at_map;           // kGrads: D, MN-major
     CUtensorMap ht_map;           // kGrads: H, MN-major
     VocabSeg seg[kMaxSegs];
@@ -72,7 +74,13 @@ struct VocabGemmParams {
     int rows;                 // tokens
     int dim;
     int bn;                   // columns of a tile, <= kVN
-    int pairs;                // products per block of K: 1, or 6 for split float32
+    // Rows of a K-major A that exist; the last a_rows % 128 of them are copied as a_tail, a multiple of
+    // 8.  Copies do not reach past the rows that exist by more than that: rows outside the tensor cost a
+    // copy more than rows inside (one token, 127 of 128 rows outside: 115 us, with one box of 8 rows 61),
+    // and what a tile holds there goes into results that nobody reads.
+    int a_rows, a_tail;
+    int a_room;               // rows of A that a stage has room for
+    int stages;               // of a_room + bn / 2 rows each
     int tiles;                // column tiles (kStats, kDlogits) or dW tiles (kGrads) of all segments
     const VocabList *list;    // nullptr: all tokens, in order (kStats)
     const long long *targets; // kStats
@@ -92,11 +100,15 @@ struct VocabGemmParams {
 
 // Part numbers of A and B in product q of a block of K, largest last so that the small ones are
 // summed while the accumulator is small (float32; the 16-bit types have one part and one product).
-__device__ __forceinline__ void pair_parts(int pairs, int q, int &a, int &b) {
+template <int T>
+__device__ __forceinline__ void pair_parts(int q, int &a, int &b) {
     // (1,1) (0,2) (2,0) (0,1) (1,0) (0,0)
-    a = pairs == 1 ? 0 : (0x010201 >> (4 * q)) & 0xF;
-    b = pairs == 1 ? 0 : (0x001021 >> (4 * q)) & 0xF;
+    a = T == kF32 ? (0x010201 >> (4 * q)) & 0xF : 0;
+    b = T == kF32 ? (0x001021 >> (4 * q)) & 0xF : 0;
 }
+// Products per block of K.
+template <int T>
+constexpr int kVPairs = T == kF32 ? 6 : 1;
 
 // A tile: its place, its operands' places and its blocks of K.
 struct VocabTile {
@@ -104,8 +116,14 @@ struct VocabTile {
     int m, n;        // tile row and column
     int k0, kn;      // first block of K and their number
     int slice;
+    int bn;          // columns
     bool dw;
 };
+
+template <int MODE>
+__host__ __device__ constexpr int tail_width(int rows) {
+    return MODE == kStats ? (rows + 15) / 16 * 16 : (rows + 63) / 64 * 64;
+}
 
 // The i-th tile of a pair; false when it has no more.  kStats and kDlogits: row tiles of one column
 // tile next to one another, so that pairs that run together share W and find H in L2.  kGrads: first
@@ -116,6 +134,7 @@ __device__ __forceinline__ bool vocab_tile(const VocabGemmParams &p, int live, i
     const int mt = (live + kVM - 1) / kVM;
     t.slice = 0;
     t.k0 = 0;
+    t.bn = p.bn;
     t.dw = false;
     if constexpr (MODE != kGrads) {
         const long long id = pair + static_cast<long long>(i) * npairs;
@@ -126,6 +145,8 @@ __device__ __forceinline__ bool vocab_tile(const VocabGemmParams &p, int live, i
         while (t.seg + 1 < p.nseg && p.seg[t.seg + 1].tile0 <= j) ++t.seg;
         t.n = j - p.seg[t.seg].tile0;
         t.kn = (p.dim + kVK - 1) / kVK;
+        // the last tile of a segment is as narrow as its rows allow (D's columns are read in blocks of K)
+        t.bn = min(p.bn, tail_width<MODE>(p.seg[t.seg].rows - t.n * p.bn));
         return true;
     } else {
         const int per_seg = p.slices * p.dh_tiles * mt;
@@ -143,6 +164,7 @@ __device__ __forceinline__ bool vocab_tile(const VocabGemmParams &p, int live, i
             const int kb = (p.seg[t.seg].rows + kVK - 1) / kVK, per = (kb + p.slices - 1) / p.slices;
             t.k0 = t.slice * per;
             t.kn = max(0, min(per, kb - t.k0));
+            if (p.dim - t.n * p.bn <= kVN / 2) t.bn = kVN / 2;
             return true;
         }
         i -= mine;
@@ -166,6 +188,7 @@ __device__ __forceinline__ bool vocab_tile(const VocabGemmParams &p, int live, i
         while (t.seg + 1 < p.nseg && p.seg[t.seg + 1].tile0 <= j) ++t.seg;
         t.m = j - p.seg[t.seg].tile0;
         t.kn = (live + kVK - 1) / kVK;
+        if (p.dim - t.n * p.bn <= kVN / 2) t.bn = kVN / 2;
         t.dw = true;
         return true;
     }
@@ -215,8 +238,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
     extern __shared__ unsigned char raw[];
     const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
     // barriers behind the stages
-    const unsigned bars = base + kVStages * kVStage;
-    const unsigned full = bars, empty = bars + 8 * kVStages, tfull = bars + 16 * kVStages, tempty = tfull + 16;
+    const unsigned bars = base + kVRing;
+    const unsigned full = bars, empty = bars + 8 * kVMaxStages, tfull = bars + 16 * kVMaxStages, tempty = tfull + 16;
     const unsigned tmem_slot = tempty + 16, abort_slot = tmem_slot + 4, drain = tmem_slot + 8;
     volatile unsigned *abort_flag = reinterpret_cast<volatile unsigned *>(raw + (abort_slot - smem_u32(raw)));
     const unsigned rank = cluster_rank();
@@ -228,7 +251,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
         asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
     };
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kVStages; ++s) init(full + 8 * s, 1), init(empty + 8 * s, 1);
+        for (int s = 0; s < kVMaxStages; ++s) init(full + 8 * s, 1), init(empty + 8 * s, 1);
         for (int a = 0; a < 2; ++a) init(tfull + 8 * a, 1), init(tempty + 8 * a, 2 * kVEpilogueWarps);
         init(drain, 1);
         *abort_flag = 0u;
@@ -243,53 +266,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
     pdl_wait();  // the kernel before this one on the stream has finished
     asm volatile("fence.proxy.async.global;" ::: "memory");  // its plain stores, before this one's copies
     const int live = p.list ? p.list->live : p.rows;
+    const unsigned S = static_cast<unsigned>(p.stages);
+    const unsigned b_at = static_cast<unsigned>(p.a_room) * kVRow;  // B's rows behind A's in a stage
+    const unsigned stage = b_at + static_cast<unsigned>(p.bn / 2) * kVRow;
 
+    const volatile unsigned never = 0;  // for waits that follow giving up
     auto give_up = [&] {
         atomicOr(p.status, 2u);
         *abort_flag = 1u;
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---- copies: this CTA's half of each operand ----
-            unsigned it = 0;  // stages filled so far
-            bool ok = true;
-            VocabTile t;
-            for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i) {
-                const CUtensorMap *am, *bm;
-                int ay, ax, by, bx;  // first element of this CTA's rows (columns) at block 0 of K
-                const int arow = t.m * kVM + static_cast<int>(rank) * 128;
-                const int brow = t.n * p.bn + static_cast<int>(rank) * (p.bn / 2);
-                const bool a_mn = MODE == kGrads && t.dw, b_mn = MODE == kGrads;
-                if constexpr (MODE != kGrads) {
-                    am = &p.a_map, bm = &p.b_map[t.seg];
-                    ax = 0, ay = arow, bx = 0, by = brow;
-                } else if (t.dw) {
-                    am = &p.at_map, bm = &p.ht_map;
-                    ax = static_cast<int>(p.seg[t.seg].col0) + arow, ay = 0, bx = brow, by = 0;
-                } else {
-                    am = &p.a_map, bm = &p.b_map[t.seg];
-                    ax = static_cast<int>(p.seg[t.seg].col0), ay = arow, bx = brow, by = 0;
+        // ---- copies: this CTA's half of each operand ----
+        const unsigned lead_full = leader_addr(full);
+        unsigned s = 0, round = 0;  // the stage to fill and how often the ring went round
+        bool ok = true;
+        VocabTile t;
+        for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i) {
+            const CUtensorMap *am, *bm;
+            int ay, ax, by, bx;  // first element of this CTA's rows (columns) at block 0 of K
+            const int row0 = t.m * kVM, arow = row0 + static_cast<int>(rank) * 128;
+            const int brow = t.n * p.bn + static_cast<int>(rank) * (t.bn / 2);
+            const bool a_mn = MODE == kGrads && t.dw, b_mn = MODE == kGrads;
+            if constexpr (MODE != kGrads) {
+                am = &p.a_map, bm = &p.b_map[t.seg];
+                ax = 0, ay = arow, bx = 0, by = brow;
+            } else if (t.dw) {
+                am = &p.at_map, bm = &p.ht_map;
+                ax = static_cast<int>(p.seg[t.seg].col0) + arow, ay = 0, bx = brow, by = 0;
+            } else {
+                am = &p.a_map, bm = &p.b_map[t.seg];
+                ax = static_cast<int>(p.seg[t.seg].col0), ay = arow, bx = brow, by = 0;
+            }
+            // what the first and the second CTA of the pair copy of each operand, in rows of a stage
+            auto a_part = [&](int row) { return row + 128 <= p.a_rows ? 128 : row < p.a_rows ? p.a_tail : 0; };
+            auto b_part = [&](int col) {  // MN-major: chunks of 64 columns, none of them all outside
+                return t.bn == kVN && col + 64 < p.dim ? 128 : col < p.dim ? 64 : 0;
+            };
+            const int a_mine = a_mn ? 128 : a_part(arow), b_mine = b_mn ? b_part(brow) : t.bn / 2;
+            const int a_both = a_mn ? 256 : a_part(row0) + a_part(row0 + 128);
+            const int b_both = b_mn ? b_part(t.n * p.bn) + b_part(t.n * p.bn + t.bn / 2) : t.bn;
+            if (!a_mn && a_mine < 128) am = &p.a_tail_map;
+            if (!b_mn && t.bn < p.bn) bm = &p.b_tail[t.seg];
+            const unsigned bytes = static_cast<unsigned>(a_both + b_both) * kVRow;
+            int k = t.k0 * kVK, q = 0;
+            for (int n = t.kn * kVPairs<T>; n > 0; --n) {
+                int pa, pb;
+                pair_parts<T>(q, pa, pb);
+                if (round && !__all_sync(~0u, mbar_wait_bounded(empty + 8 * s, (round - 1) & 1, abort_flag))) {
+                    give_up();
+                    ok = false;
+                    break;
                 }
-                const unsigned bytes = 2 * (kVHalf + static_cast<unsigned>(p.bn / 2) * kVK * 2);
-                for (int kq = 0; kq < t.kn * p.pairs; ++kq, ++it) {
-                    const int kb = t.k0 + (p.pairs == 1 ? kq : kq / p.pairs);
-                    int pa, pb;
-                    pair_parts(p.pairs, p.pairs == 1 ? 0 : kq % p.pairs, pa, pb);
-                    const unsigned s = it % kVStages, round = it / kVStages;
-                    if (*abort_flag || (round && !mbar_wait_bounded(empty + 8 * s, (round - 1) & 1))) {
-                        give_up();
-                        ok = false;
-                        break;
-                    }
-                    const unsigned bar = leader_addr(full + 8 * s);
+                if (elect_one()) {
+                    const unsigned bar = lead_full + 8 * s;
                     if (rank == 0)
                         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + 8 * s), "r"(bytes)
                                      : "memory");
-                    const unsigned a = base + s * kVStage, b = a + kVHalf;
-                    const int k = kb * kVK;
+                    const unsigned a = base + s * stage, b = a + b_at;
                     if (!a_mn) {
-                        tma_load_3d(a, am, bar, ax + k, ay, pa);
+                        if (a_mine) tma_load_3d(a, am, bar, ax + k, ay, pa);
                     } else {  // two chunks of 64 columns, 64 rows each
                         tma_load_3d(a, am, bar, ax, ay + k, pa);
                         tma_load_3d(a + 8192, am, bar, ax + 64, ay + k, pa);
@@ -297,58 +333,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                     if (!b_mn) {
                         tma_load_3d(b, bm, bar, bx + k, by, pb);
                     } else {
-                        tma_load_3d(b, bm, bar, bx, by + k, pb);
-                        if (p.bn == 256) tma_load_3d(b + 8192, bm, bar, bx + 64, by + k, pb);
+                        if (b_mine) tma_load_3d(b, bm, bar, bx, by + k, pb);
+                        if (b_mine > 64) tma_load_3d(b + 8192, bm, bar, bx + 64, by + k, pb);
                     }
                 }
+                if (++s == S) s = 0, ++round;
+                if (++q == kVPairs<T>) q = 0, k += kVK;
             }
-            // the products' last arrivals have to find this CTA still here
-            for (unsigned k = it > kVStages ? it - kVStages : 0; ok && k < it; ++k)
-                if (!mbar_wait_bounded(empty + 8 * (k % kVStages), (k / kVStages) & 1)) {
-                    give_up();
-                    ok = false;
-                }
-            if (!ok && rank == 0)  // copies in flight (of both CTAs) land before the pair leaves
-                for (unsigned k = it > kVStages ? it - kVStages : 0; k < it; ++k)
-                    mbar_wait_bounded(full + 8 * (k % kVStages), (k / kVStages) & 1);
+        }
+        // the products' last arrivals have to find this CTA still here; after a wait that ran out, the
+        // copies in flight (of both CTAs) have to land before the pair leaves
+        for (unsigned q = 0; q < S; ++q) {
+            const unsigned fills = round + (q < s);  // of stage q
+            if (fills == 0) continue;
+            if (ok && !__all_sync(~0u, mbar_wait_bounded(empty + 8 * q, (fills - 1) & 1, abort_flag))) {
+                give_up();
+                ok = false;
+            }
+            if (!ok && rank == 0) mbar_wait_bounded(full + 8 * q, (fills - 1) & 1, &never);
         }
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             // ---- products ----
-            unsigned it = 0, acc_it = 0;
+            const uint64_t desc0 = umma_desc(base, 8192);
+            unsigned s = 0, phase = 0, acc_it = 0;
             bool ok = true;
             VocabTile t;
             for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i, ++acc_it) {
                 const unsigned acc = acc_it % 2, use = acc_it / 2;
-                if (use && !mbar_wait_bounded(tempty + 8 * acc, (use - 1) & 1)) {
+                if (use && !__all_sync(~0u, mbar_wait_bounded(tempty + 8 * acc, (use - 1) & 1, abort_flag))) {
                     give_up();
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
                 const bool a_mn = MODE == kGrads && t.dw, b_mn = MODE == kGrads;
-                const uint32_t idesc = umma_idesc(T != kF16, a_mn, b_mn, static_cast<unsigned>(p.bn));
+                const uint32_t idesc = umma_idesc(T != kF16, a_mn, b_mn, static_cast<unsigned>(t.bn));
                 // 16 elements of K: 32 bytes along a K-major row, two groups of eight rows otherwise
                 const unsigned a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
-                for (int kq = 0; kq < t.kn * p.pairs; ++kq, ++it) {
-                    const unsigned s = it % kVStages;
-                    if (*abort_flag || !mbar_wait_bounded(full + 8 * s, (it / kVStages) & 1)) {
+                const unsigned d = tmem + acc * 256;
+                bool more = false;  // the first product of a tile starts the accumulator
+                for (int n = t.kn * kVPairs<T>; n > 0; --n) {
+                    if (!__all_sync(~0u, mbar_wait_bounded(full + 8 * s, phase, abort_flag))) {
                         give_up();
                         ok = false;
                         break;
                     }
                     tmem_fence_after();
-                    const uint64_t a = umma_desc(base + s * kVStage, 8192), b = umma_desc(base + s * kVStage + kVHalf, 8192);
+                    const uint64_t a = desc0 + ((s * stage) >> 4), b = a + (b_at >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (unsigned k = 0; k < kVK / 16; ++k)
-                        umma(tmem + acc * 256, a + k * a_step, b + k * b_step, idesc, kq > 0 || k > 0);
-                    umma_commit(empty + 8 * s);
+                        for (unsigned k = 0; k < kVK / 16; ++k) umma(d, a + k * a_step, b + k * b_step, idesc, more || k > 0);
+                        umma_commit(empty + 8 * s);
+                    }
+                    __syncwarp();
+                    more = true;
+                    if (++s == S) s = 0, phase ^= 1;
                 }
-                if (ok) umma_commit(tfull + 8 * acc);
+                if (ok && elect_one()) umma_commit(tfull + 8 * acc);
+                __syncwarp();
             }
             if (!ok) {  // products in flight finish before the tensor memory goes
-                umma_commit(drain);
-                mbar_wait_bounded(drain, 0);
+                if (elect_one()) umma_commit(drain);
+                __syncwarp();
+                mbar_wait_bounded(drain, 0, &never);
             }
         }
     } else if (warp >= 4) {
@@ -360,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
         for (int i = 0; vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i, ++acc_it) {
             const unsigned acc = acc_it % 2, use = acc_it / 2;
             const int r = t.m * kVM + static_cast<int>(rank) * 128 + quarter * 32 + lane;  // row of the product
-            const int c0 = half * (p.bn / 2);                                             // first column in the tile
+            const int c0 = half * (t.bn / 2);                                             // first column in the tile
             const VocabSeg &seg = p.seg[t.seg];
             const unsigned src = tmem + acc * 256 + static_cast<unsigned>(c0) + (static_cast<unsigned>(quarter * 32) << 16);
             long long y = -1;
@@ -373,13 +421,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                     y = q.y, lse = q.lse, g = q.g;
                 }
             }
-            const bool ok = mbar_wait_bounded(tfull + 8 * acc, use & 1);
-            if (__any_sync(~0u, !ok || *abort_flag)) {
+            const bool ok = mbar_wait_bounded(tfull + 8 * acc, use & 1, abort_flag);
+            if (__any_sync(~0u, !ok)) {
                 if (lane == 0) give_up();
                 break;
             }
             tmem_fence_after();
-            const int width = p.bn / 2;
+            const int width = t.bn / 2;
             if constexpr (MODE == kStats) {
                 const int col = t.n * p.bn + c0;                 // column in the segment
                 const int n = min(width, seg.rows - col);        // columns of this warp that exist
@@ -505,32 +553,45 @@ struct VocabJoinParams {
     float *loss, *lse;
 };
 
+// A running maximum m and sum s of exp(z - m) joined with another; m = -infinity and s = 0 join as nothing.
+__device__ __forceinline__ void join_stats(float &m, float &s, float qm, float qs) {
+    const float to = fmaxf(m, qm), ref = fabsf(to) == INFINITY ? 0.0f : to;
+    auto moved = [&](float a, float x) {  // an infinite maximum's sum is relative to zero
+        return a == -INFINITY ? x : x * __expf((a == INFINITY ? 0.0f : a) - ref);
+    };
+    s = moved(m, s) + moved(qm, qs);
+    m = to;
+}
+
 // Join the partial statistics of each row: lse = log sum exp, loss = lse - target's logit.  A block
-// takes 32 rows; its warps share the parts, and the first joins the warps.
+// takes 4 rows, 64 threads to a row, so that a single row's hundreds of parts are loaded at once.
 static __global__ void __launch_bounds__(256) ar_vocab_join_kernel(const __grid_constant__ VocabJoinParams p) {
-    __shared__ float ms[8][32], ss[8][32];
+    constexpr int R = 4;
+    __shared__ float ms[8][R], ss[8][R];
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const long long t = static_cast<long long>(blockIdx.x) * 32 + lane;
+    const long long t = static_cast<long long>(blockIdx.x) * R + threadIdx.x % R;
     float m = -INFINITY, s = 0.0f;
-    auto add = [&](float qm, float qs) {
-        if (qm == -INFINITY && !(qs != qs)) return;  // a part without a finite or infinite logit adds nothing
-        const float to = fmaxf(m, qm), ref = fabsf(to) == INFINITY ? 0.0f : to;
-        s = (m == -INFINITY ? s : s * __expf((m == INFINITY ? 0.0f : m) - ref)) +
-            qs * __expf((fabsf(qm) == INFINITY ? 0.0f : qm) - ref);
-        m = to;
-    };
-    if (t < p.rows)
-        for (int k = warp; k < p.parts; k += 8) {
-            const float2 q = p.part[static_cast<long long>(k) * p.rows + t];
-            add(q.x, q.y);
+    if (t < p.rows) {
+        constexpr int U = 4;
+        for (int k = threadIdx.x / R; k < p.parts; k += U * (256 / R)) {
+            float2 q[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int at = k + u * (256 / R);
+                q[u] = at < p.parts ? p.part[static_cast<long long>(at) * p.rows + t] : make_float2(-INFINITY, 0.0f);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) join_stats(m, s, q[u].x, q[u].y);
         }
-    ms[warp][lane] = m;
-    ss[warp][lane] = s;
+    }
+    for (int o = 16; o >= R; o /= 2)
+        join_stats(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+    if (lane < R) ms[warp][lane] = m, ss[warp][lane] = s;
     __syncthreads();
-    if (warp || t >= p.rows) return;
-    for (int w = 1; w < 8; ++w) add(ms[w][lane], ss[w][lane]);
+    if (threadIdx.x >= R || t >= p.rows) return;
+    for (int w = 1; w < 8; ++w) join_stats(m, s, ms[w][lane], ss[w][lane]);
     const float lse = (fabsf(m) == INFINITY ? 0.0f : m) + logf(s);
     p.lse[t] = lse;
     const long long y = p.targets[t];

@@ -20,6 +20,14 @@ __device__ __forceinline__ unsigned cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// One lane of the (whole) warp.  The warps that feed the tensor cores run their loops together and
+// only issue from one lane: what the instructions take then stays in uniform registers (a loop run by
+// lane 0 alone took 68 cycles for each product, whatever its size, and was the bound of small tiles).
+__device__ __forceinline__ bool elect_one() {
+    unsigned p;
+    asm volatile("{ .reg .pred q; elect.sync _|q, 0xFFFFFFFF; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+    return p != 0;
+}
 // The address, in the cluster's shared memory, of the leader's copy of a variable of this CTA.
 __device__ __forceinline__ unsigned leader_addr(unsigned local) {
     unsigned a;
@@ -30,20 +38,23 @@ __device__ __forceinline__ unsigned leader_addr(unsigned local) {
 __device__ __forceinline__ bool mbar_try(unsigned addr, unsigned parity) {
     unsigned done;
     asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
         : "=r"(done)
-        : "r"(addr), "r"(parity), "r"(20000u)
+        : "r"(addr), "r"(parity)
         : "memory");
     return done != 0;
 }
-// Wait for the phase of the given parity; false when kUmmaTimeoutNs ran out.  The clock is read only
-// once the first try has failed.
-__device__ __forceinline__ bool mbar_wait_bounded(unsigned addr, unsigned parity) {
-    if (mbar_try(addr, parity)) return true;
+// Wait for the phase of the given parity; false when kUmmaTimeoutNs ran out or another warp gave up.
+// The clock and the flag are read only once the first try has failed: the threads that feed the
+// tensor cores have a few hundred cycles for a block of K.
+static __device__ __noinline__ bool mbar_wait_slow(unsigned addr, unsigned parity, const volatile unsigned *abort_flag) {
     const unsigned long long deadline = global_ns() + kUmmaTimeoutNs;
     while (!mbar_try(addr, parity))
-        if (global_ns() > deadline) return false;
+        if (*abort_flag || global_ns() > deadline) return false;
     return true;
+}
+__device__ __forceinline__ bool mbar_wait_bounded(unsigned addr, unsigned parity, const volatile unsigned *abort_flag) {
+    return mbar_try(addr, parity) || mbar_wait_slow(addr, parity, abort_flag);
 }
 __device__ __forceinline__ void mbar_arrive_cluster(unsigned cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");

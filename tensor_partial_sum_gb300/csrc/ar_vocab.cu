@@ -285,7 +285,24 @@ bool make_map(CUtensorMap *m, bool f16, const void *base, size_t cols, size_t ro
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of the boxes of a segment's last column tile: half its width.
+template <int MODE>
+unsigned tail_box(size_t rows, int bn) {
+    const int left = static_cast<int>(rows % static_cast<size_t>(bn));
+    const int width = tps::tail_width<MODE>(left ? left : bn);
+    return static_cast<unsigned>((width < bn ? width : bn) / 2);
+}
+
 // A call under way: what its launches share.
+// The two maps of a K-major A: boxes of 128 rows, and of the rows left over (8 at least).
+bool make_a_maps(tps::VocabGemmParams &p, bool f16, const void *base, size_t cols, size_t rows, size_t parts, size_t ld,
+                 size_t part) {
+    p.a_rows = static_cast<int>(rows);
+    p.a_tail = static_cast<int>(round_up(rows % 128, 8));
+    return make_map(&p.a_map, f16, base, cols, rows, parts, ld, part, 128) &&
+           make_map(&p.a_tail_map, f16, base, cols, rows, parts, ld, part, p.a_tail ? static_cast<unsigned>(p.a_tail) : 8u);
+}
+
 struct Call {
     const ar_vocab *v;
     tps::CallContext c;
@@ -344,8 +361,16 @@ struct Call {
         return AR_OK;
     }
 
+    // With few rows of A a stage holds less, and more stages fit: these launches are bound by the bytes
+    // in flight.  (dW's A is a full tile of vocabulary rows.)
     template <int MODE>
-    int launch_gemm(const tps::VocabGemmParams &p, size_t tiles) const {
+    int launch_gemm(tps::VocabGemmParams &p, size_t tiles) const {
+        p.a_room = p.a_rows >= 128 || (MODE == tps::kGrads && p.tiles) ? 128 : p.a_tail;
+        // a product reads 128 rows of A wherever the stage starts: the last stage's have to lie in the ring
+        const int stage = (p.a_room + p.bn / 2) * tps::kVRow, last = tps::kVRing - 128 * tps::kVRow;
+        p.stages = tps::kVRing / stage;
+        if (p.stages > last / stage + 1) p.stages = last / stage + 1;
+        if (p.stages > tps::kVMaxStages) p.stages = tps::kVMaxStages;
         const auto fn = by_type<tps::VocabGemmParams>(v->dtype, tps::ar_vocab_gemm_kernel<MODE, tps::kF32>,
                                                       tps::ar_vocab_gemm_kernel<MODE, tps::kF16>,
                                                       tps::ar_vocab_gemm_kernel<MODE, tps::kBF16>);
@@ -428,12 +453,11 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
     p.rows = static_cast<int>(T);
     p.dim = static_cast<int>(D);
     p.bn = stats_width(v, c.sm_count / 2);
-    p.pairs = call.parts == 1 ? 1 : 6;
     p.targets = reinterpret_cast<const long long *>(v->targets);
     p.part = reinterpret_cast<float2 *>(call.ws + plan.part);
     p.picked = reinterpret_cast<float *>(call.ws + plan.picked);
     p.status = c.dev_status;
-    if (!make_map(&p.a_map, call.f16, h.base, D, h.rows, call.parts, h.ld, h.part, 128)) return AR_ERR_CUDA;
+    if (!make_a_maps(p, call.f16, h.base, D, h.rows, call.parts, h.ld, h.part)) return AR_ERR_CUDA;
     long long first[AR_MAX_RANKS], total = 0;
     for (int r = 0; r < v->n_pieces; ++r) first[r] = total, total += static_cast<long long>(v->piece_rows[r]);
     int piece = 0, done = 0;  // column tiles of earlier groups
@@ -451,7 +475,9 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
             p.seg[s].tile0 = p.tiles;
             p.tiles += static_cast<int>(tiles_of(g.rows[s], static_cast<size_t>(p.bn)));
             if (!make_map(&p.b_map[s], call.f16, w[s].base, D, w[s].rows, call.parts, w[s].ld, w[s].part,
-                          static_cast<unsigned>(p.bn / 2)))
+                          static_cast<unsigned>(p.bn / 2)) ||
+                !make_map(&p.b_tail[s], call.f16, w[s].base, D, w[s].rows, call.parts, w[s].ld, w[s].part,
+                          tail_box<tps::kStats>(g.rows[s], p.bn)))
                 return AR_ERR_CUDA;
         }
         st = call.launch_gemm<tps::kStats>(p, static_cast<size_t>(p.tiles) * tiles_of(T, tps::kVM));
@@ -470,7 +496,7 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
     j.parts = 2 * done;
     j.loss = loss;
     j.lse = lse;
-    return call.launch<tps::VocabJoinParams>(tps::ar_vocab_join_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), 256u, 0, j);
+    return call.launch<tps::VocabJoinParams>(tps::ar_vocab_join_kernel, dim3(static_cast<unsigned>((T + 3) / 4)), 256u, 0, j);
 }
 
 int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, void *const *dhidden,
@@ -558,16 +584,13 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
     memset(&p, 0, sizeof p);
     p.rows = l.rows;
     p.dim = static_cast<int>(D);
-    p.pairs = call.parts == 1 ? 1 : 6;
     p.list = l.list;
     p.row = l.row;
     p.index = l.index;
     p.d = reinterpret_cast<unsigned short *>(call.ws + plan.d);
     p.status = c.dev_status;
     const size_t mt = plan.d_rows / tps::kVM;
-    CUtensorMap h_k, h_mn;
-    if (!make_map(&h_k, call.f16, call.ws + plan.hidden, D, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld, 128) ||
-        !make_map(&h_mn, call.f16, call.ws + plan.hidden, D, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld, 64))
+    if (!make_map(&p.ht_map, call.f16, call.ws + plan.hidden, D, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld, 64))
         return AR_ERR_CUDA;
     long long first[AR_MAX_RANKS], total = 0;
     for (int r = 0; r < v->n_pieces; ++r) first[r] = total, total += static_cast<long long>(v->piece_rows[r]);
@@ -584,24 +607,26 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
         p.nseg = g.nseg;
         p.bn = tps::kVN;
         p.tiles = 0;
-        p.a_map = h_k;
+        if (!make_a_maps(p, call.f16, call.ws + plan.hidden, D, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld))
+            return AR_ERR_CUDA;
         for (int s = 0; s < g.nseg; ++s) {
             p.seg[s].first = first[g.piece[s]] + static_cast<long long>(g.row0[s]);
             p.seg[s].rows = static_cast<int>(g.rows[s]);
             p.seg[s].tile0 = p.tiles;
             p.seg[s].col0 = static_cast<long long>(p.tiles) * tps::kVN;
             p.tiles += static_cast<int>(tiles_of(g.rows[s], tps::kVN));
-            if (!make_map(&p.b_map[s], call.f16, w[s].base, D, w[s].rows, call.parts, w[s].ld, w[s].part, tps::kVN / 2))
+            if (!make_map(&p.b_map[s], call.f16, w[s].base, D, w[s].rows, call.parts, w[s].ld, w[s].part, tps::kVN / 2) ||
+                !make_map(&p.b_tail[s], call.f16, w[s].base, D, w[s].rows, call.parts, w[s].ld, w[s].part,
+                          tail_box<tps::kDlogits>(g.rows[s], p.bn)))
                 return AR_ERR_CUDA;
         }
         st = call.launch_gemm<tps::kDlogits>(p, static_cast<size_t>(p.tiles) * mt);
         if (st != AR_OK) return st;
         // dH and dW from it
         const size_t parts = call.parts, dl = static_cast<size_t>(p.d_ld), dp = static_cast<size_t>(p.d_part);
-        if (!make_map(&p.a_map, call.f16, p.d, dl, plan.d_rows, parts, dl, dp, 128) ||
-            !make_map(&p.at_map, call.f16, p.d, dl, plan.d_rows, parts, dl, dp, 64))
+        if (!make_a_maps(p, call.f16, p.d, dl, plan.k_rows, parts, dl, dp) ||
+            !make_map(&p.at_map, call.f16, p.d, dl, plan.k_rows, parts, dl, dp, 64))
             return AR_ERR_CUDA;
-        p.ht_map = h_mn;
         p.bn = D <= tps::kVN / 2 ? tps::kVN / 2 : tps::kVN;
         p.slices = plan.slices;
         p.dh_tiles = dhidden ? static_cast<int>(tiles_of(D, static_cast<size_t>(p.bn))) : 0;
