@@ -36,7 +36,9 @@ constexpr int kVRing = 6 * 256 * kVRow;     // bytes of the stages: six of full 
 constexpr int kVEpilogueWarps = 8;
 constexpr int kVThreads = 128 + 32 * kVEpilogueWarps;
 constexpr unsigned kVTmemCols = 512;        // two accumulators of 256 columns
-constexpr size_t kVSmem = static_cast<size_t>(kVRing) + 1024 + 1024;
+constexpr int kVPitch = 80;                 // bytes between a warp's staged output rows of 64 bytes
+constexpr int kVOut = kVEpilogueWarps * 32 * kVPitch;
+constexpr size_t kVSmem = static_cast<size_t>(kVRing) + kVOut + 1024 + 1024;
 
 // One counted token of a gradient call, in the order of the list.
 struct VocabRow {
@@ -194,21 +196,54 @@ __device__ __forceinline__ bool vocab_tile(const VocabGemmParams &p, int live, i
     }
 }
 
-// 32 values of a row to `n` (at most 32) elements of T at `out`: whole vectors where the row allows.
+// Store a warp's 32x32 values, row `lane` in each thread: `n` (1 to 32) elements of T to each thread's
+// `out` (nullptr: no row).  The rows go through shared memory, so that adjacent lanes store adjacent
+// bytes: rows of 64 bytes in pieces of 16 where all of them allow it, element after element otherwise
+// (each lane storing its own row, 2 bytes in 32 places at once, made dW of odd rows 5 times slower).
 template <int T>
-__device__ __forceinline__ void store_row32(char *out, const float (&v)[32], int n) {
-    constexpr int W = T == kF32 ? 32 : 16;
-    if (n >= 32 && reinterpret_cast<uintptr_t>(out) % 16 == 0) {
-        uint32_t w[W];
-        word_pack<T, W>(v, w);
+__device__ __forceinline__ void store_block(unsigned char *stage, char *out, const float (&v)[32], int n, int lane) {
+    constexpr int es = Elem<T>::bytes, per = 64 / es;  // elements of a pass
+    const unsigned long long mine = reinterpret_cast<unsigned long long>(out);
+    const bool vec = __all_sync(~0u, mine % 16 == 0) && n == 32;
 #pragma unroll
-        for (int k = 0; k < W; k += 4)
-            *reinterpret_cast<uint4 *>(out + 4 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
-        return;
+    for (int c = 0; c < 32; c += per) {
+        if (c >= n) break;
+        uint32_t w[16];
+        if constexpr (T == kF32) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(v[c + k]);
+        } else {
+            word_pack<T, 16>(v, w);
+        }
+        __syncwarp();  // the last pass has been read
+#pragma unroll
+        for (int k = 0; k < 16; k += 4)
+            *reinterpret_cast<uint4 *>(stage + lane * kVPitch + 4 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+        __syncwarp();
+        if (vec) {
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 8) {
+                const int r = r0 + lane / 4, at = lane % 4 * 16;
+                char *to = reinterpret_cast<char *>(__shfl_sync(~0u, mine, r));
+                if (to) *reinterpret_cast<uint4 *>(to + c * es + at) = *reinterpret_cast<uint4 *>(stage + r * kVPitch + at);
+            }
+        } else {
+            const int k = lane % per;
+#pragma unroll 4
+            for (int r0 = 0; r0 < 32; r0 += 32 / per) {
+                const int r = r0 + lane / per;
+                char *to = reinterpret_cast<char *>(__shfl_sync(~0u, mine, r));
+                if (to && c + k < n) {
+                    if constexpr (T == kF32) {
+                        reinterpret_cast<uint32_t *>(to)[c + k] = *reinterpret_cast<uint32_t *>(stage + r * kVPitch + 4 * k);
+                    } else {
+                        reinterpret_cast<unsigned short *>(to)[c + k] =
+                            *reinterpret_cast<unsigned short *>(stage + r * kVPitch + 2 * k);
+                    }
+                }
+            }
+        }
     }
-#pragma unroll
-    for (int k = 0; k < 32; ++k)
-        if (k < n) store_elem<T>(out, k, v[k]);
 }
 
 // The three bf16 parts of two floats, eight bits each, packed in pairs.
@@ -238,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
     extern __shared__ unsigned char raw[];
     const unsigned base = (smem_u32(raw) + 1023u) & ~1023u;
     // barriers behind the stages
-    const unsigned bars = base + kVRing;
+    const unsigned bars = base + kVRing + kVOut;
     const unsigned full = bars, empty = bars + 8 * kVMaxStages, tfull = bars + 16 * kVMaxStages, tempty = tfull + 16;
     const unsigned tmem_slot = tempty + 16, abort_slot = tmem_slot + 4, drain = tmem_slot + 8;
     volatile unsigned *abort_flag = reinterpret_cast<volatile unsigned *>(raw + (abort_slot - smem_u32(raw)));
@@ -402,6 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
     } else if (warp >= 4) {
         // ---- results: a warp reads the 32 lanes of its quarter and half of the columns ----
         const int quarter = warp % 4, half = (warp - 4) / 4;
+        unsigned char *stage_out = raw + (base - smem_u32(raw)) + kVRing + (warp - 4) * 32 * kVPitch;
         unsigned acc_it = 0;
         VocabTile t;
         const float unscale = MODE == kGrads && p.list ? p.list->unscale : 1.0f;
@@ -524,7 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                                 if (!out) *q = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
                             }
                     }
-                    if (out && c < n) store_row32<T>(out + c * es, v, min(32, n - c));
+                    if (c < n) store_block<T>(stage_out, out ? out + c * es : nullptr, v, min(32, n - c), lane);
                 }
             }
             tmem_fence_before();
@@ -625,33 +661,50 @@ static __global__ void __launch_bounds__(1024) ar_vocab_list_kernel(const __grid
         const long long y = p.targets[t];
         return y != p.ignore && y >= 0 && y < p.vocab;
     };
+    // four adjacent tokens to a thread
+    constexpr int U = 4;
     float top = 0.0f;
-    for (int t = threadIdx.x; t < p.rows; t += 1024)
-        if (counted(t)) top = fmaxf(top, fabsf(p.dloss[t]));
+    for (int t0 = U * static_cast<int>(threadIdx.x); t0 < p.rows; t0 += U * 1024)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (counted(t0 + u)) top = fmaxf(top, fabsf(p.dloss[t0 + u]));
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     if (lane == 0) tops[warp] = top;
     __syncthreads();
-    for (int w = 0; w < 32; ++w) top = fmaxf(top, tops[w]);
+    top = tops[lane];
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     if (!(top > 0.0f && top <= 3.402823466e38f)) top = 1.0f;
     int done = 0;
-    for (int t0 = 0; t0 < p.rows; t0 += 1024) {
-        const int t = t0 + static_cast<int>(threadIdx.x);
-        const bool c = counted(t);
-        const unsigned votes = __ballot_sync(~0u, c);
-        if (lane == 0) counts[warp] = __popc(votes);
+    for (int b0 = 0; b0 < p.rows; b0 += U * 1024) {
+        const int t0 = b0 + U * static_cast<int>(threadIdx.x);
+        bool c[U];
+        int mine = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) mine += c[u] = counted(t0 + u);
+        int upto = mine;  // of this warp's threads up to this one
+        for (int o = 1; o < 32; o *= 2) {
+            const int q = __shfl_up_sync(~0u, upto, o);
+            if (lane >= o) upto += q;
+        }
+        if (lane == 31) counts[warp] = upto;
         __syncthreads();
-        int before = 0, all = 0;
-        for (int w = 0; w < 32; ++w) {
-            before += w < warp ? counts[w] : 0;
-            all += counts[w];
+        int warps = counts[lane];  // of the warps up to warp `lane`
+        for (int o = 1; o < 32; o *= 2) {
+            const int q = __shfl_up_sync(~0u, warps, o);
+            if (lane >= o) warps += q;
         }
-        const int at = done + before + __popc(votes & ((1u << lane) - 1u));
-        if (c) {
-            p.row[at] = VocabRow{p.lse[t], p.dloss[t] / top * p.gain, p.targets[t]};
-            p.index[at] = t;
+        int at = done + upto - mine + (warp ? __shfl_sync(~0u, warps, warp - 1) : 0);
+        done += __shfl_sync(~0u, warps, 31);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + u;
+            if (c[u]) {
+                p.row[at] = VocabRow{p.lse[t], p.dloss[t] / top * p.gain, p.targets[t]};
+                p.index[at] = t;
+            }
+            if (t < p.rows) p.place[t] = c[u] ? at : -1;
+            at += c[u];
         }
-        if (t < p.rows) p.place[t] = c ? at : -1;
-        done += all;
         __syncthreads();
     }
     if (threadIdx.x == 0) *p.list = VocabList{done, top / p.gain};
@@ -689,7 +742,14 @@ __global__ void __launch_bounds__(256) ar_vocab_pack_kernel(const __grid_constan
             continue;
         }
         const char *src = static_cast<const char *>(p.src) + t * p.src_row;
+        const bool whole = reinterpret_cast<uintptr_t>(src) % 16 == 0;
         for (long long g = threadIdx.x; g < p.dst_ld / 8; g += blockDim.x) {
+            if constexpr (T != kF32) {
+                if (whole && 8 * g + 8 <= p.dim) {
+                    *reinterpret_cast<uint4 *>(p.dst + at * p.dst_ld + 8 * g) = __ldg(reinterpret_cast<const uint4 *>(src) + g);
+                    continue;
+                }
+            }
             float v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = 8 * g + k < p.dim ? load_elem<T, true>(src, 8 * g + k) : 0.0f;
@@ -725,18 +785,27 @@ struct VocabSumParams {
     long long dh_row[kMaxSegs];
 };
 
-// dH of a piece from its slices, in their order: blockIdx.z picks the segment, blockIdx.y strides over rows.
+// dH of a piece from its slices, in their order: blockIdx.z picks the segment, blockIdx.y strides over
+// rows, a thread takes four columns.
 template <int T>
 __global__ void __launch_bounds__(256) ar_vocab_sum_kernel(const __grid_constant__ VocabSumParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    const int live = p.list->live, c = blockIdx.x * 256 + threadIdx.x;
+    const int live = p.list->live, c = (blockIdx.x * 256 + threadIdx.x) * 4;
     if (c >= p.dim) return;
     for (int r = blockIdx.y; r < live; r += gridDim.y) {
-        float v = 0.0f;
-        for (int s = 0; s < p.slices; ++s)
-            v += p.sum[((static_cast<long long>(blockIdx.z) * p.slices + s) * p.sum_rows + r) * p.sum_ld + c];
-        store_elem<T>(p.dh[blockIdx.z] + static_cast<long long>(p.index[r]) * p.dh_row[blockIdx.z], c, v);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int s = 0; s < p.slices; ++s) {
+            const float4 q = *reinterpret_cast<const float4 *>(
+                p.sum + ((static_cast<long long>(blockIdx.z) * p.slices + s) * p.sum_rows + r) * p.sum_ld + c);
+            v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+        }
+        char *out = p.dh[blockIdx.z] + static_cast<long long>(p.index[r]) * p.dh_row[blockIdx.z];
+        const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c + k < p.dim) store_elem<T>(out, c + k, w[k]);
     }
 }
 

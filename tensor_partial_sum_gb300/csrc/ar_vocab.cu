@@ -208,23 +208,25 @@ GradPlan plan_grad(const ar_vocab *v) {
     size_t cap = group_cap(p.d_rows * 2 * parts);
     if (pack && group_cap(row) < cap) cap = group_cap(row);
     p.cap = cap < all ? cap : all;
-    // With few tiles of dH their long reductions are cut into slices, so that every pair of SMs gets
-    // some: enough for two rounds of 76 pairs, none shorter than eight blocks of K, and no more partial
-    // sums than kSliceBytes.
-    size_t longest = 0;
+    // The dH tiles reduce over the vocabulary, the dW tiles over the tokens.  Where one dH tile would take
+    // more than a pair's share of all blocks of K, its reduction is cut into slices of half a share (none
+    // shorter than eight blocks), whose partial sums (kSliceBytes at most) a last kernel adds.
+    size_t longest = 0, blocks = 0;
     int segs = 0;
+    const size_t nt = tiles_of(v->dim, tps::kVN), mt = p.d_rows / tps::kVM, kw = tiles_of(v->rows, tps::kVK);
     for (int r = 0; r < v->n_pieces; ++r) {
-        longest = v->piece_rows[r] > longest ? v->piece_rows[r] : longest;
-        segs += v->piece_rows[r] != 0;
+        const size_t n = v->piece_rows[r];
+        longest = n > longest ? n : longest;
+        segs += n != 0;
+        blocks += nt * (mt * tiles_of(n, tps::kVK) + tiles_of(n, tps::kVM) * (kw < 8 ? 8 : kw));
     }
     const bool split = round_up(longest, tps::kVN) > p.cap;
-    if (longest > p.cap) longest = p.cap;
-    const size_t tiles = p.d_rows / tps::kVM * tiles_of(v->dim, tps::kVN) * static_cast<size_t>(segs ? segs : 1);
-    const size_t slice = p.d_rows * round_up(v->dim, 8) * sizeof(float);
-    size_t s = tiles ? 152 / tiles : 1;
-    const size_t blocks = tiles_of(longest, tps::kVK);
-    if (s > blocks / 8) s = blocks / 8;
-    if (s > kSliceBytes / (slice * static_cast<size_t>(segs ? segs : 1) + 1)) s = kSliceBytes / (slice * static_cast<size_t>(segs ? segs : 1) + 1);
+    if (split) blocks = blocks / (longest / p.cap + 1), longest = p.cap;
+    const size_t share = blocks / 76 + 1, tile = tiles_of(longest, tps::kVK);
+    const size_t slice = p.d_rows * round_up(v->dim, 8) * sizeof(float) * static_cast<size_t>(segs ? segs : 1);
+    size_t s = 1;
+    if (tile > share) s = tiles_of(tile, share / 2 < 8 ? 8 : share / 2);
+    if (s > kSliceBytes / (slice + 1)) s = kSliceBytes / (slice + 1);
     p.slices = s < 2 ? 1 : static_cast<int>(s);
     p.sums = split || p.slices > 1;
     Carve c;
@@ -235,7 +237,7 @@ GradPlan plan_grad(const ar_vocab *v) {
     p.hidden = c.take(p.k_rows * row);
     p.d = c.take(p.d_rows * p.cap * 2 * parts);
     p.weights = c.take(pack ? p.cap * row : 0);
-    p.sum = c.take(p.sums ? static_cast<size_t>(p.slices) * slice * static_cast<size_t>(p.slices > 1 ? segs : 1) : 0);
+    p.sum = c.take(p.sums ? static_cast<size_t>(p.slices) * slice : 0);
     p.bytes = c.at;
     return p;
 }
@@ -668,7 +670,7 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
             st = call.launch(by_type<tps::VocabSumParams>(v->dtype, tps::ar_vocab_sum_kernel<tps::kF32>,
                                                           tps::ar_vocab_sum_kernel<tps::kF16>,
                                                           tps::ar_vocab_sum_kernel<tps::kBF16>),
-                             dim3(static_cast<unsigned>((D + 255) / 256), static_cast<unsigned>(T < 1024 ? T : 1024),
+                             dim3(static_cast<unsigned>((D + 1023) / 1024), static_cast<unsigned>(T < 4096 ? T : 4096),
                                   static_cast<unsigned>(g.nseg)),
                              256u, 0, q);
             if (st != AR_OK) return st;
