@@ -11,18 +11,59 @@ using tps::dtype_bytes;
 
 namespace {
 
-// Row blocks of the column sums: enough to fill the GPU, few enough that the
-// partial sums stay small beside the gradient (at most 128 rows of ne0).
-constexpr unsigned kMaxRowBlocks = 128;
+// Threads of a block: bx along a row (eight columns each) by `by` row groups.
+struct Shape {
+    int bx, by;
+    unsigned gx;       // blocks along a row
+    unsigned threads;
+};
 
-unsigned rows_per_block(size_t ne1) {
-    const size_t r = (ne1 + kMaxRowBlocks - 1) / kMaxRowBlocks;
-    return static_cast<unsigned>(r < 16 ? 16 : r);
+// Short rows share a block; long rows are cut into blocks of the width (half to all of `widest`) that
+// leaves the fewest threads idle.
+Shape block_shape(size_t ne0, int threads, int widest) {
+    const size_t units = (ne0 + tps::kDropCols - 1) / tps::kDropCols;
+    Shape s{};
+    if (units <= static_cast<size_t>(widest)) {
+        s.bx = static_cast<int>(units < 1 ? 1 : units);
+    } else {
+        size_t best = 0;
+        for (int t = widest; t >= widest / 2; t -= 32) {
+            const size_t cover = (units + t - 1) / t * t;
+            if (best == 0 || cover < best) best = cover, s.bx = t;
+        }
+    }
+    s.by = threads / s.bx;
+    s.gx = static_cast<unsigned>((units + s.bx - 1) / s.bx);
+    s.threads = static_cast<unsigned>((s.bx * s.by + 31) / 32 * 32);
+    return s;
 }
 
-unsigned row_blocks(size_t ne1) {
-    const unsigned r = rows_per_block(ne1);
-    return static_cast<unsigned>((ne1 + r - 1) / r);
+constexpr int kForwardThreads = 256;
+constexpr int kGradThreads = 512;
+constexpr int kGradWidest = 128;  // four row groups to a block: fewer partial sums
+
+Shape forward_shape(size_t ne0) { return block_shape(ne0, kForwardThreads, kForwardThreads); }
+Shape grad_shape(size_t ne0) { return block_shape(ne0, kGradThreads, kGradWidest); }
+
+// Row blocks of the backward pass.  With column sums, as few as fill the GPU twice (two blocks of 512
+// threads on each of 152 SMs), because each leaves ne0 partial sums; without, small ones that balance.
+unsigned rows_per_block(const ar_layout *L, int n_sums) {
+    const Shape s = grad_shape(L->ne0);
+    const size_t turn = static_cast<size_t>(s.by) * tps::kDropRows;  // rows that a block has in flight
+    size_t rows = 4 * turn;
+    if (n_sums) {
+        const size_t blocks = 304 / s.gx + 1;
+        rows = (L->ne1 + blocks - 1) / blocks;
+    }
+    // the grid's second dimension has 65535 blocks
+    const size_t least = L->ne1 / 65535 + 1;
+    if (rows < least) rows = least;
+    return static_cast<unsigned>((rows + turn - 1) / turn * turn);
+}
+
+unsigned row_blocks(const ar_layout *L, int n_sums) {
+    const size_t r = rows_per_block(L, n_sums);
+    return static_cast<unsigned>((L->ne1 + r - 1) / r);
 }
 
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
@@ -57,24 +98,35 @@ tps::DropParams drop_params(const ar_dropout &d) {
 using DropFn = void (*)(tps::ArDropParams);
 using GradFn = void (*)(tps::ArDropGradParams);
 
-template <int Td>
+template <int Td, bool ALIGNED>
 DropFn pick_wire(int wire) {
-    return wire == AR_F32   ? tps::ar_dropout_kernel<Td, tps::kF32>
-           : wire == AR_F16 ? tps::ar_dropout_kernel<Td, tps::kF16>
-                            : tps::ar_dropout_kernel<Td, tps::kBF16>;
+    return wire == AR_F32   ? tps::ar_dropout_kernel<Td, tps::kF32, ALIGNED>
+           : wire == AR_F16 ? tps::ar_dropout_kernel<Td, tps::kF16, ALIGNED>
+                            : tps::ar_dropout_kernel<Td, tps::kBF16, ALIGNED>;
 }
 
-DropFn pick(int dst, int wire) {
-    return dst == AR_F32   ? pick_wire<tps::kF32>(wire)
-           : dst == AR_F16 ? pick_wire<tps::kF16>(wire)
-                           : pick_wire<tps::kBF16>(wire);
+template <bool ALIGNED>
+DropFn pick_types(int dst, int wire) {
+    return dst == AR_F32   ? pick_wire<tps::kF32, ALIGNED>(wire)
+           : dst == AR_F16 ? pick_wire<tps::kF16, ALIGNED>(wire)
+                           : pick_wire<tps::kBF16, ALIGNED>(wire);
 }
 
+template <bool ALIGNED, bool SUMS>
 GradFn pick_grad(int dst) {
-    return dst == AR_F32   ? tps::ar_dropout_grad_kernel<tps::kF32>
-           : dst == AR_F16 ? tps::ar_dropout_grad_kernel<tps::kF16>
-                           : tps::ar_dropout_grad_kernel<tps::kBF16>;
+    return dst == AR_F32   ? tps::ar_dropout_grad_kernel<tps::kF32, ALIGNED, SUMS>
+           : dst == AR_F16 ? tps::ar_dropout_grad_kernel<tps::kF16, ALIGNED, SUMS>
+                           : tps::ar_dropout_grad_kernel<tps::kBF16, ALIGNED, SUMS>;
 }
+
+// Whether every row of every buffer starts on a vector boundary (32 bytes for f32, else 16).
+struct Alignment {
+    uintptr_t bits = 0;
+    void add(const void *p, long long stride, size_t rows) {
+        bits |= reinterpret_cast<uintptr_t>(p) | (rows > 1 ? static_cast<uintptr_t>(stride) : 0);
+    }
+    bool holds(size_t es) const { return bits % (es == 4 ? 32 : 16) == 0; }
+};
 
 int launched(cudaError_t e) {
     if (e == cudaSuccess) return AR_OK;
@@ -134,15 +186,26 @@ int ar_reduce_dropout(const void *const *srcs, void *const *dsts, int n_dsts, co
     x.res_stride = L->residual_row_bytes;
     p.drop = drop_params(*drop);
     p.bias = drop->bias;
-    const size_t gx = (L->ne0 + 255) / 256;
-    const dim3 grid(static_cast<unsigned>(gx < 4096 ? gx : 4096), static_cast<unsigned>(L->ne1 < 65535 ? L->ne1 : 65535));
-    return launched(tps::launch_dependent(pick(dst_dtype, wire_dtype), grid, 256u, 0, stream, c.pdl, p));
+    Alignment al;
+    for (int r = 0; r < c.R; ++r)
+        if (x.src[r]) al.add(x.src[r], x.src_stride[r], x.ne1);
+    for (int d = 0; d < n_dsts; ++d) al.add(x.dst[d], x.dst_stride[d], x.ne1);
+    al.add(x.residual, x.res_stride, x.ne1);
+    al.add(p.bias, 0, 1);
+    const Shape s = forward_shape(L->ne0);
+    p.bx = s.bx;
+    p.by = s.by;
+    const size_t turn = static_cast<size_t>(s.by) * tps::kDropRows, gy = (L->ne1 + turn - 1) / turn;
+    const dim3 grid(s.gx, static_cast<unsigned>(gy < 65535 ? gy : 65535));
+    const DropFn fn = al.holds(dtype_bytes(dst_dtype)) ? pick_types<true>(dst_dtype, wire_dtype)
+                                                       : pick_types<false>(dst_dtype, wire_dtype);
+    return launched(tps::launch_dependent(fn, grid, s.threads, 0, stream, c.pdl, p));
 }
 
 int ar_reduce_dropout_grad_workspace(const ar_layout *L, int n_sums, size_t *bytes) {
     if (!L || !bytes || n_sums < 0 || n_sums > 2) return AR_ERR_INVALID_ARG;
     if (L->ne1 > 0xFFFFFFFFull || L->ne0 > (1ull << 34)) return AR_ERR_TOO_LARGE;
-    *bytes = static_cast<size_t>(n_sums) * row_blocks(L->ne1) * L->ne0 * sizeof(float);
+    *bytes = L->ne0 ? static_cast<size_t>(n_sums) * row_blocks(L, n_sums) * L->ne0 * sizeof(float) : 0;
     return AR_OK;
 }
 
@@ -189,7 +252,7 @@ int ar_reduce_dropout_grad(const void *dy, void *const *dxs, int n_dxs, const ar
     if (st != AR_OK) return st;
 
     const int64_t packed = static_cast<int64_t>(L->ne0 * es);
-    const unsigned blocks = row_blocks(L->ne1);
+    const unsigned blocks = row_blocks(L, n_sums);
     float *part[2] = {nullptr, nullptr};
     int at = 0;
     for (int k = 0; k < 2; ++k)
@@ -206,13 +269,20 @@ int ar_reduce_dropout_grad(const void *dy, void *const *dxs, int n_dxs, const ar
         p.ne0 = L->ne0;
         p.ne1 = L->ne1;
         p.n_dxs = n_dxs;
-        p.rows_per_block = rows_per_block(L->ne1);
+        p.rows_per_block = rows_per_block(L, n_sums);
         p.drop = drop_params(*drop);
         p.part_bias = part[0];
         p.part_res = part[1];
-        const size_t gx = (L->ne0 + 255) / 256;
-        st = launched(tps::launch_dependent(pick_grad(dst_dtype), dim3(static_cast<unsigned>(gx < 4096 ? gx : 4096), blocks),
-                                            256u, 0, stream, c.pdl, p));
+        Alignment al;
+        al.add(dy, p.dy_stride, L->ne1);
+        for (int d = 0; d < n_dxs; ++d) al.add(p.dx[d], p.dx_stride[d], L->ne1);
+        const Shape s = grad_shape(L->ne0);
+        p.bx = s.bx;
+        p.by = s.by;
+        const bool aligned = al.holds(es);
+        const GradFn fn = n_sums ? (aligned ? pick_grad<true, true>(dst_dtype) : pick_grad<false, true>(dst_dtype))
+                                 : (aligned ? pick_grad<true, false>(dst_dtype) : pick_grad<false, false>(dst_dtype));
+        st = launched(tps::launch_dependent(fn, dim3(s.gx, blocks), s.threads, 0, stream, c.pdl, p));
         if (st != AR_OK) return st;
     }
     if (n_sums == 0) return AR_OK;
@@ -224,7 +294,7 @@ int ar_reduce_dropout_grad(const void *dy, void *const *dxs, int n_dxs, const ar
     s.ne0 = L->ne0;
     s.blocks = blocks;
     return launched(tps::launch_dependent(tps::ar_column_sum_kernel,
-                                          dim3(static_cast<unsigned>((L->ne0 + 255) / 256), n_sums), 256u, 0, stream,
+                                          dim3(static_cast<unsigned>((L->ne0 + 31) / 32), n_sums), 256u, 0, stream,
                                           c.pdl, s));
 }
 
