@@ -198,13 +198,13 @@ __device__ __forceinline__ bool vocab_tile(const VocabGemmParams &p, int live, i
 
 // Store a warp's 32x32 values, row `lane` in each thread: `n` (1 to 32) elements of T to each thread's
 // `out` (nullptr: no row).  The rows go through shared memory, so that adjacent lanes store adjacent
-// bytes: rows of 64 bytes in pieces of 16 where all of them allow it, element after element otherwise
-// (each lane storing its own row, 2 bytes in 32 places at once, made dW of odd rows 5 times slower).
+// bytes: rows of 64 bytes in pieces of 16, of 4 or of one element, whichever all of them allow (each lane storing its own row, 2 bytes in 32 places at once, made dW of odd rows 5 times slower).
 template <int T>
 __device__ __forceinline__ void store_block(unsigned char *stage, char *out, const float (&v)[32], int n, int lane) {
     constexpr int es = Elem<T>::bytes, per = 64 / es;  // elements of a pass
     const unsigned long long mine = reinterpret_cast<unsigned long long>(out);
     const bool vec = __all_sync(~0u, mine % 16 == 0) && n == 32;
+    const bool words = es == 4 || (__all_sync(~0u, mine % 4 == 0) && n % 2 == 0);
 #pragma unroll
     for (int c = 0; c < 32; c += per) {
         if (c >= n) break;
@@ -227,20 +227,21 @@ __device__ __forceinline__ void store_block(unsigned char *stage, char *out, con
                 char *to = reinterpret_cast<char *>(__shfl_sync(~0u, mine, r));
                 if (to) *reinterpret_cast<uint4 *>(to + c * es + at) = *reinterpret_cast<uint4 *>(stage + r * kVPitch + at);
             }
-        } else {
-            const int k = lane % per;
+        } else if (words) {
+            const int k = lane % 16;
 #pragma unroll 4
-            for (int r0 = 0; r0 < 32; r0 += 32 / per) {
-                const int r = r0 + lane / per;
+            for (int r0 = 0; r0 < 32; r0 += 2) {
+                const int r = r0 + lane / 16;
                 char *to = reinterpret_cast<char *>(__shfl_sync(~0u, mine, r));
-                if (to && c + k < n) {
-                    if constexpr (T == kF32) {
-                        reinterpret_cast<uint32_t *>(to)[c + k] = *reinterpret_cast<uint32_t *>(stage + r * kVPitch + 4 * k);
-                    } else {
-                        reinterpret_cast<unsigned short *>(to)[c + k] =
-                            *reinterpret_cast<unsigned short *>(stage + r * kVPitch + 2 * k);
-                    }
-                }
+                if (to && c * es + 4 * k < n * es)
+                    *reinterpret_cast<uint32_t *>(to + c * es + 4 * k) = *reinterpret_cast<uint32_t *>(stage + r * kVPitch + 4 * k);
+            }
+        } else if constexpr (T != kF32) {
+#pragma unroll 4
+            for (int r = 0; r < 32; ++r) {
+                char *to = reinterpret_cast<char *>(__shfl_sync(~0u, mine, r));
+                if (to && lane < n)
+                    reinterpret_cast<unsigned short *>(to)[lane] = *reinterpret_cast<unsigned short *>(stage + r * kVPitch + 2 * lane);
             }
         }
     }

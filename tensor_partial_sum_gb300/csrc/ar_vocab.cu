@@ -94,8 +94,9 @@ bool weights_in_place(const ar_vocab *v) {
     return true;
 }
 
-// Elements between packed rows (of hidden states or weights): 16-byte multiples.
-size_t packed_ld(const ar_vocab *v) { return round_up(v->dim, 8); }
+// Elements between packed rows (of hidden states or weights): whole blocks of K, zeros behind the row's
+// end, so that no copy of them reaches outside the tensor.
+size_t packed_ld(const ar_vocab *v) { return round_up(v->dim, tps::kVK); }
 
 // One launch's vocabulary: whole pieces, or rows [row0, row0 + rows) of one that is larger than a chunk.
 struct Group {
@@ -340,10 +341,10 @@ struct Call {
     }
 
     // The weights of a group: packed at `area` (room for `cap` rows) where they have to be; per segment
-    // the base, rows, row stride in elements and part stride of what the copies read.
+    // the base, columns, rows, row stride in elements and part stride of what the copies read.
     struct Matrix {
         const char *base;
-        size_t rows, ld, part;
+        size_t cols, rows, ld, part;
     };
     int group_weights(const Group &g, size_t area, size_t cap, Matrix *out) const {
         size_t at = 0;
@@ -351,12 +352,12 @@ struct Call {
             const size_t stride = weight_stride(v, g.piece[s]);
             const char *src = static_cast<const char *>(v->weights[g.piece[s]]) + g.row0[s] * stride;
             if (!pack) {
-                out[s] = Matrix{src, g.rows[s], stride / 2, 0};
+                out[s] = Matrix{src, v->dim, g.rows[s], stride / 2, 0};
                 continue;
             }
             char *dst = ws + area + at * ld * 2;
             at += g.rows[s];
-            out[s] = Matrix{dst, g.rows[s], ld, cap * ld};
+            out[s] = Matrix{dst, ld, g.rows[s], ld, cap * ld};
             const int st = launch_pack(pack_params(src, stride, g.rows[s], dst, cap));
             if (st != AR_OK) return st;
         }
@@ -444,9 +445,9 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
               !weights_in_place(v)};
     const size_t T = v->rows, D = v->dim;
     // the hidden states as the tiled copies read them
-    Call::Matrix h{static_cast<const char *>(v->hidden), T, row_bytes(v->hidden_row_bytes, v) / 2, 0};
+    Call::Matrix h{static_cast<const char *>(v->hidden), D, T, row_bytes(v->hidden_row_bytes, v) / 2, 0};
     if (!hidden_in_place(v)) {
-        h = Call::Matrix{call.ws + plan.hidden, T, call.ld, T * call.ld};
+        h = Call::Matrix{call.ws + plan.hidden, call.ld, T, call.ld, T * call.ld};
         st = call.launch_pack(call.pack_params(v->hidden, row_bytes(v->hidden_row_bytes, v), T, call.ws + plan.hidden, T));
         if (st != AR_OK) return st;
     }
@@ -459,7 +460,7 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
     p.part = reinterpret_cast<float2 *>(call.ws + plan.part);
     p.picked = reinterpret_cast<float *>(call.ws + plan.picked);
     p.status = c.dev_status;
-    if (!make_a_maps(p, call.f16, h.base, D, h.rows, call.parts, h.ld, h.part)) return AR_ERR_CUDA;
+    if (!make_a_maps(p, call.f16, h.base, h.cols, h.rows, call.parts, h.ld, h.part)) return AR_ERR_CUDA;
     long long first[AR_MAX_RANKS], total = 0;
     for (int r = 0; r < v->n_pieces; ++r) first[r] = total, total += static_cast<long long>(v->piece_rows[r]);
     int piece = 0, done = 0;  // column tiles of earlier groups
@@ -476,9 +477,9 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
             p.seg[s].rows = static_cast<int>(g.rows[s]);
             p.seg[s].tile0 = p.tiles;
             p.tiles += static_cast<int>(tiles_of(g.rows[s], static_cast<size_t>(p.bn)));
-            if (!make_map(&p.b_map[s], call.f16, w[s].base, D, w[s].rows, call.parts, w[s].ld, w[s].part,
+            if (!make_map(&p.b_map[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part,
                           static_cast<unsigned>(p.bn / 2)) ||
-                !make_map(&p.b_tail[s], call.f16, w[s].base, D, w[s].rows, call.parts, w[s].ld, w[s].part,
+                !make_map(&p.b_tail[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part,
                           tail_box<tps::kStats>(g.rows[s], p.bn)))
                 return AR_ERR_CUDA;
         }
@@ -592,7 +593,7 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
     p.d = reinterpret_cast<unsigned short *>(call.ws + plan.d);
     p.status = c.dev_status;
     const size_t mt = plan.d_rows / tps::kVM;
-    if (!make_map(&p.ht_map, call.f16, call.ws + plan.hidden, D, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld, 64))
+    if (!make_map(&p.ht_map, call.f16, call.ws + plan.hidden, call.ld, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld, 64))
         return AR_ERR_CUDA;
     long long first[AR_MAX_RANKS], total = 0;
     for (int r = 0; r < v->n_pieces; ++r) first[r] = total, total += static_cast<long long>(v->piece_rows[r]);
@@ -609,7 +610,7 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
         p.nseg = g.nseg;
         p.bn = tps::kVN;
         p.tiles = 0;
-        if (!make_a_maps(p, call.f16, call.ws + plan.hidden, D, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld))
+        if (!make_a_maps(p, call.f16, call.ws + plan.hidden, call.ld, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld))
             return AR_ERR_CUDA;
         for (int s = 0; s < g.nseg; ++s) {
             p.seg[s].first = first[g.piece[s]] + static_cast<long long>(g.row0[s]);
@@ -617,8 +618,8 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
             p.seg[s].tile0 = p.tiles;
             p.seg[s].col0 = static_cast<long long>(p.tiles) * tps::kVN;
             p.tiles += static_cast<int>(tiles_of(g.rows[s], tps::kVN));
-            if (!make_map(&p.b_map[s], call.f16, w[s].base, D, w[s].rows, call.parts, w[s].ld, w[s].part, tps::kVN / 2) ||
-                !make_map(&p.b_tail[s], call.f16, w[s].base, D, w[s].rows, call.parts, w[s].ld, w[s].part,
+            if (!make_map(&p.b_map[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part, tps::kVN / 2) ||
+                !make_map(&p.b_tail[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part,
                           tail_box<tps::kDlogits>(g.rows[s], p.bn)))
                 return AR_ERR_CUDA;
         }
@@ -647,7 +648,7 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
             p.seg[s].dw_row = static_cast<long long>(row_bytes(dw_rows ? dw_rows[r] : 0, v));
             p.seg[s].dw = dweights ? static_cast<char *>(dweights[r]) + g.row0[s] * static_cast<size_t>(p.seg[s].dw_row) : nullptr;
             p.tiles += static_cast<int>(tiles_of(g.rows[s], tps::kVM));
-            if (!make_map(&p.b_map[s], call.f16, w[s].base, D, w[s].rows, parts, w[s].ld, w[s].part, 64)) return AR_ERR_CUDA;
+            if (!make_map(&p.b_map[s], call.f16, w[s].base, w[s].cols, w[s].rows, parts, w[s].ld, w[s].part, 64)) return AR_ERR_CUDA;
         }
         p.tiles = dweights ? p.tiles * static_cast<int>(tiles_of(D, static_cast<size_t>(p.bn))) : 0;
         st = call.launch_gemm<tps::kGrads>(
