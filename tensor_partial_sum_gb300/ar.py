@@ -155,6 +155,7 @@ def _ptrs(xs):
 
 
 ESIZE = {AR_F32: 4, AR_F16: 2, AR_BF16: 2}
+STORAGE_NAMES = {AR_F32: "float32", AR_F16: "float16", AR_BF16: "bfloat16"}
 
 
 def _checked(xs, nelem, dcode, where, call):
@@ -200,19 +201,54 @@ def _reach(x) -> int | None:
     return st.data_ptr() + st.nbytes() - x.data_ptr()
 
 
+def _holds(x, n) -> bool:
+    """Whether a device tensor's own elements, as it lies in memory, already
+    reach n bytes past its start (a cheap answer for most tensors; _reach
+    looks at the storage)."""
+    if not getattr(x, "is_cuda", False):
+        return False
+    es = x.element_size()
+    if x.dim() == 2:
+        rows, cols = x.shape
+        down, right = x.stride()
+        return rows > 0 and cols > 0 and ((rows - 1) * down + (cols - 1) * right + 1) * es >= n
+    return x.is_contiguous() and x.numel() * es >= n
+
+
+_TORCH_CODES = None
+
+
 def _dtype_code(d) -> int:
     if isinstance(d, int):
         return d
     if isinstance(d, str):
         return DTYPE_CODES[d]
-    import torch
-    return {torch.float32: AR_F32, torch.float16: AR_F16, torch.bfloat16: AR_BF16}[d]
+    global _TORCH_CODES
+    if _TORCH_CODES is None:
+        import torch
+        _TORCH_CODES = {torch.float32: AR_F32, torch.float16: AR_F16, torch.bfloat16: AR_BF16}
+    return _TORCH_CODES[d]
+
+
+_raw_stream = None
+
+
+def _current_stream() -> int | None:
+    """Handle of torch's current stream.  torch.cuda.current_stream() builds a
+    Stream object each time, several microseconds of a small call."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if get is None or dev is None or not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream or None
+        _raw_stream = lambda: get(dev())  # noqa: E731
+    return _raw_stream() or None
 
 
 def _stream(s) -> int | None:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        return _current_stream()
     if isinstance(s, int):
         return s or None
     return s.cuda_stream or None
@@ -364,20 +400,25 @@ def _check_reach(srcs, dsts, layout, dst_dtype, call):
     if ne0 * ne1 == 0:
         return
 
-    def need(stride):
-        return (ne1 - 1) * stride + ne0 * es
+    row, more = ne0 * es, ne1 - 1
     for kind, xs, rows in (("source", srcs, layout.src_row_bytes), ("destination", dsts, layout.dst_row_bytes)):
+        given = bool(rows)
         for k, x in enumerate(xs):
+            if x is None or type(x) is int:
+                continue
+            n = more * (rows[k] if given else row) + row
+            if _holds(x, n):
+                continue
             reach = _reach(x)
-            n = need(rows[k] if rows else ne0 * es)
             if reach is not None and reach < n:
                 raise ValueError(f"{call}: {kind} {k} reaches {reach} bytes, its rows span {n}")
     res = getattr(layout, "_residual_obj", None)
-    reach = _reach(res)
-    if reach is not None:
-        n = ne0 * es if layout.residual_row_bytes == 0 else need(layout.residual_row_bytes)
-        if reach < n:
-            raise ValueError(f"{call}: the residual reaches {reach} bytes, its rows span {n}")
+    if res is None:
+        return
+    n = row if layout.residual_row_bytes == 0 else more * layout.residual_row_bytes + row
+    reach = None if _holds(res, n) else _reach(res)
+    if reach is not None and reach < n:
+        raise ValueError(f"{call}: the residual reaches {reach} bytes, its rows span {n}")
 
 
 def ar_reduce_ex(srcs, dsts, layout: ArLayout, dst_dtype, wire_dtype="bf16", stream=None) -> None:
@@ -429,12 +470,10 @@ def _typed_row(x, n, dtype, name, call):
     """A device row (tensor or address) of at least n elements of a torch dtype."""
     if x is None or isinstance(x, int):
         return
-    import torch
-    want = {AR_F32: torch.float32, AR_F16: torch.float16, AR_BF16: torch.bfloat16}[dtype]
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise TypeError(f"{call}: {name} is a {x.device.type} tensor, a device buffer is needed")
-    if x.dtype != want or not x.is_contiguous() or x.numel() < n:
-        raise ValueError(f"{call}: {name} needs {n} contiguous elements of {want}")
+    if _dtype_code(x.dtype) != dtype or not x.is_contiguous() or x.numel() < n:
+        raise ValueError(f"{call}: {name} needs {n} contiguous elements of {STORAGE_NAMES[dtype]}")
 
 
 def _workspace(need, given, stream, call):
@@ -445,7 +484,7 @@ def _workspace(need, given, stream, call):
     if given is not None:
         if isinstance(given, int):
             return given, need
-        if given.device.type != "cuda" or not given.is_contiguous():
+        if not given.is_cuda or not given.is_contiguous():
             raise TypeError(f"{call}: the workspace has to be a contiguous device tensor")
         return given, given.numel() * given.element_size()
     import torch
@@ -513,17 +552,17 @@ def ar_reduce_dropout_grad(dy, dxs, layout: ArLayout, dropout: ArDropout, dst_dt
 
 def _matrix(x, rows, dim, dtype, name, call):
     """Row stride in bytes of a device matrix [rows, dim] with adjacent columns."""
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise TypeError(f"{call}: {name} is a {x.device.type} tensor, a device buffer is needed")
     if x.dtype != dtype:
         raise TypeError(f"{call}: {name} is {x.dtype}, the hidden states are {dtype}")
-    if x.dim() != 2 or x.shape[0] != rows or x.shape[1] != dim or (dim > 1 and x.stride(1) != 1):
+    if x.dim() != 2 or tuple(x.shape) != (rows, dim) or (dim > 1 and x.stride(1) != 1):
         raise ValueError(f"{call}: {name} has to be [{rows}, {dim}] with adjacent columns")
-    return x.stride(0) * x.element_size() if rows > 1 else dim * x.element_size()
+    return (x.stride(0) if rows > 1 else dim) * x.element_size()
 
 
 def _vector(x, n, dtype, name, call):
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise TypeError(f"{call}: {name} is a {x.device.type} tensor, a device buffer is needed")
     if x.dtype != dtype or x.dim() != 1 or x.numel() != n or not x.is_contiguous():
         raise ValueError(f"{call}: {name} has to be {n} contiguous elements of {dtype}")

@@ -198,7 +198,8 @@ __device__ __forceinline__ bool vocab_tile(const VocabGemmParams &p, int live, i
 
 // Store a warp's 32x32 values, row `lane` in each thread: `n` (1 to 32) elements of T to each thread's
 // `out` (nullptr: no row).  The rows go through shared memory, so that adjacent lanes store adjacent
-// bytes: rows of 64 bytes in pieces of 16, of 4 or of one element, whichever all of them allow (each lane storing its own row, 2 bytes in 32 places at once, made dW of odd rows 5 times slower).
+// bytes: rows of 64 bytes in pieces of 16, of 4 or of one element, whichever all of them allow (each
+// lane storing its own row, 2 bytes in 32 places at once, made the dW of odd rows 2.5 times slower).
 template <int T>
 __device__ __forceinline__ void store_block(unsigned char *stage, char *out, const float (&v)[32], int n, int lane) {
     constexpr int es = Elem<T>::bytes, per = 64 / es;  // elements of a pass
