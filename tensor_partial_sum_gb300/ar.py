@@ -476,9 +476,10 @@ def _typed_row(x, n, dtype, name, call):
         raise ValueError(f"{call}: {name} needs {n} contiguous elements of {STORAGE_NAMES[dtype]}")
 
 
-def _workspace(need, given, stream, call):
+def _workspace(need, given, stream, like, call):
     """(tensor or address, bytes) of a call's workspace: the caller's, or one
-    from torch's allocator on the stream that will use it."""
+    from torch's allocator, on the device of ``like`` and the stream that will
+    use it."""
     if need == 0:
         return None, 0
     if given is not None:
@@ -488,11 +489,12 @@ def _workspace(need, given, stream, call):
             raise TypeError(f"{call}: the workspace has to be a contiguous device tensor")
         return given, given.numel() * given.element_size()
     import torch
+    device = like.device if hasattr(like, "device") else "cuda"
     if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device="cuda"), need
+        return torch.empty(need, dtype=torch.uint8, device=device), need
     s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
     with torch.cuda.stream(s):
-        return torch.empty(need, dtype=torch.uint8, device="cuda"), need
+        return torch.empty(need, dtype=torch.uint8, device=device), need
 
 
 def make_dropout(p, seed, offset=0, bias=None) -> ArDropout:
@@ -544,7 +546,7 @@ def ar_reduce_dropout_grad(dy, dxs, layout: ArLayout, dropout: ArDropout, dst_dt
     _typed_row(dresidual, layout.ne0, AR_F32, "dresidual", call)
     n_sums = (dbias is not None) + (dresidual is not None)
     need = ar_reduce_dropout_grad_workspace(layout, n_sums) if n_sums else 0
-    ws, ws_bytes = _workspace(need, workspace, stream, call)
+    ws, ws_bytes = _workspace(need, workspace, stream, dy, call)
     _check(lib().ar_reduce_dropout_grad(_ptr(dy), _ptrs(dxs), len(dxs), ctypes.byref(layout), ctypes.byref(dropout),
                                         _ptr(dbias), _ptr(dresidual), _ptr(ws), ws_bytes, _dtype_code(dst_dtype),
                                         _stream(stream)), call)
@@ -616,7 +618,7 @@ def ar_vocab_loss(hidden, weights, targets, loss, lse, ignore_index=-100, worksp
     v = make_vocab(hidden, weights, targets, ignore_index, call)
     _vector(loss, v.rows, torch.float32, "loss", call)
     _vector(lse, v.rows, torch.float32, "lse", call)
-    ws, ws_bytes = _workspace(ar_vocab_workspace(v, False), workspace, stream, call)
+    ws, ws_bytes = _workspace(ar_vocab_workspace(v, False), workspace, stream, hidden, call)
     _check(lib().ar_vocab_loss(ctypes.byref(v), loss.data_ptr(), lse.data_ptr(), _ptr(ws), ws_bytes, _stream(stream)),
            call)
 
@@ -639,6 +641,6 @@ def ar_vocab_loss_grad(hidden, weights, targets, lse, dloss, dhidden=None, dweig
             raise ValueError(f"{call}: {len(xs)} tensors in {name}, {n} vocabulary pieces")
         strides.append(None if xs is None else (ctypes.c_int64 * n)(
             *[_matrix(x, m, v.dim, hidden.dtype, f"{name}[{r}]", call) for r, (x, m) in enumerate(zip(xs, rows))]))
-    ws, ws_bytes = _workspace(ar_vocab_workspace(v, True), workspace, stream, call)
+    ws, ws_bytes = _workspace(ar_vocab_workspace(v, True), workspace, stream, hidden, call)
     _check(lib().ar_vocab_loss_grad(ctypes.byref(v), lse.data_ptr(), dloss.data_ptr(), _ptrs(dhidden), strides[0],
                                     _ptrs(dweights), strides[1], _ptr(ws), ws_bytes, _stream(stream)), call)

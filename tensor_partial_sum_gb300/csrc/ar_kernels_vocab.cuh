@@ -35,6 +35,18 @@ constexpr int kVRow = kVK * 2;              // bytes of a row of a stage
 constexpr int kVRing = 6 * 256 * kVRow;     // bytes of the stages: six of full height
 constexpr int kVEpilogueWarps = 8;
 constexpr int kVThreads = 128 + 32 * kVEpilogueWarps;
+// The tensor cores' float sums drop what falls below the running sum's last place (they do not round), so
+// a long reduction drifts: one token of 4096 elements came out 3.6e-5 off.  Where results are float32
+// (the statistics, and everything of float32 inputs) a run of products is kept short - 32 or 48 of them -
+// and the runs are added in registers, rounded to nearest.
+template <int MODE, int T>
+constexpr bool kVRuns = MODE == kStats || T == kF32;
+template <int T>
+constexpr int kVRunBlocks = T == kF32 ? 2 : 8;  // blocks of K in a run
+// Registers of the feeding and of the result warps when a thread adds up 128 columns; the launch's
+// kVLaunchRegs for each of 384 threads cover them.
+constexpr int kVFeedRegs = 80, kVSumRegs = 208, kVLaunchRegs = 168;
+static_assert(128 * kVFeedRegs + 32 * kVEpilogueWarps * kVSumRegs <= kVThreads * kVLaunchRegs, "register split");
 constexpr unsigned kVTmemCols = 512;        // two accumulators of 256 columns
 constexpr int kVPitch = 80;                 // bytes between a warp's staged output rows of 64 bytes
 constexpr int kVOut = kVEpilogueWarps * 32 * kVPitch;
@@ -100,17 +112,19 @@ struct VocabGemmParams {
     unsigned *status;
 };
 
-// Part numbers of A and B in product q of a block of K, largest last so that the small ones are
-// summed while the accumulator is small (float32; the 16-bit types have one part and one product).
+// Parts of an operand, and products of parts in a block of K.
 template <int T>
-__device__ __forceinline__ void pair_parts(int q, int &a, int &b) {
-    // (1,1) (0,2) (2,0) (0,1) (1,0) (0,0)
-    a = T == kF32 ? (0x010201 >> (4 * q)) & 0xF : 0;
-    b = T == kF32 ? (0x001021 >> (4 * q)) & 0xF : 0;
-}
-// Products per block of K.
+constexpr int kVParts = T == kF32 ? 3 : 1;
 template <int T>
 constexpr int kVPairs = T == kF32 ? 6 : 1;
+// Part numbers of A and B in product q, the largest product last, so that the small ones are summed
+// while the run is small.
+__device__ __forceinline__ constexpr int a_part_of(int pairs, int q) {  // 1 0 2 0 1 0
+    return pairs == 1 ? 0 : (0x010201 >> (4 * q)) & 0xF;
+}
+__device__ __forceinline__ constexpr int b_part_of(int pairs, int q) {  // 1 2 0 1 0 0
+    return pairs == 1 ? 0 : (0x001021 >> (4 * q)) & 0xF;
+}
 
 // A tile: its place, its operands' places and its blocks of K.
 struct VocabTile {
@@ -248,6 +262,12 @@ __device__ __forceinline__ void store_block(unsigned char *stage, char *out, con
     }
 }
 
+// Runs of products of a tile; one without blocks of K still counts as one.
+template <int MODE, int T>
+__device__ __forceinline__ int vocab_runs(const VocabTile &t) {
+    return kVRuns<MODE, T> ? max(1, (t.kn + kVRunBlocks<T> - 1) / kVRunBlocks<T>) : 1;
+}
+
 // The three bf16 parts of two floats, eight bits each, packed in pairs.
 __device__ __forceinline__ void split2(float a, float b, uint32_t (&w)[3]) {
 #pragma unroll
@@ -304,8 +324,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
     asm volatile("fence.proxy.async.global;" ::: "memory");  // its plain stores, before this one's copies
     const int live = p.list ? p.list->live : p.rows;
     const unsigned S = static_cast<unsigned>(p.stages);
-    const unsigned b_at = static_cast<unsigned>(p.a_room) * kVRow;  // B's rows behind A's in a stage
-    const unsigned stage = b_at + static_cast<unsigned>(p.bn / 2) * kVRow;
+    // a stage: the parts of A, then the parts of B
+    const unsigned a_size = static_cast<unsigned>(p.a_room) * kVRow, b_size = static_cast<unsigned>(p.bn / 2) * kVRow;
+    const unsigned b_at = kVParts<T> * a_size, stage = b_at + kVParts<T> * b_size;
 
     const volatile unsigned never = 0;  // for waits that follow giving up
     auto give_up = [&] {
@@ -313,142 +334,157 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
         *abort_flag = 1u;
     };
 
-    if (warp == 0) {
-        // ---- copies: this CTA's half of each operand ----
-        const unsigned lead_full = leader_addr(full);
-        unsigned s = 0, round = 0;  // the stage to fill and how often the ring went round
-        bool ok = true;
-        VocabTile t;
-        for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i) {
-            const CUtensorMap *am, *bm;
-            int ay, ax, by, bx;  // first element of this CTA's rows (columns) at block 0 of K
-            const int row0 = t.m * kVM, arow = row0 + static_cast<int>(rank) * 128;
-            const int brow = t.n * p.bn + static_cast<int>(rank) * (t.bn / 2);
-            const bool a_mn = MODE == kGrads && t.dw, b_mn = MODE == kGrads;
-            if constexpr (MODE != kGrads) {
-                am = &p.a_map, bm = &p.b_map[t.seg];
-                ax = 0, ay = arow, bx = 0, by = brow;
-            } else if (t.dw) {
-                am = &p.at_map, bm = &p.ht_map;
-                ax = static_cast<int>(p.seg[t.seg].col0) + arow, ay = 0, bx = brow, by = 0;
-            } else {
-                am = &p.a_map, bm = &p.b_map[t.seg];
-                ax = static_cast<int>(p.seg[t.seg].col0), ay = arow, bx = brow, by = 0;
-            }
-            // what the first and the second CTA of the pair copy of each operand, in rows of a stage
-            auto a_part = [&](int row) { return row + 128 <= p.a_rows ? 128 : row < p.a_rows ? p.a_tail : 0; };
-            auto b_part = [&](int col) {  // MN-major: chunks of 64 columns, none of them all outside
-                return t.bn == kVN && col + 64 < p.dim ? 128 : col < p.dim ? 64 : 0;
-            };
-            const int a_mine = a_mn ? 128 : a_part(arow), b_mine = b_mn ? b_part(brow) : t.bn / 2;
-            const int a_both = a_mn ? 256 : a_part(row0) + a_part(row0 + 128);
-            const int b_both = b_mn ? b_part(t.n * p.bn) + b_part(t.n * p.bn + t.bn / 2) : t.bn;
-            if (!a_mn && a_mine < 128) am = &p.a_tail_map;
-            if (!b_mn && t.bn < p.bn) bm = &p.b_tail[t.seg];
-            const unsigned bytes = static_cast<unsigned>(a_both + b_both) * kVRow;
-            int k = t.k0 * kVK, q = 0;
-            for (int n = t.kn * kVPairs<T>; n > 0; --n) {
-                int pa, pb;
-                pair_parts<T>(q, pa, pb);
-                if (round && !__all_sync(~0u, mbar_wait_bounded(empty + 8 * s, (round - 1) & 1, abort_flag))) {
-                    give_up();
-                    ok = false;
-                    break;
-                }
-                if (elect_one()) {
-                    const unsigned bar = lead_full + 8 * s;
-                    if (rank == 0)
-                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + 8 * s), "r"(bytes)
-                                     : "memory");
-                    const unsigned a = base + s * stage, b = a + b_at;
-                    if (!a_mn) {
-                        if (a_mine) tma_load_3d(a, am, bar, ax + k, ay, pa);
-                    } else {  // two chunks of 64 columns, 64 rows each
-                        tma_load_3d(a, am, bar, ax, ay + k, pa);
-                        tma_load_3d(a + 8192, am, bar, ax + 64, ay + k, pa);
-                    }
-                    if (!b_mn) {
-                        tma_load_3d(b, bm, bar, bx + k, by, pb);
-                    } else {
-                        if (b_mine) tma_load_3d(b, bm, bar, bx, by + k, pb);
-                        if (b_mine > 64) tma_load_3d(b + 8192, bm, bar, bx + 64, by + k, pb);
-                    }
-                }
-                if (++s == S) s = 0, ++round;
-                if (++q == kVPairs<T>) q = 0, k += kVK;
-            }
-        }
-        // the products' last arrivals have to find this CTA still here; after a wait that ran out, the
-        // copies in flight (of both CTAs) have to land before the pair leaves
-        for (unsigned q = 0; q < S; ++q) {
-            const unsigned fills = round + (q < s);  // of stage q
-            if (fills == 0) continue;
-            if (ok && !__all_sync(~0u, mbar_wait_bounded(empty + 8 * q, (fills - 1) & 1, abort_flag))) {
-                give_up();
-                ok = false;
-            }
-            if (!ok && rank == 0) mbar_wait_bounded(full + 8 * q, (fills - 1) & 1, &never);
-        }
-    } else if (warp == 1) {
-        if (rank == 0) {
-            // ---- products ----
-            const uint64_t desc0 = umma_desc(base, 8192);
-            unsigned s = 0, phase = 0, acc_it = 0;
+    if (warp < 4) {
+        // the whole warpgroup gives registers up, in the branch that holds its roles' code
+        if constexpr (kVRuns<MODE, T>) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kVFeedRegs));
+        if (warp == 0) {
+            // ---- copies: this CTA's half of each operand ----
+            const unsigned lead_full = leader_addr(full);
+            unsigned s = 0, round = 0;  // the stage to fill and how often the ring went round
             bool ok = true;
             VocabTile t;
-            for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i, ++acc_it) {
-                const unsigned acc = acc_it % 2, use = acc_it / 2;
-                if (use && !__all_sync(~0u, mbar_wait_bounded(tempty + 8 * acc, (use - 1) & 1, abort_flag))) {
-                    give_up();
-                    ok = false;
-                    break;
-                }
-                tmem_fence_after();
+            for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i) {
+                const CUtensorMap *am, *bm;
+                int ay, ax, by, bx;  // first element of this CTA's rows (columns) at block 0 of K
+                const int row0 = t.m * kVM, arow = row0 + static_cast<int>(rank) * 128;
+                const int brow = t.n * p.bn + static_cast<int>(rank) * (t.bn / 2);
                 const bool a_mn = MODE == kGrads && t.dw, b_mn = MODE == kGrads;
-                const uint32_t idesc = umma_idesc(T != kF16, a_mn, b_mn, static_cast<unsigned>(t.bn));
-                // 16 elements of K: 32 bytes along a K-major row, two groups of eight rows otherwise
-                const unsigned a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
-                const unsigned d = tmem + acc * 256;
-                bool more = false;  // the first product of a tile starts the accumulator
-                for (int n = t.kn * kVPairs<T>; n > 0; --n) {
-                    if (!__all_sync(~0u, mbar_wait_bounded(full + 8 * s, phase, abort_flag))) {
+                if constexpr (MODE != kGrads) {
+                    am = &p.a_map, bm = &p.b_map[t.seg];
+                    ax = 0, ay = arow, bx = 0, by = brow;
+                } else if (t.dw) {
+                    am = &p.at_map, bm = &p.ht_map;
+                    ax = static_cast<int>(p.seg[t.seg].col0) + arow, ay = 0, bx = brow, by = 0;
+                } else {
+                    am = &p.a_map, bm = &p.b_map[t.seg];
+                    ax = static_cast<int>(p.seg[t.seg].col0), ay = arow, bx = brow, by = 0;
+                }
+                // what the first and the second CTA of the pair copy of each operand, in rows of a stage
+                auto a_part = [&](int row) { return row + 128 <= p.a_rows ? 128 : row < p.a_rows ? p.a_tail : 0; };
+                auto b_part = [&](int col) {  // MN-major: chunks of 64 columns, none of them all outside
+                    return t.bn == kVN && col + 64 < p.dim ? 128 : col < p.dim ? 64 : 0;
+                };
+                const int a_mine = a_mn ? 128 : a_part(arow), b_mine = b_mn ? b_part(brow) : t.bn / 2;
+                const int a_both = a_mn ? 256 : a_part(row0) + a_part(row0 + 128);
+                const int b_both = b_mn ? b_part(t.n * p.bn) + b_part(t.n * p.bn + t.bn / 2) : t.bn;
+                if (!a_mn && a_mine < 128) am = &p.a_tail_map;
+                if (!b_mn && t.bn < p.bn) bm = &p.b_tail[t.seg];
+                const unsigned bytes = static_cast<unsigned>(a_both + b_both) * kVRow * kVParts<T>;
+                int k = t.k0 * kVK;
+                for (int n = t.kn; n > 0; --n, k += kVK) {
+                    if (round && !__all_sync(~0u, mbar_wait_bounded(empty + 8 * s, (round - 1) & 1, abort_flag))) {
                         give_up();
                         ok = false;
                         break;
                     }
-                    tmem_fence_after();
-                    const uint64_t a = desc0 + ((s * stage) >> 4), b = a + (b_at >> 4);
                     if (elect_one()) {
-#pragma unroll
-                        for (unsigned k = 0; k < kVK / 16; ++k) umma(d, a + k * a_step, b + k * b_step, idesc, more || k > 0);
-                        umma_commit(empty + 8 * s);
+                        const unsigned bar = lead_full + 8 * s;
+                        if (rank == 0)
+                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + 8 * s), "r"(bytes)
+                                         : "memory");
+    #pragma unroll
+                        for (int q = 0; q < kVParts<T>; ++q) {
+                            const unsigned a = base + s * stage + q * a_size, b = base + s * stage + b_at + q * b_size;
+                            if (!a_mn) {
+                                if (a_mine) tma_load_3d(a, am, bar, ax + k, ay, q);
+                            } else {  // two chunks of 64 columns, 64 rows each
+                                tma_load_3d(a, am, bar, ax, ay + k, q);
+                                tma_load_3d(a + 8192, am, bar, ax + 64, ay + k, q);
+                            }
+                            if (!b_mn) {
+                                tma_load_3d(b, bm, bar, bx + k, by, q);
+                            } else {
+                                if (b_mine) tma_load_3d(b, bm, bar, bx, by + k, q);
+                                if (b_mine > 64) tma_load_3d(b + 8192, bm, bar, bx + 64, by + k, q);
+                            }
+                        }
                     }
-                    __syncwarp();
-                    more = true;
-                    if (++s == S) s = 0, phase ^= 1;
+                    if (++s == S) s = 0, ++round;
                 }
-                if (ok && elect_one()) umma_commit(tfull + 8 * acc);
-                __syncwarp();
             }
-            if (!ok) {  // products in flight finish before the tensor memory goes
-                if (elect_one()) umma_commit(drain);
-                __syncwarp();
-                mbar_wait_bounded(drain, 0, &never);
+            // the products' last arrivals have to find this CTA still here; after a wait that ran out, the
+            // copies in flight (of both CTAs) have to land before the pair leaves
+            for (unsigned q = 0; q < S; ++q) {
+                const unsigned fills = round + (q < s);  // of stage q
+                if (fills == 0) continue;
+                if (ok && !__all_sync(~0u, mbar_wait_bounded(empty + 8 * q, (fills - 1) & 1, abort_flag))) {
+                    give_up();
+                    ok = false;
+                }
+                if (!ok && rank == 0) mbar_wait_bounded(full + 8 * q, (fills - 1) & 1, &never);
+            }
+        } else if (warp == 1) {
+            if (rank == 0) {
+                // ---- products ----
+                const uint64_t desc0 = umma_desc(base, 8192);
+                unsigned s = 0, phase = 0, acc_it = 0;
+                bool ok = true;
+                VocabTile t;
+                for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i) {
+                    const bool a_mn = MODE == kGrads && t.dw, b_mn = MODE == kGrads;
+                    const uint32_t idesc = umma_idesc(T != kF16, a_mn, b_mn, static_cast<unsigned>(t.bn));
+                    // 16 elements of K: 32 bytes along a K-major row, two groups of eight rows otherwise
+                    const unsigned a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
+                    for (int r = 0, runs = vocab_runs<MODE, T>(t); ok && r < runs; ++r, ++acc_it) {
+                        const unsigned acc = acc_it % 2, use = acc_it / 2;
+                        if (use && !__all_sync(~0u, mbar_wait_bounded(tempty + 8 * acc, (use - 1) & 1, abort_flag))) {
+                            give_up();
+                            ok = false;
+                            break;
+                        }
+                        tmem_fence_after();
+                        const unsigned d = tmem + acc * 256;
+                        bool more = false;  // the first product of a run starts the accumulator
+                        int n = t.kn;
+                        if constexpr (kVRuns<MODE, T>) n = min(kVRunBlocks<T>, t.kn - r * kVRunBlocks<T>);
+                        for (; n > 0; --n) {
+                            if (!__all_sync(~0u, mbar_wait_bounded(full + 8 * s, phase, abort_flag))) {
+                                give_up();
+                                ok = false;
+                                break;
+                            }
+                            tmem_fence_after();
+                            const uint64_t a0 = desc0 + ((s * stage) >> 4), b0 = a0 + (b_at >> 4);
+                            if (elect_one()) {
+    #pragma unroll
+                                for (int q = 0; q < kVPairs<T>; ++q) {
+                                    const uint64_t a = a0 + a_part_of(kVPairs<T>, q) * (a_size >> 4);
+                                    const uint64_t b = b0 + b_part_of(kVPairs<T>, q) * (b_size >> 4);
+    #pragma unroll
+                                    for (unsigned k = 0; k < kVK / 16; ++k)
+                                        umma(d, a + k * a_step, b + k * b_step, idesc, more || q > 0 || k > 0);
+                                }
+                                umma_commit(empty + 8 * s);
+                            }
+                            __syncwarp();
+                            more = true;
+                            if (++s == S) s = 0, phase ^= 1;
+                        }
+                        if (ok && elect_one()) umma_commit(tfull + 8 * acc);
+                        __syncwarp();
+                    }
+                }
+                if (!ok) {  // products in flight finish before the tensor memory goes
+                    if (elect_one()) umma_commit(drain);
+                    __syncwarp();
+                    mbar_wait_bounded(drain, 0, &never);
+                }
             }
         }
-    } else if (warp >= 4) {
+    } else {
+        if constexpr (kVRuns<MODE, T>) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kVSumRegs));
         // ---- results: a warp reads the 32 lanes of its quarter and half of the columns ----
         const int quarter = warp % 4, half = (warp - 4) / 4;
         unsigned char *stage_out = raw + (base - smem_u32(raw)) + kVRing + (warp - 4) * 32 * kVPitch;
         unsigned acc_it = 0;
         VocabTile t;
         const float unscale = MODE == kGrads && p.list ? p.list->unscale : 1.0f;
-        for (int i = 0; vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i, ++acc_it) {
-            const unsigned acc = acc_it % 2, use = acc_it / 2;
+        bool ok = true;
+        for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i) {
             const int r = t.m * kVM + static_cast<int>(rank) * 128 + quarter * 32 + lane;  // row of the product
             const int c0 = half * (t.bn / 2);                                             // first column in the tile
+            const int width = t.bn / 2;
             const VocabSeg &seg = p.seg[t.seg];
-            const unsigned src = tmem + acc * 256 + static_cast<unsigned>(c0) + (static_cast<unsigned>(quarter * 32) << 16);
             long long y = -1;
             float lse = 0.0f, g = 0.0f;
             if constexpr (MODE == kStats) {
@@ -459,21 +495,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                     y = q.y, lse = q.lse, g = q.g;
                 }
             }
-            const bool ok = mbar_wait_bounded(tfull + 8 * acc, use & 1, abort_flag);
-            if (__any_sync(~0u, !ok)) {
-                if (lane == 0) give_up();
-                break;
+            unsigned src = 0;  // the tile's accumulator in tensor memory
+            auto next_run = [&] {
+                const unsigned acc = acc_it % 2, use = acc_it / 2;
+                src = tmem + acc * 256 + static_cast<unsigned>(c0) + (static_cast<unsigned>(quarter * 32) << 16);
+                const bool got = mbar_wait_bounded(tfull + 8 * acc, use & 1, abort_flag);
+                if (__any_sync(~0u, !got)) {
+                    if (lane == 0) give_up();
+                    ok = false;
+                }
+                tmem_fence_after();
+            };
+            auto done_run = [&] {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(leader_addr(tempty + 8 * (acc_it % 2)));
+                ++acc_it;
+            };
+            float sums[kVRuns<MODE, T> ? 128 : 1];
+            if constexpr (kVRuns<MODE, T>) {
+#pragma unroll
+                for (int k = 0; k < 128; ++k) sums[k] = 0.0f;
+                for (int q = 0, runs = vocab_runs<MODE, T>(t); q < runs; ++q) {
+                    next_run();
+                    if (!ok) break;
+                    if (t.kn) {
+#pragma unroll
+                        for (int c = 0; c < 128; c += 16)
+                            if (c < width) tmem_add16(src + c, sums + c);
+                    }
+                    done_run();
+                }
+            } else {
+                next_run();
             }
-            tmem_fence_after();
-            const int width = t.bn / 2;
+            if (!ok) break;
+            auto values = [&](int c, float (&v)[32]) {  // columns c .. c + 31 of this thread's row
+                if constexpr (kVRuns<MODE, T>) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = sums[c + k];
+                } else if (t.kn) {
+                    tmem_load32(src + c, v);
+                } else {  // nothing to sum over
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = 0.0f;
+                }
+            };
             if constexpr (MODE == kStats) {
                 const int col = t.n * p.bn + c0;                 // column in the segment
                 const int n = min(width, seg.rows - col);        // columns of this warp that exist
                 const long long at = y - seg.first - col;        // the target's column here, if in [0, n)
                 float m = -INFINITY, s = 0.0f;
-                for (int c = 0; c < width; c += 32) {
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    if (c >= width) break;
                     float v[32];
-                    tmem_load32(src + c, v);
+                    values(c, v);
                     float top = -INFINITY;
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
@@ -497,9 +574,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 const int n = min(width, seg.rows - col);
                 const long long at = y - seg.first - col;
                 unsigned short *out = p.d + static_cast<long long>(r) * p.d_ld + seg.col0 + col;
-                for (int c = 0; c < width; c += 32) {
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    if (c >= width) break;
                     float v[32];
-                    tmem_load32(src + c, v);
+                    values(c, v);
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
                         const float q = __expf(v[k] - lse) - (at == c + k ? 1.0f : 0.0f);
@@ -539,14 +618,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                     if (p.sum)
                         sum = p.sum + ((static_cast<long long>(t.seg) * p.slices + t.slice) * p.sum_rows + r) * p.sum_ld + col;
                 }
-                for (int c = 0; c < width; c += 32) {
-                    float v[32];
-                    if (t.kn) {
-                        tmem_load32(src + c, v);
-                    } else {  // nothing to sum over
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = 0.0f;
-                    }
+                for (int c = 0; c < 128; c += 32) {
+                    if (c >= width) break;
+                    float v[32];
+                    values(c, v);
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] *= unscale;
                     if (sum) {
@@ -565,9 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                     if (c < n) store_block<T>(stage_out, out ? out + c * es : nullptr, v, min(32, n - c), lane);
                 }
             }
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(leader_addr(tempty + 8 * acc));
+            if constexpr (!kVRuns<MODE, T>) done_run();
         }
         if constexpr (MODE == kDlogits) asm volatile("fence.proxy.async.global;" ::: "memory");
     }

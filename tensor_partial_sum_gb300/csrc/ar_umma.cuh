@@ -47,7 +47,7 @@ __device__ __forceinline__ bool mbar_try(unsigned addr, unsigned parity) {
 // Wait for the phase of the given parity; false when kUmmaTimeoutNs ran out or another warp gave up.
 // The clock and the flag are read only once the first try has failed: the threads that feed the
 // tensor cores have a few hundred cycles for a block of K.
-static __device__ __noinline__ bool mbar_wait_slow(unsigned addr, unsigned parity, const volatile unsigned *abort_flag) {
+__device__ __forceinline__ bool mbar_wait_slow(unsigned addr, unsigned parity, const volatile unsigned *abort_flag) {
     const unsigned long long deadline = global_ns() + kUmmaTimeoutNs;
     while (!mbar_try(addr, parity))
         if (*abort_flag || global_ns() > deadline) return false;
@@ -129,6 +129,20 @@ __device__ __forceinline__ void tmem_load32(unsigned addr, float (&v)[32]) {
         : "memory");
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+}
+
+// 16 columns likewise, added to `sum`.
+__device__ __forceinline__ void tmem_add16(unsigned addr, float *sum) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+    for (int k = 0; k < 16; ++k) sum[k] = __fadd_rn(sum[k], __uint_as_float(r[k]));
 }
 
 }  // namespace tps

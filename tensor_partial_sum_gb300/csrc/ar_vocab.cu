@@ -370,7 +370,9 @@ struct Call {
     int launch_gemm(tps::VocabGemmParams &p, size_t tiles) const {
         p.a_room = p.a_rows >= 128 || (MODE == tps::kGrads && p.tiles) ? 128 : p.a_tail;
         // a product reads 128 rows of A wherever the stage starts: the last stage's have to lie in the ring
-        const int stage = (p.a_room + p.bn / 2) * tps::kVRow, last = tps::kVRing - 128 * tps::kVRow;
+        const int a = static_cast<int>(parts) * p.a_room * tps::kVRow, b = static_cast<int>(parts) * p.bn / 2 * tps::kVRow;
+        // (the last part of A: 128 rows from (parts - 1) a_room rows on)
+        const int stage = a + b, last = tps::kVRing - (static_cast<int>(parts - 1) * p.a_room + 128) * tps::kVRow;
         p.stages = tps::kVRing / stage;
         if (p.stages > last / stage + 1) p.stages = last / stage + 1;
         if (p.stages > tps::kVMaxStages) p.stages = tps::kVMaxStages;
@@ -381,6 +383,16 @@ struct Call {
                                  static_cast<int>(tps::kVSmem)) != cudaSuccess) {
             cudaGetLastError();
             return AR_ERR_CUDA;
+        }
+        if (MODE == tps::kStats || v->dtype == AR_F32) {
+            // result warps take registers that the feeding warps give up; a launch that was given fewer
+            // than the split adds up to would wait for them for ever
+            cudaFuncAttributes a;
+            if (cudaFuncGetAttributes(&a, reinterpret_cast<const void *>(fn)) != cudaSuccess) {
+                cudaGetLastError();
+                return AR_ERR_CUDA;
+            }
+            if (a.numRegs < tps::kVLaunchRegs) return AR_ERR_UNSUPPORTED;
         }
         const size_t most = static_cast<size_t>(c.sm_count / 2);
         const size_t pairs = tiles < 1 ? 1 : tiles < most ? tiles : most;
