@@ -485,6 +485,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
             const int c0 = half * (t.bn / 2);                                             // first column in the tile
             const int width = t.bn / 2;
             const VocabSeg &seg = p.seg[t.seg];
+            // rows past the end cost nothing (D's are read, as zeros, up to a whole block of K)
+            const int rows = MODE == kDlogits ? (live + kVK - 1) / kVK * kVK : MODE == kGrads && t.dw ? seg.rows : live;
+            const bool idle = r - lane >= rows;
             long long y = -1;
             float lse = 0.0f, g = 0.0f;
             if constexpr (MODE == kStats) {
@@ -519,7 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 for (int q = 0, runs = vocab_runs<MODE, T>(t); q < runs; ++q) {
                     next_run();
                     if (!ok) break;
-                    if (t.kn) {
+                    if (t.kn && !idle) {
 #pragma unroll
                         for (int c = 0; c < 128; c += 16)
                             if (c < width) tmem_add16(src + c, sums + c);
@@ -530,6 +533,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 next_run();
             }
             if (!ok) break;
+            if (idle) {
+                if constexpr (!kVRuns<MODE, T>) done_run();
+                continue;
+            }
             auto values = [&](int c, float (&v)[32]) {  // columns c .. c + 31 of this thread's row
                 if constexpr (kVRuns<MODE, T>) {
 #pragma unroll
@@ -787,9 +794,11 @@ static __global__ void __launch_bounds__(1024) ar_vocab_list_kernel(const __grid
 }
 
 struct VocabPackParams {
-    const void *src;
-    long long src_row;        // bytes
-    int rows, dim;
+    const void *src[kMaxSegs];     // matrices of a launch, blockIdx.y picks one
+    long long src_row[kMaxSegs];   // bytes
+    int rows[kMaxSegs];
+    long long dst_at[kMaxSegs];    // where a matrix's rows start in dst
+    int dim;
     unsigned short *dst;      // [parts][dst_rows][dst_ld]
     long long dst_ld, dst_part;
     const int *place;         // where row t goes (-1: nowhere), nullptr: in order
@@ -810,14 +819,15 @@ __global__ void __launch_bounds__(256) ar_vocab_pack_kernel(const __grid_constan
             for (long long c = threadIdx.x; c < p.dst_ld / 8; c += blockDim.x)
                 reinterpret_cast<uint4 *>(p.dst + q * p.dst_part + at * p.dst_ld)[c] = make_uint4(0, 0, 0, 0);
     };
-    for (int t = blockIdx.x; t < p.rows; t += gridDim.x) {
-        const int at = p.place ? p.place[t] : t;
+    const int m = blockIdx.y;
+    for (int t = blockIdx.x; t < p.rows[m]; t += gridDim.x) {
+        const long long at = p.place ? p.place[t] : p.dst_at[m] + t;
         if (at < 0) {
             for (int r = 0; r < p.n_dh; ++r)
                 for (int c = threadIdx.x; c < p.dim; c += blockDim.x) store_elem<T>(p.dh[r] + t * p.dh_row[r], c, 0.0f);
             continue;
         }
-        const char *src = static_cast<const char *>(p.src) + t * p.src_row;
+        const char *src = static_cast<const char *>(p.src[m]) + t * p.src_row[m];
         const bool whole = reinterpret_cast<uintptr_t>(src) % 16 == 0;
         for (long long g = threadIdx.x; g < p.dst_ld / 8; g += blockDim.x) {
             if constexpr (T != kF32) {

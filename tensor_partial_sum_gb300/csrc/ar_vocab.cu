@@ -14,8 +14,10 @@ namespace {
 
 // The gradient of the logits is held for one chunk of the vocabulary at a
 // time, and packed rows likewise: as many rows as fit this many bytes, at
-// least one tile.
+// least one tile.  (Packed rows get more room: a launch over a few thousand
+// rows would leave most SMs without a tile.)
 constexpr size_t kChunkBytes = 256ull << 20;
+constexpr size_t kPackBytes = 2048ull << 20;
 // Partial sums of dH that a split reduction may take.
 constexpr size_t kSliceBytes = 64ull << 20;
 
@@ -139,8 +141,8 @@ bool next_group(const ar_vocab *v, size_t cap, int &piece, size_t &row, Group &g
 }
 
 // Vocabulary rows of a group, a multiple of the tile, when each takes `bytes_per_row`.
-size_t group_cap(size_t bytes_per_row) {
-    const size_t n = kChunkBytes / (bytes_per_row ? bytes_per_row : 1) / tps::kVN * tps::kVN;
+size_t group_cap(size_t bytes, size_t bytes_per_row) {
+    const size_t n = bytes / (bytes_per_row ? bytes_per_row : 1) / tps::kVN * tps::kVN;
     return n < tps::kVN ? static_cast<size_t>(tps::kVN) : n;
 }
 
@@ -184,7 +186,7 @@ LossPlan plan_loss(const ar_vocab *v) {
     p.hidden = c.take(hidden_in_place(v) ? 0 : v->rows * row);
     const bool pack = !weights_in_place(v);
     const size_t all = padded_vocab(v);
-    p.cap = pack && group_cap(row) < all ? group_cap(row) : all;
+    p.cap = pack && group_cap(kPackBytes, row) < all ? group_cap(kPackBytes, row) : all;
     p.weights = c.take(pack ? p.cap * row : 0);
     p.bytes = c.at;
     return p;
@@ -206,8 +208,8 @@ GradPlan plan_grad(const ar_vocab *v) {
     p.k_rows = round_up(v->rows, tps::kVK);
     const bool pack = !weights_in_place(v);
     const size_t all = padded_vocab(v);
-    size_t cap = group_cap(p.d_rows * 2 * parts);
-    if (pack && group_cap(row) < cap) cap = group_cap(row);
+    size_t cap = group_cap(kChunkBytes, p.d_rows * 2 * parts);
+    if (pack && group_cap(kPackBytes, row) < cap) cap = group_cap(kPackBytes, row);
     p.cap = cap < all ? cap : all;
     // The dH tiles reduce over the vocabulary, the dW tiles over the tokens.  Where one dH tile would take
     // more than a pair's share of all blocks of K, its reduction is cut into slices of half a share (none
@@ -319,25 +321,29 @@ struct Call {
         return launched(tps::launch_dependent(fn, grid, threads, smem, stream, c.pdl, p));
     }
 
-    // Rows into packed rows at `dst`, `rows_max` rows apart in parts.
-    tps::VocabPackParams pack_params(const void *src, size_t stride, size_t rows, void *dst, size_t rows_max) const {
+    // Packed rows at `dst`, `rows_max` rows apart in parts, of the matrices that add_pack names.
+    tps::VocabPackParams pack_params(void *dst, size_t rows_max) const {
         tps::VocabPackParams p;
         memset(&p, 0, sizeof p);
-        p.src = src;
-        p.src_row = static_cast<long long>(stride);
-        p.rows = static_cast<int>(rows);
         p.dim = static_cast<int>(v->dim);
         p.dst = static_cast<unsigned short *>(dst);
         p.dst_ld = static_cast<long long>(ld);
         p.dst_part = static_cast<long long>(rows_max * ld);
         return p;
     }
-    int launch_pack(const tps::VocabPackParams &p) const {
-        const int most = c.sm_count * 16;
+    static void add_pack(tps::VocabPackParams &p, int m, const void *src, size_t stride, size_t rows, size_t at) {
+        p.src[m] = src;
+        p.src_row[m] = static_cast<long long>(stride);
+        p.rows[m] = static_cast<int>(rows);
+        p.dst_at[m] = static_cast<long long>(at);
+    }
+    int launch_pack(const tps::VocabPackParams &p, int n) const {
+        int rows = 64, most = c.sm_count * 16 / n;
+        for (int m = 0; m < n; ++m) rows = p.rows[m] > rows ? p.rows[m] : rows;
         return launch(by_type<tps::VocabPackParams>(v->dtype, tps::ar_vocab_pack_kernel<tps::kF32>,
                                                     tps::ar_vocab_pack_kernel<tps::kF16>,
                                                     tps::ar_vocab_pack_kernel<tps::kBF16>),
-                      dim3(static_cast<unsigned>(p.rows < 64 ? 64 : p.rows < most ? p.rows : most)), 256u, 0, p);
+                      dim3(static_cast<unsigned>(rows < most ? rows : most), static_cast<unsigned>(n)), 256u, 0, p);
     }
 
     // The weights of a group: packed at `area` (room for `cap` rows) where they have to be; per segment
@@ -348,6 +354,7 @@ struct Call {
     };
     int group_weights(const Group &g, size_t area, size_t cap, Matrix *out) const {
         size_t at = 0;
+        tps::VocabPackParams p = pack_params(ws + area, cap);
         for (int s = 0; s < g.nseg; ++s) {
             const size_t stride = weight_stride(v, g.piece[s]);
             const char *src = static_cast<const char *>(v->weights[g.piece[s]]) + g.row0[s] * stride;
@@ -355,13 +362,11 @@ struct Call {
                 out[s] = Matrix{src, v->dim, g.rows[s], stride / 2, 0};
                 continue;
             }
-            char *dst = ws + area + at * ld * 2;
+            add_pack(p, s, src, stride, g.rows[s], at);
+            out[s] = Matrix{ws + area + at * ld * 2, ld, g.rows[s], ld, cap * ld};
             at += g.rows[s];
-            out[s] = Matrix{dst, ld, g.rows[s], ld, cap * ld};
-            const int st = launch_pack(pack_params(src, stride, g.rows[s], dst, cap));
-            if (st != AR_OK) return st;
         }
-        return AR_OK;
+        return pack ? launch_pack(p, g.nseg) : static_cast<int>(AR_OK);
     }
 
     // With few rows of A a stage holds less, and more stages fit: these launches are bound by the bytes
@@ -460,7 +465,9 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
     Call::Matrix h{static_cast<const char *>(v->hidden), D, T, row_bytes(v->hidden_row_bytes, v) / 2, 0};
     if (!hidden_in_place(v)) {
         h = Call::Matrix{call.ws + plan.hidden, call.ld, T, call.ld, T * call.ld};
-        st = call.launch_pack(call.pack_params(v->hidden, row_bytes(v->hidden_row_bytes, v), T, call.ws + plan.hidden, T));
+        tps::VocabPackParams hp = call.pack_params(call.ws + plan.hidden, T);
+        Call::add_pack(hp, 0, v->hidden, row_bytes(v->hidden_row_bytes, v), T, 0);
+        st = call.launch_pack(hp, 1);
         if (st != AR_OK) return st;
     }
     tps::VocabGemmParams p;
@@ -579,8 +586,8 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
     l.place = reinterpret_cast<int *>(call.ws + plan.place);
     st = call.launch<tps::VocabListParams>(tps::ar_vocab_list_kernel, dim3(1), 1024u, 0, l);
     if (st != AR_OK) return st;
-    tps::VocabPackParams hp =
-        call.pack_params(v->hidden, row_bytes(v->hidden_row_bytes, v), T, call.ws + plan.hidden, plan.k_rows);
+    tps::VocabPackParams hp = call.pack_params(call.ws + plan.hidden, plan.k_rows);
+    Call::add_pack(hp, 0, v->hidden, row_bytes(v->hidden_row_bytes, v), T, 0);
     hp.place = l.place;
     hp.list = l.list;
     for (int r = 0; dhidden && r < v->n_pieces; ++r) {
@@ -592,7 +599,7 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
             cudaMemset2DAsync(dhidden[r], static_cast<size_t>(hp.dh_row[r]), 0, D * es, T, stream) != cudaSuccess)
             return launched(cudaErrorUnknown);
     }
-    st = call.launch_pack(hp);
+    st = call.launch_pack(hp, 1);
     if (st != AR_OK) return st;
 
     tps::VocabGemmParams p;
