@@ -524,8 +524,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                     if (!ok) break;
                     if (t.kn && !idle) {
 #pragma unroll
-                        for (int c = 0; c < 128; c += 16)
-                            if (c < width) tmem_add16(src + c, sums + c);
+                        for (int c = 0; c < 128; c += 32)
+                            if (c < width) tmem_add32(src + c, sums + c);
                     }
                     done_run();
                 }

@@ -38,7 +38,7 @@ __device__ __forceinline__ unsigned leader_addr(unsigned local) {
 __device__ __forceinline__ bool mbar_try(unsigned addr, unsigned parity) {
     unsigned done;
     asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
         : "=r"(done)
         : "r"(addr), "r"(parity)
         : "memory");
@@ -57,7 +57,7 @@ __device__ __forceinline__ bool mbar_wait_bounded(unsigned addr, unsigned parity
     return mbar_try(addr, parity) || mbar_wait_slow(addr, parity, abort_flag);
 }
 __device__ __forceinline__ void mbar_arrive_cluster(unsigned cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // Copy a box of a 3-D tensor into this CTA's shared memory; its bytes count on the barrier at
@@ -131,18 +131,12 @@ __device__ __forceinline__ void tmem_load32(unsigned addr, float (&v)[32]) {
     for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
 }
 
-// 16 columns likewise, added to `sum`.
-__device__ __forceinline__ void tmem_add16(unsigned addr, float *sum) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-        "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr)
-        : "memory");
+// The same, added to `sum`.
+__device__ __forceinline__ void tmem_add32(unsigned addr, float *sum) {
+    float v[32];
+    tmem_load32(addr, v);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) sum[k] = __fadd_rn(sum[k], __uint_as_float(r[k]));
+    for (int k = 0; k < 32; ++k) sum[k] = __fadd_rn(sum[k], v[k]);
 }
 
 }  // namespace tps
