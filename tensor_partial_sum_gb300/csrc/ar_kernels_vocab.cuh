@@ -141,73 +141,91 @@ __host__ __device__ constexpr int tail_width(int rows) {
     return MODE == kStats ? (rows + 15) / 16 * 16 : (rows + 63) / 64 * 64;
 }
 
-// The i-th tile of a pair; false when it has no more.  kStats and kDlogits: row tiles of one column
-// tile next to one another, so that pairs that run together share W and find H in L2.  kGrads: first
-// the dH tiles (long reductions) in turn, then the dW tiles; pairs that got one dH tile fewer take as
-// many more dW tiles as cost the same.
+// Blocks of K that storing a tile of dW takes as long as: the least a dW tile counts for.
+constexpr int kVStoreBlocks = 10;
+
+// A pair's tiles, one after another.  kStats and kDlogits: row tiles of one column tile next to one
+// another, so that pairs that run together share W and find H in L2.  kGrads: first the dH tiles (long
+// reductions) in turn, then the dW tiles; pairs that got one dH tile fewer first take as many more dW
+// tiles as cost the same.
 template <int MODE>
-__device__ __forceinline__ bool vocab_tile(const VocabGemmParams &p, int live, int i, int pair, int npairs, VocabTile &t) {
-    const int mt = (live + kVM - 1) / kVM;
-    t.slice = 0;
-    t.k0 = 0;
-    t.bn = p.bn;
-    t.dw = false;
-    if constexpr (MODE != kGrads) {
-        const long long id = pair + static_cast<long long>(i) * npairs;
-        if (mt == 0 || id >= static_cast<long long>(p.tiles) * mt) return false;
-        const int j = static_cast<int>(id / mt);
-        t.m = static_cast<int>(id % mt);
+struct VocabWalk {
+    const VocabGemmParams &p;
+    int pair, npairs, mt, kn, nt;
+    int i = 0;
+    // kGrads: dH tiles of a segment and of this pair, pairs without the last round's dH tile, the dW
+    // tiles that each of them takes more
+    int per_seg = 0, mine = 0, behind = 0, extra = 0, first = 0;
+
+    __device__ __forceinline__ VocabWalk(const VocabGemmParams &params, int live, int pair_, int npairs_)
+        : p(params), pair(pair_), npairs(npairs_), mt((live + kVM - 1) / kVM) {
+        if constexpr (MODE != kGrads) {
+            kn = (p.dim + kVK - 1) / kVK;
+            nt = 0;
+        } else {
+            kn = (live + kVK - 1) / kVK;
+            nt = (p.dim + p.bn - 1) / p.bn;
+            per_seg = p.slices * p.dh_tiles * mt;
+            const int n_long = p.nseg * per_seg, rem = n_long % npairs;
+            mine = n_long / npairs + (pair < rem);
+            behind = rem ? npairs - rem : 0;
+            if (behind) {
+                const int kw = max(kVStoreBlocks, kn), kl = (p.seg[0].rows + kVK * p.slices - 1) / (kVK * p.slices);
+                extra = min((kl + kw / 2) / kw, p.tiles / behind);
+                first = pair >= rem ? extra : 0;
+            }
+        }
+    }
+    __device__ __forceinline__ bool next(VocabTile &t) {
+        t.slice = 0;
+        t.k0 = 0;
+        t.bn = p.bn;
+        t.dw = false;
         t.seg = 0;
-        while (t.seg + 1 < p.nseg && p.seg[t.seg + 1].tile0 <= j) ++t.seg;
-        t.n = j - p.seg[t.seg].tile0;
-        t.kn = (p.dim + kVK - 1) / kVK;
-        // the last tile of a segment is as narrow as its rows allow (D's columns are read in blocks of K)
-        t.bn = min(p.bn, tail_width<MODE>(p.seg[t.seg].rows - t.n * p.bn));
-        return true;
-    } else {
-        const int per_seg = p.slices * p.dh_tiles * mt;
-        const int n_long = p.nseg * per_seg;
-        const int rem = n_long % npairs;
-        const int mine = n_long / npairs + (pair < rem);
-        if (i < mine) {
-            int id = pair + i * npairs;
-            t.seg = id / per_seg;
-            id -= t.seg * per_seg;
-            t.m = id % mt;
-            id /= mt;
-            t.n = id % p.dh_tiles;
-            t.slice = id / p.dh_tiles;
-            const int kb = (p.seg[t.seg].rows + kVK - 1) / kVK, per = (kb + p.slices - 1) / p.slices;
-            t.k0 = t.slice * per;
-            t.kn = max(0, min(per, kb - t.k0));
+        if constexpr (MODE != kGrads) {
+            const long long id = pair + static_cast<long long>(i++) * npairs;
+            if (mt == 0 || id >= static_cast<long long>(p.tiles) * mt) return false;
+            const int j = id <= 0x7FFFFFFF ? static_cast<int>(id) / mt : static_cast<int>(id / mt);
+            t.m = static_cast<int>(id - static_cast<long long>(j) * mt);
+            while (t.seg + 1 < p.nseg && p.seg[t.seg + 1].tile0 <= j) ++t.seg;
+            t.n = j - p.seg[t.seg].tile0;
+            t.kn = kn;
+            // the last tile of a segment is as narrow as its rows allow (D's columns are read in blocks of K)
+            t.bn = min(p.bn, tail_width<MODE>(p.seg[t.seg].rows - t.n * p.bn));
+            return true;
+        } else {
+            if (i < mine) {
+                int id = pair + i++ * npairs;
+                t.seg = id / per_seg;
+                id -= t.seg * per_seg;
+                t.m = id % mt;
+                id /= mt;
+                t.n = id % p.dh_tiles;
+                t.slice = id / p.dh_tiles;
+                const int kb = (p.seg[t.seg].rows + kVK - 1) / kVK, per = (kb + p.slices - 1) / p.slices;
+                t.k0 = t.slice * per;
+                t.kn = max(0, min(per, kb - t.k0));
+            } else {
+                const int q = i++ - mine;
+                const int id = q < first ? (pair - (npairs - behind)) * extra + q : extra * behind + pair + (q - first) * npairs;
+                if (id >= p.tiles) return false;
+                const int j = id / nt;
+                t.n = id - j * nt;
+                while (t.seg + 1 < p.nseg && p.seg[t.seg + 1].tile0 <= j) ++t.seg;
+                t.m = j - p.seg[t.seg].tile0;
+                t.kn = kn;
+                t.dw = true;
+            }
             if (p.dim - t.n * p.bn <= kVN / 2) t.bn = kVN / 2;
             return true;
         }
-        i -= mine;
-        const int kw = max(1, (live + kVK - 1) / kVK);
-        const int kl = (p.seg[0].rows + kVK * p.slices - 1) / (kVK * p.slices);
-        const int behind = rem ? npairs - rem : 0;
-        int extra = behind ? (kl + kw / 2) / kw : 0;
-        if (static_cast<long long>(extra) * behind > p.tiles) extra = p.tiles / behind;
-        const int first = pair >= rem && rem ? extra : 0;
-        long long id;
-        if (i < first) {
-            id = static_cast<long long>(pair - rem) * extra + i;
-        } else {
-            id = static_cast<long long>(extra) * behind + pair + static_cast<long long>(i - first) * npairs;
-        }
-        if (id >= p.tiles) return false;
-        const int nt = (p.dim + p.bn - 1) / p.bn;
-        const int j = static_cast<int>(id / nt);
-        t.n = static_cast<int>(id % nt);
-        t.seg = 0;
-        while (t.seg + 1 < p.nseg && p.seg[t.seg + 1].tile0 <= j) ++t.seg;
-        t.m = j - p.seg[t.seg].tile0;
-        t.kn = (live + kVK - 1) / kVK;
-        if (p.dim - t.n * p.bn <= kVN / 2) t.bn = kVN / 2;
-        t.dw = true;
-        return true;
     }
+};
+
+// Runs of products of a tile; one without blocks of K still counts as one.
+template <int MODE, int T>
+__device__ __forceinline__ int vocab_runs(const VocabTile &t) {
+    return kVRuns<MODE, T> ? max(1, (t.kn + kVRunBlocks<T> - 1) / kVRunBlocks<T>) : 1;
 }
 
 // Store a warp's 32x32 values, row `lane` in each thread: `n` (1 to 32) elements of T to each thread's
@@ -260,12 +278,6 @@ __device__ __forceinline__ void store_block(unsigned char *stage, char *out, con
             }
         }
     }
-}
-
-// Runs of products of a tile; one without blocks of K still counts as one.
-template <int MODE, int T>
-__device__ __forceinline__ int vocab_runs(const VocabTile &t) {
-    return kVRuns<MODE, T> ? max(1, (t.kn + kVRunBlocks<T> - 1) / kVRunBlocks<T>) : 1;
 }
 
 // The three bf16 parts of two floats, eight bits each, packed in pairs.
@@ -343,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
             unsigned s = 0, round = 0;  // the stage to fill and how often the ring went round
             bool ok = true;
             VocabTile t;
-            for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i) {
+            for (VocabWalk<MODE> walk(p, live, pair, npairs); ok && walk.next(t);) {
                 const CUtensorMap *am, *bm;
                 int ay, ax, by, bx;  // first element of this CTA's rows (columns) at block 0 of K
                 const int row0 = t.m * kVM, arow = row0 + static_cast<int>(rank) * 128;
@@ -420,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 unsigned s = 0, phase = 0, acc_it = 0;
                 bool ok = true;
                 VocabTile t;
-                for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i) {
+                for (VocabWalk<MODE> walk(p, live, pair, npairs); ok && walk.next(t);) {
                     const bool a_mn = MODE == kGrads && t.dw, b_mn = MODE == kGrads;
                     const uint32_t idesc = umma_idesc(T != kF16, a_mn, b_mn, static_cast<unsigned>(t.bn));
                     // 16 elements of K: 32 bytes along a K-major row, two groups of eight rows otherwise
@@ -480,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
         VocabTile t;
         const float unscale = MODE == kGrads && p.list ? p.list->unscale : 1.0f;
         bool ok = true;
-        for (int i = 0; ok && vocab_tile<MODE>(p, live, i, pair, npairs, t); ++i) {
+        for (VocabWalk<MODE> walk(p, live, pair, npairs); ok && walk.next(t);) {
             const int r = t.m * kVM + static_cast<int>(rank) * 128 + quarter * 32 + lane;  // row of the product
             const int c0 = half * (t.bn / 2);                                             // first column in the tile
             const int width = t.bn / 2;
@@ -828,11 +840,19 @@ __global__ void __launch_bounds__(256) ar_vocab_pack_kernel(const __grid_constan
             continue;
         }
         const char *src = static_cast<const char *>(p.src[m]) + t * p.src_row[m];
-        const bool whole = reinterpret_cast<uintptr_t>(src) % 16 == 0;
+        const bool whole = reinterpret_cast<uintptr_t>(src) % 16 == 0, words = reinterpret_cast<uintptr_t>(src) % 4 == 0;
         for (long long g = threadIdx.x; g < p.dst_ld / 8; g += blockDim.x) {
             if constexpr (T != kF32) {
                 if (whole && 8 * g + 8 <= p.dim) {
                     *reinterpret_cast<uint4 *>(p.dst + at * p.dst_ld + 8 * g) = __ldg(reinterpret_cast<const uint4 *>(src) + g);
+                    continue;
+                }
+            }
+            if constexpr (T != kF32) {  // rows on a 4-byte boundary
+                if (words && 8 * g + 8 <= p.dim) {
+                    const uint32_t *from = reinterpret_cast<const uint32_t *>(src) + 4 * g;
+                    *reinterpret_cast<uint4 *>(p.dst + at * p.dst_ld + 8 * g) =
+                        make_uint4(__ldg(from), __ldg(from + 1), __ldg(from + 2), __ldg(from + 3));
                     continue;
                 }
             }

@@ -221,7 +221,7 @@ GradPlan plan_grad(const ar_vocab *v) {
         const size_t n = v->piece_rows[r];
         longest = n > longest ? n : longest;
         segs += n != 0;
-        blocks += nt * (mt * tiles_of(n, tps::kVK) + tiles_of(n, tps::kVM) * (kw < 8 ? 8 : kw));
+        blocks += nt * (mt * tiles_of(n, tps::kVK) + tiles_of(n, tps::kVM) * (kw < tps::kVStoreBlocks ? tps::kVStoreBlocks : kw));
     }
     const bool split = round_up(longest, tps::kVN) > p.cap;
     if (split) blocks = blocks / (longest / p.cap + 1), longest = p.cap;
@@ -421,6 +421,11 @@ int ar_check_vocab(const ar_vocab *v, size_t max_elems) {
         total += v->piece_rows[r];
     }
     if (total == 0) return AR_ERR_INVALID_ARG;
+    // tiles of a launch are counted in 31 bits
+    constexpr size_t kMostTiles = 1ull << 30;
+    const size_t nt = v->dim / 128 + 1;
+    if (total / tps::kVM + AR_MAX_RANKS > kMostTiles / nt || v->rows / tps::kVM + 1 > kMostTiles / AR_MAX_RANKS / nt)
+        return AR_ERR_TOO_LARGE;
     if (v->rows > max_elems / v->dim) return AR_ERR_TOO_LARGE;
     if (v->rows == 0) return AR_OK;
     if (!valid_rows(v->hidden, v->rows, v->hidden_row_bytes, v)) return AR_ERR_INVALID_ARG;
