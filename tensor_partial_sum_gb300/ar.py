@@ -560,6 +560,8 @@ def _matrix(x, rows, dim, dtype, name, call):
         raise TypeError(f"{call}: {name} is {x.dtype}, the hidden states are {dtype}")
     if x.dim() != 2 or tuple(x.shape) != (rows, dim) or (dim > 1 and x.stride(1) != 1):
         raise ValueError(f"{call}: {name} has to be [{rows}, {dim}] with adjacent columns")
+    if rows > 1 and x.stride(0) < dim:  # an expanded tensor, for one; the library takes a stride of 0 for packed rows
+        raise ValueError(f"{call}: the rows of {name} lie over one another")
     return (x.stride(0) if rows > 1 else dim) * x.element_size()
 
 

@@ -380,6 +380,7 @@ def test_refusals_leave_the_outputs_alone():
                 lambda: tps.ar_vocab_loss(hidden, weights, targets[:15], loss, lse),
                 lambda: tps.ar_vocab_loss(hidden, weights, targets, loss[:15], lse),
                 lambda: tps.ar_vocab_loss(hidden, [w.t().contiguous().t() for w in weights], targets, loss, lse),
+                lambda: tps.ar_vocab_loss(hidden[:1].expand(16, 64), weights, targets, loss, lse),
                 lambda: tps.ar_vocab_loss_grad(hidden, weights, targets, lse, dloss, dhidden=[torch.empty_like(hidden)])):
         with pytest.raises(ValueError):
             bad()
@@ -395,3 +396,48 @@ def test_refusals_leave_the_outputs_alone():
     tps.ar_vocab_loss(hidden, weights, targets, loss, lse)
     torch.cuda.synchronize()
     assert not (loss == 5).any()
+
+
+# ---- shapes of the tiling ---------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [127, 128, 129, 255, 256, 257, 383, 385])
+def test_token_counts_around_the_tiles(dtype, T):
+    hidden, weights, targets = make(dtype, T, 72, [130, 515], seed=T, ignored=0.1)
+    check_all(dtype, hidden, weights, targets, torch.rand(T, device="cuda", generator=torch.Generator("cuda").manual_seed(T)))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [1, 8, 63, 65, 127, 129, 191, 255, 257, 320, 640, 1031])
+def test_dims_around_the_tiles(dtype, D):
+    hidden, weights, targets = make(dtype, 70, D, [300], seed=D)
+    check_all(dtype, hidden, weights, targets, torch.full((70,), 1 / 70, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [1, 15, 16, 17, 63, 65, 127, 129, 255, 257, 2000])
+def test_vocabularies_around_the_tiles(dtype, V):
+    hidden, weights, targets = make(dtype, 33, 128, [V, 3], seed=V)
+    check_all(dtype, hidden, weights, targets, torch.full((33,), 1 / 33, device="cuda"))
+
+
+@pytest.mark.parametrize("T,D,V", [(1, 4096, 20000), (20, 1248, 30000), (700, 2048, 9000), (2, 8192, 600)])
+def test_long_reductions_keep_float_precision(T, D, V):
+    """lse of 16-bit inputs within a few float roundings of 64 bits: the sums
+    of thousands of products do not drift.  (A rounding each of a logit's 32 or
+    fewer partial sums and of 32 products in a run, at most 2^-23 of the logit
+    each, signs mixed: 4 sqrt(64) 2^-23 of the largest logit.)"""
+    hidden, weights, targets = make("bf16", T, D, [V], seed=D)
+    loss, lse = loss_of(hidden, weights, targets)
+    z = hidden.double() @ weights[0].double().t()
+    tol = 4 * 8 * 2.0 ** -23 * z.abs().amax(1) + 2.0 ** -22 * (torch.logsumexp(z, 1).abs() + 1)
+    assert ((lse.double() - torch.logsumexp(z, 1)).abs() <= tol).all()
+    picked = z.gather(1, targets[:, None])[:, 0]
+    assert ((loss.double() - (torch.logsumexp(z, 1) - picked)).abs() <= 2 * tol).all()
+
+
+def test_few_tokens_large_vocabulary():
+    """Reductions over the vocabulary cut into slices."""
+    for T, D, pieces in ((1, 512, [30000]), (20, 640, [16192, 9000]), (300, 128, [50000])):
+        hidden, weights, targets = make("bf16", T, D, pieces, seed=T)
+        check_all("bf16", hidden, weights, targets, torch.full((T,), 1 / T, device="cuda"))
