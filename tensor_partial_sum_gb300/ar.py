@@ -148,7 +148,10 @@ def _ptrs(xs):
     struct costs a fraction of building a ctypes array of c_void_p."""
     if xs is None:
         return None
-    ptrs = [_ptr(x) or 0 for x in xs]
+    return _packed([_ptr(x) or 0 for x in xs])
+
+
+def _packed(ptrs):
     if len(ptrs) <= AR_MAX_RANKS:
         return _PTR_ARRAY.pack(*ptrs, *([0] * (AR_MAX_RANKS - len(ptrs))))
     return struct.pack(f"={len(ptrs)}Q", *ptrs)
@@ -201,18 +204,34 @@ def _reach(x) -> int | None:
     return st.data_ptr() + st.nbytes() - x.data_ptr()
 
 
-def _holds(x, n) -> bool:
-    """Whether a device tensor's own elements, as it lies in memory, already
-    reach n bytes past its start (a cheap answer for most tensors; _reach
-    looks at the storage)."""
-    if not getattr(x, "is_cuda", False):
-        return False
-    es = x.element_size()
-    if x.dim() == 2:
-        rows, cols = x.shape
-        down, right = x.stride()
-        return rows > 0 and cols > 0 and ((rows - 1) * down + (cols - 1) * right + 1) * es >= n
-    return x.is_contiguous() and x.numel() * es >= n
+def _layout_pointers(xs, rows, row, ne1, kind, call):
+    """Packed addresses of an ar_layout call's buffers, after checking that the
+    rows of each tensor lie inside its storage (raw addresses are the
+    caller's).  One pass: a small call's time is mostly spent here."""
+    ptrs = []
+    more = ne1 - 1
+    n = more * row + row if ne1 and row else 0
+    for k, x in enumerate(xs):
+        if x is None:
+            ptrs.append(0)
+            continue
+        if type(x) is int:
+            ptrs.append(x)
+            continue
+        if not getattr(x, "is_cuda", False):
+            _reach(x)  # refuses host tensors
+            ptrs.append(_ptr(x) or 0)
+            continue
+        if n:
+            if rows is not None:
+                n = more * rows[k] + row
+            if x.nbytes < n or not x.is_contiguous():
+                st = x.untyped_storage()
+                reach = st.nbytes() - x.storage_offset() * x.element_size()
+                if reach < n:
+                    raise ValueError(f"{call}: {kind} {k} reaches {reach} bytes, its rows span {n}")
+        ptrs.append(x.data_ptr())
+    return _packed(ptrs)
 
 
 _TORCH_CODES = None
@@ -369,6 +388,17 @@ def ar_reduce_host(h_srcs, h_dsts, d_srcs=None, d_dsts=None, nelem=None, dst_dty
                                 _ptrs(d_srcs), _ptrs(d_dsts), _stream(stream)), "ar_reduce_host")
 
 
+_I64_ARRAYS = {}
+
+
+def _i64s(values):
+    n = len(values)
+    kind = _I64_ARRAYS.get(n)
+    if kind is None:
+        kind = _I64_ARRAYS[n] = ctypes.c_int64 * n
+    return kind(*values)
+
+
 def make_layout(ne0, ne1, src_row_bytes=None, dst_row_bytes=None, residual=None, residual_row_bytes=None,
                 inactive=()) -> ArLayout:
     """An ar_layout.  With a residual, ``residual_row_bytes`` is its row
@@ -378,9 +408,9 @@ def make_layout(ne0, ne1, src_row_bytes=None, dst_row_bytes=None, residual=None,
     L = ArLayout()
     L.ne0, L.ne1 = ne0, ne1
     if src_row_bytes is not None:
-        L.src_row_bytes = (ctypes.c_int64 * len(src_row_bytes))(*src_row_bytes)
+        L.src_row_bytes = _i64s(src_row_bytes)
     if dst_row_bytes is not None:
-        L.dst_row_bytes = (ctypes.c_int64 * len(dst_row_bytes))(*dst_row_bytes)
+        L.dst_row_bytes = _i64s(dst_row_bytes)
     L.residual = _ptr(residual)
     L._residual_obj = residual  # kept for the binding's reach check
     if residual is not None and residual_row_bytes is None:
@@ -393,41 +423,30 @@ def make_layout(ne0, ne1, src_row_bytes=None, dst_row_bytes=None, residual=None,
     return L
 
 
-def _check_reach(srcs, dsts, layout, dst_dtype, call):
-    """The rows of every CUDA tensor of an ar_layout call lie inside its storage."""
-    es = ESIZE[_dtype_code(dst_dtype)]
+def _layout_buffers(srcs, dsts, layout, dcode, call):
+    """Checked, packed addresses of the sources and destinations of an
+    ar_layout call, whose residual is checked too."""
     ne0, ne1 = layout.ne0, layout.ne1
-    if ne0 * ne1 == 0:
-        return
-
-    row, more = ne0 * es, ne1 - 1
-    for kind, xs, rows in (("source", srcs, layout.src_row_bytes), ("destination", dsts, layout.dst_row_bytes)):
-        given = bool(rows)
-        for k, x in enumerate(xs):
-            if x is None or type(x) is int:
-                continue
-            n = more * (rows[k] if given else row) + row
-            if _holds(x, n):
-                continue
-            reach = _reach(x)
-            if reach is not None and reach < n:
-                raise ValueError(f"{call}: {kind} {k} reaches {reach} bytes, its rows span {n}")
-    res = getattr(layout, "_residual_obj", None)
-    if res is None:
-        return
-    n = row if layout.residual_row_bytes == 0 else more * layout.residual_row_bytes + row
-    reach = None if _holds(res, n) else _reach(res)
-    if reach is not None and reach < n:
-        raise ValueError(f"{call}: the residual reaches {reach} bytes, its rows span {n}")
+    row = ne0 * ESIZE[dcode]
+    src = _layout_pointers(srcs, layout.src_row_bytes or None, row, ne1, "source", call)
+    dst = _layout_pointers(dsts, layout.dst_row_bytes or None, row, ne1, "destination", call)
+    res = layout._residual_obj if hasattr(layout, "_residual_obj") else None
+    if res is not None and row * ne1:
+        reach = _reach(res)
+        n = row if layout.residual_row_bytes == 0 else (ne1 - 1) * layout.residual_row_bytes + row
+        if reach is not None and reach < n:
+            raise ValueError(f"{call}: the residual reaches {reach} bytes, its rows span {n}")
+    return src, dst
 
 
 def ar_reduce_ex(srcs, dsts, layout: ArLayout, dst_dtype, wire_dtype="bf16", stream=None) -> None:
     """Reduction over an ar_layout (row strides, inactive ranks as None
     sources, residual or bias).  The rows of each CUDA tensor must lie inside
     its storage."""
-    _check_reach(srcs, dsts, layout, dst_dtype, "ar_reduce_ex")
-    _check(lib().ar_reduce_ex(_ptrs(srcs), _ptrs(dsts), len(dsts), ctypes.byref(layout), _dtype_code(dst_dtype),
-                              _dtype_code(wire_dtype), _stream(stream)), "ar_reduce_ex")
+    dcode = _dtype_code(dst_dtype)
+    src, dst = _layout_buffers(srcs, dsts, layout, dcode, "ar_reduce_ex")
+    _check(lib().ar_reduce_ex(src, dst, len(dsts), ctypes.byref(layout), dcode, _dtype_code(wire_dtype),
+                              _stream(stream)), "ar_reduce_ex")
 
 
 def ar_check_layout(R, srcs, dsts, layout: ArLayout, max_elems, dst_dtype, wire_dtype) -> int:
@@ -512,11 +531,10 @@ def ar_reduce_dropout(srcs, dsts, layout: ArLayout, dropout: ArDropout, dst_dtyp
                       stream=None) -> None:
     """ar_reduce_ex with bias and dropout between the rank sum and the
     residual; the mask is a function of the dropout's seed and offset."""
-    _check_reach(srcs, dsts, layout, dst_dtype, "ar_reduce_dropout")
     dcode = _dtype_code(dst_dtype)
+    src, dst = _layout_buffers(srcs, dsts, layout, dcode, "ar_reduce_dropout")
     _typed_row(getattr(dropout, "_bias_obj", None), layout.ne0, dcode, "the bias", "ar_reduce_dropout")
-    _check(lib().ar_reduce_dropout(_ptrs(srcs), _ptrs(dsts), len(dsts), ctypes.byref(layout), ctypes.byref(dropout),
-                                   dcode, _dtype_code(wire_dtype), _stream(stream)), "ar_reduce_dropout")
+    _check(lib().ar_reduce_dropout(src, dst, len(dsts), ctypes.byref(layout), ctypes.byref(dropout), dcode, _dtype_code(wire_dtype), _stream(stream)), "ar_reduce_dropout")
 
 
 def ar_check_dropout(R, srcs, dsts, layout: ArLayout, dropout: ArDropout, max_elems, dst_dtype, wire_dtype) -> int:
@@ -541,15 +559,15 @@ def ar_reduce_dropout_grad(dy, dxs, layout: ArLayout, dropout: ArDropout, dst_dt
     the bias row and of a broadcast residual row.  ``workspace`` defaults to
     one from torch's allocator."""
     call = "ar_reduce_dropout_grad"
-    _check_reach([dy], dxs, layout, dst_dtype, call)
+    dcode = _dtype_code(dst_dtype)
+    _, dst = _layout_buffers([dy], dxs, layout, dcode, call)
     _typed_row(dbias, layout.ne0, AR_F32, "dbias", call)
     _typed_row(dresidual, layout.ne0, AR_F32, "dresidual", call)
     n_sums = (dbias is not None) + (dresidual is not None)
     need = ar_reduce_dropout_grad_workspace(layout, n_sums) if n_sums else 0
     ws, ws_bytes = _workspace(need, workspace, stream, dy, call)
-    _check(lib().ar_reduce_dropout_grad(_ptr(dy), _ptrs(dxs), len(dxs), ctypes.byref(layout), ctypes.byref(dropout),
-                                        _ptr(dbias), _ptr(dresidual), _ptr(ws), ws_bytes, _dtype_code(dst_dtype),
-                                        _stream(stream)), call)
+    _check(lib().ar_reduce_dropout_grad(_ptr(dy), dst, len(dxs), ctypes.byref(layout), ctypes.byref(dropout),
+                                        _ptr(dbias), _ptr(dresidual), _ptr(ws), ws_bytes, dcode, _stream(stream)), call)
 
 
 def _matrix(x, rows, dim, dtype, name, call):
