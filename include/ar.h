@@ -193,8 +193,10 @@ typedef enum {
     AR_Q_HOST_CHUNK_BYTES = 9,  /* ar_reduce_host pipeline chunk, bytes per buffer (default 4 MiB;
                                    at most 64 chunks per call) */
     AR_Q_DEVICE_STATUS = 10,    /* device-side status word (bit 0: a bounded wait of the TMA
-                                   variant ran out); reading it synchronises with the device;
-                                   set it to 0 to clear it */
+                                   variant ran out; bit 1: one of ar_vocab_loss or
+                                   ar_vocab_loss_grad, after two seconds - the call's results are
+                                   then unspecified and the context stays usable); reading it
+                                   synchronises with the device; set it to 0 to clear it */
     AR_Q_TMA_DROP_TILE = 11     /* test hook for failure detection, -1 (default) = off: TMA
                                    launches never load tile n, so the CTA that owns it waits
                                    for data that never comes until its bound (100 ms) runs out,
@@ -448,7 +450,16 @@ int ar_reduce_dropout_grad_workspace(const ar_layout *layout, int n_sums, size_t
  * A token whose target is ignore_index has loss 0 and adds nothing to any
  * gradient, whatever its hidden state holds (infinities and NaN included); a
  * target that is neither ignore_index nor a row of the vocabulary gives the
- * loss NaN and no gradient.  Products of 16-bit types are summed in float.
+ * loss NaN and no gradient.
+ * Products of 16-bit types are exact and summed in float: the statistics in
+ * runs of 512 terms, which are added rounded to nearest (the tensor cores'
+ * own sums are not rounded but cut off, and drift over long reductions).
+ * Float inputs are split into three bf16 parts each; six products of parts
+ * give a float product to 2^-21 at worst, 2^-24 on average.  The gradient of
+ * the logits is held in the 16-bit type (float inputs: in three parts) for
+ * one chunk of the vocabulary at a time, relative to the largest |dloss|: one
+ * rounding more than the outputs' own.  Infinite float inputs give NaN where
+ * the formula has an infinity.
  */
 typedef struct {
     size_t rows;                      /* tokens; rows * dim <= max_elems */

@@ -152,9 +152,11 @@ size_t padded_vocab(const ar_vocab *v) {
     return n;
 }
 
-// Columns of a kStats tile.  With one tile row the call is bound by reading W, and pairs that share
-// the column tiles unevenly wait: take the width (a multiple of 16, at least half a tile) that leaves the
-// least to the busiest pair.  With more tile rows the widest tile moves the fewest bytes per product.
+// Columns of a kStats tile.  With one tile row the call is bound by reading W in rounds of one tile a
+// pair.  A round takes as long as its width and some 56 columns more (one token of 4096 elements: 22.7 us at
+// 256 columns, 20.0 at 224, 15.7 at 176, 13.4 at 128), so the width, a multiple of 16 and at least half a tile,
+// that makes the rounds cheapest is taken: 32768 rows 50.2 us at 224, 52.6 at 256 and 61.7 at 128, 8000 rows
+// 21.9 us at 128 and 27.6 at 256.  With more tile rows the widest tile moves the fewest bytes per product.
 int stats_width(const ar_vocab *v, int pairs) {
     if (v->rows > tps::kVM) return tps::kVN;
     size_t best = SIZE_MAX;
@@ -162,7 +164,7 @@ int stats_width(const ar_vocab *v, int pairs) {
     for (int n = tps::kVN; n >= tps::kVN / 2; n -= 16) {
         size_t tiles = 0;
         for (int r = 0; r < v->n_pieces; ++r) tiles += tiles_of(v->piece_rows[r], static_cast<size_t>(n));
-        const size_t cost = tiles_of(tiles, static_cast<size_t>(pairs)) * static_cast<size_t>(n);
+        const size_t cost = tiles_of(tiles, static_cast<size_t>(pairs)) * static_cast<size_t>(n + 56);
         if (cost < best) best = cost, bn = n;
     }
     return bn;

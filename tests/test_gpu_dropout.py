@@ -284,3 +284,24 @@ def test_refusals_leave_the_outputs_alone():
     assert (y == 5).all()
     with pytest.raises(ValueError):
         tps.ar_reduce_dropout_grad(x, [y], lay, drop, "f32", dbias=torch.empty(15, device="cuda"))
+
+
+def test_rows_past_32_bit_offsets():
+    """Narrow rows of buffers of several GB, forward and backward."""
+    ne0, ne1, wide, p = 72, 2100, 1 << 20, 0.25
+    tps.ar_init(1, ne0 * ne1)
+    assert (ne1 - 1) * wide * 4 > 1 << 32
+    x, y = (torch.empty((ne1, wide), device="cuda")[:, 5:5 + ne0] for _ in range(2))
+    x.copy_(torch.randn((ne1, ne0), device="cuda", generator=torch.Generator("cuda").manual_seed(3)))
+    lay = tps.make_layout(ne0, ne1, [wide * 4], [wide * 4])
+    drop = tps.make_dropout(p, SEED, OFFSET)
+    keep = torch.from_numpy(keep_mask(ne0, ne1, p, SEED, OFFSET)).cuda()
+    want = torch.where(keep, x * float(scale_of(p)), 0.0)
+    tps.ar_reduce_dropout([x], [y], lay, drop, "f32", "f32")
+    assert torch.equal(y, want)
+    y.zero_()
+    db = torch.empty(ne0, device="cuda")
+    tps.ar_reduce_dropout_grad(x, [y], lay, drop, "f32", dbias=db)
+    assert torch.equal(y, want)
+    bound = ne1 * 2.0 ** -24 * want.double().abs().sum(0)  # as in run_grad
+    assert ((db.double() - want.double().sum(0)).abs() <= bound).all()

@@ -441,3 +441,39 @@ def test_few_tokens_large_vocabulary():
     for T, D, pieces in ((1, 512, [30000]), (20, 640, [16192, 9000]), (300, 128, [50000])):
         hidden, weights, targets = make("bf16", T, D, pieces, seed=T)
         check_all("bf16", hidden, weights, targets, torch.full((T,), 1 / T, device="cuda"))
+
+
+def test_rows_past_32_bit_offsets():
+    """Weights, their gradients and the hidden states as narrow views of
+    buffers of several GB."""
+    T, D, V, wide = 300, 64, 70000, 32768
+    hidden, weights, targets = make("bf16", T, D, [V], seed=21)
+    big_w = torch.empty((V, wide), dtype=torch.bfloat16, device="cuda")
+    big_w[:, 7 * D:8 * D] = weights[0]
+    big_h = torch.empty((T, 1 << 23), dtype=torch.bfloat16, device="cuda")
+    big_h[:, :D] = hidden
+    big_d = torch.empty((V, wide), dtype=torch.bfloat16, device="cuda")
+    h, w, d = big_h[:, :D], [big_w[:, 7 * D:8 * D]], [big_d[:, D:2 * D]]
+    assert (V - 1) * wide * 2 > 1 << 32 and (T - 1) * (1 << 23) * 2 > 1 << 32
+    dloss = torch.full((T,), 1 / T, device="cuda")
+    loss, lse = loss_of(h, w, targets)
+    plain = formula(hidden, weights, targets)
+    near(lse, plain["lse"], "lse")
+    near(loss, plain["loss"], "loss")
+    tps.ar_vocab_loss_grad(h, w, targets, lse, dloss, dhidden=None, dweights=d, ignore_index=IGNORE)
+    want = formula(hidden, weights, targets, dloss, "bf16")
+    near(d[0], want["dweights"][0], "dweights")
+    out = torch.empty_like(big_h)[:, 2 * D:3 * D]
+    tps.ar_vocab_loss_grad(h, w, targets, lse, dloss, dhidden=[out], ignore_index=IGNORE)
+    near(out, want["dhidden"][0], "dhidden")
+
+
+def test_many_pieces_some_empty():
+    hidden, weights, targets = make("bf16", 90, 96, [0, 5, 300, 0, 1, 64, 257, 0, 12, 700, 3, 0, 90, 256, 2, 40], seed=22, ignored=0.2)
+    check_all("bf16", hidden, weights, targets, torch.full((90,), 1 / 90, device="cuda"))
+
+
+@pytest.mark.parametrize("T", [4095, 4097, 20000])
+def test_long_token_lists(T):
+    hidden, weights, targets = make("bf16", T, 64, [200, 60], seed=T, ignored=0.5)
+    check_all("bf16", hidden, weights, targets, torch.full((T,), 1 / T, device="cuda"))
