@@ -1,6 +1,10 @@
 """GB300-native partial-sum reduction (the reduction step of a
 tensor-parallel AllReduce) behind a small C ABI.
 
+Next to the reduction are the training operators around it: dropout joined to
+the sum (``ar_reduce_dropout``) and the loss over a vocabulary split into
+pieces (``ar_vocab_loss``), each with its gradient.
+
 The compute path is ``libtps_ar.so`` (hand-written CUDA for sm_103a);
 ``tensor_partial_sum_gb300.ar`` is a ctypes binding with the same names as
 the C entry points.  The first call fails loudly (RuntimeError) when the
