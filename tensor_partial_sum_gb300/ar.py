@@ -399,6 +399,29 @@ def _i64s(values):
     return kind(*values)
 
 
+_SIZE_ARRAYS = {}
+
+
+def _sizes(values):
+    n = len(values)
+    kind = _SIZE_ARRAYS.get(n)
+    if kind is None:
+        kind = _SIZE_ARRAYS[n] = ctypes.c_size_t * n
+    return kind(*values)
+
+
+_torch_module = None
+
+
+def _torch():
+    """torch, imported with the first call that needs it."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def make_layout(ne0, ne1, src_row_bytes=None, dst_row_bytes=None, residual=None, residual_row_bytes=None,
                 inactive=()) -> ArLayout:
     """An ar_layout.  With a residual, ``residual_row_bytes`` is its row
@@ -507,7 +530,7 @@ def _workspace(need, given, stream, like, call):
         if not given.is_cuda or not given.is_contiguous():
             raise TypeError(f"{call}: the workspace has to be a contiguous device tensor")
         return given, given.numel() * given.element_size()
-    import torch
+    torch = _torch()
     device = like.device if hasattr(like, "device") else "cuda"
     if stream is None:
         return torch.empty(need, dtype=torch.uint8, device=device), need
@@ -576,7 +599,11 @@ def _matrix(x, rows, dim, dtype, name, call):
         raise TypeError(f"{call}: {name} is a {x.device.type} tensor, a device buffer is needed")
     if x.dtype != dtype:
         raise TypeError(f"{call}: {name} is {x.dtype}, the hidden states are {dtype}")
-    if x.dim() != 2 or tuple(x.shape) != (rows, dim) or (dim > 1 and x.stride(1) != 1):
+    if tuple(x.shape) != (rows, dim):
+        raise ValueError(f"{call}: {name} has to be [{rows}, {dim}] with adjacent columns")
+    if x.is_contiguous():
+        return dim * x.element_size()
+    if dim > 1 and x.stride(1) != 1:
         raise ValueError(f"{call}: {name} has to be [{rows}, {dim}] with adjacent columns")
     if rows > 1 and x.stride(0) < dim:  # an expanded tensor, for one; the library takes a stride of 0 for packed rows
         raise ValueError(f"{call}: the rows of {name} lie over one another")
@@ -594,25 +621,26 @@ def make_vocab(hidden, weights, targets, ignore_index=-100, call="make_vocab") -
     """An ar_vocab of torch tensors: ``hidden`` [tokens, dim], one [rows, dim]
     matrix per vocabulary piece in ``weights``, and int64 ``targets``
     [tokens] that count through the pieces in order."""
-    import torch
     if hidden.dim() != 2:
         raise ValueError(f"{call}: hidden has to be [tokens, dim]")
     T, D = hidden.shape
-    if not 1 <= len(weights) <= AR_MAX_RANKS:
-        raise ValueError(f"{call}: {len(weights)} vocabulary pieces, 1 to {AR_MAX_RANKS} are possible")
-    _vector(targets, T, torch.int64, "targets", call)
+    dtype = hidden.dtype
+    n = len(weights)
+    if not 1 <= n <= AR_MAX_RANKS:
+        raise ValueError(f"{call}: {n} vocabulary pieces, 1 to {AR_MAX_RANKS} are possible")
+    _vector(targets, T, _torch().int64, "targets", call)
     v = ArVocab()
     v.rows, v.dim, v.hidden = T, D, hidden.data_ptr()
-    v.hidden_row_bytes = _matrix(hidden, T, D, hidden.dtype, "hidden", call)
-    n = v.n_pieces = len(weights)
-    v.weight_row_bytes = (ctypes.c_int64 * n)(*[_matrix(w, w.shape[0], D, hidden.dtype, f"weights[{r}]", call)
-                                                for r, w in enumerate(weights)])
-    v.piece_rows = (ctypes.c_size_t * n)(*[w.shape[0] for w in weights])
-    v._pointers = _ptrs(weights)
+    v.hidden_row_bytes = _matrix(hidden, T, D, dtype, "hidden", call)
+    v.n_pieces = n
+    rows = [w.shape[0] for w in weights]
+    v.weight_row_bytes = _i64s([_matrix(w, m, D, dtype, "a piece of weights", call) for w, m in zip(weights, rows)])
+    v.piece_rows = _sizes(rows)
+    v._pointers = _packed([w.data_ptr() for w in weights])
     v.weights = v._pointers
     v.targets, v.ignore_index = targets.data_ptr(), ignore_index
-    v.dtype = _dtype_code(hidden.dtype)
-    v._keep = (hidden, list(weights), targets)
+    v.dtype = _dtype_code(dtype)
+    v._keep = (hidden, weights, targets)
     return v
 
 
@@ -633,11 +661,11 @@ def ar_vocab_loss(hidden, weights, targets, loss, lse, ignore_index=-100, worksp
     the ``weights`` pieces, without keeping the logits: float32 ``loss`` and
     ``lse`` (log-sum-exp) of each token.  ``workspace`` defaults to one from
     torch's allocator."""
-    import torch
     call = "ar_vocab_loss"
     v = make_vocab(hidden, weights, targets, ignore_index, call)
-    _vector(loss, v.rows, torch.float32, "loss", call)
-    _vector(lse, v.rows, torch.float32, "lse", call)
+    f32, T = _torch().float32, v.rows
+    _vector(loss, T, f32, "loss", call)
+    _vector(lse, T, f32, "lse", call)
     ws, ws_bytes = _workspace(ar_vocab_workspace(v, False), workspace, stream, hidden, call)
     _check(lib().ar_vocab_loss(ctypes.byref(v), loss.data_ptr(), lse.data_ptr(), _ptr(ws), ws_bytes, _stream(stream)),
            call)
@@ -649,18 +677,16 @@ def ar_vocab_loss_grad(hidden, weights, targets, lse, dloss, dhidden=None, dweig
     states per piece into ``dhidden`` (ar_reduce sums them), each piece's
     weight gradient into ``dweights``; either may be None.  ``lse`` is
     ar_vocab_loss's, ``dloss`` the float32 gradient of each token's loss."""
-    import torch
     call = "ar_vocab_loss_grad"
     v = make_vocab(hidden, weights, targets, ignore_index, call)
-    _vector(lse, v.rows, torch.float32, "lse", call)
-    _vector(dloss, v.rows, torch.float32, "dloss", call)
-    n = v.n_pieces
+    f32, T, D, n, dtype = _torch().float32, v.rows, v.dim, v.n_pieces, hidden.dtype
+    _vector(lse, T, f32, "lse", call)
+    _vector(dloss, T, f32, "dloss", call)
     strides = []
-    for name, xs, rows in (("dhidden", dhidden, [v.rows] * n), ("dweights", dweights, [w.shape[0] for w in weights])):
+    for name, xs, rows in (("dhidden", dhidden, [T] * n), ("dweights", dweights, [w.shape[0] for w in weights])):
         if xs is not None and len(xs) != n:
             raise ValueError(f"{call}: {len(xs)} tensors in {name}, {n} vocabulary pieces")
-        strides.append(None if xs is None else (ctypes.c_int64 * n)(
-            *[_matrix(x, m, v.dim, hidden.dtype, f"{name}[{r}]", call) for r, (x, m) in enumerate(zip(xs, rows))]))
+        strides.append(None if xs is None else _i64s([_matrix(x, m, D, dtype, name, call) for x, m in zip(xs, rows)]))
     ws, ws_bytes = _workspace(ar_vocab_workspace(v, True), workspace, stream, hidden, call)
     _check(lib().ar_vocab_loss_grad(ctypes.byref(v), lse.data_ptr(), dloss.data_ptr(), _ptrs(dhidden), strides[0],
                                     _ptrs(dweights), strides[1], _ptr(ws), ws_bytes, _stream(stream)), call)

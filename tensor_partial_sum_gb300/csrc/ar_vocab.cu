@@ -340,12 +340,15 @@ struct Call {
         p.dst_at[m] = static_cast<long long>(at);
     }
     int launch_pack(const tps::VocabPackParams &p, int n) const {
-        int rows = 64, most = c.sm_count * 16 / n;
+        // a thread for each eight elements of a row, as far as 256 go: idle ones cost bytes in flight
+        const size_t groups = ld / 8, threads = groups < 256 ? round_up(groups, 32) : 256;
+        int rows = 64, most = c.sm_count * static_cast<int>(4096 / threads) / n;
         for (int m = 0; m < n; ++m) rows = p.rows[m] > rows ? p.rows[m] : rows;
         return launch(by_type<tps::VocabPackParams>(v->dtype, tps::ar_vocab_pack_kernel<tps::kF32>,
                                                     tps::ar_vocab_pack_kernel<tps::kF16>,
                                                     tps::ar_vocab_pack_kernel<tps::kBF16>),
-                      dim3(static_cast<unsigned>(rows < most ? rows : most), static_cast<unsigned>(n)), 256u, 0, p);
+                      dim3(static_cast<unsigned>(rows < most ? rows : most), static_cast<unsigned>(n)),
+                      static_cast<unsigned>(threads), 0, p);
     }
 
     // The weights of a group: packed at `area` (room for `cap` rows) where they have to be; per segment
