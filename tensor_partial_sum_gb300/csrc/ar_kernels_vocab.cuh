@@ -11,6 +11,11 @@
 //   kDlogits turns a tile of recomputed logits into a tile of D, held in
 //            16 bits for one chunk of the vocabulary;
 //   kGrads   stores tiles of dH and dW.
+// With 64 tokens or fewer, kStatsFew and kDlogitsFew do the first two the
+// other way round, z^T = W H^T: the tensor cores' time goes by the narrow
+// side, so tiles of vocabulary rows by a few tokens cost next to nothing and
+// reading W is what is left (4 tokens of 5136 elements, six pieces of 1640 rows:
+// an eager call 49 -> 40 us; 3 float tokens of 7232, 19671 rows: 489 -> 398).
 // Small kernels around it list the counted tokens, pack rows that the tiled
 // copies cannot read in place, and join partial results.
 //
@@ -24,7 +29,10 @@
 
 namespace tps {
 
-enum VocabMode { kStats = 0, kDlogits = 1, kGrads = 2 };
+enum VocabMode { kStats = 0, kDlogits = 1, kGrads = 2, kStatsFew = 3, kDlogitsFew = 4 };
+template <int MODE>
+constexpr bool kVFew = MODE == kStatsFew || MODE == kDlogitsFew;
+constexpr int kFewTokens = 64;
 
 constexpr int kMaxSegs = 16;
 constexpr int kVM = 256;      // rows of a tile, 128 in each CTA
@@ -40,11 +48,13 @@ constexpr int kVThreads = 128 + 32 * kVEpilogueWarps;
 // (the statistics, and everything of float32 inputs) a run of products is kept short - 32 or 48 of them -
 // and the runs are added in registers, rounded to nearest.
 template <int MODE, int T>
-constexpr bool kVRuns = MODE == kStats || T == kF32;
+constexpr bool kVRuns = MODE == kStats || MODE == kStatsFew || T == kF32;
 template <int T>
 constexpr int kVRunBlocks = T == kF32 ? 2 : 8;  // blocks of K in a run
 // Registers of the feeding and of the result warps when a thread adds up 128 columns; the launch's
 // kVLaunchRegs for each of 384 threads cover them.
+template <int MODE, int T>
+constexpr bool kVSplitRegs = kVRuns<MODE, T> && !kVFew<MODE>;
 constexpr int kVFeedRegs = 80, kVSumRegs = 208, kVLaunchRegs = 168;
 static_assert(128 * kVFeedRegs + 32 * kVEpilogueWarps * kVSumRegs <= kVThreads * kVLaunchRegs, "register split");
 constexpr unsigned kVTmemCols = 512;        // two accumulators of 256 columns
@@ -94,6 +104,8 @@ struct VocabGemmParams {
     // and what a tile holds there goes into results that nobody reads.
     int a_rows, a_tail;
     int a_room;               // rows of A that a stage has room for
+    int few_rows;             // kStatsFew, kDlogitsFew: vocabulary rows of a tile in each CTA (b_map's boxes;
+                              // b_tail's: the rows left over), and a_map has boxes of bn / 2 tokens
     int stages;               // of a_room + bn / 2 rows each
     int tiles;                // column tiles (kStats, kDlogits) or dW tiles (kGrads) of all segments
     const VocabList *list;    // nullptr: all tokens, in order (kStats)
@@ -184,6 +196,14 @@ struct VocabWalk {
         t.seg = 0;
         if constexpr (MODE != kGrads) {
             const long long id = pair + static_cast<long long>(i++) * npairs;
+            if constexpr (kVFew<MODE>) {  // tiles of vocabulary rows by all tokens
+                if (mt == 0 || id >= p.tiles) return false;
+                while (t.seg + 1 < p.nseg && p.seg[t.seg + 1].tile0 <= id) ++t.seg;
+                t.m = static_cast<int>(id) - p.seg[t.seg].tile0;
+                t.n = 0;
+                t.kn = kn;
+                return true;
+            }
             if (mt == 0 || id >= static_cast<long long>(p.tiles) * mt) return false;
             const int j = id <= 0x7FFFFFFF ? static_cast<int>(id) / mt : static_cast<int>(id / mt);
             t.m = static_cast<int>(id - static_cast<long long>(j) * mt);
@@ -292,6 +312,19 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t (&w)[3]) {
     }
 }
 
+// Combine 32 columns over the warp's lanes: lane k's x[0] becomes column k's result (31 exchanges
+// where a reduction of each column would take 160).
+template <int O = 16, typename Op>
+__device__ __forceinline__ void fold_columns(float (&x)[32], int lane, Op op) {
+    const bool high = lane & O;
+#pragma unroll
+    for (int k = 0; k < O; ++k) {
+        const float give = high ? x[k] : x[k + O], keep = high ? x[k + O] : x[k];
+        x[k] = op(keep, __shfl_xor_sync(~0u, give, O));
+    }
+    if constexpr (O > 1) fold_columns<O / 2>(x, lane, op);
+}
+
 // ---- the product kernel ---------------------------------------------------------
 //
 // Warps: 0 copies tiles in, 1 issues the products (in the leader), 2 owns the
@@ -348,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
 
     if (warp < 4) {
         // the whole warpgroup gives registers up, in the branch that holds its roles' code
-        if constexpr (kVRuns<MODE, T>) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kVFeedRegs));
+        if constexpr (kVSplitRegs<MODE, T>) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kVFeedRegs));
         if (warp == 0) {
             // ---- copies: this CTA's half of each operand ----
             const unsigned lead_full = leader_addr(full);
@@ -376,11 +409,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 auto b_part = [&](int col) {  // MN-major: chunks of 64 columns, none of them all outside
                     return t.bn == kVN && col + 64 < p.dim ? 128 : col < p.dim ? 64 : 0;
                 };
-                const int a_mine = a_mn ? 128 : a_part(arow), b_mine = b_mn ? b_part(brow) : t.bn / 2;
-                const int a_both = a_mn ? 256 : a_part(row0) + a_part(row0 + 128);
-                const int b_both = b_mn ? b_part(t.n * p.bn) + b_part(t.n * p.bn + t.bn / 2) : t.bn;
+                int a_mine = a_mn ? 128 : a_part(arow), b_mine = b_mn ? b_part(brow) : t.bn / 2;
+                int a_both = a_mn ? 256 : a_part(row0) + a_part(row0 + 128);
+                int b_both = b_mn ? b_part(t.n * p.bn) + b_part(t.n * p.bn + t.bn / 2) : t.bn;
                 if (!a_mn && a_mine < 128) am = &p.a_tail_map;
                 if (!b_mn && t.bn < p.bn) bm = &p.b_tail[t.seg];
+                if constexpr (kVFew<MODE>) {  // A: vocabulary rows, B: tokens
+                    const int mh = p.few_rows, rows = p.seg[t.seg].rows, w0 = 2 * t.m * mh;
+                    auto part = [&](int row) { return row + mh <= rows ? mh : row < rows ? (rows % mh + 7) / 8 * 8 : 0; };
+                    ay = w0 + static_cast<int>(rank) * mh, by = static_cast<int>(rank) * (p.bn / 2);
+                    a_mine = part(ay), a_both = part(w0) + part(w0 + mh);
+                    b_mine = by < p.a_rows ? p.bn / 2 : 0, b_both = p.bn / 2 < p.a_rows ? p.bn : p.bn / 2;
+                    am = ay + mh <= rows ? &p.b_map[t.seg] : &p.b_tail[t.seg];
+                    bm = &p.a_map;
+                }
                 const unsigned bytes = static_cast<unsigned>(a_both + b_both) * kVRow * kVParts<T>;
                 int k = t.k0 * kVK;
                 for (int n = t.kn; n > 0; --n, k += kVK) {
@@ -404,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                                 tma_load_3d(a + 8192, am, bar, ax + 64, ay + k, q);
                             }
                             if (!b_mn) {
-                                tma_load_3d(b, bm, bar, bx + k, by, q);
+                                if (b_mine) tma_load_3d(b, bm, bar, bx + k, by, q);
                             } else {
                                 if (b_mine) tma_load_3d(b, bm, bar, bx, by + k, q);
                                 if (b_mine > 64) tma_load_3d(b + 8192, bm, bar, bx + 64, by + k, q);
@@ -484,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
             }
         }
     } else {
-        if constexpr (kVRuns<MODE, T>) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kVSumRegs));
+        if constexpr (kVSplitRegs<MODE, T>) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kVSumRegs));
         // ---- results: a warp reads the 32 lanes of its quarter and half of the columns ----
         const int quarter = warp % 4, half = (warp - 4) / 4;
         unsigned char *stage_out = raw + (base - smem_u32(raw)) + kVRing + (warp - 4) * 32 * kVPitch;
@@ -493,13 +535,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
         const float unscale = MODE == kGrads && p.list ? p.list->unscale : 1.0f;
         bool ok = true;
         for (VocabWalk<MODE> walk(p, live, pair, npairs); ok && walk.next(t);) {
-            const int r = t.m * kVM + static_cast<int>(rank) * 128 + quarter * 32 + lane;  // row of the product
-            const int c0 = half * (t.bn / 2);                                             // first column in the tile
-            const int width = t.bn / 2;
             const VocabSeg &seg = p.seg[t.seg];
+            // row of the product, first column in the tile and number of columns
+            const int in_cta = quarter * 32 + lane;
+            const int r = kVFew<MODE> ? (2 * t.m + static_cast<int>(rank)) * p.few_rows + in_cta
+                                      : t.m * kVM + static_cast<int>(rank) * 128 + in_cta;
+            const int c0 = half * (kVFew<MODE> ? 32 : t.bn / 2);
+            const int width = kVFew<MODE> ? min(32, t.bn - c0) : t.bn / 2;
             // rows past the end cost nothing (D's are read, as zeros, up to a whole block of K)
             const int rows = MODE == kDlogits ? (live + kVK - 1) / kVK * kVK : MODE == kGrads && t.dw ? seg.rows : live;
-            const bool idle = r - lane >= rows;
+            const bool idle = kVFew<MODE> ? quarter * 32 >= p.few_rows || (MODE == kStatsFew && c0 >= live) : r - lane >= rows;
             long long y = -1;
             float lse = 0.0f, g = 0.0f;
             if constexpr (MODE == kStats) {
@@ -508,6 +553,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 if (r < live) {
                     const VocabRow q = p.row[r];
                     y = q.y, lse = q.lse, g = q.g;
+                }
+            } else if constexpr (kVFew<MODE>) {  // lane k: token c0 + k
+                if (c0 + lane < live) {
+                    if constexpr (MODE == kStatsFew) {
+                        y = p.targets[c0 + lane];
+                    } else {
+                        const VocabRow q = p.row[c0 + lane];
+                        y = q.y, lse = q.lse, g = q.g;
+                    }
                 }
             }
             unsigned src = 0;  // the tile's accumulator in tensor memory
@@ -527,16 +581,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 if (lane == 0) mbar_arrive_cluster(leader_addr(tempty + 8 * (acc_it % 2)));
                 ++acc_it;
             };
-            float sums[kVRuns<MODE, T> ? 128 : 1];
+            constexpr int kCols = kVFew<MODE> ? 32 : 128;  // of a thread
+            float sums[kVRuns<MODE, T> ? kCols : 1];
             if constexpr (kVRuns<MODE, T>) {
 #pragma unroll
-                for (int k = 0; k < 128; ++k) sums[k] = 0.0f;
+                for (int k = 0; k < kCols; ++k) sums[k] = 0.0f;
                 for (int q = 0, runs = vocab_runs<MODE, T>(t); q < runs; ++q) {
                     next_run();
                     if (!ok) break;
                     if (t.kn && !idle) {
 #pragma unroll
-                        for (int c = 0; c < 128; c += 32)
+                        for (int c = 0; c < kCols; c += 32)
                             if (c < width) tmem_add32(src + c, sums + c);
                     }
                     done_run();
@@ -553,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 if constexpr (kVRuns<MODE, T>) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = sums[c + k];
-                } else if (t.kn) {
+                } else if (t.kn && width > 0) {
                     tmem_load32(src + c, v);
                 } else {  // nothing to sum over
 #pragma unroll
@@ -623,6 +678,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                         }
                     }
                 }
+            } else if constexpr (MODE == kStatsFew) {
+                // lane: vocabulary row r, v[k]: token c0 + k.  The maxima of the 32 columns over the 32 lanes by
+                // halving: each step gives away half of the columns, until lane k holds column k's.
+                const bool exists = in_cta < p.few_rows && r < seg.rows;
+                float v[32], top[32];
+                values(0, v);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) top[k] = exists ? v[k] : -INFINITY;
+                fold_columns(top, lane, [](float a, float b) { return fmaxf(a, b); });
+                float m = top[0], add[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float mk = __shfl_sync(~0u, m, k), ref = fabsf(mk) == INFINITY ? 0.0f : mk;
+                    add[k] = exists ? __expf(v[k] - ref) : 0.0f;
+                }
+                fold_columns(add, lane, [](float a, float b) { return a + b; });
+                const int token = c0 + lane;
+                // the target's logit: lane `at` of this warp holds it in v[lane]
+                const long long at = y - seg.first - (r - lane);
+                const bool here = token < live && at >= 0 && at < 32 && r - lane + at < seg.rows && quarter * 32 + at < p.few_rows;
+                if (__any_sync(~0u, here)) {
+                    float z = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float got = __shfl_sync(~0u, v[k], __shfl_sync(~0u, static_cast<int>(at) & 31, k));
+                        if (lane == k) z = got;
+                    }
+                    if (here) p.picked[token] = z;
+                }
+                const int quarters = (p.few_rows + 31) / 32;
+                if (token < live)
+                    p.part[(static_cast<long long>(2 * (seg.tile0 + t.m) + static_cast<int>(rank)) * quarters + quarter) * p.rows + token] =
+                        make_float2(m, add[0]);
+            } else if constexpr (MODE == kDlogitsFew) {
+                float v[32];
+                values(0, v);
+                const long long at = y - seg.first - (r - lane);
+                const int mine_at = at >= 0 && at < 32 ? static_cast<int>(at) : -1;
+                // D[token][r]: adjacent lanes adjacent columns; zeros up to whole blocks of K either way
+                const bool store = in_cta < p.few_rows && r < (seg.rows + kVK - 1) / kVK * kVK;
+                unsigned short *out = p.d + seg.col0 + r + static_cast<long long>(c0) * p.d_ld;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float l = __shfl_sync(~0u, lse, k), f = __shfl_sync(~0u, g, k);
+                    const int a = __shfl_sync(~0u, mine_at, k);
+                    const float q = __expf(v[k] - l) - (a == lane ? 1.0f : 0.0f);
+                    const float d = c0 + k < live && r < seg.rows ? q * f : 0.0f;
+                    if constexpr (T != kF32) {
+                        if (store) store_elem<T>(out, k * p.d_ld, d);
+                    } else {
+                        uint32_t w[3];
+                        split2(d, 0.0f, w);
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+                            if (store) out[part * p.d_part + k * p.d_ld] = static_cast<unsigned short>(w[part] & 0xFFFFu);
+                    }
+                }
             } else {
                 const int col = t.n * p.bn + c0;
                 const int n = min(width, p.dim - col);
@@ -662,7 +774,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
             }
             if constexpr (!kVRuns<MODE, T>) done_run();
         }
-        if constexpr (MODE == kDlogits) asm volatile("fence.proxy.async.global;" ::: "memory");
+        if constexpr (MODE == kDlogits || MODE == kDlogitsFew) asm volatile("fence.proxy.async.global;" ::: "memory");
     }
     __syncthreads();
     __syncwarp();

@@ -170,6 +170,20 @@ int stats_width(const ar_vocab *v, int pairs) {
     return bn;
 }
 
+// Few tokens: vocabulary rows of a tile in each CTA, a multiple of `step`, so that the rounds of one tile a pair are
+// cheapest (a round costs its rows and some 24 more).
+int few_rows(const ar_vocab *v, int pairs, int step) {
+    size_t best = SIZE_MAX;
+    int rows = 128;
+    for (int n = 128; n >= 32; n -= step) {
+        size_t tiles = 0;
+        for (int r = 0; r < v->n_pieces; ++r) tiles += tiles_of(v->piece_rows[r], static_cast<size_t>(2 * n));
+        const size_t cost = tiles_of(tiles, static_cast<size_t>(pairs)) * static_cast<size_t>(2 * n + 24);
+        if (cost < best) best = cost, rows = n;
+    }
+    return rows;
+}
+
 struct LossPlan {
     size_t cap;  // vocabulary rows of a group
     size_t part, picked, hidden, weights, bytes;
@@ -183,6 +197,10 @@ LossPlan plan_loss(const ar_vocab *v) {
     const size_t narrow = v->rows > tps::kVM ? tps::kVN : tps::kVN / 2;
     size_t tiles = 0;
     for (int r = 0; r < v->n_pieces; ++r) tiles += tiles_of(v->piece_rows[r], narrow);
+    if (v->rows <= tps::kFewTokens) {  // one for each 32 vocabulary rows; few_rows may leave 24 of 32 unused
+        tiles = 0;
+        for (int r = 0; r < v->n_pieces; ++r) tiles += 4 * tiles_of(v->piece_rows[r], 64);
+    }
     p.part = c.take(2 * tiles * v->rows * sizeof(float2));
     p.picked = c.take(v->rows * sizeof(float));
     p.hidden = c.take(hidden_in_place(v) ? 0 : v->rows * row);
@@ -292,6 +310,18 @@ bool make_map(CUtensorMap *m, bool f16, const void *base, size_t cols, size_t ro
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Few tokens: the map of the hidden states, in boxes of half the tokens (rounded up to 16), and the rows left over of
+// a segment's last tile.
+bool make_few_map(tps::VocabGemmParams &p, bool f16, const void *base, size_t cols, size_t rows, size_t parts, size_t ld,
+                  size_t part) {
+    p.a_rows = static_cast<int>(rows);
+    return make_map(&p.a_map, f16, base, cols, rows, parts, ld, part, static_cast<unsigned>(p.bn / 2));
+}
+unsigned few_tail(size_t rows, int few) {
+    const size_t left = rows % static_cast<size_t>(few);
+    return static_cast<unsigned>(left ? round_up(left, 8) : 8);
+}
+
 // Rows of the boxes of a segment's last column tile: half its width.
 template <int MODE>
 unsigned tail_box(size_t rows, int bn) {
@@ -378,7 +408,8 @@ struct Call {
     // in flight.  (dW's A is a full tile of vocabulary rows.)
     template <int MODE>
     int launch_gemm(tps::VocabGemmParams &p, size_t tiles) const {
-        p.a_room = p.a_rows >= 128 || (MODE == tps::kGrads && p.tiles) ? 128 : p.a_tail;
+        if (tps::kVFew<MODE>) p.a_room = p.few_rows;
+        else p.a_room = p.a_rows >= 128 || (MODE == tps::kGrads && p.tiles) ? 128 : p.a_tail;
         // a product reads 128 rows of A wherever the stage starts: the last stage's have to lie in the ring
         const int a = static_cast<int>(parts) * p.a_room * tps::kVRow, b = static_cast<int>(parts) * p.bn / 2 * tps::kVRow;
         // (the last part of A: 128 rows from (parts - 1) a_room rows on)
@@ -394,7 +425,7 @@ struct Call {
             cudaGetLastError();
             return AR_ERR_CUDA;
         }
-        if (MODE == tps::kStats || v->dtype == AR_F32) {
+        if (!tps::kVFew<MODE> && (MODE == tps::kStats || v->dtype == AR_F32)) {
             // result warps take registers that the feeding warps give up; a launch that was given fewer
             // than the split adds up to would wait for them for ever
             cudaFuncAttributes a;
@@ -484,12 +515,18 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
     memset(&p, 0, sizeof p);
     p.rows = static_cast<int>(T);
     p.dim = static_cast<int>(D);
-    p.bn = stats_width(v, c.sm_count / 2);
+    const bool few = T <= tps::kFewTokens;
+    p.bn = few ? static_cast<int>(round_up(T, 16)) : stats_width(v, c.sm_count / 2);
+    p.few_rows = few ? few_rows(v, c.sm_count / 2, 8) : 0;
     p.targets = reinterpret_cast<const long long *>(v->targets);
     p.part = reinterpret_cast<float2 *>(call.ws + plan.part);
     p.picked = reinterpret_cast<float *>(call.ws + plan.picked);
     p.status = c.dev_status;
-    if (!make_a_maps(p, call.f16, h.base, h.cols, h.rows, call.parts, h.ld, h.part)) return AR_ERR_CUDA;
+    if (!(few ? make_few_map(p, call.f16, h.base, h.cols, h.rows, call.parts, h.ld, h.part)
+              : make_a_maps(p, call.f16, h.base, h.cols, h.rows, call.parts, h.ld, h.part)))
+        return AR_ERR_CUDA;
+    const int tile = few ? 2 * p.few_rows : p.bn;                   // vocabulary rows of a tile
+    const int per_tile = few ? 2 * ((p.few_rows + 31) / 32) : 2;  // statistics it leaves for a token
     long long first[AR_MAX_RANKS], total = 0;
     for (int r = 0; r < v->n_pieces; ++r) first[r] = total, total += static_cast<long long>(v->piece_rows[r]);
     int piece = 0, done = 0;  // column tiles of earlier groups
@@ -505,16 +542,17 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
             p.seg[s].first = first[g.piece[s]] + static_cast<long long>(g.row0[s]);
             p.seg[s].rows = static_cast<int>(g.rows[s]);
             p.seg[s].tile0 = p.tiles;
-            p.tiles += static_cast<int>(tiles_of(g.rows[s], static_cast<size_t>(p.bn)));
+            p.tiles += static_cast<int>(tiles_of(g.rows[s], static_cast<size_t>(tile)));
+            const unsigned tail = few ? few_tail(g.rows[s], p.few_rows) : tail_box<tps::kStats>(g.rows[s], p.bn);
             if (!make_map(&p.b_map[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part,
-                          static_cast<unsigned>(p.bn / 2)) ||
-                !make_map(&p.b_tail[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part,
-                          tail_box<tps::kStats>(g.rows[s], p.bn)))
+                          static_cast<unsigned>(tile / 2)) ||
+                !make_map(&p.b_tail[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part, tail))
                 return AR_ERR_CUDA;
         }
-        st = call.launch_gemm<tps::kStats>(p, static_cast<size_t>(p.tiles) * tiles_of(T, tps::kVM));
+        st = few ? call.launch_gemm<tps::kStatsFew>(p, static_cast<size_t>(p.tiles))
+                 : call.launch_gemm<tps::kStats>(p, static_cast<size_t>(p.tiles) * tiles_of(T, tps::kVM));
         if (st != AR_OK) return st;
-        p.part += 2ll * p.tiles * static_cast<long long>(T);
+        p.part += static_cast<long long>(per_tile) * p.tiles * static_cast<long long>(T);
         done += p.tiles;
     }
     tps::VocabJoinParams j;
@@ -525,7 +563,7 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
     j.ignore = v->ignore_index;
     j.vocab = total;
     j.rows = p.rows;
-    j.parts = 2 * done;
+    j.parts = per_tile * done;
     j.loss = loss;
     j.lse = lse;
     return call.launch<tps::VocabJoinParams>(tps::ar_vocab_join_kernel, dim3(static_cast<unsigned>((T + 3) / 4)), 256u, 0, j);
@@ -622,6 +660,7 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
     p.d = reinterpret_cast<unsigned short *>(call.ws + plan.d);
     p.status = c.dev_status;
     const size_t mt = plan.d_rows / tps::kVM;
+    const bool few = T <= tps::kFewTokens;
     if (!make_map(&p.ht_map, call.f16, call.ws + plan.hidden, call.ld, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld, 64))
         return AR_ERR_CUDA;
     long long first[AR_MAX_RANKS], total = 0;
@@ -637,22 +676,29 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
         p.d_ld = static_cast<long long>(g.padded);
         p.d_part = p.d_ld * static_cast<long long>(plan.d_rows);
         p.nseg = g.nseg;
-        p.bn = tps::kVN;
+        p.bn = few ? static_cast<int>(round_up(T, 16)) : static_cast<int>(tps::kVN);
+        p.few_rows = few ? few_rows(v, c.sm_count / 2, 32) : 0;  // whole blocks of K: D's columns are zeroed to there
+        const int tile = few ? 2 * p.few_rows : p.bn;
         p.tiles = 0;
-        if (!make_a_maps(p, call.f16, call.ws + plan.hidden, call.ld, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld))
+        if (!(few ? make_few_map(p, call.f16, call.ws + plan.hidden, call.ld, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld)
+                  : make_a_maps(p, call.f16, call.ws + plan.hidden, call.ld, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld)))
             return AR_ERR_CUDA;
+        long long col = 0;
         for (int s = 0; s < g.nseg; ++s) {
             p.seg[s].first = first[g.piece[s]] + static_cast<long long>(g.row0[s]);
             p.seg[s].rows = static_cast<int>(g.rows[s]);
             p.seg[s].tile0 = p.tiles;
-            p.seg[s].col0 = static_cast<long long>(p.tiles) * tps::kVN;
-            p.tiles += static_cast<int>(tiles_of(g.rows[s], tps::kVN));
-            if (!make_map(&p.b_map[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part, tps::kVN / 2) ||
-                !make_map(&p.b_tail[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part,
-                          tail_box<tps::kDlogits>(g.rows[s], p.bn)))
+            p.seg[s].col0 = col;
+            col += static_cast<long long>(round_up(g.rows[s], tps::kVN));
+            p.tiles += static_cast<int>(tiles_of(g.rows[s], static_cast<size_t>(tile)));
+            const unsigned tail = few ? few_tail(g.rows[s], p.few_rows) : tail_box<tps::kDlogits>(g.rows[s], p.bn);
+            if (!make_map(&p.b_map[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part,
+                          static_cast<unsigned>(tile / 2)) ||
+                !make_map(&p.b_tail[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part, tail))
                 return AR_ERR_CUDA;
         }
-        st = call.launch_gemm<tps::kDlogits>(p, static_cast<size_t>(p.tiles) * mt);
+        st = few ? call.launch_gemm<tps::kDlogitsFew>(p, static_cast<size_t>(p.tiles))
+                 : call.launch_gemm<tps::kDlogits>(p, static_cast<size_t>(p.tiles) * mt);
         if (st != AR_OK) return st;
         // dH and dW from it
         const size_t parts = call.parts, dl = static_cast<size_t>(p.d_ld), dp = static_cast<size_t>(p.d_part);
