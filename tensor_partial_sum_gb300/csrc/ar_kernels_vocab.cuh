@@ -807,9 +807,10 @@ __device__ __forceinline__ void join_stats(float &m, float &s, float qm, float q
 }
 
 // Join the partial statistics of each row: lse = log sum exp, loss = lse - target's logit.  A block
-// takes 4 rows, 64 threads to a row, so that a single row's hundreds of parts are loaded at once.
-static __global__ void __launch_bounds__(256) ar_vocab_join_kernel(const __grid_constant__ VocabJoinParams p) {
-    constexpr int R = 4;
+// takes R rows (4, or one of few tokens), 256 / R threads to a row, so that a single row's hundreds of
+// parts are loaded at once.
+template <int R>
+__global__ void __launch_bounds__(256) ar_vocab_join_kernel(const __grid_constant__ VocabJoinParams p) {
     __shared__ float ms[8][R], ss[8][R];
     pdl_launch_dependents();
     pdl_wait();

@@ -566,7 +566,9 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
     j.parts = per_tile * done;
     j.loss = loss;
     j.lse = lse;
-    return call.launch<tps::VocabJoinParams>(tps::ar_vocab_join_kernel, dim3(static_cast<unsigned>((T + 3) / 4)), 256u, 0, j);
+    return few ? call.launch<tps::VocabJoinParams>(tps::ar_vocab_join_kernel<1>, dim3(static_cast<unsigned>(T)), 256u, 0, j)
+               : call.launch<tps::VocabJoinParams>(tps::ar_vocab_join_kernel<4>, dim3(static_cast<unsigned>((T + 3) / 4)),
+                                                   256u, 0, j);
 }
 
 int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, void *const *dhidden,
