@@ -51,6 +51,11 @@ template <int MODE, int T>
 constexpr bool kVRuns = MODE == kStats || MODE == kStatsFew || T == kF32;
 template <int T>
 constexpr int kVRunBlocks = T == kF32 ? 2 : 8;  // blocks of K in a run
+// Blocks of K in a stage.  A round of the ring - wait, copies, products, commit - takes the feeding warps about 400
+// cycles, more than the products of narrow tiles: those share one between two blocks (three parts fill a
+// stage by themselves).
+template <int MODE, int T>
+constexpr int kVBlocks = kVFew<MODE> && T != kF32 ? 2 : 1;
 // Registers of the feeding and of the result warps when a thread adds up 128 columns; the launch's
 // kVLaunchRegs for each of 384 threads cover them.
 template <int MODE, int T>
@@ -369,9 +374,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
     asm volatile("fence.proxy.async.global;" ::: "memory");  // its plain stores, before this one's copies
     const int live = p.list ? p.list->live : p.rows;
     const unsigned S = static_cast<unsigned>(p.stages);
-    // a stage: the parts of A, then the parts of B
+    // a block of K: the parts of A, then the parts of B
     const unsigned a_size = static_cast<unsigned>(p.a_room) * kVRow, b_size = static_cast<unsigned>(p.bn / 2) * kVRow;
-    const unsigned b_at = kVParts<T> * a_size, stage = b_at + kVParts<T> * b_size;
+    const unsigned b_at = kVParts<T> * a_size, block = b_at + kVParts<T> * b_size, stage = kVBlocks<MODE, T> * block;
 
     const volatile unsigned never = 0;  // for waits that follow giving up
     auto give_up = [&] {
@@ -425,7 +430,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 }
                 const unsigned bytes = static_cast<unsigned>(a_both + b_both) * kVRow * kVParts<T>;
                 int k = t.k0 * kVK;
-                for (int n = t.kn; n > 0; --n, k += kVK) {
+                constexpr int U = kVBlocks<MODE, T>;
+                for (int n = t.kn; n > 0; n -= U, k += U * kVK) {
                     if (round && !__all_sync(~0u, mbar_wait_bounded(empty + 8 * s, (round - 1) & 1, abort_flag))) {
                         give_up();
                         ok = false;
@@ -434,22 +440,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                     if (elect_one()) {
                         const unsigned bar = lead_full + 8 * s;
                         if (rank == 0)
-                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + 8 * s), "r"(bytes)
+                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + 8 * s),
+                                         "r"(min(n, U) * bytes)
                                          : "memory");
-    #pragma unroll
-                        for (int q = 0; q < kVParts<T>; ++q) {
-                            const unsigned a = base + s * stage + q * a_size, b = base + s * stage + b_at + q * b_size;
-                            if (!a_mn) {
-                                if (a_mine) tma_load_3d(a, am, bar, ax + k, ay, q);
-                            } else {  // two chunks of 64 columns, 64 rows each
-                                tma_load_3d(a, am, bar, ax, ay + k, q);
-                                tma_load_3d(a + 8192, am, bar, ax + 64, ay + k, q);
-                            }
-                            if (!b_mn) {
-                                if (b_mine) tma_load_3d(b, bm, bar, bx + k, by, q);
-                            } else {
-                                if (b_mine) tma_load_3d(b, bm, bar, bx, by + k, q);
-                                if (b_mine > 64) tma_load_3d(b + 8192, bm, bar, bx + 64, by + k, q);
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            if (u >= n) break;
+                            const int ku = k + u * kVK;
+#pragma unroll
+                            for (int q = 0; q < kVParts<T>; ++q) {
+                                const unsigned a = base + s * stage + u * block + q * a_size;
+                                const unsigned b = base + s * stage + u * block + b_at + q * b_size;
+                                if (!a_mn) {
+                                    if (a_mine) tma_load_3d(a, am, bar, ax + ku, ay, q);
+                                } else {  // two chunks of 64 columns, 64 rows each
+                                    tma_load_3d(a, am, bar, ax, ay + ku, q);
+                                    tma_load_3d(a + 8192, am, bar, ax + 64, ay + ku, q);
+                                }
+                                if (!b_mn) {
+                                    if (b_mine) tma_load_3d(b, bm, bar, bx + ku, by, q);
+                                } else {
+                                    if (b_mine) tma_load_3d(b, bm, bar, bx, by + ku, q);
+                                    if (b_mine > 64) tma_load_3d(b + 8192, bm, bar, bx + 64, by + ku, q);
+                                }
                             }
                         }
                     }
@@ -491,22 +504,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                         bool more = false;  // the first product of a run starts the accumulator
                         int n = t.kn;
                         if constexpr (kVRuns<MODE, T>) n = min(kVRunBlocks<T>, t.kn - r * kVRunBlocks<T>);
-                        for (; n > 0; --n) {
+                        for (; n > 0; n -= kVBlocks<MODE, T>) {
                             if (!__all_sync(~0u, mbar_wait_bounded(full + 8 * s, phase, abort_flag))) {
                                 give_up();
                                 ok = false;
                                 break;
                             }
                             tmem_fence_after();
-                            const uint64_t a0 = desc0 + ((s * stage) >> 4), b0 = a0 + (b_at >> 4);
+                            const uint64_t stage0 = desc0 + ((s * stage) >> 4);
                             if (elect_one()) {
-    #pragma unroll
-                                for (int q = 0; q < kVPairs<T>; ++q) {
-                                    const uint64_t a = a0 + a_part_of(kVPairs<T>, q) * (a_size >> 4);
-                                    const uint64_t b = b0 + b_part_of(kVPairs<T>, q) * (b_size >> 4);
-    #pragma unroll
-                                    for (unsigned k = 0; k < kVK / 16; ++k)
-                                        umma(d, a + k * a_step, b + k * b_step, idesc, more || q > 0 || k > 0);
+#pragma unroll
+                                for (int u = 0; u < kVBlocks<MODE, T>; ++u) {
+                                    if (u >= n) break;
+                                    const uint64_t a0 = stage0 + ((u * block) >> 4), b0 = a0 + (b_at >> 4);
+#pragma unroll
+                                    for (int q = 0; q < kVPairs<T>; ++q) {
+                                        const uint64_t a = a0 + a_part_of(kVPairs<T>, q) * (a_size >> 4);
+                                        const uint64_t b = b0 + b_part_of(kVPairs<T>, q) * (b_size >> 4);
+#pragma unroll
+                                        for (unsigned k = 0; k < kVK / 16; ++k)
+                                            umma(d, a + k * a_step, b + k * b_step, idesc, more || u > 0 || q > 0 || k > 0);
+                                    }
                                 }
                                 umma_commit(empty + 8 * s);
                             }

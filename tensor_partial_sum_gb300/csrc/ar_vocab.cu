@@ -411,9 +411,11 @@ struct Call {
         if (tps::kVFew<MODE>) p.a_room = p.few_rows;
         else p.a_room = p.a_rows >= 128 || (MODE == tps::kGrads && p.tiles) ? 128 : p.a_tail;
         // a product reads 128 rows of A wherever the stage starts: the last stage's have to lie in the ring
-        const int a = static_cast<int>(parts) * p.a_room * tps::kVRow, b = static_cast<int>(parts) * p.bn / 2 * tps::kVRow;
-        // (the last part of A: 128 rows from (parts - 1) a_room rows on)
-        const int stage = a + b, last = tps::kVRing - (static_cast<int>(parts - 1) * p.a_room + 128) * tps::kVRow;
+        const int block = static_cast<int>(parts) * (p.a_room + p.bn / 2) * tps::kVRow;
+        const int blocks = parts == 1 ? tps::kVBlocks<MODE, tps::kBF16> : tps::kVBlocks<MODE, tps::kF32>;
+        // (the last part of A of the last block: 128 rows from (parts - 1) a_room rows on)
+        const int stage = blocks * block;
+        const int last = tps::kVRing - (blocks - 1) * block - (static_cast<int>(parts - 1) * p.a_room + 128) * tps::kVRow;
         p.stages = tps::kVRing / stage;
         if (p.stages > last / stage + 1) p.stages = last / stage + 1;
         if (p.stages > tps::kVMaxStages) p.stages = tps::kVMaxStages;
