@@ -152,19 +152,21 @@ size_t padded_vocab(const ar_vocab *v) {
     return n;
 }
 
-// Columns of a kStats tile.  With one tile row the call is bound by reading W in rounds of one tile a
-// pair.  A round takes as long as its width and some 56 columns more (one token of 4096 elements: 22.7 us at
-// 256 columns, 20.0 at 224, 15.7 at 176, 13.4 at 128), so the width, a multiple of 16 and at least half a tile,
-// that makes the rounds cheapest is taken: 32768 rows 50.2 us at 224, 52.6 at 256 and 61.7 at 128, 8000 rows
-// 21.9 us at 128 and 27.6 at 256.  With more tile rows the widest tile moves the fewest bytes per product.
-int stats_width(const ar_vocab *v, int pairs) {
-    if (v->rows > tps::kVM) return tps::kVN;
+constexpr size_t kPairs = 76;  // of SMs on a GB300: what the plans are made for
+
+// Columns of a kStats tile, a multiple of 16 and at least half a tile: the width that makes the rounds of one
+// tile a pair cheapest.  With one tile row a round is bound by reading W and takes as long as its width and some
+// 56 columns more (one token of 4096 elements: 22.7 us at 256 columns, 20.0 at 224, 15.7 at 176, 13.4 at 128;
+// 32768 rows 50.2 us at 224, 52.6 at 256 and 61.7 at 128); with more tile rows it is bound by the products,
+// and narrow tiles copy more of H for each.
+int stats_width(const ar_vocab *v) {
+    const size_t mt = tiles_of(v->rows, tps::kVM), fixed = mt > 1 ? 24 : 56;
     size_t best = SIZE_MAX;
     int bn = tps::kVN;
     for (int n = tps::kVN; n >= tps::kVN / 2; n -= 16) {
         size_t tiles = 0;
         for (int r = 0; r < v->n_pieces; ++r) tiles += tiles_of(v->piece_rows[r], static_cast<size_t>(n));
-        const size_t cost = tiles_of(tiles, static_cast<size_t>(pairs)) * static_cast<size_t>(n + 56);
+        const size_t cost = tiles_of(tiles * mt, kPairs) * (static_cast<size_t>(n) + fixed);
         if (cost < best) best = cost, bn = n;
     }
     return bn;
@@ -172,13 +174,13 @@ int stats_width(const ar_vocab *v, int pairs) {
 
 // Few tokens: vocabulary rows of a tile in each CTA, a multiple of `step`, so that the rounds of one tile a pair are
 // cheapest (a round costs its rows and some 24 more).
-int few_rows(const ar_vocab *v, int pairs, int step) {
+int few_rows(const ar_vocab *v, int step) {
     size_t best = SIZE_MAX;
     int rows = 128;
     for (int n = 128; n >= 32; n -= step) {
         size_t tiles = 0;
         for (int r = 0; r < v->n_pieces; ++r) tiles += tiles_of(v->piece_rows[r], static_cast<size_t>(2 * n));
-        const size_t cost = tiles_of(tiles, static_cast<size_t>(pairs)) * static_cast<size_t>(2 * n + 24);
+        const size_t cost = tiles_of(tiles, kPairs) * static_cast<size_t>(2 * n + 24);
         if (cost < best) best = cost, rows = n;
     }
     return rows;
@@ -193,10 +195,8 @@ LossPlan plan_loss(const ar_vocab *v) {
     LossPlan p{};
     const size_t row = packed_ld(v) * 2 * static_cast<size_t>(parts_of(v));
     Carve c;
-    // statistics for each half tile; the narrowest tile that stats_width may take makes the most of them
-    const size_t narrow = v->rows > tps::kVM ? tps::kVN : tps::kVN / 2;
-    size_t tiles = 0;
-    for (int r = 0; r < v->n_pieces; ++r) tiles += tiles_of(v->piece_rows[r], narrow);
+    size_t tiles = 0;  // with statistics for each half
+    for (int r = 0; r < v->n_pieces; ++r) tiles += tiles_of(v->piece_rows[r], static_cast<size_t>(stats_width(v)));
     if (v->rows <= tps::kFewTokens) {  // one for each 32 vocabulary rows; few_rows may leave 24 of 32 unused
         tiles = 0;
         for (int r = 0; r < v->n_pieces; ++r) tiles += 4 * tiles_of(v->piece_rows[r], 64);
@@ -245,7 +245,7 @@ GradPlan plan_grad(const ar_vocab *v) {
     }
     const bool split = round_up(longest, tps::kVN) > p.cap;
     if (split) blocks = blocks / (longest / p.cap + 1), longest = p.cap;
-    const size_t share = blocks / 76 + 1, tile = tiles_of(longest, tps::kVK);
+    const size_t share = blocks / kPairs + 1, tile = tiles_of(longest, tps::kVK);
     const size_t slice = p.d_rows * round_up(v->dim, 8) * sizeof(float) * static_cast<size_t>(segs ? segs : 1);
     size_t s = 1;
     if (tile > share) s = tiles_of(tile, share / 2 < 8 ? 8 : share / 2);
@@ -518,8 +518,8 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
     p.rows = static_cast<int>(T);
     p.dim = static_cast<int>(D);
     const bool few = T <= tps::kFewTokens;
-    p.bn = few ? static_cast<int>(round_up(T, 16)) : stats_width(v, c.sm_count / 2);
-    p.few_rows = few ? few_rows(v, c.sm_count / 2, 8) : 0;
+    p.bn = few ? static_cast<int>(round_up(T, 16)) : stats_width(v);
+    p.few_rows = few ? few_rows(v, 8) : 0;
     p.targets = reinterpret_cast<const long long *>(v->targets);
     p.part = reinterpret_cast<float2 *>(call.ws + plan.part);
     p.picked = reinterpret_cast<float *>(call.ws + plan.picked);
@@ -681,7 +681,7 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
         p.d_part = p.d_ld * static_cast<long long>(plan.d_rows);
         p.nseg = g.nseg;
         p.bn = few ? static_cast<int>(round_up(T, 16)) : static_cast<int>(tps::kVN);
-        p.few_rows = few ? few_rows(v, c.sm_count / 2, 32) : 0;  // whole blocks of K: D's columns are zeroed to there
+        p.few_rows = few ? few_rows(v, 32) : 0;  // whole blocks of K: D's columns are zeroed to there
         const int tile = few ? 2 * p.few_rows : p.bn;
         p.tiles = 0;
         if (!(few ? make_few_map(p, call.f16, call.ws + plan.hidden, call.ld, plan.k_rows, call.parts, call.ld, plan.k_rows * call.ld)
