@@ -16,6 +16,10 @@
 // side, so tiles of vocabulary rows by a few tokens cost next to nothing and
 // reading W is what is left (4 tokens of 5136 elements, six pieces of 1640 rows:
 // an eager call 49 -> 40 us; 3 float tokens of 7232, 19671 rows: 489 -> 398).
+// Their D of 16-bit inputs is held in two parts (kGradsFew): with few tokens
+// the rounding of the targets' entries does not average out (gradients up to
+// 1.65 times as far off as a float computation rounded once), and the second
+// product is hidden behind W.
 // Small kernels around it list the counted tokens, pack rows that the tiled
 // copies cannot read in place, and join partial results.
 //
@@ -29,10 +33,12 @@
 
 namespace tps {
 
-enum VocabMode { kStats = 0, kDlogits = 1, kGrads = 2, kStatsFew = 3, kDlogitsFew = 4 };
+enum VocabMode { kStats = 0, kDlogits = 1, kGrads = 2, kStatsFew = 3, kDlogitsFew = 4, kGradsFew = 5 };
 template <int MODE>
 constexpr bool kVFew = MODE == kStatsFew || MODE == kDlogitsFew;
 constexpr int kFewTokens = 64;
+template <int MODE>
+constexpr bool kVGrads = MODE == kGrads || MODE == kGradsFew;
 
 constexpr int kMaxSegs = 16;
 constexpr int kVM = 256;      // rows of a tile, 128 in each CTA
@@ -129,18 +135,20 @@ struct VocabGemmParams {
     unsigned *status;
 };
 
-// Parts of an operand, and products of parts in a block of K.
-template <int T>
-constexpr int kVParts = T == kF32 ? 3 : 1;
-template <int T>
-constexpr int kVPairs = T == kF32 ? 6 : 1;
+// Parts of the operands, and products of parts in a block of K.
+template <int MODE, int T>
+constexpr int kVPartsA = T == kF32 ? 3 : MODE == kGradsFew ? 2 : 1;
+template <int MODE, int T>
+constexpr int kVPartsB = T == kF32 ? 3 : 1;
+template <int MODE, int T>
+constexpr int kVPairs = T == kF32 ? 6 : kVPartsA<MODE, T>;
 // Part numbers of A and B in product q, the largest product last, so that the small ones are summed
 // while the run is small.
-__device__ __forceinline__ constexpr int a_part_of(int pairs, int q) {  // 1 0 2 0 1 0
-    return pairs == 1 ? 0 : (0x010201 >> (4 * q)) & 0xF;
+__device__ __forceinline__ constexpr int a_part_of(int pairs, int q) {  // of six: 1 0 2 0 1 0
+    return pairs == 6 ? (0x010201 >> (4 * q)) & 0xF : pairs - 1 - q;
 }
-__device__ __forceinline__ constexpr int b_part_of(int pairs, int q) {  // 1 2 0 1 0 0
-    return pairs == 1 ? 0 : (0x001021 >> (4 * q)) & 0xF;
+__device__ __forceinline__ constexpr int b_part_of(int pairs, int q) {  // of six: 1 2 0 1 0 0
+    return pairs == 6 ? (0x001021 >> (4 * q)) & 0xF : 0;
 }
 
 // A tile: its place, its operands' places and its blocks of K.
@@ -176,7 +184,7 @@ struct VocabWalk {
 
     __device__ __forceinline__ VocabWalk(const VocabGemmParams &params, int live, int pair_, int npairs_)
         : p(params), pair(pair_), npairs(npairs_), mt((live + kVM - 1) / kVM) {
-        if constexpr (MODE != kGrads) {
+        if constexpr (!kVGrads<MODE>) {
             kn = (p.dim + kVK - 1) / kVK;
             nt = 0;
         } else {
@@ -199,7 +207,7 @@ struct VocabWalk {
         t.bn = p.bn;
         t.dw = false;
         t.seg = 0;
-        if constexpr (MODE != kGrads) {
+        if constexpr (!kVGrads<MODE>) {
             const long long id = pair + static_cast<long long>(i++) * npairs;
             if constexpr (kVFew<MODE>) {  // tiles of vocabulary rows by all tokens
                 if (mt == 0 || id >= p.tiles) return false;
@@ -381,7 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
     const unsigned S = static_cast<unsigned>(p.stages);
     // a block of K: the parts of A, then the parts of B
     const unsigned a_size = static_cast<unsigned>(p.a_room) * kVRow, b_size = static_cast<unsigned>(p.bn / 2) * kVRow;
-    const unsigned b_at = kVParts<T> * a_size, block = b_at + kVParts<T> * b_size, stage = kVBlocks<MODE, T> * block;
+    const unsigned b_at = kVPartsA<MODE, T> * a_size, block = b_at + kVPartsB<MODE, T> * b_size, stage = kVBlocks<MODE, T> * block;
 
     const volatile unsigned never = 0;  // for waits that follow giving up
     auto give_up = [&] {
@@ -403,8 +411,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 int ay, ax, by, bx;  // first element of this CTA's rows (columns) at block 0 of K
                 const int row0 = t.m * kVM, arow = row0 + static_cast<int>(rank) * 128;
                 const int brow = t.n * p.bn + static_cast<int>(rank) * (t.bn / 2);
-                const bool a_mn = MODE == kGrads && t.dw, b_mn = MODE == kGrads;
-                if constexpr (MODE != kGrads) {
+                const bool a_mn = kVGrads<MODE> && t.dw, b_mn = kVGrads<MODE>;
+                if constexpr (!kVGrads<MODE>) {
                     am = &p.a_map, bm = &p.b_map[t.seg];
                     ax = 0, ay = arow, bx = 0, by = brow;
                 } else if (t.dw) {
@@ -433,7 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                     am = ay + mh <= rows ? &p.b_map[t.seg] : &p.b_tail[t.seg];
                     bm = &p.a_map;
                 }
-                const unsigned bytes = static_cast<unsigned>(a_both + b_both) * kVRow * kVParts<T>;
+                const unsigned bytes = static_cast<unsigned>(kVPartsA<MODE, T> * a_both + kVPartsB<MODE, T> * b_both) * kVRow;
                 int k = t.k0 * kVK;
                 constexpr int U = kVBlocks<MODE, T>;
                 for (int n = t.kn; n > 0; n -= U, k += U * kVK) {
@@ -453,15 +461,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                             if (u >= n) break;
                             const int ku = k + u * kVK;
 #pragma unroll
-                            for (int q = 0; q < kVParts<T>; ++q) {
+                            for (int q = 0; q < kVPartsA<MODE, T>; ++q) {
                                 const unsigned a = base + s * stage + u * block + q * a_size;
-                                const unsigned b = base + s * stage + u * block + b_at + q * b_size;
                                 if (!a_mn) {
                                     if (a_mine) tma_load_3d(a, am, bar, ax + ku, ay, q);
                                 } else {  // two chunks of 64 columns, 64 rows each
                                     tma_load_3d(a, am, bar, ax, ay + ku, q);
                                     tma_load_3d(a + 8192, am, bar, ax + 64, ay + ku, q);
                                 }
+                            }
+#pragma unroll
+                            for (int q = 0; q < kVPartsB<MODE, T>; ++q) {
+                                const unsigned b = base + s * stage + u * block + b_at + q * b_size;
                                 if (!b_mn) {
                                     if (b_mine) tma_load_3d(b, bm, bar, bx + ku, by, q);
                                 } else {
@@ -493,7 +504,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 bool ok = true;
                 VocabTile t;
                 for (VocabWalk<MODE> walk(p, live, pair, npairs); ok && walk.next(t);) {
-                    const bool a_mn = MODE == kGrads && t.dw, b_mn = MODE == kGrads;
+                    const bool a_mn = kVGrads<MODE> && t.dw, b_mn = kVGrads<MODE>;
                     const uint32_t idesc = umma_idesc(T != kF16, a_mn, b_mn, static_cast<unsigned>(t.bn));
                     // 16 elements of K: 32 bytes along a K-major row, two groups of eight rows otherwise
                     const unsigned a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
@@ -523,9 +534,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                                     if (u >= n) break;
                                     const uint64_t a0 = stage0 + ((u * block) >> 4), b0 = a0 + (b_at >> 4);
 #pragma unroll
-                                    for (int q = 0; q < kVPairs<T>; ++q) {
-                                        const uint64_t a = a0 + a_part_of(kVPairs<T>, q) * (a_size >> 4);
-                                        const uint64_t b = b0 + b_part_of(kVPairs<T>, q) * (b_size >> 4);
+                                    for (int q = 0; q < kVPairs<MODE, T>; ++q) {
+                                        const uint64_t a = a0 + a_part_of(kVPairs<MODE, T>, q) * (a_size >> 4);
+                                        const uint64_t b = b0 + b_part_of(kVPairs<MODE, T>, q) * (b_size >> 4);
 #pragma unroll
                                         for (unsigned k = 0; k < kVK / 16; ++k)
                                             umma(d, a + k * a_step, b + k * b_step, idesc, more || u > 0 || q > 0 || k > 0);
@@ -555,7 +566,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
         unsigned char *stage_out = raw + (base - smem_u32(raw)) + kVRing + (warp - 4) * 32 * kVPitch;
         unsigned acc_it = 0;
         VocabTile t;
-        const float unscale = MODE == kGrads && p.list ? p.list->unscale : 1.0f;
+        const float unscale = kVGrads<MODE> && p.list ? p.list->unscale : 1.0f;
         bool ok = true;
         for (VocabWalk<MODE> walk(p, live, pair, npairs); ok && walk.next(t);) {
             const VocabSeg &seg = p.seg[t.seg];
@@ -566,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
             const int c0 = half * (kVFew<MODE> ? 32 : t.bn / 2);
             const int width = kVFew<MODE> ? min(32, t.bn - c0) : t.bn / 2;
             // rows past the end cost nothing (D's are read, as zeros, up to a whole block of K)
-            const int rows = MODE == kDlogits ? (live + kVK - 1) / kVK * kVK : MODE == kGrads && t.dw ? seg.rows : live;
+            const int rows = MODE == kDlogits ? (live + kVK - 1) / kVK * kVK : kVGrads<MODE> && t.dw ? seg.rows : live;
             const bool idle = kVFew<MODE> ? quarter * 32 >= p.few_rows || (MODE == kStatsFew && c0 >= live) : r - lane >= rows;
             long long y = -1;
             float lse = 0.0f, g = 0.0f;
@@ -748,8 +759,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                     const int a = __shfl_sync(~0u, mine_at, k);
                     const float q = __expf(v[k] - l) - (a == lane ? 1.0f : 0.0f);
                     const float d = c0 + k < live && r < seg.rows ? q * f : 0.0f;
-                    if constexpr (T != kF32) {
-                        if (store) store_elem<T>(out, k * p.d_ld, d);
+                    if constexpr (T != kF32) {  // the rounded value and what it lacks
+                        float lo, hi;
+                        widen2<T>(narrow2<T>(d, d), lo, hi);
+                        if (store) {
+                            store_elem<T>(out, k * p.d_ld, d);
+                            store_elem<T>(out, p.d_part + k * p.d_ld, fabsf(d) <= 3.402823466e38f ? d - lo : 0.0f);
+                        }
                     } else {
                         uint32_t w[3];
                         split2(d, 0.0f, w);

@@ -83,6 +83,9 @@ size_t tiles_of(size_t n, size_t tile) { return (n + tile - 1) / tile; }
 
 int parts_of(const ar_vocab *v) { return v->dtype == AR_F32 ? 3 : 1; }
 
+// Parts of D: 16-bit types hold it in one, in two with few tokens.
+int d_parts_of(const ar_vocab *v) { return v->dtype == AR_F32 ? 3 : v->rows <= tps::kFewTokens ? 2 : 1; }
+
 // Rows that the tiled copies can read in place: 16-bit, starts and strides on 16-byte boundaries.
 bool in_place(const void *p, size_t stride, const ar_vocab *v) {
     return v->dtype != AR_F32 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 16 == 0;
@@ -223,12 +226,13 @@ struct GradPlan {
 
 GradPlan plan_grad(const ar_vocab *v) {
     GradPlan p{};
-    const size_t parts = static_cast<size_t>(parts_of(v)), row = packed_ld(v) * 2 * parts;
+    const size_t parts = static_cast<size_t>(parts_of(v)), d_parts = static_cast<size_t>(d_parts_of(v));
+    const size_t row = packed_ld(v) * 2 * parts;
     p.d_rows = round_up(v->rows, tps::kVM);
     p.k_rows = round_up(v->rows, tps::kVK);
     const bool pack = !weights_in_place(v);
     const size_t all = padded_vocab(v);
-    size_t cap = group_cap(kChunkBytes, p.d_rows * 2 * parts);
+    size_t cap = group_cap(kChunkBytes, p.d_rows * 2 * d_parts);
     if (pack && group_cap(kPackBytes, row) < cap) cap = group_cap(kPackBytes, row);
     p.cap = cap < all ? cap : all;
     // The dH tiles reduce over the vocabulary, the dW tiles over the tokens.  Where one dH tile would take
@@ -258,7 +262,7 @@ GradPlan plan_grad(const ar_vocab *v) {
     p.index = c.take(v->rows * sizeof(int));
     p.place = c.take(v->rows * sizeof(int));
     p.hidden = c.take(p.k_rows * row);
-    p.d = c.take(p.d_rows * p.cap * 2 * parts);
+    p.d = c.take(p.d_rows * p.cap * 2 * d_parts);
     p.weights = c.take(pack ? p.cap * row : 0);
     p.sum = c.take(p.sums ? static_cast<size_t>(p.slices) * slice : 0);
     p.bytes = c.at;
@@ -409,17 +413,20 @@ struct Call {
     template <int MODE>
     int launch_gemm(tps::VocabGemmParams &p, size_t tiles) const {
         if (tps::kVFew<MODE>) p.a_room = p.few_rows;
-        else p.a_room = p.a_rows >= 128 || (MODE == tps::kGrads && p.tiles) ? 128 : p.a_tail;
+        else p.a_room = p.a_rows >= 128 || (tps::kVGrads<MODE> && p.tiles) ? 128 : p.a_tail;
         // a product reads 128 rows of A wherever the stage starts: the last stage's have to lie in the ring
-        const int block = static_cast<int>(parts) * (p.a_room + p.bn / 2) * tps::kVRow;
-        const int blocks = parts == 1 ? tps::kVBlocks<MODE, tps::kBF16> : tps::kVBlocks<MODE, tps::kF32>;
-        // (the last part of A of the last block: 128 rows from (parts - 1) a_room rows on)
-        const int stage = blocks * block;
-        const int last = tps::kVRing - (blocks - 1) * block - (static_cast<int>(parts - 1) * p.a_room + 128) * tps::kVRow;
+        const bool f32 = parts == 3;
+        const int pa = f32 ? tps::kVPartsA<MODE, tps::kF32> : tps::kVPartsA<MODE, tps::kBF16>;
+        const int pb = f32 ? tps::kVPartsB<MODE, tps::kF32> : tps::kVPartsB<MODE, tps::kBF16>;
+        const int blocks = f32 ? tps::kVBlocks<MODE, tps::kF32> : tps::kVBlocks<MODE, tps::kBF16>;
+        // (the last part of A of the last block: 128 rows from (pa - 1) a_room rows on)
+        const int block = (pa * p.a_room + pb * p.bn / 2) * tps::kVRow, stage = blocks * block;
+        const int last = tps::kVRing - (blocks - 1) * block - ((pa - 1) * p.a_room + 128) * tps::kVRow;
         p.stages = tps::kVRing / stage;
         if (p.stages > last / stage + 1) p.stages = last / stage + 1;
         if (p.stages > tps::kVMaxStages) p.stages = tps::kVMaxStages;
-        const auto fn = by_type<tps::VocabGemmParams>(v->dtype, tps::ar_vocab_gemm_kernel<MODE, tps::kF32>,
+        constexpr int kMode32 = MODE == tps::kGradsFew ? static_cast<int>(tps::kGrads) : MODE;  // float: parts enough
+        const auto fn = by_type<tps::VocabGemmParams>(v->dtype, tps::ar_vocab_gemm_kernel<kMode32, tps::kF32>,
                                                       tps::ar_vocab_gemm_kernel<MODE, tps::kF16>,
                                                       tps::ar_vocab_gemm_kernel<MODE, tps::kBF16>);
         if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -705,9 +712,9 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
                  : call.launch_gemm<tps::kDlogits>(p, static_cast<size_t>(p.tiles) * mt);
         if (st != AR_OK) return st;
         // dH and dW from it
-        const size_t parts = call.parts, dl = static_cast<size_t>(p.d_ld), dp = static_cast<size_t>(p.d_part);
-        if (!make_a_maps(p, call.f16, p.d, dl, plan.k_rows, parts, dl, dp) ||
-            !make_map(&p.at_map, call.f16, p.d, dl, plan.k_rows, parts, dl, dp, 64))
+        const size_t parts = call.parts, dparts = static_cast<size_t>(d_parts_of(v)), dl = static_cast<size_t>(p.d_ld), dp = static_cast<size_t>(p.d_part);
+        if (!make_a_maps(p, call.f16, p.d, dl, plan.k_rows, dparts, dl, dp) ||
+            !make_map(&p.at_map, call.f16, p.d, dl, plan.k_rows, dparts, dl, dp, 64))
             return AR_ERR_CUDA;
         p.bn = D <= tps::kVN / 2 ? tps::kVN / 2 : tps::kVN;
         p.slices = plan.slices;
@@ -730,8 +737,8 @@ int ar_vocab_loss_grad(const ar_vocab *v, const float *lse, const float *dloss, 
             if (!make_map(&p.b_map[s], call.f16, w[s].base, w[s].cols, w[s].rows, parts, w[s].ld, w[s].part, 64)) return AR_ERR_CUDA;
         }
         p.tiles = dweights ? p.tiles * static_cast<int>(tiles_of(D, static_cast<size_t>(p.bn))) : 0;
-        st = call.launch_gemm<tps::kGrads>(
-            p, static_cast<size_t>(p.tiles) + static_cast<size_t>(g.nseg * p.slices * p.dh_tiles) * mt);
+        const size_t tiles = static_cast<size_t>(p.tiles) + static_cast<size_t>(g.nseg * p.slices * p.dh_tiles) * mt;
+        st = dparts == 2 ? call.launch_gemm<tps::kGradsFew>(p, tiles) : call.launch_gemm<tps::kGrads>(p, tiles);
         if (st != AR_OK) return st;
         if (dhidden && plan.slices > 1 && g.ends) {
             tps::VocabSumParams q;
