@@ -455,11 +455,11 @@ int ar_reduce_dropout_grad_workspace(const ar_layout *layout, int n_sums, size_t
  * runs of 512 terms, which are added rounded to nearest (the tensor cores'
  * own sums are not rounded but cut off, and drift over long reductions).
  * Float inputs are split into three bf16 parts each; six products of parts
- * give a float product to 2^-21 at worst, 2^-24 on average.  The gradient of
- * the logits is held in the 16-bit type (float inputs: in three parts) for
- * one chunk of the vocabulary at a time, relative to the largest |dloss|: one
- * rounding more than the outputs' own.  Infinite float inputs give NaN where
- * the formula has an infinity.
+ * give a float product to 2^-25.  The gradient of the logits is held in the
+ * 16-bit type for one chunk of the vocabulary at a time, relative to the
+ * largest |dloss|: one rounding more than the outputs' own (with 64 tokens or
+ * fewer in two parts, float inputs in three: none).  Infinite float inputs
+ * give NaN where the formula has an infinity.
  */
 typedef struct {
     size_t rows;                      /* tokens; rows * dim <= max_elems */

@@ -24,8 +24,8 @@
 // copies cannot read in place, and join partial results.
 //
 // Float32 inputs go through the same tensor cores: x = x1 + x2 + x3 with three
-// bf16 parts of eight bits each (exact), and the six largest of the nine
-// products; the ones left out are below 2^-21 of the whole, 2^-24 on average.
+// bf16 parts (exact), and the six largest of the nine products; the ones left
+// out are below 2^-25 of the whole.
 #pragma once
 
 #include "ar_kernels.cuh"
@@ -313,16 +313,31 @@ __device__ __forceinline__ void store_block(unsigned char *stage, char *out, con
     }
 }
 
-// The three bf16 parts of two floats, eight bits each, packed in pairs.
+// The three bf16 parts of two floats, each the nearest to what is left: the parts have signs of their
+// own, so that what the missing products of parts leave out averages out (cut off instead of rounded, a
+// step of five tokens had gradients 6.7e-6 off).  ANY: any floats, else finite ones that no rounding
+// makes infinite.
+template <bool ANY>
 __device__ __forceinline__ void split2(float a, float b, uint32_t (&w)[3]) {
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-        const uint32_t ha = __float_as_uint(a) & 0xFFFF0000u, hb = __float_as_uint(b) & 0xFFFF0000u;
-        w[q] = (ha >> 16) | hb;
-        // an infinity or NaN is all in the first part
-        a = fabsf(a) <= 3.402823466e38f ? a - __uint_as_float(ha) : 0.0f;
-        b = fabsf(b) <= 3.402823466e38f ? b - __uint_as_float(hb) : 0.0f;
+    w[0] = pack_bf16x2(a, b);
+    if constexpr (ANY) {
+        // a finite number that would round to infinity is cut off; an infinity or NaN is all in the first part
+        if (fabsf(bf16_lo(w[0])) == INFINITY && fabsf(a) != INFINITY) w[0] = (w[0] & 0xFFFF0000u) | (__float_as_uint(a) >> 16);
+        if (fabsf(bf16_hi(w[0])) == INFINITY && fabsf(b) != INFINITY) w[0] = (w[0] & 0xFFFFu) | (__float_as_uint(b) & 0xFFFF0000u);
+        a = fabsf(a) <= 3.402823466e38f ? a - bf16_lo(w[0]) : 0.0f;
+        b = fabsf(b) <= 3.402823466e38f ? b - bf16_hi(w[0]) : 0.0f;
+    } else {
+        a -= bf16_lo(w[0]), b -= bf16_hi(w[0]);
     }
+    w[1] = pack_bf16x2(a, b);
+    w[2] = pack_bf16x2(a - bf16_lo(w[1]), b - bf16_hi(w[1]));
+}
+
+// softmax from a logit less the row's log-sum-exp; float inputs want more of it than the fast
+// exponential has (its argument's rounding, 1e-6 at -16).
+template <int T>
+__device__ __forceinline__ float soft(float x) {
+    return T == kF32 ? expf(x) : __expf(x);
 }
 
 // Combine 32 columns over the warp's lanes: lane k's x[0] becomes column k's result (31 exchanges
@@ -687,9 +702,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                     if (c >= width) break;
                     float v[32];
                     values(c, v);
+                    // the target's probability less one, exact where it is nearly sure
+                    float target = 0.0f;
+                    if (at >= c && at < c + 32) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (at == c + k) target = v[k];
+                        target = expm1f(target - lse);
+                    }
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        const float q = __expf(v[k] - lse) - (at == c + k ? 1.0f : 0.0f);
+                        const float q = at == c + k ? target : soft<T>(v[k] - lse);
                         v[k] = r < live && c + k < n ? q * g : 0.0f;
                     }
                     // rows past the list and columns past the segment hold zeros: whole blocks of K are read
@@ -704,7 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                         for (int k = 0; k < 32; k += 8) {
                             uint32_t w[4][3];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) split2(v[k + 2 * e], v[k + 2 * e + 1], w[e]);
+                            for (int e = 0; e < 4; ++e) split2<false>(v[k + 2 * e], v[k + 2 * e + 1], w[e]);
 #pragma unroll
                             for (int q = 0; q < 3; ++q)
                                 *reinterpret_cast<uint4 *>(out + q * p.d_part + c + k) =
@@ -750,6 +773,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 values(0, v);
                 const long long at = y - seg.first - (r - lane);
                 const int mine_at = at >= 0 && at < 32 ? static_cast<int>(at) : -1;
+                const bool some = __any_sync(~0u, mine_at >= 0);
                 // D[token][r]: adjacent lanes adjacent columns; zeros up to whole blocks of K either way
                 const bool store = in_cta < p.few_rows && r < (seg.rows + kVK - 1) / kVK * kVK;
                 unsigned short *out = p.d + seg.col0 + r + static_cast<long long>(c0) * p.d_ld;
@@ -757,7 +781,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                 for (int k = 0; k < 32; ++k) {
                     const float l = __shfl_sync(~0u, lse, k), f = __shfl_sync(~0u, g, k);
                     const int a = __shfl_sync(~0u, mine_at, k);
-                    const float q = __expf(v[k] - l) - (a == lane ? 1.0f : 0.0f);
+                    float q = soft<T>(v[k] - l);
+                    if (some && a == lane) q = expm1f(v[k] - l);  // the target's, exact where it is nearly sure
                     const float d = c0 + k < live && r < seg.rows ? q * f : 0.0f;
                     if constexpr (T != kF32) {  // the rounded value and what it lacks
                         float lo, hi;
@@ -768,7 +793,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                         }
                     } else {
                         uint32_t w[3];
-                        split2(d, 0.0f, w);
+                        split2<false>(d, 0.0f, w);
 #pragma unroll
                         for (int part = 0; part < 3; ++part)
                             if (store) out[part * p.d_part + k * p.d_ld] = static_cast<unsigned short>(w[part] & 0xFFFFu);
@@ -1019,7 +1044,7 @@ __global__ void __launch_bounds__(256) ar_vocab_pack_kernel(const __grid_constan
             } else {
                 uint32_t w[4][3];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) split2(v[2 * e], v[2 * e + 1], w[e]);
+                for (int e = 0; e < 4; ++e) split2<true>(v[2 * e], v[2 * e + 1], w[e]);
 #pragma unroll
                 for (int q = 0; q < 3; ++q)
                     *reinterpret_cast<uint4 *>(out + q * p.dst_part) = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
