@@ -452,7 +452,7 @@ int ar_reduce_dropout_grad_workspace(const ar_layout *layout, int n_sums, size_t
  * target that is neither ignore_index nor a row of the vocabulary gives the
  * loss NaN and no gradient.
  * Products of 16-bit types are exact and summed in float: the statistics in
- * runs of 512 terms, which are added rounded to nearest (the tensor cores'
+ * runs of at most 512 terms, which are added rounded to nearest (the tensor cores'
  * own sums are not rounded but cut off, and drift over long reductions).
  * Float inputs are split into three bf16 parts each; six products of parts
  * give a float product to 2^-25.  The gradient of the logits is held in the

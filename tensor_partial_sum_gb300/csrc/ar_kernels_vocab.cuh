@@ -51,17 +51,20 @@ constexpr int kVEpilogueWarps = 8;
 constexpr int kVThreads = 128 + 32 * kVEpilogueWarps;
 // The tensor cores' float sums drop what falls below the running sum's last place (they do not round), so
 // a long reduction drifts: one token of 4096 elements came out 3.6e-5 off.  Where results are float32
-// (the statistics, and everything of float32 inputs) a run of products is kept short - 32 or 48 of them -
-// and the runs are added in registers, rounded to nearest.
+// (the statistics, and everything of float32 inputs) a run of products is kept short and the runs are
+// added in registers, rounded to nearest.  Half as long a run is off by half as much and costs one
+// hand-over more: with 32 products the prompt's statistics are 2.7e-7 off (a float computation 6.1e-7) in 286 us,
+// with 16 they take 306; few tokens wait for W and get 16 for nothing; float32 gets 24 (345 -> 355 us a
+// step), which halves the gradients' error to below a float computation's.
 template <int MODE, int T>
 constexpr bool kVRuns = MODE == kStats || MODE == kStatsFew || T == kF32;
-template <int T>
-constexpr int kVRunBlocks = T == kF32 ? 2 : 8;  // blocks of K in a run
+template <int MODE, int T>
+constexpr int kVRunBlocks = T == kF32 ? 1 : kVFew<MODE> ? 4 : 8;  // blocks of K in a run
 // Blocks of K in a stage.  A round of the ring - wait, copies, products, commit - takes the feeding warps about 400
 // cycles, more than the products of narrow tiles: those share one between two blocks (three parts fill a
 // stage by themselves).
 template <int MODE, int T>
-constexpr int kVBlocks = kVFew<MODE> && T != kF32 ? 2 : 1;
+constexpr int kVBlocks = kVFew<MODE> && T != kF32 ? 2 : 1;  // a run is whole stages
 // Registers of the feeding and of the result warps when a thread adds up 128 columns; the launch's
 // kVLaunchRegs for each of 384 threads cover them.
 template <int MODE, int T>
@@ -258,7 +261,7 @@ struct VocabWalk {
 // Runs of products of a tile; one without blocks of K still counts as one.
 template <int MODE, int T>
 __device__ __forceinline__ int vocab_runs(const VocabTile &t) {
-    return kVRuns<MODE, T> ? max(1, (t.kn + kVRunBlocks<T> - 1) / kVRunBlocks<T>) : 1;
+    return kVRuns<MODE, T> ? max(1, (t.kn + kVRunBlocks<MODE, T> - 1) / kVRunBlocks<MODE, T>) : 1;
 }
 
 // Store a warp's 32x32 values, row `lane` in each thread: `n` (1 to 32) elements of T to each thread's
@@ -534,7 +537,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                         const unsigned d = tmem + acc * 256;
                         bool more = false;  // the first product of a run starts the accumulator
                         int n = t.kn;
-                        if constexpr (kVRuns<MODE, T>) n = min(kVRunBlocks<T>, t.kn - r * kVRunBlocks<T>);
+                        if constexpr (kVRuns<MODE, T>) n = min(kVRunBlocks<MODE, T>, t.kn - r * kVRunBlocks<MODE, T>);
                         for (; n > 0; n -= kVBlocks<MODE, T>) {
                             if (!__all_sync(~0u, mbar_wait_bounded(full + 8 * s, phase, abort_flag))) {
                                 give_up();
