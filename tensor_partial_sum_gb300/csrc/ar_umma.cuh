@@ -71,9 +71,6 @@ __device__ __forceinline__ void tma_load_3d(unsigned smem_dst, const CUtensorMap
         "l"(map), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
-__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
 
 // Shared-memory operand descriptor of a 128-byte swizzled tile (its start 1024-byte aligned).
 //   K-major: rows of 64 elements along K, eight-row groups 1024 bytes apart (`lead` unused).
