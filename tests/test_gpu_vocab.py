@@ -477,3 +477,28 @@ def test_many_pieces_some_empty():
 def test_long_token_lists(T):
     hidden, weights, targets = make("bf16", T, 64, [200, 60], seed=T, ignored=0.5)
     check_all("bf16", hidden, weights, targets, torch.full((T,), 1 / T, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [1, 4, 5, 16, 17])
+@pytest.mark.parametrize("pad,lead,D", [(3, 0, 77), (5, 1, 333), (0, 0, 1023), (0, 3, 64)])
+def test_few_tokens_against_rows_off_boundaries(dtype, T, pad, lead, D):
+    hidden, weights, targets = make(dtype, T, D, [333, 0, 1, 2050], seed=T + D, ignored=0.2, pad=pad, lead=lead)
+    check_all(dtype, hidden, weights, targets, torch.full((T,), 1 / T, device="cuda"), pad, lead)
+
+
+def test_few_float_tokens_with_infinite_and_nan_logits():
+    h = torch.zeros((3, 40), device="cuda")
+    w = torch.zeros((100, 40), device="cuda")
+    w[:, 0] = torch.linspace(-1, 1, 100, device="cuda")
+    w[7, 1], w[9, 2] = float("inf"), float("nan")
+    h[:, 0] = 2
+    h[1, 1] = 1
+    targets = torch.tensor([3, 3, IGNORE], device="cuda")
+    loss, lse = loss_of(h, [w], targets)
+    # row 7 meets a zero times infinity, row 9 a zero times NaN, in every token
+    assert torch.isnan(lse).all() and torch.isnan(loss[:2]).all() and loss[2] == 0
+    w[9, 2] = 0
+    w[7, 1] = 0
+    _, lse = loss_of(h, [w], targets)
+    assert torch.allclose(lse, torch.logsumexp(h @ w.t(), 1), rtol=1e-6)
