@@ -21,7 +21,8 @@ SOURCES = [os.path.join(CSRC, f) for f in ("ar.cu", "ar_kernels_f32.cu", "ar_ker
                                              "ar_dropout.cu", "ar_vocab.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ar_kernels.cuh", "ar_kernels_ex.cuh", "ar_kernels_tma.cuh",
                                                    "ar_dispatch.h", "ar_context.h", "ar_philox.cuh",
-                                                   "ar_kernels_dropout.cuh", "ar_kernels_vocab.cuh", "ar_umma.cuh")] + [os.path.join(INCLUDE, "ar.h")]
+                                                   "ar_kernels_dropout.cuh", "ar_kernels_vocab.cuh", "ar_vocab_plan.h",
+                                                   "ar_umma.cuh")] + [os.path.join(INCLUDE, "ar.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -30,20 +30,16 @@
 
 #include "ar_kernels.cuh"
 #include "ar_umma.cuh"
+#include "ar_vocab_plan.h"
 
 namespace tps {
 
 enum VocabMode { kStats = 0, kDlogits = 1, kGrads = 2, kStatsFew = 3, kDlogitsFew = 4, kGradsFew = 5 };
 template <int MODE>
 constexpr bool kVFew = MODE == kStatsFew || MODE == kDlogitsFew;
-constexpr int kFewTokens = 64;
 template <int MODE>
 constexpr bool kVGrads = MODE == kGrads || MODE == kGradsFew;
 
-constexpr int kMaxSegs = 16;
-constexpr int kVM = 256;      // rows of a tile, 128 in each CTA
-constexpr int kVN = 256;      // columns of a tile (at most), half of B's rows in each CTA
-constexpr int kVK = 64;       // elements of the reduction per stage: 128 bytes
 constexpr int kVMaxStages = 32;
 constexpr int kVRow = kVK * 2;              // bytes of a row of a stage
 constexpr int kVRing = 6 * 256 * kVRow;     // bytes of the stages: six of full height
@@ -75,18 +71,6 @@ constexpr unsigned kVTmemCols = 512;        // two accumulators of 256 columns
 constexpr int kVPitch = 80;                 // bytes between a warp's staged output rows of 64 bytes
 constexpr int kVOut = kVEpilogueWarps * 32 * kVPitch;
 constexpr size_t kVSmem = static_cast<size_t>(kVRing) + kVOut + 1024 + 1024;
-
-// One counted token of a gradient call, in the order of the list.
-struct VocabRow {
-    float lse, g;   // g: dloss / max |dloss| (times 2^14 for f16)
-    long long y;    // global vocabulary row of the target
-};
-
-// What the list kernel leaves for the others.
-struct VocabList {
-    int live;      // counted tokens
-    float unscale; // what undoes the scaling of VocabRow::g
-};
 
 // One vocabulary segment of a launch: (part of) a piece.
 struct VocabSeg {
@@ -168,9 +152,6 @@ template <int MODE>
 __host__ __device__ constexpr int tail_width(int rows) {
     return MODE == kStats ? (rows + 15) / 16 * 16 : (rows + 63) / 64 * 64;
 }
-
-// Blocks of K that storing a tile of dW takes as long as: the least a dW tile counts for.
-constexpr int kVStoreBlocks = 10;
 
 // A pair's tiles, one after another.  kStats and kDlogits: row tiles of one column tile next to one
 // another, so that pairs that run together share W and find H in L2.  kGrads: first the dH tiles (long
