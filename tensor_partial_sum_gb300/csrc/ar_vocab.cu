@@ -300,8 +300,8 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
     p.rows = static_cast<int>(T);
     p.dim = static_cast<int>(D);
     const bool few = T <= tps::kFewTokens;
-    p.bn = few ? static_cast<int>(round_up(T, 16)) : stats_width(v);
-    p.few_rows = few ? few_rows(v, 8) : 0;
+    p.bn = plan.tile.bn;
+    p.few_rows = plan.tile.few_rows;
     p.targets = reinterpret_cast<const long long *>(v->targets);
     p.part = reinterpret_cast<float2 *>(call.ws + plan.part);
     p.picked = reinterpret_cast<float *>(call.ws + plan.picked);
@@ -309,11 +309,9 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
     if (!(few ? make_few_map(p, call.f16, h.base, h.cols, h.rows, call.parts, h.ld, h.part)
               : make_a_maps(p, call.f16, h.base, h.cols, h.rows, call.parts, h.ld, h.part)))
         return AR_ERR_CUDA;
-    const int tile = few ? 2 * p.few_rows : p.bn;                   // vocabulary rows of a tile
-    const int per_tile = few ? 2 * ((p.few_rows + 31) / 32) : 2;  // statistics it leaves for a token
     long long first[AR_MAX_RANKS], total = 0;
     for (int r = 0; r < v->n_pieces; ++r) first[r] = total, total += static_cast<long long>(v->piece_rows[r]);
-    int piece = 0, done = 0;  // column tiles of earlier groups
+    int piece = 0;
     size_t row = 0;
     Group g;
     while (next_group(v, plan.cap, piece, row, g)) {
@@ -326,18 +324,17 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
             p.seg[s].first = first[g.piece[s]] + static_cast<long long>(g.row0[s]);
             p.seg[s].rows = static_cast<int>(g.rows[s]);
             p.seg[s].tile0 = p.tiles;
-            p.tiles += static_cast<int>(tiles_of(g.rows[s], static_cast<size_t>(tile)));
+            p.tiles += static_cast<int>(tiles_of(g.rows[s], plan.tile.rows));
             const unsigned tail = few ? few_tail(g.rows[s], p.few_rows) : tail_box<tps::kStats>(g.rows[s], p.bn);
             if (!make_map(&p.b_map[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part,
-                          static_cast<unsigned>(tile / 2)) ||
+                          static_cast<unsigned>(plan.tile.rows / 2)) ||
                 !make_map(&p.b_tail[s], call.f16, w[s].base, w[s].cols, w[s].rows, call.parts, w[s].ld, w[s].part, tail))
                 return AR_ERR_CUDA;
         }
         st = few ? call.launch_gemm<tps::kStatsFew>(p, static_cast<size_t>(p.tiles))
                  : call.launch_gemm<tps::kStats>(p, static_cast<size_t>(p.tiles) * tiles_of(T, tps::kVM));
         if (st != AR_OK) return st;
-        p.part += static_cast<long long>(per_tile) * p.tiles * static_cast<long long>(T);
-        done += p.tiles;
+        p.part += plan.tile.parts * static_cast<size_t>(p.tiles) * T;
     }
     tps::VocabJoinParams j;
     memset(&j, 0, sizeof j);
@@ -347,7 +344,7 @@ int ar_vocab_loss(const ar_vocab *v, float *loss, float *lse, void *ws, size_t w
     j.ignore = v->ignore_index;
     j.vocab = total;
     j.rows = p.rows;
-    j.parts = per_tile * done;
+    j.parts = static_cast<int>(plan.parts);
     j.loss = loss;
     j.lse = lse;
     return few ? call.launch<tps::VocabJoinParams>(tps::ar_vocab_join_kernel<1>, dim3(static_cast<unsigned>(T)), 256u, 0, j)

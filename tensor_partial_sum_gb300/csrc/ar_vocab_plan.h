@@ -179,27 +179,48 @@ inline int few_rows(const ar_vocab *v, int step) {
     return rows;
 }
 
+// Tiles of the statistics.
+struct StatsTile {
+    int bn, few_rows;  // of the launch; few_rows: with few tokens, else 0
+    size_t rows;       // vocabulary rows
+    size_t parts;      // statistics that a tile leaves for a token: of each half of its columns, or (few tokens) of
+                       // every 32 vocabulary rows of each CTA
+};
+
+inline StatsTile stats_tile(const ar_vocab *v) {
+    if (v->rows > kFewTokens) {
+        const int bn = stats_width(v);
+        return StatsTile{bn, 0, static_cast<size_t>(bn), 2};
+    }
+    const int n = few_rows(v, 8);
+    return StatsTile{static_cast<int>(round_up(v->rows, 16)), n, static_cast<size_t>(2 * n), 2 * tiles_of(static_cast<size_t>(n), 32)};
+}
+
 struct LossPlan {
-    size_t cap;  // vocabulary rows of a group
+    StatsTile tile;
+    size_t cap;    // vocabulary rows of a group
+    size_t parts;  // statistics of a token
     size_t part, picked, hidden, weights, bytes;
 };
 
 inline LossPlan plan_loss(const ar_vocab *v) {
     LossPlan p{};
+    p.tile = stats_tile(v);
     const size_t row = packed_ld(v) * 2 * static_cast<size_t>(parts_of(v));
-    Carve c;
-    size_t tiles = 0;  // with statistics for each half
-    for (int r = 0; r < v->n_pieces; ++r) tiles += tiles_of(v->piece_rows[r], static_cast<size_t>(stats_width(v)));
-    if (v->rows <= kFewTokens) {  // one for each 32 vocabulary rows; few_rows may leave 24 of 32 unused
-        tiles = 0;
-        for (int r = 0; r < v->n_pieces; ++r) tiles += 4 * tiles_of(v->piece_rows[r], 64);
-    }
-    p.part = c.take(2 * tiles * v->rows * sizeof(float2));
-    p.picked = c.take(v->rows * sizeof(float));
-    p.hidden = c.take(hidden_in_place(v) ? 0 : v->rows * row);
     const bool pack = !weights_in_place(v);
     const size_t all = padded_vocab(v);
     p.cap = pack && group_cap(kPackBytes, row) < all ? group_cap(kPackBytes, row) : all;
+    // counted group by group, as the launches are: each cut of a piece may leave one more tile, because `cap` is no
+    // multiple of a tile's rows
+    int piece = 0;
+    size_t at = 0;
+    Group g;
+    while (next_group(v, p.cap, piece, at, g))
+        for (int s = 0; s < g.nseg; ++s) p.parts += p.tile.parts * tiles_of(g.rows[s], p.tile.rows);
+    Carve c;
+    p.part = c.take(p.parts * v->rows * 2 * sizeof(float));
+    p.picked = c.take(v->rows * sizeof(float));
+    p.hidden = c.take(hidden_in_place(v) ? 0 : v->rows * row);
     p.weights = c.take(pack ? p.cap * row : 0);
     p.bytes = c.at;
     return p;
