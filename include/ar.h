@@ -457,7 +457,7 @@ int ar_reduce_dropout_grad_workspace(const ar_layout *layout, int n_sums, size_t
  * Float inputs are split into three bf16 parts each; six products of parts
  * give a float product to 2^-25.  The gradient of the logits is held in the
  * 16-bit type for one chunk of the vocabulary at a time, relative to the
- * largest |dloss|: one rounding more than the outputs' own (with 64 tokens or
+ * largest finite |dloss|: one rounding more than the outputs' own (with 64 tokens or
  * fewer in two parts, float inputs in three: none).  Infinite float inputs
  * give NaN where the formula has an infinity.
  */

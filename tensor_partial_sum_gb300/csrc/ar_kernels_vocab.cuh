@@ -902,8 +902,8 @@ struct VocabListParams {
     int *place;       // [rows] list entry, -1: not counted
 };
 
-// List the counted tokens in order, one block.  D is held as (softmax - onehot) dloss / max |dloss|,
-// so that rounding it to 16 bits costs the same whatever the scale of dloss, and costs nothing where
+// List the counted tokens in order, one block.  D is held as (softmax - onehot) dloss / max |dloss| (of
+// the finite ones), so that rounding it to 16 bits costs the same whatever the scale of dloss, and costs nothing where
 // all dloss are alike and the probability is small; f16 moves up by 2^14 so that probabilities keep
 // their eleven bits down to 2^-28.
 static __global__ void __launch_bounds__(1024) ar_vocab_list_kernel(const __grid_constant__ VocabListParams p) {
@@ -923,13 +923,16 @@ static __global__ void __launch_bounds__(1024) ar_vocab_list_kernel(const __grid
     for (int t0 = U * static_cast<int>(threadIdx.x); t0 < p.rows; t0 += U * 1024)
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (counted(t0 + u)) top = fmaxf(top, fabsf(p.dloss[t0 + u]));
+            if (counted(t0 + u)) {
+                const float a = fabsf(p.dloss[t0 + u]);
+                if (a <= 3.402823466e38f) top = fmaxf(top, a);  // an infinity or NaN is its own token's affair
+            }
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     if (lane == 0) tops[warp] = top;
     __syncthreads();
     top = tops[lane];
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    if (!(top > 0.0f && top <= 3.402823466e38f)) top = 1.0f;
+    if (top == 0.0f) top = 1.0f;
     int done = 0;
     for (int b0 = 0; b0 < p.rows; b0 += U * 1024) {
         const int t0 = b0 + U * static_cast<int>(threadIdx.x);

@@ -22,7 +22,7 @@ constexpr int kVStoreBlocks = 10;
 
 // One counted token of a gradient call, in the order of the list.
 struct VocabRow {
-    float lse, g;   // g: dloss / max |dloss| (times 2^14 for f16)
+    float lse, g;   // g: dloss / max |dloss| of the finite ones (times 2^14 for f16)
     long long y;    // global vocabulary row of the target
 };
 
