@@ -451,9 +451,10 @@ int ar_reduce_dropout_grad_workspace(const ar_layout *layout, int n_sums, size_t
  * gradient, whatever its hidden state holds (infinities and NaN included); a
  * target that is neither ignore_index nor a row of the vocabulary gives the
  * loss NaN and no gradient.
- * Products of 16-bit types are exact and summed in float: the statistics in
+ * Products of 16-bit types are exact and summed in float: the logits in
  * runs of at most 512 terms, which are added rounded to nearest (the tensor cores'
- * own sums are not rounded but cut off, and drift over long reductions).
+ * own sums are not rounded but cut off, and drift over long reductions), and alike
+ * in both calls; the gradients in one run, below their own rounding.
  * Float inputs are split into three bf16 parts each; six products of parts
  * give a float product to 2^-25.  The gradient of the logits is held in the
  * 16-bit type for one chunk of the vocabulary at a time, relative to the

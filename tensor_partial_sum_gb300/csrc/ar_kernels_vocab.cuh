@@ -46,14 +46,15 @@ constexpr int kVRing = 6 * 256 * kVRow;     // bytes of the stages: six of full 
 constexpr int kVEpilogueWarps = 8;
 constexpr int kVThreads = 128 + 32 * kVEpilogueWarps;
 // The tensor cores' float sums drop what falls below the running sum's last place (they do not round), so
-// a long reduction drifts: one token of 4096 elements came out 3.6e-5 off.  Where results are float32
-// (the statistics, and everything of float32 inputs) a run of products is kept short and the runs are
-// added in registers, rounded to nearest.  Half as long a run is off by half as much and costs one
+// a long reduction drifts: one token of 4096 elements came out 3.6e-5 off.  Where that would be seen (the
+// logits, of the statistics and of D, and everything of float32 inputs) a run of products is kept short and the
+// runs are added in registers, rounded to nearest.  The logits of D take the statistics' runs, so that a logit less the
+// log-sum-exp holds no drift of its own (in one run, a target with p = 1 - 1e-5 had a gradient of the wrong sign).  Half as long a run is off by half as much and costs one
 // hand-over more: with 32 products the prompt's statistics are 2.7e-7 off (a float computation 6.1e-7) in 286 us,
 // with 16 they take 306; few tokens wait for W and get 16 for nothing; float32 gets 24 (345 -> 355 us a
 // step), which halves the gradients' error to below a float computation's.
 template <int MODE, int T>
-constexpr bool kVRuns = MODE == kStats || MODE == kStatsFew || T == kF32;
+constexpr bool kVRuns = !kVGrads<MODE> || T == kF32;
 template <int MODE, int T>
 constexpr int kVRunBlocks = T == kF32 ? 1 : kVFew<MODE> ? 4 : 8;  // blocks of K in a run
 // Blocks of K in a stage.  A round of the ring - wait, copies, products, commit - takes the feeding warps about 400
@@ -686,7 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                     if (c >= width) break;
                     float v[32];
                     values(c, v);
-                    // the target's probability less one, exact where it is nearly sure
+                    // the target's probability less one, which keeps its bits where it is nearly sure
                     float target = 0.0f;
                     if (at >= c && at < c + 32) {
 #pragma unroll
@@ -766,7 +767,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
                     const float l = __shfl_sync(~0u, lse, k), f = __shfl_sync(~0u, g, k);
                     const int a = __shfl_sync(~0u, mine_at, k);
                     float q = soft<T>(v[k] - l);
-                    if (some && a == lane) q = expm1f(v[k] - l);  // the target's, exact where it is nearly sure
+                    if (some && a == lane) q = expm1f(v[k] - l);  // the target's, see kDlogits
                     const float d = c0 + k < live && r < seg.rows ? q * f : 0.0f;
                     if constexpr (T != kF32) {  // the rounded value and what it lacks
                         float lo, hi;

@@ -209,7 +209,7 @@ struct Call {
             cudaGetLastError();
             return AR_ERR_CUDA;
         }
-        if (!tps::kVFew<MODE> && (MODE == tps::kStats || v->dtype == AR_F32)) {
+        if (v->dtype == AR_F32 ? tps::kVSplitRegs<MODE, tps::kF32> : tps::kVSplitRegs<MODE, tps::kBF16>) {
             // result warps take registers that the feeding warps give up; a launch that was given fewer
             // than the split adds up to would wait for them for ever
             cudaFuncAttributes a;

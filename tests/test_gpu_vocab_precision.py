@@ -39,3 +39,55 @@ def test_one_infinite_dloss_leaves_other_tokens_alone(dtype, T, bad):
         assert torch.isfinite(a[others]).all() and torch.equal(a[others], b[others])
         assert not torch.isfinite(a[7]).all()
     assert not any(torch.isfinite(w).all() for w in dw)
+
+
+def nearly_sure(dtype, T, D):
+    """Tokens whose target has 1 - p of 1e-6 to 1e-3, half of them with a
+    positive, half with a negative logit, all products of a logit of one sign.
+    Element D - 2 + k of a hidden gradient is the logits' gradient of row k
+    (k = 0, 1: the targets), because only that row holds a one there."""
+    gen = torch.Generator(device="cuda").manual_seed(D + T)
+
+    def noise(*shape):
+        return 1 + 0.2 * (torch.rand(shape, device="cuda", generator=gen) - 0.5)
+    V, n = 200, (D - 2) // 2
+    w = torch.zeros((V, D), device="cuda")
+    w[:, :n], w[:, n:2 * n] = -7 / n * noise(V, n), -20 / n * noise(V, n)
+    w[0, :n], w[0, n:2 * n] = 6 / n * noise(n), -20 / n * noise(n)
+    w[1, :n], w[1, n:2 * n] = -7 / n * noise(n), -6 / n * noise(n)
+    w[0, D - 2] = w[1, D - 1] = 1
+    h = torch.zeros((T, D), device="cuda")
+    targets = torch.arange(T, device="cuda") % 2
+    scale = torch.linspace(1.0, 1.4, T, device="cuda")[:, None]
+    h[:, :n] = (targets == 0)[:, None] * scale * noise(T, n)
+    h[:, n:2 * n] = (targets == 1)[:, None] * scale * noise(T, n)
+    dt = DTYPES[dtype]
+    return h.to(dt), w.to(dt), targets
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [20, 64, 66, 300])
+@pytest.mark.parametrize("D", [8194, 8250])
+def test_target_entry_of_nearly_sure_tokens(dtype, T, D):
+    """The target's p - 1 to the bits that a float log-sum-exp leaves it: the
+    gradient's logits and the loss's drift alike or not at all.
+
+    Off by half a unit of the lse (at most 2^-22 below 16), by a rounding of a
+    sum between 1 and 2 for each of the 128 columns of a thread and of a few
+    joins (2^-24 each), and, relative to itself, by the logits' own errors in
+    the other rows (their drift, below 2^-12) and two roundings to the type."""
+    hidden, w, targets = nearly_sure(dtype, T, D)
+    _, lse = loss_of(hidden, [w], targets)
+    dh, _ = grads_of(hidden, [w], targets, lse, torch.ones(T, device="cuda"), want=("dhidden",))
+    z = hidden.double() @ w.double().t()
+    rest = z.clone()
+    rest.scatter_(1, targets[:, None], float("-inf"))
+    picked = z.gather(1, targets[:, None])[:, 0]
+    other = torch.logsumexp(rest, 1) - picked            # log of (1 - p) / p
+    want = -torch.sigmoid(other)
+    assert (picked[targets == 0] > 5).all() and (picked[targets == 1] < -5).all() and picked.abs().max() < 16
+    assert want.abs().min() < 1e-5 and want.abs().max() < 2e-3
+    got = dh[0][:, D - 2:].double().gather(1, targets[:, None])[:, 0]
+    tol = 2.0 ** -22 + 136 * 2.0 ** -24 + want.abs() * (2.0 ** -12 + 2 * UNIT[dtype]) + (2.0 ** -24 if dtype == "f16" else 0)
+    err = (got - want).abs()
+    assert (err <= tol).all(), f"off by {err.max().item():.3g}, {(err / tol).max().item():.3g} times what is allowed"
