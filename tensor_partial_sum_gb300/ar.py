@@ -210,7 +210,8 @@ def _layout_pointers(xs, rows, row, ne1, kind, call):
     caller's).  One pass: a small call's time is mostly spent here."""
     ptrs = []
     more = ne1 - 1
-    n = more * row + row if ne1 and row else 0
+    n = more * row + row
+    empty = not (ne1 and row)  # such a call touches no buffer
     for k, x in enumerate(xs):
         if x is None:
             ptrs.append(0)
@@ -218,18 +219,18 @@ def _layout_pointers(xs, rows, row, ne1, kind, call):
         if type(x) is int:
             ptrs.append(x)
             continue
-        if not getattr(x, "is_cuda", False):
-            _reach(x)  # refuses host tensors
+        if empty or not getattr(x, "is_cuda", False):
+            if not empty:
+                _reach(x)  # refuses host tensors
             ptrs.append(_ptr(x) or 0)
             continue
-        if n:
-            if rows is not None:
-                n = more * rows[k] + row
-            if x.nbytes < n or not x.is_contiguous():
-                st = x.untyped_storage()
-                reach = st.nbytes() - x.storage_offset() * x.element_size()
-                if reach < n:
-                    raise ValueError(f"{call}: {kind} {k} reaches {reach} bytes, its rows span {n}")
+        if rows is not None:
+            n = more * rows[k] + row
+        if x.nbytes < n or not x.is_contiguous():
+            st = x.untyped_storage()
+            reach = st.nbytes() - x.storage_offset() * x.element_size()
+            if reach < n:
+                raise ValueError(f"{call}: {kind} {k} reaches {reach} bytes, its rows span {n}")
         ptrs.append(x.data_ptr())
     return _packed(ptrs)
 
