@@ -91,3 +91,67 @@ def test_target_entry_of_nearly_sure_tokens(dtype, T, D):
     tol = 2.0 ** -22 + 136 * 2.0 ** -24 + want.abs() * (2.0 ** -12 + 2 * UNIT[dtype]) + (2.0 ** -24 if dtype == "f16" else 0)
     err = (got - want).abs()
     assert (err <= tol).all(), f"off by {err.max().item():.3g}, {(err / tol).max().item():.3g} times what is allowed"
+
+
+def one_sign_bound(z):
+    """Of a logit whose products all have one sign: a run's 32 products of 16
+    terms are cut off by at most two units in the last place of a running sum
+    that is half its end on average, the (up to 16) runs are added with half a
+    unit each.  Some 40 times 2^-23 of the logit; the log-sum-exp adds half a
+    unit of its own and of the logarithm, and 136 roundings of a sum near 1."""
+    return (32 + 8 + 2) * 2.0 ** -23 * z.abs().amax(1) + 136 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [5, 64, 66, 300])
+def test_log_sum_exp_of_long_sums_of_one_sign(dtype, T):
+    """Sums that only grow, where whatever is cut off adds up."""
+    hidden, w, targets = nearly_sure(dtype, T, 8194)
+    loss, lse = loss_of(hidden, [w], targets)
+    z = hidden.double() @ w.double().t()
+    want = torch.logsumexp(z, 1)
+    near_rows = z.gather(1, targets[:, None])
+    tol = one_sign_bound(near_rows)
+    assert ((lse.double() - want).abs() <= tol).all()
+    # the loss is a difference of two sums with the same drift
+    tol = 2.0 ** -22 + 136 * 2.0 ** -24 + 2.0 ** -12 * (want - near_rows[:, 0])
+    assert ((loss.double() - (want - near_rows[:, 0])).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("T,D,pieces", [(2, 230, [25929]), (5, 384, [2884] * 8), (12, 187, [51812]), (64, 1024, [9000, 700]),
+                                        (65, 640, [20000]), (300, 512, [10000, 5000]), (700, 1031, [4000, 77])])
+def test_float_gradients_are_no_worse_than_a_float_computation(T, D, pieces):
+    """Errors against 64 bits, relative to the whole gradient: at most twice
+    those of elementary float operations, and two roundings (2^-22)."""
+    hidden, weights, targets = make("f32", T, D, pieces, seed=D, ignored=0.1)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    dloss = torch.rand(T, device="cuda", generator=gen)
+    loss, lse = loss_of(hidden, weights, targets)
+    dh, dw = grads_of(hidden, weights, targets, lse, dloss)
+
+    def step(dtype):
+        h, ws = hidden.to(dtype), [w.to(dtype) for w in weights]
+        z = h @ torch.cat(ws).t()
+        top = z.amax(1, keepdim=True)
+        s = top[:, 0] + (z - top).exp().sum(1).log()
+        counted = targets >= 0
+        at = torch.where(counted, targets, 0)[:, None]
+        ls = torch.where(counted, s - z.gather(1, at)[:, 0], 0.0)
+        d = (z - s[:, None]).exp()
+        d.scatter_add_(1, at, torch.full_like(at, -1, dtype=dtype))
+        d *= torch.where(counted, dloss.to(dtype), 0.0)[:, None]
+        parts = d.split([w.shape[0] for w in ws], 1)
+        return [ls, s], [p @ w for p, w in zip(parts, ws)] + [p.t() @ h for p in parts]
+
+    allow = torch.backends.cuda.matmul.allow_tf32
+    torch.backends.cuda.matmul.allow_tf32 = False
+    try:
+        plain_values, plain = step(torch.float32)
+    finally:
+        torch.backends.cuda.matmul.allow_tf32 = allow
+    values, exact = step(torch.float64)
+    unit = 2 * 2.0 ** -23 * values[1].abs().max() + 2.0 ** -22
+    for got, mine, want in zip((loss, lse), plain_values, values):
+        assert (got.double() - want).abs().max() <= 2 * (mine.double() - want).abs().max() + unit
+    for got, mine, want in zip(dh + dw, plain, exact):
+        assert (got.double() - want).norm() <= 2 * (mine.double() - want).norm() + 2.0 ** -22 * want.norm()
