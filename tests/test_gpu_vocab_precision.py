@@ -155,3 +155,25 @@ def test_float_gradients_are_no_worse_than_a_float_computation(T, D, pieces):
         assert (got.double() - want).abs().max() <= 2 * (mine.double() - want).abs().max() + unit
     for got, mine, want in zip(dh + dw, plain, exact):
         assert (got.double() - want).norm() <= 2 * (mine.double() - want).norm() + 2.0 ** -22 * want.norm()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [48, 512])
+@pytest.mark.parametrize("V,depth", [(100, 3.1), (1000, 6.3), (20000, 9.1), (100000, 11.3), (100000, 15.7)])
+def test_many_small_terms_next_to_a_large_one(dtype, T, V, depth):
+    """Row 0 has the logit 0, all others have one far below it, and together
+    they weigh as much: the sum keeps them as well as a float computation does.
+
+    At most twice its error in the mean over the tokens, and half a unit."""
+    dt = DTYPES[dtype]
+    h, w = torch.zeros((T, 8), device="cuda", dtype=dt), torch.zeros((V, 8), device="cuda", dtype=dt)
+    h[:, 0] = torch.linspace(1, 1.05, T, device="cuda").to(dt)
+    w[1:, 0] = -depth
+    _, lse = loss_of(h, [w], torch.zeros(T, dtype=torch.int64, device="cuda"))
+    z = h.double() @ w.double().t()
+    want = torch.logsumexp(z, 1)
+    plain = z.float().exp().sum(1).log()                    # the logits are exact, the largest is 0
+
+    def off(x):
+        return (x.double() - want).square().mean().sqrt().item()
+    assert off(lse) <= 2 * off(plain) + 2.0 ** -24 * (want.abs().max().item() + 1)
