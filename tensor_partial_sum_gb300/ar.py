@@ -558,7 +558,8 @@ def ar_reduce_dropout(srcs, dsts, layout: ArLayout, dropout: ArDropout, dst_dtyp
     dcode = _dtype_code(dst_dtype)
     src, dst = _layout_buffers(srcs, dsts, layout, dcode, "ar_reduce_dropout")
     _typed_row(getattr(dropout, "_bias_obj", None), layout.ne0, dcode, "the bias", "ar_reduce_dropout")
-    _check(lib().ar_reduce_dropout(src, dst, len(dsts), ctypes.byref(layout), ctypes.byref(dropout), dcode, _dtype_code(wire_dtype), _stream(stream)), "ar_reduce_dropout")
+    _check(lib().ar_reduce_dropout(src, dst, len(dsts), ctypes.byref(layout), ctypes.byref(dropout), dcode,
+                                   _dtype_code(wire_dtype), _stream(stream)), "ar_reduce_dropout")
 
 
 def ar_check_dropout(R, srcs, dsts, layout: ArLayout, dropout: ArDropout, max_elems, dst_dtype, wire_dtype) -> int:

@@ -8,6 +8,8 @@
 
 #include <cuda_runtime.h>
 
+#include "ar.h"
+
 namespace tps {
 
 // The part of the context that a launch outside ar.cu needs.
@@ -32,6 +34,19 @@ int check_launch_device(const CallContext &c);
 
 // Bytes of an element, 0 for an unknown ar_dtype.
 inline size_t dtype_bytes(int dtype) { return dtype == 0 ? 4 : (dtype == 1 || dtype == 2) ? 2 : 0; }
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+inline bool spans_overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na && nb && x < y + nb && y < x + na;
+}
+
+// The status of a launch, whose error is cleared.
+inline int launched(cudaError_t e) {
+    if (e == cudaSuccess) return AR_OK;
+    cudaGetLastError();
+    return AR_ERR_CUDA;
+}
 
 // Launch a kernel that runs griddepcontrol.launch_dependents and
 // griddepcontrol.wait before it loads or stores anything: as a programmatic

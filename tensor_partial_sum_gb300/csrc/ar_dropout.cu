@@ -8,6 +8,8 @@
 #include "ar_kernels_dropout.cuh"
 
 using tps::dtype_bytes;
+using tps::launched;
+using tps::spans_overlap;
 
 namespace {
 
@@ -72,11 +74,6 @@ unsigned rows_per_block(const ar_layout *L, int n_sums) {
 unsigned row_blocks(const ar_layout *L, int n_sums) {
     const size_t r = rows_per_block(L, n_sums);
     return static_cast<unsigned>((L->ne1 + r - 1) / r);
-}
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return na && nb && x < y + nb && y < x + na;
 }
 
 // Bytes from the first element of a strided tensor to the end of its last row.
@@ -144,12 +141,6 @@ struct Alignment {
     bool holds(size_t es) const { return bits % (es == 4 ? 32 : 16) == 0; }
 };
 
-int launched(cudaError_t e) {
-    if (e == cudaSuccess) return AR_OK;
-    cudaGetLastError();
-    return AR_ERR_CUDA;
-}
-
 }  // namespace
 
 extern "C" {
@@ -164,7 +155,7 @@ int ar_check_dropout(int R, const void *const *srcs, void *const *dsts, int n_ds
         const size_t es = dtype_bytes(dst_dtype);
         if (reinterpret_cast<uintptr_t>(drop->bias) % es) return AR_ERR_INVALID_ARG;
         for (int d = 0; d < n_dsts; ++d)
-            if (overlap(drop->bias, L->ne0 * es, dsts[d], span_bytes(L, L->dst_row_bytes, d, es)))
+            if (spans_overlap(drop->bias, L->ne0 * es, dsts[d], span_bytes(L, L->dst_row_bytes, d, es)))
                 return AR_ERR_OVERLAP;
     }
     return AR_OK;
@@ -254,19 +245,19 @@ int ar_reduce_dropout_grad(const void *dy, void *const *dxs, int n_dxs, const ar
     for (int k = 0; k < 2; ++k) {
         if (!sums[k]) continue;
         if (reinterpret_cast<uintptr_t>(sums[k]) % sizeof(float)) return AR_ERR_INVALID_ARG;
-        if (overlap(sums[k], row, ws, need) || (k && overlap(sums[0], sums[0] ? row : 0, sums[1], row)))
+        if (spans_overlap(sums[k], row, ws, need) || (k && spans_overlap(sums[0], sums[0] ? row : 0, sums[1], row)))
             return AR_ERR_OVERLAP;
     }
     if (L->ne1 > 0) {
         const size_t in = span_bytes(L, L->src_row_bytes, 0, es);
-        if (overlap(ws, need, dy, in)) return AR_ERR_OVERLAP;
+        if (spans_overlap(ws, need, dy, in)) return AR_ERR_OVERLAP;
         for (int k = 0; k < 2; ++k)
-            if (sums[k] && overlap(sums[k], row, dy, in)) return AR_ERR_OVERLAP;
+            if (sums[k] && spans_overlap(sums[k], row, dy, in)) return AR_ERR_OVERLAP;
         for (int d = 0; d < n_dxs; ++d) {
             const size_t out = span_bytes(L, L->dst_row_bytes, d, es);
-            if (overlap(ws, need, dxs[d], out)) return AR_ERR_OVERLAP;
+            if (spans_overlap(ws, need, dxs[d], out)) return AR_ERR_OVERLAP;
             for (int k = 0; k < 2; ++k)
-                if (sums[k] && overlap(sums[k], row, dxs[d], out)) return AR_ERR_OVERLAP;
+                if (sums[k] && spans_overlap(sums[k], row, dxs[d], out)) return AR_ERR_OVERLAP;
         }
     }
     st = tps::check_launch_device(c);

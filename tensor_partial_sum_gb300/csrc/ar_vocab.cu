@@ -9,6 +9,7 @@
 #include "ar_kernels_vocab.cuh"
 
 using tps::dtype_bytes;
+using tps::launched;
 using namespace tps::plan;
 
 namespace {
@@ -28,10 +29,7 @@ struct Span {
     size_t n;
 };
 
-bool overlap(const Span &a, const Span &b) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.n && b.n && x < y + b.n && y < x + a.n;
-}
+bool overlap(const Span &a, const Span &b) { return tps::spans_overlap(a.p, a.n, b.p, b.n); }
 
 // Whether an output overlaps an input or another output.
 bool any_overlap(const Span *in, int n_in, const Span *out, int n_out) {
@@ -42,12 +40,6 @@ bool any_overlap(const Span *in, int n_in, const Span *out, int n_out) {
             if (overlap(out[o], out[q])) return true;
     }
     return false;
-}
-
-int launched(cudaError_t e) {
-    if (e == cudaSuccess) return AR_OK;
-    cudaGetLastError();
-    return AR_ERR_CUDA;
 }
 
 template <typename P>
@@ -109,7 +101,6 @@ unsigned tail_box(size_t rows, int bn) {
     return static_cast<unsigned>((width < bn ? width : bn) / 2);
 }
 
-// A call under way: what its launches share.
 // The two maps of a K-major A: boxes of 128 rows, and of the rows left over (8 at least).
 bool make_a_maps(tps::VocabGemmParams &p, bool f16, const void *base, size_t cols, size_t rows, size_t parts, size_t ld,
                  size_t part) {
@@ -119,6 +110,7 @@ bool make_a_maps(tps::VocabGemmParams &p, bool f16, const void *base, size_t col
            make_map(&p.a_tail_map, f16, base, cols, rows, parts, ld, part, p.a_tail ? static_cast<unsigned>(p.a_tail) : 8u);
 }
 
+// A call under way: what its launches share.
 struct Call {
     const ar_vocab *v;
     tps::CallContext c;
