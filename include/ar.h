@@ -510,7 +510,13 @@ int ar_check_vocab(const ar_vocab *v, size_t max_elems);
 
 /* Workspace of ar_vocab_loss (grad = 0) or ar_vocab_loss_grad (grad = 1) for
  * these arguments (host only; pointers are not read, their alignment and the
- * strides count). */
+ * strides count).  What can be large in it: copies of the weights in rows that
+ * the tiled copies can read (6 bytes an element of float weights, 2 of 16-bit
+ * ones off 16-byte boundaries, none otherwise), at most 2 GiB at a time; for
+ * the gradients a copy of the hidden states, the logits' gradient of one chunk
+ * of the vocabulary (256 MiB at most, or 256 vocabulary rows where that is
+ * more) and up to 64 MiB of partial sums (or one float copy of the hidden
+ * states' gradient for each piece where that is more). */
 int ar_vocab_workspace(const ar_vocab *v, int grad, size_t *bytes);
 
 #ifdef __cplusplus

@@ -356,10 +356,11 @@ __device__ __forceinline__ void sum_pairs(float (&x)[32]) {
 // tile while the epilogue reads the last.  Every wait is bounded; one that
 // runs out sets bit 1 of the status word, and the pair winds down.
 //
-// bf16, 2048 tokens, dim 4096, 32768 vocabulary rows: statistics 288 us, D 297, dH
-// and dW 539 (1.91, 1.85 and 2.04 PFLOP/s; cuBLAS peaks at 1.96), the tensor cores
-// 94 to 97% busy: they bound it, and in longer work the power cap does (4096 x
-// 4096 x 131072, four products: 10.0 ms, 1.77 PFLOP/s).
+// bf16, 2048 tokens, dim 4096, 32768 vocabulary rows: statistics 288 us, D 307, dH
+// and dW 531 (1.91, 1.79 and 2.07 PFLOP/s; cuBLAS peaks at 1.96), the tensor cores
+// 94, 86 and 97% busy: they bound it, and in longer work the power cap does (4096 x
+// 4096 x 131072, four products: 10.0 ms, 1.76 PFLOP/s).  D took 297 us with its logits in
+// one run; see kVRuns for why it does not.
 template <int MODE, int T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kVThreads, 1)
     ar_vocab_gemm_kernel(const __grid_constant__ VocabGemmParams p) {
