@@ -42,3 +42,12 @@ def test_losses_of_a_cut_vocabulary(dtype, T, D, pieces, pad):
     near(loss, want["loss"], "loss")
     del hidden, weights
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,D,pieces,pad", [(20, 64, [300000], 0), (5, 72, [280000, 100, 300001], 0), (1, 40, [530000], 3),
+                                            (66, 64, [400000, 33], 0), (600, 64, [120000, 250001], 1)])
+def test_gradients_of_a_cut_vocabulary(dtype, T, D, pieces, pad):
+    """More vocabulary rows than one chunk of the logits' gradient, from one token on."""
+    hidden, weights, targets = make(dtype, T, D, pieces, seed=T, pad=pad)
+    check_all(dtype, hidden, weights, targets, torch.linspace(0.5, 1, T, device="cuda"), pad)
