@@ -315,7 +315,7 @@ def _own_policy(s):
     tps = _library(1, s["T"])
     tps.ar_policy_loss(s["nll"], s["offsets"], s["advantages"], s["totals"], dnll=s["dnll"], old_nll=s["old_nll"],
                        ref_nll=s["ref_nll"], mask=s["mask"], clip_low=CLIP_LOW, clip_high=CLIP_HIGH,
-                       kl_weight=s["kl"], mean=s["mean"])
+                       kl_weight=s["kl"], mean=s["mean"], token_advantages=s["per_token"])
     return {"totals": s["totals"], "dnll": s["dnll"]}
 
 
