@@ -519,6 +519,181 @@ int ar_check_vocab(const ar_vocab *v, size_t max_elems);
  * states' gradient for each piece where that is more). */
 int ar_vocab_workspace(const ar_vocab *v, int grad, size_t *bytes);
 
+/* ---- normalisation, 8-bit checkpoints, policy loss -------------------------
+ * What stands around the reduction in a transformer layer and behind the
+ * vocabulary loss.  No counterpart in the pages either; the conventions of the
+ * training operators hold.
+ */
+
+/*
+ * An activation kept in 8 bits for the backward pass.  AR_CHECKPOINT_BLOCK
+ * adjacent elements of a row share a power of two, the smallest 2^e (e >= -127)
+ * with max |x| <= 448 * 2^e (AR_E4M3: four-bit exponents, three-bit fractions,
+ * as in the OCP 8-bit floating point specification) or 127 * 2^e (AR_INT8).  An
+ * element's code is x * 2^-e rounded to nearest, ties to even, and stands for
+ * code * 2^e; the block's scale byte is e + 127.  A block that holds an infinity
+ * or a NaN has the scale byte 255, and all of its elements stand for NaN.
+ * AR_E4M3 is off by at most 2^-4 of an element (or 2^-10 * 2^e), AR_INT8 by less
+ * than 1/127 of the block's largest element.
+ */
+typedef enum { AR_E4M3 = 0, AR_INT8 = 1 } ar_code;
+#define AR_CHECKPOINT_BLOCK 32
+typedef struct {
+    size_t ne0, ne1;          /* elements of a row, rows */
+    int format;               /* ar_code */
+    void *codes;              /* ne1 rows of ne0 bytes, each on a 16-byte boundary */
+    int64_t code_row_bytes;   /* row stride, a multiple of 16; 0: ne0 rounded up to 16 */
+    void *scales;             /* ne1 rows of ceil(ne0 / 32) bytes */
+    int64_t scale_row_bytes;  /* row stride; 0: packed */
+} ar_checkpoint;
+
+/*
+ * ar_checkpoint_pack / ar_checkpoint_unpack -- write a tensor of ne1 rows at
+ * `row_bytes` (0: packed) as a checkpoint, and read it back as the values that
+ * the codes stand for, at most the type's largest finite one in magnitude.
+ * Bytes between the rows of codes and scales are left alone.  The tensor may
+ * not overlap the checkpoint.  ne0 * ne1 <= max_elems.
+ */
+int ar_checkpoint_pack(const void *src, int64_t row_bytes, const ar_checkpoint *c, int dtype, cudaStream_t stream);
+int ar_checkpoint_unpack(const ar_checkpoint *c, void *dst, int64_t row_bytes, int dtype, cudaStream_t stream);
+
+/* Host-only validation of either call (no CUDA call). */
+int ar_check_checkpoint(const ar_checkpoint *c, const void *tensor, int64_t row_bytes, size_t max_elems, int dtype);
+
+typedef enum { AR_NORM_LAYER = 0, AR_NORM_RMS = 1 } ar_norm_kind;
+typedef struct {
+    int kind;           /* ar_norm_kind */
+    float eps;          /* added to the variance, finite and >= 0 */
+    const void *weight; /* NULL (ones), or ne0 T_dst elements */
+    const void *shift;  /* NULL (zeros), or ne0 T_dst elements */
+    const void *bias;   /* NULL, or one row of ne0 T_dst elements added to the rank sum */
+} ar_norm;
+
+/* What a forward pass keeps; every part is optional. */
+typedef struct {
+    void *const *sums;               /* n_sums T_dst tensors that receive the sum h */
+    const int64_t *sum_row_bytes;    /* their row strides, or NULL: packed */
+    int n_sums;                      /* 0..16 */
+    float *mean, *rstd;              /* NULL, or ne1 floats */
+    const ar_checkpoint *checkpoint; /* NULL, or where h is written in 8 bits */
+} ar_norm_kept;
+
+/*
+ * ar_reduce_norm -- ar_reduce_ex with a bias between the rank fold and the
+ * residual, and every row of the sum normalised:
+ *   a = fold_r wire(src[r][row][i]);  a = a + bias[i];  a = a + residual[row][i];
+ *   h = T_dst(a)                                 (each step rounded to float)
+ *   mean[row] = sum_i h / ne0                    (AR_NORM_RMS: 0)
+ *   rstd[row] = 1 / sqrt(sum_i (h - mean)^2 / ne0 + eps)
+ *   dst[d][row][i] = T_dst((h - mean) * rstd * weight[i] + shift[i])
+ * What is normalised is the sum as it is stored, so that the backward pass sees
+ * the same h.  Statistics are float sums in a fixed order: the same call gives
+ * the same bits.  Rows whose squares leave the float range do not keep the formula.
+ * Layout, in-place and overlap rules as for ar_reduce_ex, for the sums as for
+ * the destinations: a sum may be exactly a source or exactly the residual
+ * (h = h + allreduce(partials) in place); outputs may not overlap one another, nor the rows
+ * of weight, shift and bias.  `kept` may be NULL.
+ */
+int ar_reduce_norm(const void *const *srcs, void *const *dsts, int n_dsts, const ar_layout *layout,
+                   const ar_norm *norm, const ar_norm_kept *kept, int dst_dtype, int wire_dtype, cudaStream_t stream);
+
+/* Host-only validation of an ar_reduce_norm call (no CUDA call). */
+int ar_check_norm(int R, const void *const *srcs, void *const *dsts, int n_dsts, const ar_layout *layout,
+                  const ar_norm *norm, const ar_norm_kept *kept, size_t max_elems, int dst_dtype, int wire_dtype);
+
+/*
+ * ar_reduce_norm_grad -- the backward pass of ar_reduce_norm:
+ *   x = (h - mean[row]) * rstd[row];  g = dy[row][i] * weight[i]
+ *   dh = rstd * (g - sum_i g / ne0 - x * sum_i (g x) / ne0) + dsum[row][i]
+ *                                                (AR_NORM_RMS: without sum_i g / ne0)
+ *   dx[d][row][i] = T_dst(dh)                    d = 0 .. n_dxs-1
+ *   dweight[i] = sum over rows of dy x;  dshift[i] = sum over rows of dy
+ *   dbias[i]   = sum over rows of dh, unrounded: also the gradient of a residual
+ *                row broadcast with stride 0
+ * Rounding (through the wire type, to T_dst, to a checkpoint) is differentiated
+ * as the identity, so dx is the gradient of every active rank's partial and of a
+ * full residual.
+ *   dy         T_dst, ne1 rows at layout->src_row_bytes[0]
+ *   h          the sum as kept, ne1 rows at layout->src_row_bytes[1], or NULL:
+ *   checkpoint the sum in 8 bits (exactly one of the two)
+ *   mean, rstd as ar_reduce_norm wrote them (mean is not read with AR_NORM_RMS)
+ *   dsum       layout->residual at its row stride: the gradient that reaches h
+ *              on the residual stream, or NULL; inactive_mask has to be 0
+ *   dxs        1..16, at layout->dst_row_bytes; one may be exactly dy, h or dsum
+ *   norm       as in the forward call; shift and bias are not read
+ *   dweight, dshift, dbias  NULL, or ne0 floats each
+ *   workspace  16-byte aligned device memory of ar_reduce_norm_grad_workspace
+ *              bytes (NULL where that is 0); its contents do not matter
+ * Sums are taken in a fixed order: the same call gives the same bits.
+ */
+int ar_reduce_norm_grad(const void *dy, const void *h, const ar_checkpoint *checkpoint, const float *mean,
+                        const float *rstd, void *const *dxs, int n_dxs, const ar_layout *layout, const ar_norm *norm,
+                        float *dweight, float *dshift, float *dbias, void *workspace, size_t workspace_bytes,
+                        int dst_dtype, cudaStream_t stream);
+
+/* Workspace of an ar_reduce_norm_grad call with n_sums (0..3) of dweight, dshift
+ * and dbias given (host only, needs no context). */
+int ar_reduce_norm_grad_workspace(const ar_layout *layout, int n_sums, size_t *bytes);
+
+/*
+ * Clipped policy loss with a KL term over tokens that lie in sequences one
+ * after another.  nll, old and ref are negative log-likelihoods as
+ * ar_vocab_loss writes them: of the policy, of the policy that sampled the
+ * tokens, and of a reference.  For a counted token t of sequence s:
+ *   x = old[t] - nll[t];  ratio = exp(x);  A = its advantage
+ *   gain = min(ratio * A, clamp(ratio, 1 - clip_low, 1 + clip_high) * A)
+ *   d = nll[t] - ref[t];  kl = exp(d) - d - 1
+ *   loss[t] = -gain + kl_weight * kl
+ *   total = scale * sum_t w[t] loss[t]
+ * with w = 1 (AR_POLICY_SUM), 1 / counted tokens (AR_POLICY_TOKENS), or
+ * 1 / (counted tokens of s * sequences that have some) (AR_POLICY_SEQUENCES).
+ * Whether a ratio is outside of the clip range is decided from x and
+ * log(1 + clip_high), log(1 - clip_low) in 64 bits; outside, on the side that the
+ * minimum takes, the gradient of the gain is 0.  A token whose advantage is 0 has gain 0.
+ * A token does not count where its mask byte is 0 or where it lies in no
+ * sequence; whatever it holds (infinities and NaN included) then changes nothing
+ * and its gradient is 0.
+ */
+typedef enum { AR_POLICY_SUM = 0, AR_POLICY_TOKENS = 1, AR_POLICY_SEQUENCES = 2 } ar_policy_mean;
+typedef struct {
+    size_t tokens;            /* <= max_elems, < 2^32 */
+    size_t sequences;         /* < 2^31; 0: no token counts */
+    const int64_t *offsets;   /* device, sequences + 1: tokens offsets[s] .. offsets[s + 1] - 1 are those of
+                                 sequence s; not decreasing, within 0 .. tokens (no token outside of the
+                                 arrays is touched whatever they hold) */
+    const float *nll;         /* device, tokens floats */
+    const float *old_nll;     /* device, tokens floats, or NULL: x = 0 (sampled by this very policy) */
+    const float *ref_nll;     /* device, tokens floats, or NULL: no KL term */
+    const float *advantages;  /* device, one float for each sequence or token */
+    int token_advantages;     /* 0: sequences advantages, 1: tokens of them */
+    const uint8_t *mask;      /* device, tokens bytes, or NULL: every token of a sequence counts */
+    double clip_low, clip_high; /* 0 <= clip_low <= 1 (1: no lower limit), 0 <= clip_high (infinity: no upper limit) */
+    double kl_weight;         /* finite and >= 0 */
+    double scale;             /* finite: of the loss and of its gradient (a loss scale, say) */
+    int mean;                 /* ar_policy_mean */
+} ar_policy;
+
+/*
+ * ar_policy_loss -- the loss and its gradient.
+ *   totals     4 floats (device): total; its parts -scale * sum w gain and
+ *              scale * sum w kl (without kl_weight); the share of the counted tokens that
+ *              are clipped.
+ *   dnll       NULL, or tokens floats: the gradient of total, which
+ *              ar_vocab_loss_grad takes as dloss.  Written whole.
+ *   workspace  16-byte aligned device memory of ar_policy_workspace bytes; its
+ *              contents do not matter.
+ * dnll may be exactly nll, old_nll or ref_nll; otherwise outputs and workspace overlap neither
+ * each other nor an input.  The same call gives the same bits.
+ */
+int ar_policy_loss(const ar_policy *p, float *totals, float *dnll, void *workspace, size_t workspace_bytes,
+                   cudaStream_t stream);
+
+/* Host-only checks of an ar_policy (no CUDA call). */
+int ar_check_policy(const ar_policy *p, size_t max_elems);
+
+/* Workspace of ar_policy_loss (host only; pointers are not read). */
+int ar_policy_workspace(const ar_policy *p, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -3,7 +3,10 @@ tensor-parallel AllReduce) behind a small C ABI.
 
 Next to the reduction are the training operators around it: dropout joined to
 the sum (``ar_reduce_dropout``) and the loss over a vocabulary split into
-pieces (``ar_vocab_loss``), each with its gradient.
+pieces (``ar_vocab_loss``), each with its gradient; the normalisation of the
+summed residual stream (``ar_reduce_norm``) with its gradient, 8-bit
+checkpoints of activations (``ar_checkpoint_pack``), and a clipped policy loss
+on top of the vocabulary's (``ar_policy_loss``).
 
 The compute path is ``libtps_ar.so`` (hand-written CUDA for sm_103a);
 ``tensor_partial_sum_gb300.ar`` is a ctypes binding with the same names as
@@ -18,4 +21,7 @@ from .ar import (  # noqa: F401
     ArDropout, make_dropout, ar_reduce_dropout, ar_check_dropout, ar_reduce_dropout_grad,
     ar_reduce_dropout_grad_workspace, ArVocab, make_vocab, ar_check_vocab, ar_vocab_workspace, ar_vocab_loss,
     ar_vocab_loss_grad,
+    ArNorm, make_norm, ar_reduce_norm, ar_check_norm, ar_reduce_norm_grad, ar_reduce_norm_grad_workspace,
+    ArCheckpoint, AR_CHECKPOINT_BLOCK, make_checkpoint, empty_checkpoint, ar_checkpoint_pack, ar_checkpoint_unpack,
+    ar_check_checkpoint, ArPolicy, make_policy, ar_check_policy, ar_policy_workspace, ar_policy_loss,
 )

@@ -52,6 +52,35 @@ class ArVocab(ctypes.Structure):
                 ("ignore_index", ctypes.c_int64), ("dtype", ctypes.c_int)]
 
 
+class ArCheckpoint(ctypes.Structure):
+    """ar_checkpoint of include/ar.h."""
+    _fields_ = [("ne0", ctypes.c_size_t), ("ne1", ctypes.c_size_t), ("format", ctypes.c_int),
+                ("codes", ctypes.c_void_p), ("code_row_bytes", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("scale_row_bytes", ctypes.c_int64)]
+
+
+class ArNorm(ctypes.Structure):
+    """ar_norm of include/ar.h."""
+    _fields_ = [("kind", ctypes.c_int), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("shift", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class ArNormKept(ctypes.Structure):
+    """ar_norm_kept of include/ar.h."""
+    _fields_ = [("sums", ctypes.c_char_p), ("sum_row_bytes", ctypes.POINTER(ctypes.c_int64)),
+                ("n_sums", ctypes.c_int), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("checkpoint", ctypes.POINTER(ArCheckpoint))]
+
+
+class ArPolicy(ctypes.Structure):
+    """ar_policy of include/ar.h."""
+    _fields_ = [("tokens", ctypes.c_size_t), ("sequences", ctypes.c_size_t), ("offsets", ctypes.c_void_p),
+                ("nll", ctypes.c_void_p), ("old_nll", ctypes.c_void_p), ("ref_nll", ctypes.c_void_p),
+                ("advantages", ctypes.c_void_p), ("token_advantages", ctypes.c_int), ("mask", ctypes.c_void_p),
+                ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double), ("kl_weight", ctypes.c_double),
+                ("scale", ctypes.c_double), ("mean", ctypes.c_int)]
+
+
 class ARError(RuntimeError):
     def __init__(self, status: int, call: str):
         self.status = status
@@ -117,6 +146,21 @@ def lib() -> ctypes.CDLL:
         L.ar_check_vocab.restype = i
         L.ar_vocab_workspace.argtypes = [vcp, i, szp]
         L.ar_vocab_workspace.restype = i
+        np_, kp, cp, plp = (ctypes.POINTER(t) for t in (ArNorm, ArNormKept, ArCheckpoint, ArPolicy))
+        L.ar_reduce_norm.argtypes = [pp, pp, i, lp, np_, kp, i, i, vp]
+        L.ar_check_norm.argtypes = [i, pp, pp, i, lp, np_, kp, sz, i, i]
+        L.ar_reduce_norm_grad.argtypes = [vp, vp, cp, vp, vp, pp, i, lp, np_, vp, vp, vp, vp, sz, i, vp]
+        L.ar_reduce_norm_grad_workspace.argtypes = [lp, i, szp]
+        L.ar_checkpoint_pack.argtypes = [vp, i64, cp, i, vp]
+        L.ar_checkpoint_unpack.argtypes = [cp, vp, i64, i, vp]
+        L.ar_check_checkpoint.argtypes = [cp, vp, i64, sz, i]
+        L.ar_policy_loss.argtypes = [plp, vp, vp, vp, sz, vp]
+        L.ar_check_policy.argtypes = [plp, sz]
+        L.ar_policy_workspace.argtypes = [plp, szp]
+        for f in (L.ar_reduce_norm, L.ar_check_norm, L.ar_reduce_norm_grad, L.ar_reduce_norm_grad_workspace,
+                  L.ar_checkpoint_pack, L.ar_checkpoint_unpack, L.ar_check_checkpoint, L.ar_policy_loss,
+                  L.ar_check_policy, L.ar_policy_workspace):
+            f.restype = i
         _lib = L
     return _lib
 
@@ -692,3 +736,213 @@ def ar_vocab_loss_grad(hidden, weights, targets, lse, dloss, dhidden=None, dweig
     ws, ws_bytes = _workspace(ar_vocab_workspace(v, True), workspace, stream, hidden, call)
     _check(lib().ar_vocab_loss_grad(ctypes.byref(v), lse.data_ptr(), dloss.data_ptr(), _ptrs(dhidden), strides[0],
                                     _ptrs(dweights), strides[1], _ptr(ws), ws_bytes, _stream(stream)), call)
+
+
+# ---- normalisation, 8-bit checkpoints, policy loss -----------------------------
+
+CODES = {"e4m3": 0, "int8": 1}
+AR_CHECKPOINT_BLOCK = 32
+NORM_KINDS = {"layer": 0, "rms": 1}
+POLICY_MEANS = {"sum": 0, "tokens": 1, "sequences": 2}
+
+
+def make_checkpoint(codes, scales, ne0, format="e4m3", call="make_checkpoint") -> ArCheckpoint:
+    """An ar_checkpoint in torch buffers: uint8 ``codes`` [rows, at least ne0]
+    whose rows start on 16-byte boundaries, and uint8 ``scales`` [rows, at
+    least ceil(ne0 / 32)]."""
+    u8 = _torch().uint8
+    blocks = -(-ne0 // AR_CHECKPOINT_BLOCK)
+    for x, n, name in ((codes, ne0, "codes"), (scales, blocks, "scales")):
+        if not x.is_cuda:
+            raise TypeError(f"{call}: {name} is a {x.device.type} tensor, a device buffer is needed")
+        if x.dtype != u8 or x.dim() != 2 or x.shape[1] < n or (x.shape[1] > 1 and x.stride(1) != 1):
+            raise ValueError(f"{call}: {name} has to be uint8 [rows, {n}] with adjacent columns")
+    rows = codes.shape[0]
+    if scales.shape[0] != rows:
+        raise ValueError(f"{call}: {rows} rows of codes, {scales.shape[0]} of scales")
+    c = ArCheckpoint(ne0, rows, CODES[format], codes.data_ptr(), 0, scales.data_ptr(), 0)
+    if rows > 1:
+        if codes.stride(0) < ne0 or scales.stride(0) < blocks:  # an expanded tensor, for one
+            raise ValueError(f"{call}: rows lie over one another")
+        c.code_row_bytes, c.scale_row_bytes = codes.stride(0), scales.stride(0)
+    c._keep = (codes, scales)
+    return c
+
+
+def empty_checkpoint(ne0, ne1, format="e4m3", device="cuda") -> ArCheckpoint:
+    """An ar_checkpoint for ne1 rows of ne0 elements, in buffers of its own."""
+    torch = _torch()
+    codes = torch.empty((ne1, -(-ne0 // 16) * 16), dtype=torch.uint8, device=device)
+    scales = torch.empty((ne1, -(-ne0 // AR_CHECKPOINT_BLOCK)), dtype=torch.uint8, device=device)
+    return make_checkpoint(codes, scales, ne0, format, "empty_checkpoint")
+
+
+def ar_checkpoint_pack(src, checkpoint: ArCheckpoint, stream=None) -> None:
+    """Write the matrix ``src`` as an 8-bit checkpoint."""
+    call = "ar_checkpoint_pack"
+    row = _matrix(src, checkpoint.ne1, checkpoint.ne0, src.dtype, "src", call)
+    _check(lib().ar_checkpoint_pack(src.data_ptr(), row, ctypes.byref(checkpoint), _dtype_code(src.dtype),
+                                    _stream(stream)), call)
+
+
+def ar_checkpoint_unpack(checkpoint: ArCheckpoint, dst, stream=None) -> None:
+    """Write what an 8-bit checkpoint stands for into the matrix ``dst``."""
+    call = "ar_checkpoint_unpack"
+    row = _matrix(dst, checkpoint.ne1, checkpoint.ne0, dst.dtype, "dst", call)
+    _check(lib().ar_checkpoint_unpack(ctypes.byref(checkpoint), dst.data_ptr(), row, _dtype_code(dst.dtype),
+                                      _stream(stream)), call)
+
+
+def ar_check_checkpoint(checkpoint: ArCheckpoint, tensor, row_bytes, max_elems, dtype) -> int:
+    """Host-only validation of a pack or unpack call; returns the status."""
+    return lib().ar_check_checkpoint(ctypes.byref(checkpoint), _ptr(tensor), row_bytes, max_elems, _dtype_code(dtype))
+
+
+def make_norm(eps=1e-5, weight=None, shift=None, bias=None, kind="layer") -> ArNorm:
+    """An ar_norm: "layer" or "rms", with optional weight and shift rows and a
+    bias row that is added to the rank sum."""
+    n = ArNorm(NORM_KINDS[kind], eps, _ptr(weight), _ptr(shift), _ptr(bias))
+    n._rows = (weight, shift, bias)  # kept alive, and for the binding's checks
+    return n
+
+
+def _norm_rows(norm, ne0, dcode, call):
+    for x, name in zip(getattr(norm, "_rows", ()), ("the weight", "the shift", "the bias")):
+        if x is not None:
+            _typed_row(x, ne0, dcode, name, call)
+
+
+def _norm_kept(layout, dcode, sums, sum_row_bytes, mean, rstd, checkpoint, call):
+    """The ar_norm_kept of an ar_reduce_norm call, its buffers checked."""
+    ne0, ne1 = layout.ne0, layout.ne1
+    k = ArNormKept()
+    if sums:
+        rows = None if sum_row_bytes is None else _i64s(sum_row_bytes)
+        k.n_sums = len(sums)
+        k._pointers = _layout_pointers(sums, rows, ne0 * ESIZE[dcode], ne1, "sum", call)
+        k.sums = k._pointers
+        if rows is not None:
+            k.sum_row_bytes = rows
+    if mean is not None:
+        _typed_row(mean, ne1, AR_F32, "mean", call)
+        k.mean = _ptr(mean)
+    if rstd is not None:
+        _typed_row(rstd, ne1, AR_F32, "rstd", call)
+        k.rstd = _ptr(rstd)
+    if checkpoint is not None:
+        k.checkpoint = ctypes.pointer(checkpoint)
+    return k
+
+
+def ar_reduce_norm(srcs, dsts, layout: ArLayout, norm: ArNorm, dst_dtype, wire_dtype="bf16", sums=(), sum_row_bytes=None,
+                   mean=None, rstd=None, checkpoint=None, stream=None) -> None:
+    """The rank sum with bias and residual, each of its rows normalised into
+    every tensor of ``dsts``.  What a backward pass needs is kept on request:
+    the sum itself in every tensor of ``sums`` or as an 8-bit ``checkpoint``,
+    and each row's float32 ``mean`` and ``rstd``."""
+    call = "ar_reduce_norm"
+    dcode = _dtype_code(dst_dtype)
+    src, dst = _layout_buffers(srcs, dsts, layout, dcode, call)
+    _norm_rows(norm, layout.ne0, dcode, call)
+    kept = _norm_kept(layout, dcode, sums, sum_row_bytes, mean, rstd, checkpoint, call)
+    _check(lib().ar_reduce_norm(src, dst, len(dsts), ctypes.byref(layout), ctypes.byref(norm), ctypes.byref(kept), dcode,
+                                _dtype_code(wire_dtype), _stream(stream)), call)
+
+
+def ar_check_norm(R, srcs, dsts, layout: ArLayout, norm: ArNorm, max_elems, dst_dtype, wire_dtype, sums=(),
+                  sum_row_bytes=None, mean=None, rstd=None, checkpoint=None) -> int:
+    """Host-only validation of an ar_reduce_norm call; returns the status."""
+    dcode = _dtype_code(dst_dtype)
+    kept = _norm_kept(layout, dcode, sums, sum_row_bytes, mean, rstd, checkpoint, "ar_check_norm")
+    return lib().ar_check_norm(R, _ptrs(srcs), _ptrs(dsts), len(dsts), ctypes.byref(layout), ctypes.byref(norm),
+                               ctypes.byref(kept), max_elems, dcode, _dtype_code(wire_dtype))
+
+
+def ar_reduce_norm_grad_workspace(layout: ArLayout, n_sums: int) -> int:
+    """Workspace bytes of an ar_reduce_norm_grad call with ``n_sums`` of
+    dweight, dshift and dbias."""
+    n = ctypes.c_size_t(0)
+    _check(lib().ar_reduce_norm_grad_workspace(ctypes.byref(layout), n_sums, ctypes.byref(n)),
+           "ar_reduce_norm_grad_workspace")
+    return n.value
+
+
+def ar_reduce_norm_grad(dy, kept, dxs, layout: ArLayout, norm: ArNorm, mean, rstd, dst_dtype, dweight=None, dshift=None,
+                        dbias=None, workspace=None, stream=None) -> None:
+    """The backward pass of ar_reduce_norm from the ``kept`` sum (a tensor, or
+    the checkpoint that the forward call wrote): the gradient of the partials
+    and the residual into every tensor of ``dxs``, and, where asked for, the
+    float32 gradients of weight, shift and bias row.  The layout's residual is
+    the gradient that reaches the sum on the residual stream, its source
+    strides are those of ``dy`` and a kept tensor."""
+    call = "ar_reduce_norm_grad"
+    dcode = _dtype_code(dst_dtype)
+    saved = isinstance(kept, ArCheckpoint)
+    src, dst = _layout_buffers([dy] if saved else [dy, kept], dxs, layout, dcode, call)
+    ne0, ne1 = layout.ne0, layout.ne1
+    _norm_rows(norm, ne0, dcode, call)
+    n_sums = 0
+    for x, n, name in ((mean, ne1, "mean"), (rstd, ne1, "rstd"), (dweight, ne0, "dweight"), (dshift, ne0, "dshift"),
+                       (dbias, ne0, "dbias")):
+        if x is not None:
+            _typed_row(x, n, AR_F32, name, call)
+            n_sums += name[0] == "d"
+    ws, ws_bytes = _workspace(ar_reduce_norm_grad_workspace(layout, n_sums), workspace, stream, dy, call)
+    _check(lib().ar_reduce_norm_grad(_ptr(dy), None if saved else _ptr(kept), ctypes.byref(kept) if saved else None,
+                                     _ptr(mean), _ptr(rstd), dst, len(dxs), ctypes.byref(layout), ctypes.byref(norm),
+                                     _ptr(dweight), _ptr(dshift), _ptr(dbias), _ptr(ws), ws_bytes, dcode,
+                                     _stream(stream)), call)
+
+
+def make_policy(nll, offsets, advantages, old_nll=None, ref_nll=None, mask=None, clip_low=0.2, clip_high=0.2,
+                kl_weight=0.0, scale=1.0, mean="tokens", token_advantages=False, call="make_policy") -> ArPolicy:
+    """An ar_policy of torch tensors: float32 ``nll`` [tokens] (and ``old_nll``,
+    ``ref_nll``), int64 ``offsets`` [sequences + 1], float32 ``advantages``
+    [sequences] (with ``token_advantages`` [tokens]), and a uint8 or bool
+    ``mask`` [tokens]."""
+    torch = _torch()
+    T, S = nll.numel(), offsets.numel() - 1
+    if S < 0:
+        raise ValueError(f"{call}: offsets need at least one element")
+    _vector(offsets, S + 1, torch.int64, "offsets", call)
+    for x, n, name in ((nll, T, "nll"), (old_nll, T, "old_nll"), (ref_nll, T, "ref_nll"),
+                       (advantages, T if token_advantages else S, "advantages")):
+        if x is not None:
+            _vector(x, n, torch.float32, name, call)
+    if mask is not None:
+        _vector(mask, T, torch.bool if mask.dtype == torch.bool else torch.uint8, "mask", call)
+    p = ArPolicy(T, S, offsets.data_ptr(), nll.data_ptr(), _ptr(old_nll), _ptr(ref_nll), _ptr(advantages),
+                 int(token_advantages), _ptr(mask), clip_low, clip_high, kl_weight, scale, POLICY_MEANS[mean])
+    p._keep = (nll, offsets, advantages, old_nll, ref_nll, mask)
+    return p
+
+
+def ar_check_policy(p: ArPolicy, max_elems) -> int:
+    """Host-only checks of an ar_policy; returns the status."""
+    return lib().ar_check_policy(ctypes.byref(p), max_elems)
+
+
+def ar_policy_workspace(p: ArPolicy) -> int:
+    """Workspace bytes of ar_policy_loss."""
+    n = ctypes.c_size_t(0)
+    _check(lib().ar_policy_workspace(ctypes.byref(p), ctypes.byref(n)), "ar_policy_workspace")
+    return n.value
+
+
+def ar_policy_loss(nll, offsets, advantages, totals, dnll=None, old_nll=None, ref_nll=None, mask=None, clip_low=0.2,
+                   clip_high=0.2, kl_weight=0.0, scale=1.0, mean="tokens", token_advantages=False, workspace=None,
+                   stream=None) -> None:
+    """Clipped policy loss with a KL term over sequences of tokens: float32
+    ``totals`` [4] (loss, its policy part, the KL term, the clipped share of
+    the counted tokens) and, where given, the gradient ``dnll`` [tokens], which
+    ar_vocab_loss_grad takes as its ``dloss``.  ``nll`` is what ar_vocab_loss
+    wrote; ``workspace`` defaults to one from torch's allocator."""
+    call = "ar_policy_loss"
+    p = make_policy(nll, offsets, advantages, old_nll, ref_nll, mask, clip_low, clip_high, kl_weight, scale, mean,
+                    token_advantages, call)
+    f32 = _torch().float32
+    _vector(totals, 4, f32, "totals", call)
+    if dnll is not None:
+        _vector(dnll, p.tokens, f32, "dnll", call)
+    ws, ws_bytes = _workspace(ar_policy_workspace(p), workspace, stream, nll, call)
+    _check(lib().ar_policy_loss(ctypes.byref(p), totals.data_ptr(), _ptr(dnll), _ptr(ws), ws_bytes, _stream(stream)), call)

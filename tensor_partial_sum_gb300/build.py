@@ -18,11 +18,12 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libtps_ar.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("ar.cu", "ar_kernels_f32.cu", "ar_kernels_f16.cu", "ar_kernels_bf16.cu",
-                                             "ar_dropout.cu", "ar_vocab.cu")]
+                                             "ar_dropout.cu", "ar_vocab.cu", "ar_norm.cu", "ar_policy.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ar_kernels.cuh", "ar_kernels_ex.cuh", "ar_kernels_tma.cuh",
                                                    "ar_dispatch.h", "ar_context.h", "ar_philox.cuh",
                                                    "ar_kernels_dropout.cuh", "ar_kernels_vocab.cuh", "ar_vocab_plan.h",
-                                                   "ar_umma.cuh")] + [os.path.join(INCLUDE, "ar.h")]
+                                                   "ar_umma.cuh", "ar_buffers.h", "ar_codes.cuh", "ar_kernels_norm.cuh",
+                                                   "ar_kernels_policy.cuh")] + [os.path.join(INCLUDE, "ar.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,0 +1,331 @@
+// Device code of ar_policy_loss.
+//
+// The means need counts before the first gradient can be written, so the mask is read once for them and the
+// tokens once for the rest: zero the counts, count, compute, join the blocks' sums.  Counts are integers, whose
+// order of adding does not matter; floats are added in a fixed order.
+#pragma once
+
+#include <climits>
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "ar_kernels.cuh"
+
+namespace tps {
+
+constexpr int kPolicyThreads = 256;
+constexpr int kPolicyEach = 8;  // adjacent tokens of a thread
+constexpr int kPolicyChunk = kPolicyThreads * kPolicyEach;
+
+struct PolicyCounts {
+    unsigned ticket;
+    unsigned tokens;     // counted tokens
+    unsigned sequences;  // sequences that have some
+    unsigned pad;
+};
+
+struct PolicyParams {
+    unsigned tokens;
+    unsigned sequences;
+    const long long *offsets;
+    const float *nll, *old_nll, *ref_nll, *adv;
+    const uint8_t *mask;
+    int token_adv, mean, vec;  // vec: every array of tokens starts on a 16-byte boundary
+    double log_high, log_low;  // log(1 + clip_high), log(1 - clip_low)
+    float limit_high, limit_low;
+    double kl_weight, scale;
+    float *totals, *dnll;
+    PolicyCounts *counts;
+    unsigned *per_sequence;  // counted tokens of each sequence (the mean over sequences)
+    double *part;            // [block][4]: gain, kl, clipped, counted
+    unsigned blocks;
+};
+
+// How many of the sequences + 1 offsets are <= t, found by a warp, 32 probes at a time.  Stays within 0 ..
+// sequences + 1 whatever the offsets hold.
+__device__ __forceinline__ unsigned offsets_upto_warp(const PolicyParams &p, long long t) {
+    unsigned lo = 0, n = p.sequences + 1;
+    const unsigned lane = threadIdx.x % 32;
+    while (n > 0) {
+        const unsigned step = (n + 31) / 32, at = (lane + 1) * step - 1;
+        const bool le = at < n && p.offsets[lo + at] <= t;
+        const unsigned k = __ffs(~__ballot_sync(~0u, le)) - 1;  // 32 probes true: 32 (ffs of 0 is 0)
+        const unsigned found = k > 32 ? 32 : k;
+        lo += found * step;
+        n -= found * step;
+        n = n < step - 1 ? n : step - 1;
+    }
+    return lo;
+}
+// The same for one thread between lo and hi, which bound it.
+__device__ __forceinline__ unsigned offsets_upto(const PolicyParams &p, long long t, unsigned lo, unsigned hi) {
+    while (lo < hi) {
+        const unsigned mid = lo + (hi - lo) / 2;
+        if (p.offsets[mid] <= t)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Walks a thread's tokens through the sequences.  `upto` is the number of offsets <= the token, so the token's
+// sequence is upto - 1, none for 0 and sequences + 1.
+struct SequenceWalk {
+    unsigned upto, most;
+    long long next;  // the offset that ends this sequence
+    __device__ __forceinline__ void seek(const PolicyParams &p, long long t, unsigned lo, unsigned hi) {
+        most = hi;
+        upto = offsets_upto(p, t, lo, hi);
+        next = upto < hi ? p.offsets[upto] : LLONG_MAX;  // the chunk ends before the offset behind `hi`
+    }
+    __device__ __forceinline__ void advance(const PolicyParams &p, long long t) {
+        if (t >= next) seek(p, t, upto, most);
+    }
+    __device__ __forceinline__ bool inside(const PolicyParams &p) const { return upto > 0 && upto <= p.sequences; }
+};
+
+// The bounds of a chunk's offsets: those of its first and its last token.  `room`: 2 words.
+__device__ __forceinline__ void chunk_bounds(const PolicyParams &p, unsigned long long first, unsigned long long last,
+                                             unsigned *room) {
+    const int warp = threadIdx.x / 32;
+    if (warp < 2) {
+        const unsigned n = p.sequences ? offsets_upto_warp(p, static_cast<long long>(warp ? last : first)) : 0;
+        if (threadIdx.x % 32 == 0) room[warp] = n;
+    }
+    __syncthreads();
+}
+
+static __global__ void __launch_bounds__(256) ar_policy_zero_kernel(const __grid_constant__ PolicyParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i == 0) *p.counts = PolicyCounts{};
+    if (p.mean == 2 && i < p.sequences) p.per_sequence[i] = 0u;
+}
+
+template <int N>
+__device__ __forceinline__ unsigned block_count(unsigned n, unsigned *room) {
+    n = __reduce_add_sync(~0u, n);
+    if (threadIdx.x % 32 == 0) room[threadIdx.x / 32] = n;
+    __syncthreads();
+    unsigned s = 0;
+#pragma unroll
+    for (int k = 0; k < N / 32; ++k) s += room[k];
+    __syncthreads();
+    return s;
+}
+
+// Counted tokens, of each sequence where the mean is over sequences.
+static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_count_kernel(const __grid_constant__ PolicyParams p) {
+    __shared__ unsigned bounds[2], room[kPolicyThreads / 32];
+    __shared__ bool last_block;
+    pdl_launch_dependents();
+    pdl_wait();
+    const unsigned long long first = static_cast<unsigned long long>(blockIdx.x) * kPolicyChunk;
+    const unsigned long long end = first + kPolicyChunk < p.tokens ? first + kPolicyChunk : p.tokens;
+    unsigned counted = 0;
+    chunk_bounds(p, first, end - 1, bounds);
+    const unsigned long long t0 = first + threadIdx.x * kPolicyEach;
+    if (p.sequences && t0 < end) {
+        SequenceWalk w;
+        w.seek(p, static_cast<long long>(t0), bounds[0], bounds[1]);
+        unsigned here = 0, at = w.upto;
+        for (int k = 0; k < kPolicyEach && t0 + k < end; ++k) {
+            w.advance(p, static_cast<long long>(t0 + k));
+            if (p.mean == 2 && w.upto != at) {
+                if (here) atomicAdd(p.per_sequence + at - 1, here);
+                counted += here;
+                here = 0;
+                at = w.upto;
+            }
+            here += w.inside(p) && (!p.mask || p.mask[t0 + k]);
+        }
+        counted += here;
+        if (p.mean == 2 && here) atomicAdd(p.per_sequence + at - 1, here);
+    }
+    counted = block_count<kPolicyThreads>(counted, room);
+    if (threadIdx.x == 0) {
+        if (counted) atomicAdd(&p.counts->tokens, counted);
+        __threadfence();
+        last_block = atomicAdd(&p.counts->ticket, 1u) == gridDim.x - 1;
+    }
+    if (p.mean != 2) return;
+    __syncthreads();
+    if (!last_block) return;
+    __threadfence();
+    unsigned some = 0;
+    for (unsigned s = threadIdx.x; s < p.sequences; s += blockDim.x) some += __ldcg(p.per_sequence + s) > 0;
+    some = block_count<kPolicyThreads>(some, room);
+    if (threadIdx.x == 0) p.counts->sequences = some;
+}
+
+// exp(d) - d - 1 and its derivative exp(d) - 1.  Near zero the first is d^2 / 2 + d^3 / 6 + ..., of which the
+// difference would leave nothing: nine terms are off by less than 2^-27 of it up to |d| = 1/2.
+__device__ __forceinline__ void kl_terms(float d, float &kl, float &slope) {
+    if (fabsf(d) < 0.5f) {
+        float s = 1.0f / 3628800.0f;
+        s = fmaf(s, d, 1.0f / 362880.0f);
+        s = fmaf(s, d, 1.0f / 40320.0f);
+        s = fmaf(s, d, 1.0f / 5040.0f);
+        s = fmaf(s, d, 1.0f / 720.0f);
+        s = fmaf(s, d, 1.0f / 120.0f);
+        s = fmaf(s, d, 1.0f / 24.0f);
+        s = fmaf(s, d, 1.0f / 6.0f);
+        s = fmaf(s, d, 0.5f);
+        kl = s * d * d;
+        slope = kl + d;
+    } else {
+        slope = expf(d) - 1.0f;
+        kl = slope - d;
+    }
+}
+
+// Whether old - nll lies above (below) a 64-bit limit.  The rounded difference decides unless it is the rounded
+// limit itself, because rounding keeps the order.
+__device__ __forceinline__ bool above(float x, float old_nll, float nll, double limit) {
+    const float l = static_cast<float>(limit);
+    return x > l || (x == l && static_cast<double>(old_nll) - static_cast<double>(nll) > limit);
+}
+__device__ __forceinline__ bool below(float x, float old_nll, float nll, double limit) {
+    const float l = static_cast<float>(limit);
+    return x < l || (x == l && static_cast<double>(old_nll) - static_cast<double>(nll) < limit);
+}
+
+struct PolicySums {
+    float gain = 0.0f, kl = 0.0f;
+    unsigned clipped = 0, counted = 0;
+};
+
+// One counted token: its part of the sums under `weight`, and the gradient of its loss.
+__device__ __forceinline__ float policy_token(const PolicyParams &p, float nll, float old_nll, float ref_nll, float adv,
+                                              float weight, float beta, PolicySums &s) {
+    const float x = p.old_nll ? old_nll - nll : 0.0f;
+    const bool clipped = p.old_nll && ((adv > 0.0f && above(x, old_nll, nll, p.log_high)) ||
+                                       (adv < 0.0f && below(x, old_nll, nll, p.log_low)));
+    const float slope = clipped || adv == 0.0f ? 0.0f : expf(x) * adv;
+    const float gain = clipped ? (adv > 0.0f ? p.limit_high : p.limit_low) * adv : slope;
+    float kl = 0.0f, dkl = 0.0f;
+    if (p.ref_nll) kl_terms(nll - ref_nll, kl, dkl);
+    s.gain += weight * gain;
+    s.kl += weight * kl;
+    s.clipped += clipped;
+    s.counted += 1;
+    return beta == 0.0f ? slope : fmaf(beta, dkl, slope);
+}
+
+// Eight adjacent floats from token t on, those before `end`.
+__device__ __forceinline__ void tokens8(const float *a, unsigned long long t, unsigned long long end, int vec, float (&v)[8]) {
+    if (vec && t + 8 <= end) {
+        const float4 q = *reinterpret_cast<const float4 *>(a + t), r = *reinterpret_cast<const float4 *>(a + t + 4);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w, v[4] = r.x, v[5] = r.y, v[6] = r.z, v[7] = r.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = t + k < end ? a[t + k] : 0.0f;
+    }
+}
+
+static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_kernel(const __grid_constant__ PolicyParams p) {
+    __shared__ unsigned bounds[2];
+    __shared__ float room[4][kPolicyThreads / 32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const unsigned long long first = static_cast<unsigned long long>(blockIdx.x) * kPolicyChunk;
+    const unsigned long long end = first + kPolicyChunk < p.tokens ? first + kPolicyChunk : p.tokens;
+    const unsigned long long t0 = first + threadIdx.x * kPolicyEach;
+    const bool mine = t0 < end;
+    float nll[8], old_nll[8], ref_nll[8], adv[8], out[8];
+    unsigned counts = 0;
+    if (mine) {
+        tokens8(p.nll, t0, end, p.vec, nll);
+        if (p.old_nll) tokens8(p.old_nll, t0, end, p.vec, old_nll);
+        if (p.ref_nll) tokens8(p.ref_nll, t0, end, p.vec, ref_nll);
+        if (p.token_adv) tokens8(p.adv, t0, end, p.vec, adv);
+        if (!p.mask) {
+            counts = 0xFFu;
+        } else if (p.vec && t0 + 8 <= end) {
+            const uint2 m = *reinterpret_cast<const uint2 *>(p.mask + t0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) counts |= static_cast<unsigned>(((k < 4 ? m.x : m.y) >> (8 * (k & 3)) & 0xFFu) != 0) << k;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) counts |= static_cast<unsigned>(t0 + k < end && p.mask[t0 + k] != 0) << k;
+        }
+    }
+    chunk_bounds(p, first, end - 1, bounds);
+    PolicySums s;
+    if (mine) {
+        const unsigned n = p.mean == 0 ? 1u : p.mean == 1 ? p.counts->tokens : p.counts->sequences;
+        const float base = static_cast<float>(p.scale / (n ? n : 1u)), beta = static_cast<float>(p.kl_weight);
+        SequenceWalk w;
+        unsigned at = ~0u;
+        float a = 0.0f, weight = 1.0f;
+        if (p.sequences) w.seek(p, static_cast<long long>(t0), bounds[0], bounds[1]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            out[k] = 0.0f;
+            if (!((counts >> k) & 1u) || t0 + k >= end || !p.sequences) continue;
+            w.advance(p, static_cast<long long>(t0 + k));
+            if (!w.inside(p)) continue;
+            if (w.upto != at) {
+                at = w.upto;
+                if (!p.token_adv) a = p.adv[at - 1];
+                if (p.mean == 2) weight = 1.0f / static_cast<float>(p.per_sequence[at - 1]);
+            }
+            out[k] = policy_token(p, nll[k], old_nll[k], ref_nll[k], p.token_adv ? adv[k] : a, weight, beta, s) * (base * weight);
+        }
+        if (p.dnll) {
+            if (p.vec && t0 + 8 <= end) {
+                *reinterpret_cast<float4 *>(p.dnll + t0) = make_float4(out[0], out[1], out[2], out[3]);
+                *reinterpret_cast<float4 *>(p.dnll + t0 + 4) = make_float4(out[4], out[5], out[6], out[7]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (t0 + k < end) p.dnll[t0 + k] = out[k];
+            }
+        }
+    }
+    float v[4] = {s.gain, s.kl, static_cast<float>(s.clipped), static_cast<float>(s.counted)};  // counts: at most 2048
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) v[k] += __shfl_xor_sync(~0u, v[k], m);
+        if (threadIdx.x % 32 == 0) room[k][threadIdx.x / 32] = v[k];
+    }
+    __syncthreads();
+    if (threadIdx.x < 4) {
+        double sum = 0.0;
+        for (int q = 0; q < kPolicyThreads / 32; ++q) sum += room[threadIdx.x][q];
+        p.part[blockIdx.x * 4ull + threadIdx.x] = sum;
+    }
+}
+
+// The blocks' sums in a fixed order, and the totals.
+static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_join_kernel(const __grid_constant__ PolicyParams p) {
+    __shared__ double room[kPolicyThreads];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int which = threadIdx.x % 4;
+    double s = 0.0;
+    for (unsigned b = threadIdx.x / 4; b < p.blocks; b += kPolicyThreads / 4) s += p.part[b * 4ull + which];
+    room[threadIdx.x] = s;
+    for (int n = kPolicyThreads / 2; n >= 4; n >>= 1) {
+        __syncthreads();
+        if (threadIdx.x < n) room[threadIdx.x] += room[threadIdx.x + n];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const double counted = room[3] > 0.0 ? room[3] : 1.0;
+        const unsigned some = p.mean == 2 && p.blocks ? p.counts->sequences : 1u;
+        const double n = p.mean == 1 ? counted : some ? some : 1u;
+        const double gain = 0.0 - p.scale * room[0] / n, kl = p.scale * room[1] / n;
+        p.totals[0] = static_cast<float>(p.kl_weight == 0.0 ? gain : gain + p.kl_weight * kl);
+        p.totals[1] = static_cast<float>(gain);
+        p.totals[2] = static_cast<float>(kl);
+        p.totals[3] = static_cast<float>(room[2] / counted);
+    }
+}
+
+}  // namespace tps
