@@ -50,24 +50,38 @@ inline int launched(cudaError_t e) {
 
 // Launch a kernel that runs griddepcontrol.launch_dependents and
 // griddepcontrol.wait before it loads or stores anything: as a programmatic
-// dependent of the kernel before it on the stream when `pdl`, else plainly.
+// dependent of the kernel before it on the stream when `pdl`, else plainly; in
+// clusters of `cluster` blocks along x.
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*fn)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
-                             bool pdl, Args... args) {
+cudaError_t launch_clustered(void (*fn)(Params...), dim3 grid, unsigned cluster, unsigned threads, size_t smem,
+                             cudaStream_t stream, bool pdl, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
     // Not on the default streams: their implicit ordering against other
     // streams is left exactly as a plain launch has it.
     const bool default_stream = stream == nullptr || stream == cudaStreamLegacy || stream == cudaStreamPerThread;
-    cfg.numAttrs = (pdl && !default_stream) ? 1 : 0;
+    if (pdl && !default_stream) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = cluster;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
     return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*fn)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                             bool pdl, Args... args) {
+    return launch_clustered(fn, grid, 1u, threads, smem, stream, pdl, args...);
 }
 
 }  // namespace tps

@@ -119,7 +119,67 @@ int row_groups(size_t ne1, unsigned *rows_per_block) {
     return static_cast<int>((ne1 + rows - 1) / rows);
 }
 
+// How the forward pass lays a row over threads: `bx` lanes of a warp (WARP), or the threads of `cluster` blocks,
+// each with U units of eight columns.
+struct RowShape {
+    bool warp;
+    int U, bx, cluster;  // U = 0: too long for registers
+    unsigned threads;
+};
+
+RowShape forward_shape(size_t ne0, size_t ne1) {
+    const size_t units = (ne0 + 7) / 8;
+    RowShape s{};
+    s.cluster = 1;
+    if (units <= 128) {
+        s.warp = true;
+        s.threads = 128;
+        s.U = units <= 32 ? 1 : units <= 64 ? 2 : 4;
+        s.bx = 32;
+        while (s.bx > 4 && static_cast<size_t>(s.bx) / 2 >= units) s.bx /= 2;
+        return s;
+    }
+    size_t share = units;
+    while (share > tps::kRowThreads * 4 && s.cluster < tps::kRowBlocks) share = (units + (s.cluster *= 2) - 1) / s.cluster;
+    if (share > tps::kRowThreads * 4) return s;
+    s.U = share <= tps::kRowThreads ? 1 : share <= tps::kRowThreads * 2 ? 2 : 4;
+    s.threads = static_cast<unsigned>(((share + s.U - 1) / s.U + 31) / 32 * 32);
+    s.bx = static_cast<int>(s.threads);
+    return s;
+}
+
 using NormFn = void (*)(tps::NormParams);
+
+template <int Td, bool ALIGNED>
+NormFn pick_forward(const RowShape &s) {
+    if (s.warp)
+        return s.U == 1   ? tps::ar_norm_kernel<Td, ALIGNED, 1, true>
+               : s.U == 2 ? tps::ar_norm_kernel<Td, ALIGNED, 2, true>
+                          : tps::ar_norm_kernel<Td, ALIGNED, 4, true>;
+    return s.U == 1   ? tps::ar_norm_kernel<Td, ALIGNED, 1, false>
+           : s.U == 2 ? tps::ar_norm_kernel<Td, ALIGNED, 2, false>
+                      : tps::ar_norm_kernel<Td, ALIGNED, 4, false>;
+}
+
+NormFn forward_kernel(int dtype, bool aligned, const RowShape &s) {
+    if (aligned)
+        return dtype == AR_F32   ? pick_forward<tps::kF32, true>(s)
+               : dtype == AR_F16 ? pick_forward<tps::kF16, true>(s)
+                                 : pick_forward<tps::kBF16, true>(s);
+    return dtype == AR_F32   ? pick_forward<tps::kF32, false>(s)
+           : dtype == AR_F16 ? pick_forward<tps::kF16, false>(s)
+                             : pick_forward<tps::kBF16, false>(s);
+}
+
+// Whether every row of every buffer starts on a vector boundary (32 bytes for f32, else 16).
+struct Alignment {
+    uintptr_t bits = 0;
+    void add(const void *p, long long stride, size_t rows) {
+        bits |= reinterpret_cast<uintptr_t>(p) | (rows > 1 ? static_cast<uintptr_t>(stride) : 0);
+    }
+    bool holds(size_t es) const { return bits % (es == 4 ? 32 : 16) == 0; }
+};
+
 using GradFn = void (*)(tps::NormGradParams);
 
 }  // namespace
@@ -241,11 +301,29 @@ int ar_reduce_norm(const void *const *srcs, void *const *dsts, int n_dsts, const
     p.weight = norm->weight;
     p.shift = norm->shift;
     p.bias = norm->bias;
-    const NormFn fn = by_type<NormFn>(dst_dtype, tps::ar_norm_any_kernel<tps::kF32>, tps::ar_norm_any_kernel<tps::kF16>,
-                                      tps::ar_norm_any_kernel<tps::kBF16>);
-    const size_t blocks = L->ne1 < 65535 ? L->ne1 : 65535;
-    return launched(tps::launch_dependent(fn, dim3(static_cast<unsigned>(blocks)), static_cast<unsigned>(kAnyThreads), 0,
-                                          stream, c.pdl, p));
+    const RowShape s = forward_shape(L->ne0, L->ne1);
+    if (s.U == 0) {
+        const NormFn any = by_type<NormFn>(dst_dtype, tps::ar_norm_any_kernel<tps::kF32>, tps::ar_norm_any_kernel<tps::kF16>,
+                                           tps::ar_norm_any_kernel<tps::kBF16>);
+        const size_t blocks = L->ne1 < 65535 ? L->ne1 : 65535;
+        return launched(tps::launch_dependent(any, dim3(static_cast<unsigned>(blocks)), static_cast<unsigned>(kAnyThreads), 0,
+                                              stream, c.pdl, p));
+    }
+    Alignment al;
+    for (int r = 0; r < c.R; ++r)
+        if (x.src[r]) al.add(x.src[r], x.src_stride[r], x.ne1);
+    for (int d = 0; d < n_dsts; ++d) al.add(x.dst[d], x.dst_stride[d], x.ne1);
+    for (int k = 0; k < p.n_sums; ++k) al.add(p.sum[k], p.sum_stride[k], x.ne1);
+    al.add(x.residual, x.res_stride, x.ne1);
+    for (const void *row : {p.weight, p.shift, p.bias}) al.add(row, 0, 1);
+    p.bx = s.bx;
+    p.cluster = s.cluster;
+    const size_t turn = s.warp ? s.threads / s.bx : 1, most = (1u << 30) / s.cluster;
+    size_t groups = (L->ne1 + turn - 1) / turn;
+    if (groups > most) groups = most;
+    return launched(tps::launch_clustered(forward_kernel(dst_dtype, al.holds(dtype_bytes(dst_dtype)), s),
+                                          dim3(static_cast<unsigned>(groups * s.cluster)), static_cast<unsigned>(s.cluster),
+                                          s.threads, 0, stream, c.pdl, p));
 }
 
 int ar_reduce_norm_grad_workspace(const ar_layout *L, int n_sums, size_t *bytes) {
