@@ -7,6 +7,13 @@
 
 namespace tps {
 
+// A tensor's rows; no byte in front of the first or behind the last element is read.
+struct RowSource {
+    const char *base;
+    long long stride;
+    const char *end;
+};
+
 struct NormParams {
     ArExParams ex;
     void *sum[kMaxDsts];
@@ -18,13 +25,17 @@ struct NormParams {
     const void *weight, *shift, *bias;
     float *mean, *rstd;
     CodeRows kept;
-    int bx;       // threads along a row in a block
+    // rows through shared memory
+    RowSource source[kMaxRanks + 1];  // the active ranks in order, then the residual
+    int n_sources;
+    int bx;       // lanes along a row (a warp's)
     int cluster;  // blocks along a row
+    int stages;   // rows in the ring
+    int vecs;     // 16-byte vectors of a unit and row in it
 };
 
 struct NormGradParams {
-    const void *dy, *h, *dsum;  // h nullptr: kept in 8 bits
-    long long dy_stride, h_stride, dsum_stride;
+    RowSource dy, h, dsum;  // h.base nullptr: kept in 8 bits; dsum.base nullptr: none
     CodeRows kept;
     const float *mean, *rstd;
     void *dx[kMaxDsts];
@@ -34,8 +45,11 @@ struct NormGradParams {
     float inv_n;
     unsigned long long ne0, ne1;
     const void *weight;
-    float *part[3];  // [row block][ne0] partial column sums of dweight, dshift, dbias; nullptr: not wanted
-    float *row_sums; // [2][ne1]: sum g and sum g x of each row
+    float *part[3];  // [row block][part_ld] partial column sums of dweight, dshift, dbias; nullptr: not wanted
+    unsigned long long part_ld;
+    int bx, cluster, stages, vecs;
+    // rows of any length
+    float *row_sums;  // [2][ne1]: sum g and sum g x of each row
     unsigned rows_per_block;
 };
 
@@ -270,127 +284,258 @@ __device__ __forceinline__ void encode8(const CodeRows &c, size_t row, unsigned 
         c.scales[static_cast<long long>(row) * c.scale_row + static_cast<long long>(col / kCodeBlock)] = static_cast<uint8_t>(byte);
 }
 
-// A row in the registers of bx lanes (WARP: several rows a block, no barrier), of a block, or of a cluster's
-// blocks; a thread holds U units of eight columns.
+// ---- rows through shared memory -----------------------------------------------------
+//
+// A thread copies the vectors of its own columns into shared memory some rows ahead and reads them back itself, so
+// no barrier guards the ring, and what is in flight takes no registers.  Rows that start off a 16-byte boundary
+// are copied as the aligned vectors around each unit of eight columns and shifted into place on the way out.
+
+__device__ __forceinline__ void copy_async(unsigned to, const char *from, unsigned bytes) {
+    // the bytes after `bytes` become 0
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until all but the newest `ahead` (0..3) groups of this thread have landed.
+__device__ __forceinline__ void copy_wait(int ahead) {
+    if (ahead == 0)
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (ahead == 1)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (ahead == 2)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+template <int T, bool ALIGNED>
+constexpr int kUnitVecs = kWords8<T> / 4 + (ALIGNED ? 0 : 1);  // 16-byte vectors of a unit in the ring
+
+// Copy the vectors of the unit at `at` to `to`, `step` bytes apart.
+template <int T, bool ALIGNED>
+__device__ __forceinline__ void unit_copy(unsigned to, unsigned step, const char *at, const RowSource &s) {
+    constexpr int V = kUnitVecs<T, ALIGNED>;
+    const unsigned off = ALIGNED ? 0u : static_cast<unsigned>(reinterpret_cast<uintptr_t>(at) & 15);
+    const char *from = at - off;
+    if (from >= s.base && from + 16 * V <= s.end) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v < V - 1 || ALIGNED || off) copy_async(to + v * step, from + 16 * v, 16);
+        return;
+    }
+    // next to the tensor's ends
+    for (int v = 0; v < V; ++v, from += 16, to += step) {
+        if (from >= s.base && from < s.end) {
+            const long long left = s.end - from;
+            copy_async(to, from, left < 16 ? static_cast<unsigned>(left) : 16u);
+        } else {
+            // in front of the first element, or nothing at all: element by element
+            for (int e = 0; e < 16; e += Elem<T>::bytes) {
+                const bool inside = from + e >= s.base && from + e < s.end;
+                if constexpr (T == kF32) {
+                    const uint32_t x = inside ? *reinterpret_cast<const uint32_t *>(from + e) : 0u;
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + e), "r"(x) : "memory");
+                } else {
+                    const unsigned short x = inside ? *reinterpret_cast<const unsigned short *>(from + e) : static_cast<unsigned short>(0);
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + e), "h"(x) : "memory");
+                }
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint4 read_shared(unsigned at) {
+    uint4 q;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
+    return q;
+}
+
+// The words of the unit that unit_copy brought from an address whose low bits are `low`.
+template <int T, bool ALIGNED>
+__device__ __forceinline__ void unit_read(unsigned from, unsigned step, unsigned low, uint32_t (&w)[kWords8<T>]) {
+    constexpr int NW = kWords8<T>;
+    if constexpr (ALIGNED) {
+#pragma unroll
+        for (int k = 0; k < NW; k += 4) {
+            const uint4 q = read_shared(from + k / 4 * step);
+            w[k] = q.x, w[k + 1] = q.y, w[k + 2] = q.z, w[k + 3] = q.w;
+        }
+    } else {
+        uint32_t s[NW + 4];
+#pragma unroll
+        for (int k = 0; k < NW + 4; k += 4) {
+            const uint4 q = read_shared(from + k / 4 * step);
+            s[k] = q.x, s[k + 1] = q.y, s[k + 2] = q.z, s[k + 3] = q.w;
+        }
+        shift_words<NW>(s, low & 15, w);
+    }
+}
+
+// Set the elements from `n` (0..8) on to zero.
+template <int T>
+__device__ __forceinline__ void keep_first(uint32_t (&w)[kWords8<T>], unsigned long long n) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k >= n) {
+            if constexpr (T == kF32)
+                w[k] = 0u;
+            else
+                w[k / 2] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+        }
+}
+
+// The words of eight elements of a row that stays for the whole launch.
+template <int T, bool ALIGNED>
+__device__ __forceinline__ void row_words(const void *row, unsigned long long col, unsigned long long ne0, uint32_t (&w)[kWords8<T>]) {
+    if (!row || col >= ne0) {
+#pragma unroll
+        for (int k = 0; k < kWords8<T>; ++k) w[k] = 0u;
+        return;
+    }
+    Raw8<T, ALIGNED> raw;
+    const char *at = static_cast<const char *>(row) + col * Elem<T>::bytes;
+    load8<T, ALIGNED>(at, col, ne0, col + 8 <= ne0, raw);
+    raw8_words<T, ALIGNED>(raw, at, w);
+}
+
+// Which columns a thread holds: units of eight, bx apart, in the bx lanes of a warp (WARP: 1 / bx of the block's
+// threads to a row) or in the blocks of a cluster.
+template <bool WARP>
+struct RowThread {
+    int bx, by, tx, ty, cluster;
+    unsigned rank;
+    unsigned long long unit0;
+    size_t group, groups;
+    template <int U>
+    __device__ __forceinline__ void set(int p_bx, int p_cluster) {
+        const int t = static_cast<int>(threadIdx.x);
+        bx = WARP ? p_bx : static_cast<int>(blockDim.x);
+        by = WARP ? static_cast<int>(blockDim.x) / bx : 1;
+        tx = WARP ? t & (bx - 1) : t;
+        ty = WARP ? t / bx : 0;
+        cluster = WARP ? 1 : p_cluster;
+        rank = cluster == 1 ? 0u : cluster_rank();
+        unit0 = static_cast<unsigned long long>(rank) * bx * U + tx;
+        group = blockIdx.x / static_cast<unsigned>(cluster);
+        groups = gridDim.x / static_cast<unsigned>(cluster);
+    }
+    __device__ __forceinline__ unsigned long long col(int u) const { return (unit0 + static_cast<unsigned long long>(u) * bx) * 8; }
+    // For store8: whether the lanes before and after hold the columns before and after.
+    __device__ __forceinline__ bool prev() const { return tx > 0 && threadIdx.x % 32 > 0; }
+    __device__ __forceinline__ bool next(int u, unsigned long long ne0) const {
+        return tx + 1 < bx && threadIdx.x % 32 < 31 && col(u) + 16 <= ne0;
+    }
+};
+
+// The forward pass: persistent blocks, `stages` rows of the R operands and the residual in the ring.
 template <int Td, bool ALIGNED, int U, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : kRowThreads, WARP ? (U < 4 ? 8 : 4) : U < 4 ? 2 : 1)
-    ar_norm_kernel(const __grid_constant__ NormParams p) {
-    constexpr int NW = kWords8<Td>, RB = 16 / NW / U > 0 ? 16 / NW / U : 1;
+__global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_norm_kernel(const __grid_constant__ NormParams p) {
+    constexpr int NW = kWords8<Td>, V = kUnitVecs<Td, ALIGNED>;
+    extern __shared__ uint4 ring[];
     __shared__ RowRoom room[WARP ? 1 : 2];
     pdl_launch_dependents();
     const ArExParams &x = p.ex;
-    const int bx = WARP ? p.bx : static_cast<int>(blockDim.x), by = WARP ? 128 / bx : 1;
-    const int tx = WARP ? static_cast<int>(threadIdx.x) & (bx - 1) : static_cast<int>(threadIdx.x);
-    const int ty = WARP ? static_cast<int>(threadIdx.x) / bx : 0;
-    const int cluster = WARP ? 1 : p.cluster;
-    const unsigned rank = WARP || cluster == 1 ? 0u : cluster_rank();
-    const unsigned long long unit0 = static_cast<unsigned long long>(rank) * bx * U + tx;
-    auto col_of = [&](int u) { return (unit0 + static_cast<unsigned long long>(u) * bx) * 8; };
+    RowThread<WARP> t;
+    t.template set<U>(p.bx, p.cluster);
+    const unsigned step = blockDim.x * 16u * U;             // from a unit's vector to its next
+    const unsigned mine = static_cast<unsigned>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16u;
+    const unsigned stage_bytes = step * static_cast<unsigned>(p.vecs);
     pdl_wait();
-    if (!WARP && cluster > 1) cluster_barrier();  // every block of the cluster runs before one writes to another
-    const size_t group = blockIdx.x / static_cast<unsigned>(cluster), groups = gridDim.x / static_cast<unsigned>(cluster);
-    for (size_t row0 = group * by; row0 < x.ne1; row0 += groups * by) {
-        const size_t row = row0 + ty;
+    if (!WARP && t.cluster > 1) cluster_barrier();  // every block of the cluster runs before one writes to another
+    uint32_t weight[U][NW], shift[U][NW], bias[U][NW];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        row_words<Td, ALIGNED>(p.bias, t.col(u), x.ne0, bias[u]);
+        row_words<Td, ALIGNED>(p.weight, t.col(u), x.ne0, weight[u]);
+        row_words<Td, ALIGNED>(p.shift, t.col(u), x.ne0, shift[u]);
+    }
+    auto issue = [&](size_t row, int stage) {
+        if (row < x.ne1) {
+            unsigned to = mine + static_cast<unsigned>(stage) * stage_bytes;
+            for (int s = 0; s < p.n_sources; ++s) {
+                const RowSource &src = p.source[s];
+                const char *at = src.base + static_cast<long long>(row) * src.stride;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (t.col(u) < x.ne0)
+                        unit_copy<Td, ALIGNED>(to + u * (blockDim.x * 16u), step, at + t.col(u) * Elem<Td>::bytes, src);
+                to += V * step;
+            }
+        }
+        copy_commit();
+    };
+    const size_t turn = t.groups * t.by;
+    size_t ahead = t.group * t.by + t.ty;
+    int put = 0, get = 0;
+    for (int s = 0; s + 1 < p.stages; ++s, ahead += turn) issue(ahead, put++);
+    for (size_t row0 = t.group * t.by; row0 < x.ne1; row0 += turn, ahead += turn) {
+        issue(ahead, put);
+        if (++put == p.stages) put = 0;
+        copy_wait(p.stages - 1);
+        const size_t row = row0 + t.ty;
         const bool in_row = row < x.ne1;
         const long long r64 = static_cast<long long>(row);
+        const unsigned from = mine + static_cast<unsigned>(get) * stage_bytes;
+        if (++get == p.stages) get = 0;
         uint32_t h[U][NW];
         {
             float acc[U][8];
-            Raw8<Td, ALIGNED> res[U];
-            auto res_at = [&](int u) {
-                return static_cast<const char *>(x.residual) + r64 * x.res_stride + static_cast<long long>(col_of(u)) * Elem<Td>::bytes;
+            // operand s of the ring, widened
+            auto operand = [&](int s, int u, float (&v)[8]) {
+                uint32_t w[NW];
+                const RowSource &src = p.source[s];
+                unit_read<Td, ALIGNED>(from + static_cast<unsigned>(s) * V * step + u * (blockDim.x * 16u), step,
+                                       static_cast<unsigned>(reinterpret_cast<uintptr_t>(src.base)) +
+                                           static_cast<unsigned>(row) * static_cast<unsigned>(src.stride) +
+                                           static_cast<unsigned>(t.col(u)) * Elem<Td>::bytes,
+                                       w);
+                widen8<Td>(w, v);
             };
-            if (x.residual) {
+            int s = 0;
+            for (int r = 0; r < x.R; ++r) {
+                const bool active = !((x.inactive >> r) & 1u);
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (in_row && col_of(u) < x.ne0) load8<Td, ALIGNED>(res_at(u), col_of(u), x.ne0, col_of(u) + 8 <= x.ne0, res[u]);
-            }
-            for (int r0 = 0; r0 < x.R; r0 += RB) {
-                Raw8<Td, ALIGNED> in[RB][U];
-                auto at = [&](int j, int u) {
-                    return static_cast<const char *>(x.src[r0 + j]) + r64 * x.src_stride[r0 + j] +
-                           static_cast<long long>(col_of(u)) * Elem<Td>::bytes;
-                };
-#pragma unroll
-                for (int j = 0; j < RB; ++j)
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (in_row && col_of(u) < x.ne0 && r0 + j < x.R && !((x.inactive >> (r0 + j)) & 1u))
-                            load8<Td, ALIGNED>(at(j, u), col_of(u), x.ne0, col_of(u) + 8 <= x.ne0, in[j][u]);
-#pragma unroll
-                for (int j = 0; j < RB; ++j) {
-                    if (r0 + j >= x.R) break;
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        float v[8] = {};  // an inactive rank adds +0
-                        if (in_row && col_of(u) < x.ne0 && !((x.inactive >> (r0 + j)) & 1u)) {
-                            uint32_t w[NW];
-                            raw8_words<Td, ALIGNED>(in[j][u], at(j, u), w);
-                            widen8<Td>(w, v);
-                            wire8<Td>(p.wire, v);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) acc[u][k] = r0 + j == 0 ? v[k] : __fadd_rn(acc[u][k], v[k]);
+                for (int u = 0; u < U; ++u) {
+                    float v[8] = {};  // an inactive rank adds +0
+                    if (active) {
+                        operand(s, u, v);
+                        wire8<Td>(p.wire, v);
                     }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) acc[u][k] = r == 0 ? v[k] : __fadd_rn(acc[u][k], v[k]);
                 }
+                s += active;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const bool on = in_row && col_of(u) < x.ne0;
                 float v[8];
-                uint32_t w[NW];
-                if (on && p.bias) {
-                    Raw8<Td, ALIGNED> b;
-                    const char *at = static_cast<const char *>(p.bias) + col_of(u) * Elem<Td>::bytes;
-                    load8<Td, ALIGNED>(at, col_of(u), x.ne0, col_of(u) + 8 <= x.ne0, b);
-                    raw8_words<Td, ALIGNED>(b, at, w);
-                    widen8<Td>(w, v);
+                if (p.bias) {
+                    widen8<Td>(bias[u], v);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) acc[u][k] = __fadd_rn(acc[u][k], v[k]);
                 }
-                if (on && x.residual) {
-                    raw8_words<Td, ALIGNED>(res[u], res_at(u), w);
-                    widen8<Td>(w, v);
+                if (x.residual) {
+                    operand(s, u, v);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) acc[u][k] = __fadd_rn(acc[u][k], v[k]);
                 }
                 word_pack<Td, NW>(acc[u], h[u]);
-                if (!on) {
-#pragma unroll
-                    for (int k = 0; k < NW; ++k) h[u][k] = 0u;
-                } else if (col_of(u) + 8 > x.ne0) {
-                    // nothing behind the row's end, where the sums look
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (col_of(u) + k >= x.ne0) {
-                            if constexpr (Td == kF32)
-                                h[u][k] = 0u;
-                            else
-                                h[u][k / 2] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                        }
-                }
+                // nothing behind the row's end, where the sums look
+                const unsigned long long col = t.col(u);
+                if (!in_row || col + 8 > x.ne0) keep_first<Td>(h[u], in_row && col < x.ne0 ? x.ne0 - col : 0);
             }
         }
-        auto ends = [&](int u, bool &on, bool &whole, bool &prev, bool &next) {
-            const unsigned long long col = col_of(u);
-            on = in_row && col < x.ne0;
-            whole = col + 8 <= x.ne0;
-            prev = tx > 0 && threadIdx.x % 32 > 0;
-            next = tx + 1 < bx && threadIdx.x % 32 < 31 && col + 16 <= x.ne0;
-        };
         if (p.n_sums || p.kept.codes) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                bool on, whole, prev, next;
-                ends(u, on, whole, prev, next);
+                const unsigned long long col = t.col(u);
+                const bool on = in_row && col < x.ne0;
                 for (int s = 0; s < p.n_sums; ++s)
-                    store8<Td, ALIGNED>(static_cast<char *>(p.sum[s]) + r64 * p.sum_stride[s] +
-                                            static_cast<long long>(col_of(u)) * Elem<Td>::bytes,
-                                        h[u], col_of(u), x.ne0, whole, on, prev, next);
+                    store8<Td, ALIGNED>(static_cast<char *>(p.sum[s]) + r64 * p.sum_stride[s] + static_cast<long long>(col) * Elem<Td>::bytes,
+                                        h[u], col, x.ne0, col + 8 <= x.ne0, on, t.prev(), t.next(u, x.ne0));
                 if (p.kept.codes) {
                     float v[8];
                     widen8<Td>(h[u], v);
-                    encode8<NW>(p.kept, row, col_of(u), x.ne0, v, on);
+                    encode8<NW>(p.kept, row, col, x.ne0, v, on);
                 }
             }
         }
@@ -402,7 +547,7 @@ __global__ void __launch_bounds__(WARP ? 128 : kRowThreads, WARP ? (U < 4 ? 8 : 
                 widen8<Td>(h[u], v);
                 a += add8(v);
             }
-            row_sum2<WARP>(a, b, bx, cluster, rank, room[0]);
+            row_sum2<WARP>(a, b, t.bx, t.cluster, t.rank, room[0]);
             m = a * p.inv_n;
         }
         a = b = 0.0f;
@@ -412,50 +557,253 @@ __global__ void __launch_bounds__(WARP ? 128 : kRowThreads, WARP ? (U < 4 ? 8 : 
             widen8<Td>(h[u], v);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                v[k] = col_of(u) + k < x.ne0 ? v[k] - m : 0.0f;
+                v[k] = t.col(u) + k < x.ne0 ? v[k] - m : 0.0f;
                 q[k] = v[k] * v[k];
             }
             a += add8(v);
             b += add8(q);
         }
-        row_sum2<WARP>(a, b, bx, cluster, rank, room[WARP ? 0 : 1]);
+        row_sum2<WARP>(a, b, t.bx, t.cluster, t.rank, room[WARP ? 0 : 1]);
         const float off = p.rms ? 0.0f : a * p.inv_n;
         const float rstd = norm_rstd(b * p.inv_n, off, p.eps);
-        if (in_row && unit0 == 0) {
+        if (in_row && t.unit0 == 0) {
             if (p.mean) p.mean[row] = norm_mean(m, off);
             if (p.rstd) p.rstd[row] = rstd;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            bool on, whole, prev, next;
-            ends(u, on, whole, prev, next);
+            const unsigned long long col = t.col(u);
             float v[8], f[8];
             uint32_t w[NW];
             widen8<Td>(h[u], v);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = ((v[k] - m) - off) * rstd;
-            auto factors = [&](const void *from) {
-                Raw8<Td, ALIGNED> raw;
-                const char *at = static_cast<const char *>(from) + col_of(u) * Elem<Td>::bytes;
-                load8<Td, ALIGNED>(at, col_of(u), x.ne0, whole, raw);
-                raw8_words<Td, ALIGNED>(raw, at, w);
-                widen8<Td>(w, f);
-            };
-            if (on && p.weight) {
-                factors(p.weight);
+            if (p.weight) {
+                widen8<Td>(weight[u], f);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] *= f[k];
             }
-            if (on && p.shift) {
-                factors(p.shift);
+            if (p.shift) {
+                widen8<Td>(shift[u], f);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] += f[k];
             }
             word_pack<Td, NW>(v, w);
             for (int d = 0; d < x.n_dsts; ++d)
-                store8<Td, ALIGNED>(static_cast<char *>(x.dst[d]) + r64 * x.dst_stride[d] +
-                                        static_cast<long long>(col_of(u)) * Elem<Td>::bytes,
-                                    w, col_of(u), x.ne0, whole, on, prev, next);
+                store8<Td, ALIGNED>(static_cast<char *>(x.dst[d]) + r64 * x.dst_stride[d] + static_cast<long long>(col) * Elem<Td>::bytes,
+                                    w, col, x.ne0, col + 8 <= x.ne0, in_row && col < x.ne0, t.prev(), t.next(u, x.ne0));
+        }
+    }
+}
+
+// The values of eight codes and their scale byte.
+__device__ __forceinline__ void decode8(int format, uint2 c, unsigned byte, float (&v)[8]) {
+    const float scale = scale_value(byte);
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+        decode2(format, (k < 4 ? c.x : c.y) >> (8 * (k & 3)), v[k], v[k + 1]);
+        v[k] *= scale;
+        v[k + 1] *= scale;
+    }
+}
+
+// The backward pass in one pass over the rows: persistent blocks, dy, the kept sum and dsum of `stages` rows in the
+// ring.  The row's two sums are formed from one reading of the ring, the results from a second; a thread adds up its
+// columns over its block's rows in registers.
+template <int Td, bool ALIGNED, int U, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_norm_grad_kernel(const __grid_constant__ NormGradParams p) {
+    constexpr int NW = kWords8<Td>, V = kUnitVecs<Td, ALIGNED>;
+    extern __shared__ uint4 ring[];
+    __shared__ RowRoom room[WARP ? 1 : 2];
+    pdl_launch_dependents();
+    RowThread<WARP> t;
+    t.template set<U>(p.bx, p.cluster);
+    const unsigned step = blockDim.x * 16u * U;
+    const unsigned mine = static_cast<unsigned>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16u;
+    const unsigned stage_bytes = step * static_cast<unsigned>(p.vecs);
+    const unsigned at_h = V * step, at_dsum = at_h + (p.kept.codes ? 1u : V) * step;
+    pdl_wait();
+    if (!WARP && t.cluster > 1) cluster_barrier();
+    uint32_t weight[U][NW];
+    float sw[U][8] = {}, ss[U][8] = {}, sb[U][8] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) row_words<Td, ALIGNED>(p.weight, t.col(u), p.ne0, weight[u]);
+    auto issue = [&](size_t row, int stage) {
+        if (row < p.ne1) {
+            const unsigned to = mine + static_cast<unsigned>(stage) * stage_bytes;
+            const long long r64 = static_cast<long long>(row);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t.col(u) >= p.ne0) continue;
+                const unsigned slot = to + u * (blockDim.x * 16u);
+                const unsigned long long at = t.col(u) * Elem<Td>::bytes;
+                unit_copy<Td, ALIGNED>(slot, step, p.dy.base + r64 * p.dy.stride + at, p.dy);
+                if (p.kept.codes) {
+                    const unsigned long long left = p.ne0 - t.col(u);
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(slot + at_h),
+                                 "l"(p.kept.codes + r64 * p.kept.code_row + t.col(u)), "r"(left < 8 ? static_cast<unsigned>(left) : 8u)
+                                 : "memory");
+                } else {
+                    unit_copy<Td, ALIGNED>(slot + at_h, step, p.h.base + r64 * p.h.stride + at, p.h);
+                }
+                if (p.dsum.base) unit_copy<Td, ALIGNED>(slot + at_dsum, step, p.dsum.base + r64 * p.dsum.stride + at, p.dsum);
+            }
+        }
+        copy_commit();
+    };
+    // what is read straight into registers, a row ahead
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    unsigned next_scale[U] = {};
+    auto fetch = [&](size_t row) {
+        if (row >= p.ne1) return;
+        next_mean = p.rms ? 0.0f : p.mean[row];
+        next_rstd = p.rstd[row];
+        if (p.kept.codes) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (t.col(u) < p.ne0)
+                    next_scale[u] = p.kept.scales[static_cast<long long>(row) * p.kept.scale_row + static_cast<long long>(t.col(u) / kCodeBlock)];
+        }
+    };
+    const size_t turn = t.groups * t.by;
+    size_t ahead = t.group * t.by + t.ty;
+    int put = 0, get = 0, parity = 0;
+    fetch(ahead);
+    for (int s = 0; s + 1 < p.stages; ++s, ahead += turn) issue(ahead, put++);
+    for (size_t row0 = t.group * t.by; row0 < p.ne1; row0 += turn, ahead += turn, parity ^= 1) {
+        issue(ahead, put);
+        if (++put == p.stages) put = 0;
+        const size_t row = row0 + t.ty;
+        const bool in_row = row < p.ne1;
+        const long long r64 = static_cast<long long>(row);
+        const float mean = next_mean, rstd = next_rstd;
+        unsigned scale[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) scale[u] = next_scale[u];
+        fetch(row + turn);
+        copy_wait(p.stages - 1);
+        const unsigned from = mine + static_cast<unsigned>(get) * stage_bytes;
+        if (++get == p.stages) get = 0;
+        auto low = [&](const RowSource &s, int u) {
+            return static_cast<unsigned>(reinterpret_cast<uintptr_t>(s.base)) + static_cast<unsigned>(row) * static_cast<unsigned>(s.stride) +
+                   static_cast<unsigned>(t.col(u)) * Elem<Td>::bytes;
+        };
+        // dy and x of unit u, dy = 0 and x finite outside of the row
+        auto operands = [&](int u, float (&dy)[8], float (&xv)[8]) {
+            const unsigned slot = from + u * (blockDim.x * 16u);
+            const unsigned long long col = t.col(u);
+            const bool whole = in_row && col + 8 <= p.ne0;
+            const unsigned long long n = in_row && col < p.ne0 ? p.ne0 - col : 0;
+            uint32_t w[NW];
+            unit_read<Td, ALIGNED>(slot, step, low(p.dy, u), w);
+            if (!whole) keep_first<Td>(w, n);
+            widen8<Td>(w, dy);
+            if (p.kept.codes) {
+                uint2 c;
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(c.x), "=r"(c.y) : "r"(slot + at_h) : "memory");
+                decode8(p.kept.format, c, scale[u], xv);
+                if (!whole) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) xv[k] = k < n ? xv[k] : 0.0f;
+                }
+            } else {
+                unit_read<Td, ALIGNED>(slot + at_h, step, low(p.h, u), w);
+                if (!whole) keep_first<Td>(w, n);
+                widen8<Td>(w, xv);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) xv[k] = (xv[k] - mean) * rstd;
+            if (!whole) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) xv[k] = k < n ? xv[k] : 0.0f;
+            }
+        };
+        auto weighed = [&](int u, const float (&dy)[8], float (&g)[8]) {
+            if (p.weight) {
+                float f[8];
+                widen8<Td>(weight[u], f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) g[k] = dy[k] * f[k];
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) g[k] = dy[k];
+            }
+        };
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float dy[8], xv[8], g[8];
+            operands(u, dy, xv);
+            weighed(u, dy, g);
+            a += add8(g);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) xv[k] *= g[k];
+            b += add8(xv);
+        }
+        row_sum2<WARP>(a, b, t.bx, t.cluster, t.rank, room[WARP ? 0 : parity]);
+        const float c1 = p.rms ? 0.0f : a * p.inv_n, c2 = b * p.inv_n;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned long long col = t.col(u);
+            const bool on = in_row && col < p.ne0;
+            float dy[8], xv[8], d[8];
+            operands(u, dy, xv);
+            weighed(u, dy, d);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                d[k] = (d[k] - c1 - xv[k] * c2) * rstd;
+                sw[u][k] += dy[k] * xv[k];
+                ss[u][k] += dy[k];
+            }
+            uint32_t w[NW];
+            if (p.dsum.base) {
+                float f[8];
+                unit_read<Td, ALIGNED>(from + at_dsum + u * (blockDim.x * 16u), step, low(p.dsum, u), w);
+                widen8<Td>(w, f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) d[k] += f[k];
+            }
+            if (on) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sb[u][k] += d[k];  // columns behind the row's end are not looked at
+            }
+            word_pack<Td, NW>(d, w);
+            for (int k = 0; k < p.n_dxs; ++k)
+                store8<Td, ALIGNED>(static_cast<char *>(p.dx[k]) + r64 * p.dx_stride[k] + static_cast<long long>(col) * Elem<Td>::bytes,
+                                    w, col, p.ne0, col + 8 <= p.ne0, on, t.prev(), t.next(u, p.ne0));
+        }
+    }
+    copy_wait(0);
+    // this block's column sums; in the WARP form its row groups' are added in order
+#pragma unroll
+    for (int which = 0; which < 3; ++which) {
+        if (!p.part[which]) continue;
+        float *row = p.part[which] + t.group * p.part_ld;
+        if constexpr (WARP) {
+            float *sums = reinterpret_cast<float *>(ring);
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    sums[((t.ty * U + u) * 8 + k) * t.bx + t.tx] = which == 0 ? sw[u][k] : which == 1 ? ss[u][k] : sb[u][k];
+            __syncthreads();
+            const int width = t.bx * U * 8;
+            for (int c = threadIdx.x; c < width; c += blockDim.x) {
+                // column c of the block: unit c / 8, held by lane unit % bx as its unit / bx-th
+                const int unit = c / 8, at = (unit / t.bx * 8 + c % 8) * t.bx + unit % t.bx;
+                float s = 0.0f;
+                for (int y = 0; y < t.by; ++y) s += sums[y * width + at];
+                if (static_cast<unsigned long long>(c) < p.ne0) row[c] = s;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t.col(u) >= p.ne0) continue;
+                const float(&v)[8] = which == 0 ? sw[u] : which == 1 ? ss[u] : sb[u];
+                *reinterpret_cast<float4 *>(row + t.col(u)) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4 *>(row + t.col(u) + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            }
         }
     }
 }
@@ -465,9 +813,9 @@ template <int Td>
 __device__ __forceinline__ void grad_elem(const NormGradParams &p, size_t row, size_t i, float mean, float rstd, float &dy,
                                           float &g, float &x) {
     const long long at = static_cast<long long>(i);
-    dy = load_elem<Td, false>(static_cast<const char *>(p.dy) + static_cast<long long>(row) * p.dy_stride, at);
-    const float h = p.h ? load_elem<Td, false>(static_cast<const char *>(p.h) + static_cast<long long>(row) * p.h_stride, at)
-                        : decode_elem(p.kept, row, i);
+    dy = load_elem<Td, false>(p.dy.base + static_cast<long long>(row) * p.dy.stride, at);
+    const float h = p.h.base ? load_elem<Td, false>(p.h.base + static_cast<long long>(row) * p.h.stride, at)
+                             : decode_elem(p.kept, row, i);
     g = p.weight ? dy * load_elem<Td, false>(p.weight, at) : dy;
     x = (h - mean) * rstd;
 }
@@ -511,9 +859,8 @@ __global__ void __launch_bounds__(256) ar_norm_grad_any_kernel(const __grid_cons
             float d = g - x * (p.row_sums[p.ne1 + row] * p.inv_n);
             if (!p.rms) d -= p.row_sums[row] * p.inv_n;
             d *= rstd;
-            if (p.dsum)
-                d += load_elem<Td, false>(static_cast<const char *>(p.dsum) + static_cast<long long>(row) * p.dsum_stride,
-                                          static_cast<long long>(i));
+            if (p.dsum.base)
+                d += load_elem<Td, false>(p.dsum.base + static_cast<long long>(row) * p.dsum.stride, static_cast<long long>(i));
             s[0] += dy * x;
             s[1] += dy;
             s[2] += d;
@@ -528,7 +875,7 @@ __global__ void __launch_bounds__(256) ar_norm_grad_any_kernel(const __grid_cons
     if (g0 < 3 && i < p.ne0 && p.part[g0]) {
         float t = 0.0f;
         for (int q = 0; q < 8; ++q) t += sums[g0][q][c];
-        p.part[g0][blockIdx.y * p.ne0 + i] = t;
+        p.part[g0][blockIdx.y * p.part_ld + i] = t;
     }
 }
 
@@ -537,7 +884,7 @@ __global__ void __launch_bounds__(256) ar_norm_grad_any_kernel(const __grid_cons
 struct NormColumnSums {
     const float *part[3];
     float *out[3];
-    unsigned long long ne0;
+    unsigned long long ne0, ld;
     unsigned blocks;
 };
 
@@ -551,7 +898,7 @@ static __global__ void __launch_bounds__(256) ar_norm_column_sum_kernel(const __
     float s = 0.0f;
     if (i < p.ne0) {
 #pragma unroll 8
-        for (unsigned b = g; b < p.blocks; b += 8) s += part[b * p.ne0 + i];
+        for (unsigned b = g; b < p.blocks; b += 8) s += part[b * p.ld + i];
     }
     sums[g][c] = s;
     __syncthreads();

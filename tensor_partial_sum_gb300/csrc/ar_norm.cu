@@ -110,65 +110,128 @@ int wire_of(int dst, int wire) { return dst == wire ? AR_F32 : wire; }
 
 constexpr int kAnyThreads = 512;
 
-int row_groups(size_t ne1, unsigned *rows_per_block) {
-    // 64 rows or more to a block, at most 304 blocks of rows
-    const size_t least = 64, most = 304;
-    size_t rows = (ne1 + most - 1) / most;
-    if (rows < least) rows = least;
-    *rows_per_block = static_cast<unsigned>(rows);
-    return static_cast<int>((ne1 + rows - 1) / rows);
-}
-
-// How the forward pass lays a row over threads: `bx` lanes of a warp (WARP), or the threads of `cluster` blocks,
-// each with U units of eight columns.
+// How a row lies over threads: `bx` lanes of a warp (warp), or the threads of `cluster` blocks, each with U units of
+// eight columns; `vecs` vectors of a unit and row in the ring, `stages` rows deep.
 struct RowShape {
     bool warp;
-    int U, bx, cluster;  // U = 0: too long for registers
+    int U, bx, cluster, stages, vecs;  // U = 0: too long
     unsigned threads;
+    int resident;  // blocks on an SM
+    size_t smem;
 };
 
-RowShape forward_shape(size_t ne0, size_t ne1) {
+// Dynamic shared memory of each of n blocks on an SM, next to 2 KB of their own and 1 KB of the system's.
+constexpr size_t ring_bytes(size_t n) { return 227 * 1024 / n - 3 * 1024; }
+constexpr size_t kSMs = 152;
+
+// `most_u`: the most units that the kernel holds; vecs: 16-byte vectors of a unit and row.
+RowShape row_shape(size_t ne0, size_t ne1, int vecs, int most_u) {
     const size_t units = (ne0 + 7) / 8;
     RowShape s{};
     s.cluster = 1;
-    if (units <= 128) {
+    s.vecs = vecs;
+    if (units <= 64) {
         s.warp = true;
-        s.threads = 128;
-        s.U = units <= 32 ? 1 : units <= 64 ? 2 : 4;
+        s.threads = 256;
+        s.U = units <= 32 ? 1 : 2;
         s.bx = 32;
         while (s.bx > 4 && static_cast<size_t>(s.bx) / 2 >= units) s.bx /= 2;
-        return s;
+    } else {
+        auto share = [&] { return (units + s.cluster - 1) / s.cluster; };
+        auto bytes = [&] { return share() * 16 * static_cast<size_t>(vecs); };
+        auto fits = [&](size_t rows) {
+            return share() <= static_cast<size_t>(tps::kRowThreads) * most_u && bytes() * rows <= ring_bytes(1);
+        };
+        while (s.cluster < tps::kRowBlocks && !fits(2)) s.cluster *= 2;
+        if (!fits(1)) return s;
+        // few rows: the blocks that would be idle share them
+        while (s.cluster < tps::kRowBlocks && ne1 * s.cluster * 2 <= kSMs && share() >= 128) s.cluster *= 2;
+        s.U = share() <= 128 ? 1 : share() <= 1024 ? 2 : 4;
+        s.threads = static_cast<unsigned>(((share() + s.U - 1) / s.U + 31) / 32 * 32);
+        s.bx = static_cast<int>(s.threads);
     }
-    size_t share = units;
-    while (share > tps::kRowThreads * 4 && s.cluster < tps::kRowBlocks) share = (units + (s.cluster *= 2) - 1) / s.cluster;
-    if (share > tps::kRowThreads * 4) return s;
-    s.U = share <= tps::kRowThreads ? 1 : share <= tps::kRowThreads * 2 ? 2 : 4;
-    s.threads = static_cast<unsigned>(((share + s.U - 1) / s.U + 31) / 32 * 32);
-    s.bx = static_cast<int>(s.threads);
+    // rows ahead before blocks: two rows at least, four at most
+    const size_t row = static_cast<size_t>(s.threads) * s.U * 16 * vecs;
+    s.resident = static_cast<int>(tps::kRowThreads / s.threads);
+    while (s.resident > 1 && row * 2 > ring_bytes(s.resident)) --s.resident;
+    const size_t rows = ring_bytes(s.resident) / row;
+    s.stages = static_cast<int>(rows < 1 ? 1 : rows > 4 ? 4 : rows);
+    s.smem = row * s.stages;
+    if (s.smem > ring_bytes(1)) s.U = 0;
     return s;
 }
+
+// Blocks of a launch over ne1 rows, whole clusters.
+size_t row_grid(const RowShape &s, size_t ne1) {
+    const size_t turn = s.warp ? s.threads / s.bx : 1;
+    const size_t most = kSMs * s.resident / s.cluster;
+    const size_t groups = (ne1 + turn - 1) / turn;
+    return (groups < most ? groups : most) * s.cluster;
+}
+
+// Rows of partial column sums: of the element-wise form (64 rows or more each) and at most of the other.
+size_t any_rows(size_t ne1) {
+    const size_t rows = (ne1 + 303) / 304;
+    return rows < 64 ? 64 : rows;
+}
+size_t any_blocks(size_t ne1) { return (ne1 + any_rows(ne1) - 1) / any_rows(ne1); }
+size_t ring_blocks(size_t ne0, size_t ne1) {
+    // 512 threads of at most two units on an SM
+    const size_t units = (ne0 + 7) / 8, most = kSMs * (units <= 64 ? 2 : (1024 + units - 1) / units);
+    return ne1 < most ? ne1 : most;
+}
+size_t part_ld(size_t ne0) { return (ne0 + 7) / 8 * 8; }
+
+template <typename Fn>
+int allow_ring(Fn fn, const RowShape &s) {
+    if (s.smem <= 44 * 1024) return AR_OK;  // 48 KB with what the kernel declares itself
+    return launched(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ring_bytes(1))));
+}
+
+int vecs_of(size_t es, bool aligned) { return static_cast<int>(es) / 2 + (aligned ? 0 : 1); }
 
 using NormFn = void (*)(tps::NormParams);
 
 template <int Td, bool ALIGNED>
 NormFn pick_forward(const RowShape &s) {
-    if (s.warp)
-        return s.U == 1   ? tps::ar_norm_kernel<Td, ALIGNED, 1, true>
-               : s.U == 2 ? tps::ar_norm_kernel<Td, ALIGNED, 2, true>
-                          : tps::ar_norm_kernel<Td, ALIGNED, 4, true>;
+    if (s.warp) return s.U == 1 ? tps::ar_norm_kernel<Td, ALIGNED, 1, true> : tps::ar_norm_kernel<Td, ALIGNED, 2, true>;
     return s.U == 1   ? tps::ar_norm_kernel<Td, ALIGNED, 1, false>
            : s.U == 2 ? tps::ar_norm_kernel<Td, ALIGNED, 2, false>
                       : tps::ar_norm_kernel<Td, ALIGNED, 4, false>;
 }
 
-NormFn forward_kernel(int dtype, bool aligned, const RowShape &s) {
+using GradFn = void (*)(tps::NormGradParams);
+
+template <int Td, bool ALIGNED>
+GradFn pick_backward(const RowShape &s) {
+    if (s.warp) return s.U == 1 ? tps::ar_norm_grad_kernel<Td, ALIGNED, 1, true> : tps::ar_norm_grad_kernel<Td, ALIGNED, 2, true>;
+    return s.U == 1 ? tps::ar_norm_grad_kernel<Td, ALIGNED, 1, false> : tps::ar_norm_grad_kernel<Td, ALIGNED, 2, false>;
+}
+
+template <typename Fn, template <int, bool> class Pick>
+Fn pick_rows(int dtype, bool aligned, const RowShape &s) {
     if (aligned)
-        return dtype == AR_F32   ? pick_forward<tps::kF32, true>(s)
-               : dtype == AR_F16 ? pick_forward<tps::kF16, true>(s)
-                                 : pick_forward<tps::kBF16, true>(s);
-    return dtype == AR_F32   ? pick_forward<tps::kF32, false>(s)
-           : dtype == AR_F16 ? pick_forward<tps::kF16, false>(s)
-                             : pick_forward<tps::kBF16, false>(s);
+        return dtype == AR_F32   ? Pick<tps::kF32, true>::of(s)
+               : dtype == AR_F16 ? Pick<tps::kF16, true>::of(s)
+                                 : Pick<tps::kBF16, true>::of(s);
+    return dtype == AR_F32   ? Pick<tps::kF32, false>::of(s)
+           : dtype == AR_F16 ? Pick<tps::kF16, false>::of(s)
+                             : Pick<tps::kBF16, false>::of(s);
+}
+
+template <int Td, bool ALIGNED>
+struct Forward {
+    static NormFn of(const RowShape &s) { return pick_forward<Td, ALIGNED>(s); }
+};
+template <int Td, bool ALIGNED>
+struct Backward {
+    static GradFn of(const RowShape &s) { return pick_backward<Td, ALIGNED>(s); }
+};
+
+// A tensor's rows and where they end; `rows` of them, one where the stride is 0.
+tps::RowSource source_of(const void *p, long long stride, size_t rows, size_t row) {
+    const char *base = static_cast<const char *>(p);
+    return tps::RowSource{base, stride, base ? base + (rows - 1) * static_cast<size_t>(stride) + row : nullptr};
 }
 
 // Whether every row of every buffer starts on a vector boundary (32 bytes for f32, else 16).
@@ -179,8 +242,6 @@ struct Alignment {
     }
     bool holds(size_t es) const { return bits % (es == 4 ? 32 : 16) == 0; }
 };
-
-using GradFn = void (*)(tps::NormGradParams);
 
 }  // namespace
 
@@ -301,7 +362,20 @@ int ar_reduce_norm(const void *const *srcs, void *const *dsts, int n_dsts, const
     p.weight = norm->weight;
     p.shift = norm->shift;
     p.bias = norm->bias;
-    const RowShape s = forward_shape(L->ne0, L->ne1);
+    Alignment al;
+    for (int r = 0; r < c.R; ++r)
+        if (x.src[r]) {
+            al.add(x.src[r], x.src_stride[r], x.ne1);
+            p.source[p.n_sources++] = source_of(x.src[r], x.src_stride[r], x.ne1, packed);
+        }
+    for (int d = 0; d < n_dsts; ++d) al.add(x.dst[d], x.dst_stride[d], x.ne1);
+    for (int k = 0; k < p.n_sums; ++k) al.add(p.sum[k], p.sum_stride[k], x.ne1);
+    al.add(x.residual, x.res_stride, x.ne1);
+    if (x.residual) p.source[p.n_sources++] = source_of(x.residual, x.res_stride, x.ne1, packed);
+    for (const void *row : {p.weight, p.shift, p.bias}) al.add(row, 0, 1);
+    const size_t es = dtype_bytes(dst_dtype);
+    const bool aligned = al.holds(es);
+    const RowShape s = row_shape(L->ne0, L->ne1, vecs_of(es, aligned) * (p.n_sources ? p.n_sources : 1), 4);
     if (s.U == 0) {
         const NormFn any = by_type<NormFn>(dst_dtype, tps::ar_norm_any_kernel<tps::kF32>, tps::ar_norm_any_kernel<tps::kF16>,
                                            tps::ar_norm_any_kernel<tps::kBF16>);
@@ -309,29 +383,24 @@ int ar_reduce_norm(const void *const *srcs, void *const *dsts, int n_dsts, const
         return launched(tps::launch_dependent(any, dim3(static_cast<unsigned>(blocks)), static_cast<unsigned>(kAnyThreads), 0,
                                               stream, c.pdl, p));
     }
-    Alignment al;
-    for (int r = 0; r < c.R; ++r)
-        if (x.src[r]) al.add(x.src[r], x.src_stride[r], x.ne1);
-    for (int d = 0; d < n_dsts; ++d) al.add(x.dst[d], x.dst_stride[d], x.ne1);
-    for (int k = 0; k < p.n_sums; ++k) al.add(p.sum[k], p.sum_stride[k], x.ne1);
-    al.add(x.residual, x.res_stride, x.ne1);
-    for (const void *row : {p.weight, p.shift, p.bias}) al.add(row, 0, 1);
     p.bx = s.bx;
     p.cluster = s.cluster;
-    const size_t turn = s.warp ? s.threads / s.bx : 1, most = (1u << 30) / s.cluster;
-    size_t groups = (L->ne1 + turn - 1) / turn;
-    if (groups > most) groups = most;
-    return launched(tps::launch_clustered(forward_kernel(dst_dtype, al.holds(dtype_bytes(dst_dtype)), s),
-                                          dim3(static_cast<unsigned>(groups * s.cluster)), static_cast<unsigned>(s.cluster),
-                                          s.threads, 0, stream, c.pdl, p));
+    p.stages = s.stages;
+    p.vecs = s.vecs;
+    const NormFn fn = pick_rows<NormFn, Forward>(dst_dtype, aligned, s);
+    st = allow_ring(fn, s);
+    if (st != AR_OK) return st;
+    return launched(tps::launch_clustered(fn, dim3(static_cast<unsigned>(row_grid(s, L->ne1))), static_cast<unsigned>(s.cluster),
+                                          s.threads, s.smem, stream, c.pdl, p));
 }
 
 int ar_reduce_norm_grad_workspace(const ar_layout *L, int n_sums, size_t *bytes) {
     if (!L || !bytes || n_sums < 0 || n_sums > 3) return AR_ERR_INVALID_ARG;
-    if (L->ne0 && L->ne1 > SIZE_MAX / L->ne0 / 16) return AR_ERR_TOO_LARGE;
-    unsigned rows;
-    const size_t blocks = static_cast<size_t>(row_groups(L->ne1, &rows));
-    *bytes = L->ne0 ? (2 * L->ne1 + static_cast<size_t>(n_sums) * blocks * L->ne0) * sizeof(float) : 0;
+    if (L->ne0 > SIZE_MAX / 16 || (L->ne0 && L->ne1 > SIZE_MAX / L->ne0 / 16)) return AR_ERR_TOO_LARGE;
+    // which path a call takes depends on its pointers: room for the larger
+    const size_t any = 2 * L->ne1 + static_cast<size_t>(n_sums) * any_blocks(L->ne1) * part_ld(L->ne0);
+    const size_t ring = static_cast<size_t>(n_sums) * ring_blocks(L->ne0, L->ne1) * part_ld(L->ne0);
+    *bytes = L->ne0 ? (any > ring ? any : ring) * sizeof(float) : 0;
     return AR_OK;
 }
 
@@ -393,41 +462,68 @@ int ar_reduce_norm_grad(const void *dy, const void *h, const ar_checkpoint *ck, 
 
     tps::NormGradParams p;
     memset(&p, 0, sizeof p);
-    const unsigned blocks = static_cast<unsigned>(row_groups(L->ne1, &p.rows_per_block));
-    p.row_sums = static_cast<float *>(ws);
-    float *at = p.row_sums + 2 * L->ne1;
-    for (int k = 0; k < 3; ++k)
-        if (sums[k]) p.part[k] = at, at += static_cast<size_t>(blocks) * L->ne0;
+    size_t blocks = 0;
+    p.part_ld = part_ld(L->ne0);
+    auto place = [&](float *at) {
+        for (int k = 0; k < 3; ++k)
+            if (sums[k]) p.part[k] = at, at += blocks * p.part_ld;
+    };
     if (L->ne1 > 0) {
-        p.dy = dy;
-        p.dy_stride = static_cast<long long>(row_stride(L->src_row_bytes, 0, packed));
-        p.h = h;
-        if (h) p.h_stride = static_cast<long long>(row_stride(L->src_row_bytes, 1, packed));
+        Alignment al;
+        auto given_rows = [&](const void *t, long long stride) {
+            al.add(t, stride, L->ne1);
+            return source_of(t, stride, L->ne1, packed);
+        };
+        p.dy = given_rows(dy, static_cast<long long>(row_stride(L->src_row_bytes, 0, packed)));
+        if (h) p.h = given_rows(h, static_cast<long long>(row_stride(L->src_row_bytes, 1, packed)));
+        if (L->residual) p.dsum = given_rows(L->residual, L->residual_row_bytes);
         p.kept = code_rows(ck);
-        p.dsum = L->residual;
-        p.dsum_stride = L->residual_row_bytes;
         p.mean = mean;
         p.rstd = rstd;
         for (int d = 0; d < n_dxs; ++d) {
             p.dx[d] = dxs[d];
             p.dx_stride[d] = static_cast<long long>(row_stride(L->dst_row_bytes, d, packed));
+            al.add(p.dx[d], p.dx_stride[d], L->ne1);
         }
+        al.add(norm->weight, 0, 1);
         p.n_dxs = n_dxs;
         p.rms = rms;
         p.inv_n = 1.0f / static_cast<float>(L->ne0);
         p.ne0 = L->ne0;
         p.ne1 = L->ne1;
         p.weight = norm->weight;
-        const GradFn stats = by_type<GradFn>(dst_dtype, tps::ar_norm_row_sums_kernel<tps::kF32>,
-                                             tps::ar_norm_row_sums_kernel<tps::kF16>, tps::ar_norm_row_sums_kernel<tps::kBF16>);
-        const GradFn fn = by_type<GradFn>(dst_dtype, tps::ar_norm_grad_any_kernel<tps::kF32>,
-                                          tps::ar_norm_grad_any_kernel<tps::kF16>, tps::ar_norm_grad_any_kernel<tps::kBF16>);
-        const size_t rows = L->ne1 < 65535 ? L->ne1 : 65535;
-        st = launched(tps::launch_dependent(stats, dim3(static_cast<unsigned>(rows)), static_cast<unsigned>(kAnyThreads), 0,
-                                            stream, c.pdl, p));
-        if (st != AR_OK) return st;
-        st = launched(tps::launch_dependent(fn, dim3(static_cast<unsigned>((L->ne0 + 31) / 32), blocks), 256u, 0, stream,
-                                            c.pdl, p));
+        const bool aligned = al.holds(es);
+        const int v = vecs_of(es, aligned);
+        const RowShape s = row_shape(L->ne0, L->ne1, v + (h ? v : 1) + (L->residual ? v : 0), 2);
+        if (s.U) {
+            const size_t grid = row_grid(s, L->ne1);
+            blocks = grid / s.cluster;
+            place(static_cast<float *>(ws));
+            p.bx = s.bx;
+            p.cluster = s.cluster;
+            p.stages = s.stages;
+            p.vecs = s.vecs;
+            const GradFn fn = pick_rows<GradFn, Backward>(dst_dtype, aligned, s);
+            st = allow_ring(fn, s);
+            if (st != AR_OK) return st;
+            st = launched(tps::launch_clustered(fn, dim3(static_cast<unsigned>(grid)), static_cast<unsigned>(s.cluster), s.threads,
+                                                s.smem, stream, c.pdl, p));
+        } else {
+            blocks = any_blocks(L->ne1);
+            p.row_sums = static_cast<float *>(ws);
+            place(p.row_sums + 2 * L->ne1);
+            p.rows_per_block = static_cast<unsigned>(any_rows(L->ne1));
+            const GradFn stats = by_type<GradFn>(dst_dtype, tps::ar_norm_row_sums_kernel<tps::kF32>,
+                                                 tps::ar_norm_row_sums_kernel<tps::kF16>, tps::ar_norm_row_sums_kernel<tps::kBF16>);
+            const GradFn fn = by_type<GradFn>(dst_dtype, tps::ar_norm_grad_any_kernel<tps::kF32>,
+                                              tps::ar_norm_grad_any_kernel<tps::kF16>, tps::ar_norm_grad_any_kernel<tps::kBF16>);
+            const size_t rows = L->ne1 < 65535 ? L->ne1 : 65535;
+            st = launched(tps::launch_dependent(stats, dim3(static_cast<unsigned>(rows)), static_cast<unsigned>(kAnyThreads), 0,
+                                                stream, c.pdl, p));
+            if (st != AR_OK) return st;
+            st = launched(tps::launch_dependent(fn, dim3(static_cast<unsigned>((L->ne0 + 31) / 32), static_cast<unsigned>(blocks)), 256u,
+                                                0, stream, c.pdl, p));
+        }
         if (st != AR_OK) return st;
     }
     if (n_sums == 0) return AR_OK;
@@ -437,7 +533,8 @@ int ar_reduce_norm_grad(const void *dy, const void *h, const ar_checkpoint *ck, 
     for (int k = 0; k < 3; ++k)
         if (sums[k]) s.part[n] = p.part[k], s.out[n++] = sums[k];
     s.ne0 = L->ne0;
-    s.blocks = L->ne1 ? blocks : 0;
+    s.ld = p.part_ld;
+    s.blocks = static_cast<unsigned>(blocks);
     return launched(tps::launch_dependent(tps::ar_norm_column_sum_kernel,
                                           dim3(static_cast<unsigned>((L->ne0 + 31) / 32), static_cast<unsigned>(n_sums)),
                                           256u, 0, stream, c.pdl, s));
