@@ -3,15 +3,19 @@
 
 #include "ar_codes.cuh"
 #include "ar_kernels_ex.cuh"
+#include "ar_pairs.cuh"
 #include "ar_rows8.cuh"
 
 namespace tps {
 
-// A tensor's rows; no byte in front of the first or behind the last element is read.
+// A tensor's rows; no byte in front of the first or behind the last element is read.  `apart`: rows are 64 bytes or
+// more apart, so that only the first and the last row's vectors can reach outside.
 struct RowSource {
-    const char *base;
-    long long stride;
-    const char *end;
+    const char *base, *end;
+    long long wide;   // the stride, and where it fits 32 bits:
+    unsigned stride;
+    int apart;
+    __device__ __forceinline__ const char *row(unsigned r) const { return base + static_cast<unsigned long long>(r) * stride; }
 };
 
 struct NormParams {
@@ -28,10 +32,11 @@ struct NormParams {
     // rows through shared memory
     RowSource source[kMaxRanks + 1];  // the active ranks in order, then the residual
     int n_sources;
-    int bx;       // lanes along a row (a warp's)
-    int cluster;  // blocks along a row
-    int stages;   // rows in the ring
-    int vecs;     // 16-byte vectors of a unit and row in it
+    int apart;         // every source's rows are
+    int rows_aligned;  // weight, shift and bias start on 16-byte boundaries
+    int bx;            // lanes along a row (a warp's)
+    int units;         // of a thread
+    int cluster_bits;  // log2 of the blocks along a row
 };
 
 struct NormGradParams {
@@ -122,7 +127,7 @@ __device__ __forceinline__ float norm_mean(float m, float off) { return off == o
 // which would make a number of a NaN.
 __device__ __forceinline__ float norm_rstd(float square, float off, float eps) {
     const float v = square - off * off;
-    return 1.0f / sqrtf((v < 0.0f ? 0.0f : v) + eps);
+    return __frsqrt_rn((v < 0.0f ? 0.0f : v) + eps);
 }
 
 // A row of any length to a block, element by element: the sum is formed three times (for the mean, the squares,
@@ -176,19 +181,8 @@ __global__ void __launch_bounds__(512) ar_norm_any_kernel(const __grid_constant_
 // ---- rows in registers ------------------------------------------------------------
 
 constexpr int kRowBlocks = 8;   // most blocks of a cluster along a row
-constexpr int kRowThreads = 512;
-
-// A wire rounding chosen at run time, of a unit's eight operands.
-template <int Td>
-__device__ __forceinline__ void wire8(int wire, float (&v)[8]) {
-    if (wire == kF16) {
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) wire2<Td, kF16>(v[k], v[k + 1]);
-    } else if (wire == kBF16) {
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) wire2<Td, kBF16>(v[k], v[k + 1]);
-    }
-}
+constexpr int kRowThreads = 512;   // of the backward pass, at most
+constexpr int kNormThreads = 128;  // of the forward pass
 
 __device__ __forceinline__ unsigned cluster_rank() {
     unsigned r;
@@ -205,83 +199,56 @@ __device__ __forceinline__ void store_remote(const float *mine, unsigned rank, f
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(v) : "memory");
 }
 
-// Where the warps of a row's blocks leave their part of two sums.  Two of them in turn need one barrier a sum:
-// the next write to a room comes behind the barrier of the other.
+// Where the warps of a row's blocks leave their parts of sums.  Two rooms in turn need one barrier a sum: the next
+// write to a room comes behind the barrier of the other.
 struct RowRoom {
-    float a[kRowBlocks * kRowThreads / 32], b[kRowBlocks * kRowThreads / 32];
+    float2 v[kRowBlocks * kRowThreads / 32];
 };
 
-// The sums of a and b over a row, the same in all its threads and in a fixed order: over the `bx` lanes of a warp
+// The sums of a (and b) over a row, the same in all its threads and in a fixed order: over the `bx` lanes of a warp
 // (WARP), over the block, or over the blocks of a cluster, which write into each other's shared memory.
-template <bool WARP>
-__device__ __forceinline__ void row_sum2(float &a, float &b, int bx, int cluster, unsigned rank, RowRoom &room) {
+template <bool WARP, bool BOTH>
+__device__ __forceinline__ void row_sum(float &a, float &b, int bx, int cluster, unsigned rank, RowRoom &room) {
     if constexpr (WARP) {
         for (int k = bx / 2; k > 0; k >>= 1) {
             a += __shfl_xor_sync(~0u, a, k);
-            b += __shfl_xor_sync(~0u, b, k);
+            if constexpr (BOTH) b += __shfl_xor_sync(~0u, b, k);
         }
     } else {
+        auto lanes = [&] {
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1) {
-            a += __shfl_xor_sync(~0u, a, k);
-            b += __shfl_xor_sync(~0u, b, k);
-        }
+            for (int k = 16; k > 0; k >>= 1) {
+                a += __shfl_xor_sync(~0u, a, k);
+                if constexpr (BOTH) b += __shfl_xor_sync(~0u, b, k);
+            }
+        };
+        lanes();
         const int lane = threadIdx.x % 32, warps = static_cast<int>(blockDim.x) / 32, warp = threadIdx.x / 32;
-        int n = warps;
         if (cluster == 1) {
-            if (lane == 0) room.a[warp] = a, room.b[warp] = b;
+            if (lane == 0) room.v[warp] = make_float2(a, b);
             __syncthreads();
+            a = room.v[0].x, b = room.v[0].y;
+            for (int k = 1; k < warps; ++k) {
+                const float2 q = room.v[k];
+                a += q.x;
+                if constexpr (BOTH) b += q.y;
+            }
         } else {
-            n *= cluster;
             const int at = static_cast<int>(rank) * warps + warp;
             if (lane < cluster) {
-                store_remote(&room.a[at], static_cast<unsigned>(lane), a);
-                store_remote(&room.b[at], static_cast<unsigned>(lane), b);
+                store_remote(&room.v[at].x, static_cast<unsigned>(lane), a);
+                store_remote(&room.v[at].y, static_cast<unsigned>(lane), b);
             }
             cluster_barrier();
-        }
-        a = b = 0.0f;
-        for (int k = lane; k < n; k += 32) a += room.a[k], b += room.b[k];
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) {
-            a += __shfl_xor_sync(~0u, a, k);
-            b += __shfl_xor_sync(~0u, b, k);
+            a = b = 0.0f;
+            for (int k = lane; k < cluster * warps; k += 32) a += room.v[k].x, b += room.v[k].y;
+            lanes();
         }
     }
 }
 
 __device__ __forceinline__ float add8(const float (&v)[8]) {
     return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-}
-
-// The codes of eight columns from `col` on, of values that are 0 behind the row; four adjacent lanes hold a block
-// of 32 columns.  The whole warp calls.
-template <int NW>
-__device__ __forceinline__ void encode8(const CodeRows &c, size_t row, unsigned long long col, unsigned long long ne0,
-                                        const float (&v)[8], bool on) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-    top = max(top, __shfl_xor_sync(~0u, top, 1));
-    top = max(top, __shfl_xor_sync(~0u, top, 2));
-    if (!on) return;
-    const unsigned byte = scale_byte(c.format, top);
-    const float inv = scale_inverse(byte);
-    uint32_t w[2] = {};
-    if (byte != 255u) {
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) w[k / 4] |= encode2(c.format, v[k] * inv, v[k + 1] * inv) << (8 * (k & 3));
-    }
-    uint8_t *at = c.codes + static_cast<long long>(row) * c.code_row + static_cast<long long>(col);
-    if (col + 8 <= ne0) {
-        asm volatile("st.global.cs.v2.b32 [%0], {%1, %2};" ::"l"(at), "r"(w[0]), "r"(w[1]) : "memory");
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (col + k < ne0) at[k] = static_cast<uint8_t>(w[k / 4] >> (8 * (k & 3)));
-    }
-    if (col % kCodeBlock == 0)
-        c.scales[static_cast<long long>(row) * c.scale_row + static_cast<long long>(col / kCodeBlock)] = static_cast<uint8_t>(byte);
 }
 
 // ---- rows through shared memory -----------------------------------------------------
@@ -310,13 +277,13 @@ __device__ __forceinline__ void copy_wait(int ahead) {
 template <int T, bool ALIGNED>
 constexpr int kUnitVecs = kWords8<T> / 4 + (ALIGNED ? 0 : 1);  // 16-byte vectors of a unit in the ring
 
-// Copy the vectors of the unit at `at` to `to`, `step` bytes apart.
+// Copy the vectors of the unit at `at` to `to`, `step` bytes apart; `inner`: those around it lie inside the tensor.
 template <int T, bool ALIGNED>
-__device__ __forceinline__ void unit_copy(unsigned to, unsigned step, const char *at, const RowSource &s) {
+__device__ __forceinline__ void unit_copy(unsigned to, unsigned step, const char *at, const RowSource &s, bool inner) {
     constexpr int V = kUnitVecs<T, ALIGNED>;
     const unsigned off = ALIGNED ? 0u : static_cast<unsigned>(reinterpret_cast<uintptr_t>(at) & 15);
     const char *from = at - off;
-    if (from >= s.base && from + 16 * V <= s.end) {
+    if (inner || (from >= s.base && from + 16 * V <= s.end)) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (v < V - 1 || ALIGNED || off) copy_async(to + v * step, from + 16 * v, 16);
@@ -372,7 +339,7 @@ __device__ __forceinline__ void unit_read(unsigned from, unsigned step, unsigned
 
 // Set the elements from `n` (0..8) on to zero.
 template <int T>
-__device__ __forceinline__ void keep_first(uint32_t (&w)[kWords8<T>], unsigned long long n) {
+__device__ __forceinline__ void keep_first(uint32_t (&w)[kWords8<T>], int n) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         if (k >= n) {
@@ -399,14 +366,14 @@ __device__ __forceinline__ void row_words(const void *row, unsigned long long co
 
 // Which columns a thread holds: units of eight, bx apart, in the bx lanes of a warp (WARP: 1 / bx of the block's
 // threads to a row) or in the blocks of a cluster.
-template <bool WARP>
+template <int U, bool WARP>
 struct RowThread {
     int bx, by, tx, ty, cluster;
-    unsigned rank;
-    unsigned long long unit0;
+    unsigned rank, col0;  // of unit 0
+    int have[U];          // columns of each unit inside the row, 0..8
+    bool prev;            // for store8: the lane before holds the columns before
     size_t group, groups;
-    template <int U>
-    __device__ __forceinline__ void set(int p_bx, int p_cluster) {
+    __device__ __forceinline__ RowThread(int p_bx, int p_cluster, unsigned ne0) {
         const int t = static_cast<int>(threadIdx.x);
         bx = WARP ? p_bx : static_cast<int>(blockDim.x);
         by = WARP ? static_cast<int>(blockDim.x) / bx : 1;
@@ -414,184 +381,303 @@ struct RowThread {
         ty = WARP ? t / bx : 0;
         cluster = WARP ? 1 : p_cluster;
         rank = cluster == 1 ? 0u : cluster_rank();
-        unit0 = static_cast<unsigned long long>(rank) * bx * U + tx;
+        col0 = (rank * static_cast<unsigned>(bx) * U + static_cast<unsigned>(tx)) * 8u;
+        prev = tx > 0 && threadIdx.x % 32 > 0;
         group = blockIdx.x / static_cast<unsigned>(cluster);
         groups = gridDim.x / static_cast<unsigned>(cluster);
+#pragma unroll
+        for (int u = 0; u < U; ++u) have[u] = col(u) >= ne0 ? 0 : ne0 - col(u) >= 8 ? 8 : static_cast<int>(ne0 - col(u));
     }
-    __device__ __forceinline__ unsigned long long col(int u) const { return (unit0 + static_cast<unsigned long long>(u) * bx) * 8; }
-    // For store8: whether the lanes before and after hold the columns before and after.
-    __device__ __forceinline__ bool prev() const { return tx > 0 && threadIdx.x % 32 > 0; }
-    __device__ __forceinline__ bool next(int u, unsigned long long ne0) const {
+    __device__ __forceinline__ unsigned col(int u) const { return col0 + static_cast<unsigned>(u * bx) * 8u; }
+    // For store8: the lane after holds the columns after.
+    __device__ __forceinline__ bool next(int u, unsigned ne0) const {
         return tx + 1 < bx && threadIdx.x % 32 < 31 && col(u) + 16 <= ne0;
     }
 };
 
-// The forward pass: persistent blocks, `stages` rows of the R operands and the residual in the ring.
-template <int Td, bool ALIGNED, int U, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_norm_kernel(const __grid_constant__ NormParams p) {
-    constexpr int NW = kWords8<Td>, V = kUnitVecs<Td, ALIGNED>;
-    extern __shared__ uint4 ring[];
+// 32-bit words of a unit: 32 bytes from 32-byte boundaries, else eight columns.
+template <int T, bool ALIGNED>
+constexpr int kUnitWords = ALIGNED ? 8 : kWords8<T>;
+
+// A unit as loaded: its own words, or the aligned vectors around it with the bytes to shift by.
+template <int T, bool ALIGNED>
+struct Unit {
+    uint32_t w[kUnitWords<T, ALIGNED> + (ALIGNED ? 0 : 4)];
+    unsigned shift;
+};
+
+// `have` elements at `at`, one by one.
+template <int T, int W>
+__device__ __forceinline__ void element_words(const char *at, int have, uint32_t (&w)[W]) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = 0u;
+#pragma unroll
+    for (int k = 0; k < kCols<T, W>; ++k)
+        if (k < have) {
+            if constexpr (T == kF32)
+                w[k] = *reinterpret_cast<const volatile uint32_t *>(at + 4 * k);
+            else
+                w[k / 2] |= static_cast<uint32_t>(*reinterpret_cast<const volatile unsigned short *>(at + 2 * k)) << (16 * (k & 1));
+        }
+}
+
+// Load the unit at `at`, of which `have` columns are inside the row; `inner`: the vectors around it lie inside the
+// tensor.
+template <int T, bool ALIGNED>
+__device__ __forceinline__ void unit_load(Unit<T, ALIGNED> &r, const char *at, const RowSource &s, bool inner, int have) {
+    constexpr int W = kUnitWords<T, ALIGNED>;
+    if constexpr (ALIGNED) {
+        if (have == kCols<T, W>)
+            load_words<4 * W, false>(at, r.w);
+        else
+            element_words<T, W>(at, have, r.w);
+    } else {
+        const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(at) & 15);
+        const char *from = at - off;
+        r.shift = off;
+        if (inner || (from >= s.base && from + 4 * W + 16 <= s.end)) {
+#pragma unroll
+            for (int k = 0; k < W + 4; k += 4)
+                if (k < W || off) load_words<16, false>(from + 4 * k, reinterpret_cast<uint32_t(&)[4]>(r.w[k]));
+            return;
+        }
+        r.shift = 0;
+        element_words<T, W>(at, have, reinterpret_cast<uint32_t(&)[W]>(r.w));
+    }
+}
+template <int T, bool ALIGNED>
+__device__ __forceinline__ void unit_pairs(const Unit<T, ALIGNED> &r, pair_t (&v)[kCols<T, kUnitWords<T, ALIGNED>> / 2]) {
+    constexpr int W = kUnitWords<T, ALIGNED>;
+    if constexpr (ALIGNED) {
+        widen_pairs<T, W>(r.w, v);
+    } else {
+        uint32_t w[W];
+        shift_words<W>(r.w, r.shift, w);
+        widen_pairs<T, W>(w, v);
+    }
+}
+// A unit of a row that every block reads, through L1.
+template <int T, int W>
+__device__ __forceinline__ void row_unit(const void *row, unsigned col, int have, bool aligned, uint32_t (&w)[W]) {
+    const char *at = static_cast<const char *>(row) + col * Elem<T>::bytes;
+    if (aligned && have == kCols<T, W>) {
+#pragma unroll
+        for (int k = 0; k < W; k += 4) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(at + 4 * k));
+            w[k] = q.x, w[k + 1] = q.y, w[k + 2] = q.z, w[k + 3] = q.w;
+        }
+    } else {
+        element_words<T, W>(at, have, w);
+    }
+}
+
+// Store a unit at `at`; see store8 for units off 16-byte boundaries.  The whole warp calls.
+template <int T, bool ALIGNED>
+__device__ __forceinline__ void unit_store(char *at, const uint32_t (&w)[kUnitWords<T, ALIGNED>], unsigned col, unsigned ne0, int have,
+                                           bool prev, bool lane_next) {
+    constexpr int W = kUnitWords<T, ALIGNED>;
+    if constexpr (!ALIGNED) {
+        store8<T, false>(at, w, col, ne0, have == 8, have > 0, prev, lane_next && col + 16 <= ne0);
+    } else if (have == kCols<T, W>) {
+        store_words<4 * W>(at, w);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kCols<T, W>; ++k)
+            if (k < have) {
+                if constexpr (T == kF32)
+                    *reinterpret_cast<uint32_t *>(at + 4 * k) = w[k];
+                else
+                    *reinterpret_cast<unsigned short *>(at + 2 * k) = static_cast<unsigned short>(w[k / 2] >> (16 * (k & 1)));
+            }
+    }
+}
+
+// The codes of a unit's columns from `col` on, of values that are 0 behind the row; the lanes that hold a block of 32
+// columns are adjacent.  The whole warp calls.
+template <int N>
+__device__ __forceinline__ void unit_encode(const CodeRows &c, unsigned row, unsigned col, int have, const pair_t (&v)[N]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float2 f = halves(v[k]);
+        top = max(top, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
+    }
+    top = max(top, __shfl_xor_sync(~0u, top, 1));
+    if constexpr (N == 4) top = max(top, __shfl_xor_sync(~0u, top, 2));
+    if (!have) return;
+    const unsigned byte = scale_byte(c.format, top);
+    const pair_t inv = both(scale_inverse(byte));
+    uint32_t w[N / 2] = {};
+    if (byte != 255u) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float2 f = halves(mul2(v[k], inv));
+            w[k / 2] |= encode2(c.format, f.x, f.y) << (16 * (k & 1));
+        }
+    }
+    uint8_t *at = c.codes + row * static_cast<unsigned long long>(c.code_row) + col;
+    if (have == 2 * N) {
+        if constexpr (N == 8)
+            asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+        else
+            asm volatile("st.global.cs.v2.b32 [%0], {%1, %2};" ::"l"(at), "r"(w[0]), "r"(w[1]) : "memory");
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2 * N; ++k)
+            if (k < have) at[k] = static_cast<uint8_t>(w[k / 4] >> (8 * (k & 3)));
+    }
+    if (col % kCodeBlock == 0) c.scales[row * static_cast<unsigned long long>(c.scale_row) + col / kCodeBlock] = static_cast<uint8_t>(byte);
+}
+
+// Blocks on an SM: 72 registers a thread, 80 where a unit has 16 columns, 96 where it is shifted into place in rows
+// that share a block.
+template <int Td, bool ALIGNED, bool WARP>
+constexpr int kNormBlocks = ALIGNED ? (WARP || Td != kF32 ? 6 : 7) : (WARP ? 5 : 7);
+
+// The forward pass: bx lanes of a warp, a block or a cluster's blocks to a row, each thread with `units` units one
+// after another.  The sum h of a thread's columns waits in shared memory for the row's statistics, where only the
+// thread itself reads it: no barrier, few registers, and enough blocks on an SM that their phases overlap.
+template <int Td, bool ALIGNED, bool WARP>
+__global__ void __launch_bounds__(kNormThreads, kNormBlocks<Td, ALIGNED, WARP>) ar_norm_kernel(const __grid_constant__ NormParams p) {
+    constexpr int W = kUnitWords<Td, ALIGNED>, C = kCols<Td, W>, N = C / 2, RB = 16 / W;
+    extern __shared__ uint4 held[];
     __shared__ RowRoom room[WARP ? 1 : 2];
     pdl_launch_dependents();
     const ArExParams &x = p.ex;
-    RowThread<WARP> t;
-    t.template set<U>(p.bx, p.cluster);
-    const unsigned step = blockDim.x * 16u * U;             // from a unit's vector to its next
-    const unsigned mine = static_cast<unsigned>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16u;
-    const unsigned stage_bytes = step * static_cast<unsigned>(p.vecs);
+    const int T = static_cast<int>(blockDim.x), bx = WARP ? p.bx : T, by = WARP ? T / bx : 1, units = p.units;
+    const int tx = WARP ? static_cast<int>(threadIdx.x) & (bx - 1) : static_cast<int>(threadIdx.x);
+    const int ty = WARP ? static_cast<int>(threadIdx.x) / bx : 0;
+    const int cluster = WARP ? 1 : 1 << p.cluster_bits;
+    const unsigned rank = cluster == 1 ? 0u : cluster_rank();
+    const unsigned ne0 = static_cast<unsigned>(x.ne0), ne1 = static_cast<unsigned>(x.ne1);
+    const unsigned col0 = (rank * static_cast<unsigned>(bx * units) + static_cast<unsigned>(tx)) * C, hop = static_cast<unsigned>(bx) * C;
+    const unsigned group = blockIdx.x >> (WARP ? 0 : p.cluster_bits), groups = gridDim.x >> (WARP ? 0 : p.cluster_bits);
+    const int ranks = p.n_sources - (x.residual != nullptr);
+    // every sum starts from -0, which changes no operand; an inactive rank adds +0, which turns a -0 into +0
+    const pair_t start = both(x.inactive ? 0.0f : -0.0f);
+    const bool prev = tx > 0 && threadIdx.x % 32 > 0, lane_next = tx + 1 < bx && threadIdx.x % 32 < 31;
+    uint4 *const mine = held + threadIdx.x;
     pdl_wait();
-    if (!WARP && t.cluster > 1) cluster_barrier();  // every block of the cluster runs before one writes to another
-    uint32_t weight[U][NW], shift[U][NW], bias[U][NW];
+    if (!WARP && cluster > 1) cluster_barrier();  // every block of the cluster runs before one writes to another
+    for (unsigned row0 = group * by; row0 < ne1; row0 += groups * by) {
+        const unsigned row = row0 + static_cast<unsigned>(ty);
+        const bool in_row = row < ne1, inner = p.apart && row > 0 && row + 1 < ne1;
+        // how many columns of the unit at `col` are inside the row
+        auto inside = [&](unsigned col) { return !in_row || col >= ne0 ? 0 : ne0 - col >= C ? C : static_cast<int>(ne0 - col); };
+        auto put = [&](void *base, long long stride, unsigned col, int have, const uint32_t(&w)[W]) {
+            unit_store<Td, ALIGNED>(static_cast<char *>(base) + static_cast<unsigned long long>(row) * static_cast<unsigned>(stride) +
+                                        col * Elem<Td>::bytes,
+                                    w, col, ne0, have, prev, lane_next);
+        };
+        float m = 0.0f, a = 0.0f, b = 0.0f;
+        unsigned col = col0;
+        for (int u = 0; u < units; ++u, col += hop) {
+            const int have = inside(col);
+            const unsigned at = col * Elem<Td>::bytes;
+            pair_t acc[N];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        row_words<Td, ALIGNED>(p.bias, t.col(u), x.ne0, bias[u]);
-        row_words<Td, ALIGNED>(p.weight, t.col(u), x.ne0, weight[u]);
-        row_words<Td, ALIGNED>(p.shift, t.col(u), x.ne0, shift[u]);
-    }
-    auto issue = [&](size_t row, int stage) {
-        if (row < x.ne1) {
-            unsigned to = mine + static_cast<unsigned>(stage) * stage_bytes;
-            for (int s = 0; s < p.n_sources; ++s) {
-                const RowSource &src = p.source[s];
-                const char *at = src.base + static_cast<long long>(row) * src.stride;
+            for (int k = 0; k < N; ++k) acc[k] = start;
+            if (have) {
+                Unit<Td, ALIGNED> res;
+                pair_t v[N];
+                if (x.residual) unit_load<Td, ALIGNED>(res, p.source[ranks].row(row) + at, p.source[ranks], inner, have);
+                for (int s0 = 0; s0 < ranks; s0 += RB) {
+                    Unit<Td, ALIGNED> in[RB];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (t.col(u) < x.ne0)
-                        unit_copy<Td, ALIGNED>(to + u * (blockDim.x * 16u), step, at + t.col(u) * Elem<Td>::bytes, src);
-                to += V * step;
-            }
-        }
-        copy_commit();
-    };
-    const size_t turn = t.groups * t.by;
-    size_t ahead = t.group * t.by + t.ty;
-    int put = 0, get = 0;
-    for (int s = 0; s + 1 < p.stages; ++s, ahead += turn) issue(ahead, put++);
-    for (size_t row0 = t.group * t.by; row0 < x.ne1; row0 += turn, ahead += turn) {
-        issue(ahead, put);
-        if (++put == p.stages) put = 0;
-        copy_wait(p.stages - 1);
-        const size_t row = row0 + t.ty;
-        const bool in_row = row < x.ne1;
-        const long long r64 = static_cast<long long>(row);
-        const unsigned from = mine + static_cast<unsigned>(get) * stage_bytes;
-        if (++get == p.stages) get = 0;
-        uint32_t h[U][NW];
-        {
-            float acc[U][8];
-            // operand s of the ring, widened
-            auto operand = [&](int s, int u, float (&v)[8]) {
-                uint32_t w[NW];
-                const RowSource &src = p.source[s];
-                unit_read<Td, ALIGNED>(from + static_cast<unsigned>(s) * V * step + u * (blockDim.x * 16u), step,
-                                       static_cast<unsigned>(reinterpret_cast<uintptr_t>(src.base)) +
-                                           static_cast<unsigned>(row) * static_cast<unsigned>(src.stride) +
-                                           static_cast<unsigned>(t.col(u)) * Elem<Td>::bytes,
-                                       w);
-                widen8<Td>(w, v);
-            };
-            int s = 0;
-            for (int r = 0; r < x.R; ++r) {
-                const bool active = !((x.inactive >> r) & 1u);
+                    for (int j = 0; j < RB; ++j)
+                        if (s0 + j < ranks) unit_load<Td, ALIGNED>(in[j], p.source[s0 + j].row(row) + at, p.source[s0 + j], inner, have);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float v[8] = {};  // an inactive rank adds +0
-                    if (active) {
-                        operand(s, u, v);
-                        wire8<Td>(p.wire, v);
+                    for (int j = 0; j < RB; ++j) {
+                        if (s0 + j >= ranks) break;
+                        unit_pairs<Td, ALIGNED>(in[j], v);
+                        wire_pairs<Td>(p.wire, v);
+#pragma unroll
+                        for (int k = 0; k < N; ++k) acc[k] = add2(acc[k], v[k]);
                     }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) acc[u][k] = r == 0 ? v[k] : __fadd_rn(acc[u][k], v[k]);
                 }
-                s += active;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float v[8];
                 if (p.bias) {
-                    widen8<Td>(bias[u], v);
+                    uint32_t w[W];
+                    row_unit<Td, W>(p.bias, col, have, p.rows_aligned, w);
+                    widen_pairs<Td, W>(w, v);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) acc[u][k] = __fadd_rn(acc[u][k], v[k]);
+                    for (int k = 0; k < N; ++k) acc[k] = add2(acc[k], v[k]);
                 }
                 if (x.residual) {
-                    operand(s, u, v);
+                    unit_pairs<Td, ALIGNED>(res, v);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) acc[u][k] = __fadd_rn(acc[u][k], v[k]);
-                }
-                word_pack<Td, NW>(acc[u], h[u]);
-                // nothing behind the row's end, where the sums look
-                const unsigned long long col = t.col(u);
-                if (!in_row || col + 8 > x.ne0) keep_first<Td>(h[u], in_row && col < x.ne0 ? x.ne0 - col : 0);
-            }
-        }
-        if (p.n_sums || p.kept.codes) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const unsigned long long col = t.col(u);
-                const bool on = in_row && col < x.ne0;
-                for (int s = 0; s < p.n_sums; ++s)
-                    store8<Td, ALIGNED>(static_cast<char *>(p.sum[s]) + r64 * p.sum_stride[s] + static_cast<long long>(col) * Elem<Td>::bytes,
-                                        h[u], col, x.ne0, col + 8 <= x.ne0, on, t.prev(), t.next(u, x.ne0));
-                if (p.kept.codes) {
-                    float v[8];
-                    widen8<Td>(h[u], v);
-                    encode8<NW>(p.kept, row, col, x.ne0, v, on);
+                    for (int k = 0; k < N; ++k) acc[k] = add2(acc[k], v[k]);
                 }
             }
+            if (have < C) first_pairs(acc, have);  // nothing behind the row's end, where the sums look
+            uint32_t h[W];
+            round_pairs<Td, W>(acc, h);
+#pragma unroll
+            for (int k = 0; k < W; k += 4) mine[(u * (W / 4) + k / 4) * T] = make_uint4(h[k], h[k + 1], h[k + 2], h[k + 3]);
+            for (int s = 0; s < p.n_sums; ++s) put(p.sum[s], p.sum_stride[s], col, have, h);
+            widen_pairs<Td, W>(h, acc);
+            if (p.kept.codes) unit_encode(p.kept, row, col, have, acc);
+            a += sum_pairs(acc);
         }
-        float m = 0.0f, a = 0.0f, b = 0.0f;
+        auto take = [&](int u, pair_t(&v)[N]) {
+            uint32_t h[W];
+#pragma unroll
+            for (int k = 0; k < W; k += 4) {
+                const uint4 q = mine[(u * (W / 4) + k / 4) * T];
+                h[k] = q.x, h[k + 1] = q.y, h[k + 2] = q.z, h[k + 3] = q.w;
+            }
+            widen_pairs<Td, W>(h, v);
+        };
         if (!p.rms) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float v[8];
-                widen8<Td>(h[u], v);
-                a += add8(v);
-            }
-            row_sum2<WARP>(a, b, t.bx, t.cluster, t.rank, room[0]);
+            row_sum<WARP, false>(a, b, bx, cluster, rank, room[0]);
             m = a * p.inv_n;
         }
         a = b = 0.0f;
+        col = col0;
+        const pair_t minus_m = both(-m);
+        for (int u = 0; u < units; ++u, col += hop) {
+            pair_t v[N], q = 0;
+            take(u, v);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float v[8], q[8];
-            widen8<Td>(h[u], v);
+            for (int k = 0; k < N; ++k) v[k] = add2(v[k], minus_m);
+            const int have = inside(col);
+            if (have < C) first_pairs(v, have);
+            a += sum_pairs(v);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                v[k] = t.col(u) + k < x.ne0 ? v[k] - m : 0.0f;
-                q[k] = v[k] * v[k];
-            }
-            a += add8(v);
-            b += add8(q);
+            for (int k = 0; k < N; ++k) q = fma2(v[k], v[k], q);
+            const float2 f = halves(q);
+            b += f.x + f.y;
         }
-        row_sum2<WARP>(a, b, t.bx, t.cluster, t.rank, room[WARP ? 0 : 1]);
+        row_sum<WARP, true>(a, b, bx, cluster, rank, room[WARP ? 0 : 1]);
         const float off = p.rms ? 0.0f : a * p.inv_n;
         const float rstd = norm_rstd(b * p.inv_n, off, p.eps);
-        if (in_row && t.unit0 == 0) {
+        if (in_row && col0 == 0) {
             if (p.mean) p.mean[row] = norm_mean(m, off);
             if (p.rstd) p.rstd[row] = rstd;
         }
+        // ((h - m) - off) rstd
+        const pair_t scale = both(rstd), rest = both(-off * rstd);
+        col = col0;
+        for (int u = 0; u < units; ++u, col += hop) {
+            const int have = inside(col);
+            pair_t v[N], f[N];
+            uint32_t w[W], g[W];
+            if (p.weight) row_unit<Td, W>(p.weight, col, have, p.rows_aligned, w);
+            if (p.shift) row_unit<Td, W>(p.shift, col, have, p.rows_aligned, g);
+            take(u, v);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const unsigned long long col = t.col(u);
-            float v[8], f[8];
-            uint32_t w[NW];
-            widen8<Td>(h[u], v);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = ((v[k] - m) - off) * rstd;
+            for (int k = 0; k < N; ++k) v[k] = fma2(add2(v[k], minus_m), scale, rest);
             if (p.weight) {
-                widen8<Td>(weight[u], f);
+                widen_pairs<Td, W>(w, f);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] *= f[k];
+                for (int k = 0; k < N; ++k) v[k] = mul2(v[k], f[k]);
             }
             if (p.shift) {
-                widen8<Td>(shift[u], f);
+                widen_pairs<Td, W>(g, f);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] += f[k];
+                for (int k = 0; k < N; ++k) v[k] = add2(v[k], f[k]);
             }
-            word_pack<Td, NW>(v, w);
-            for (int d = 0; d < x.n_dsts; ++d)
-                store8<Td, ALIGNED>(static_cast<char *>(x.dst[d]) + r64 * x.dst_stride[d] + static_cast<long long>(col) * Elem<Td>::bytes,
-                                    w, col, x.ne0, col + 8 <= x.ne0, in_row && col < x.ne0, t.prev(), t.next(u, x.ne0));
+            round_pairs<Td, W>(v, w);
+            for (int d = 0; d < x.n_dsts; ++d) put(x.dst[d], x.dst_stride[d], col, have, w);
         }
     }
 }
@@ -616,8 +702,8 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
     extern __shared__ uint4 ring[];
     __shared__ RowRoom room[WARP ? 1 : 2];
     pdl_launch_dependents();
-    RowThread<WARP> t;
-    t.template set<U>(p.bx, p.cluster);
+    const unsigned ne0 = static_cast<unsigned>(p.ne0);
+    const RowThread<U, WARP> t(p.bx, p.cluster, ne0);
     const unsigned step = blockDim.x * 16u * U;
     const unsigned mine = static_cast<unsigned>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16u;
     const unsigned stage_bytes = step * static_cast<unsigned>(p.vecs);
@@ -632,21 +718,22 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
         if (row < p.ne1) {
             const unsigned to = mine + static_cast<unsigned>(stage) * stage_bytes;
             const long long r64 = static_cast<long long>(row);
+            const bool between = row > 0 && row + 1 < p.ne1;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (t.col(u) >= p.ne0) continue;
+                if (!t.have[u]) continue;
                 const unsigned slot = to + u * (blockDim.x * 16u);
-                const unsigned long long at = t.col(u) * Elem<Td>::bytes;
-                unit_copy<Td, ALIGNED>(slot, step, p.dy.base + r64 * p.dy.stride + at, p.dy);
+                const unsigned at = t.col(u) * Elem<Td>::bytes;
+                unit_copy<Td, ALIGNED>(slot, step, p.dy.row(static_cast<unsigned>(row)) + at, p.dy, between && p.dy.apart);
                 if (p.kept.codes) {
-                    const unsigned long long left = p.ne0 - t.col(u);
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(slot + at_h),
-                                 "l"(p.kept.codes + r64 * p.kept.code_row + t.col(u)), "r"(left < 8 ? static_cast<unsigned>(left) : 8u)
+                                 "l"(p.kept.codes + r64 * p.kept.code_row + t.col(u)), "r"(t.have[u])
                                  : "memory");
                 } else {
-                    unit_copy<Td, ALIGNED>(slot + at_h, step, p.h.base + r64 * p.h.stride + at, p.h);
+                    unit_copy<Td, ALIGNED>(slot + at_h, step, p.h.row(static_cast<unsigned>(row)) + at, p.h, between && p.h.apart);
                 }
-                if (p.dsum.base) unit_copy<Td, ALIGNED>(slot + at_dsum, step, p.dsum.base + r64 * p.dsum.stride + at, p.dsum);
+                if (p.dsum.base) unit_copy<Td, ALIGNED>(slot + at_dsum, step, p.dsum.row(static_cast<unsigned>(row)) + at, p.dsum,
+                                                            between && p.dsum.apart);
             }
         }
         copy_commit();
@@ -661,7 +748,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
         if (p.kept.codes) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (t.col(u) < p.ne0)
+                if (t.have[u])
                     next_scale[u] = p.kept.scales[static_cast<long long>(row) * p.kept.scale_row + static_cast<long long>(t.col(u) / kCodeBlock)];
         }
     };
@@ -686,14 +773,13 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
         if (++get == p.stages) get = 0;
         auto low = [&](const RowSource &s, int u) {
             return static_cast<unsigned>(reinterpret_cast<uintptr_t>(s.base)) + static_cast<unsigned>(row) * static_cast<unsigned>(s.stride) +
-                   static_cast<unsigned>(t.col(u)) * Elem<Td>::bytes;
+                   t.col(u) * Elem<Td>::bytes;
         };
         // dy and x of unit u, dy = 0 and x finite outside of the row
         auto operands = [&](int u, float (&dy)[8], float (&xv)[8]) {
             const unsigned slot = from + u * (blockDim.x * 16u);
-            const unsigned long long col = t.col(u);
-            const bool whole = in_row && col + 8 <= p.ne0;
-            const unsigned long long n = in_row && col < p.ne0 ? p.ne0 - col : 0;
+            const int n = in_row ? t.have[u] : 0;
+            const bool whole = n == 8;
             uint32_t w[NW];
             unit_read<Td, ALIGNED>(slot, step, low(p.dy, u), w);
             if (!whole) keep_first<Td>(w, n);
@@ -702,13 +788,8 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
                 uint2 c;
                 asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(c.x), "=r"(c.y) : "r"(slot + at_h) : "memory");
                 decode8(p.kept.format, c, scale[u], xv);
-                if (!whole) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) xv[k] = k < n ? xv[k] : 0.0f;
-                }
             } else {
                 unit_read<Td, ALIGNED>(slot + at_h, step, low(p.h, u), w);
-                if (!whole) keep_first<Td>(w, n);
                 widen8<Td>(w, xv);
             }
 #pragma unroll
@@ -737,15 +818,13 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
             weighed(u, dy, g);
             a += add8(g);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) xv[k] *= g[k];
-            b += add8(xv);
+            for (int k = 0; k < 8; ++k) b = fmaf(g[k], xv[k], b);
         }
-        row_sum2<WARP>(a, b, t.bx, t.cluster, t.rank, room[WARP ? 0 : parity]);
+        row_sum<WARP, true>(a, b, t.bx, t.cluster, t.rank, room[WARP ? 0 : parity]);
         const float c1 = p.rms ? 0.0f : a * p.inv_n, c2 = b * p.inv_n;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const unsigned long long col = t.col(u);
-            const bool on = in_row && col < p.ne0;
+            const bool on = in_row && t.have[u];
             float dy[8], xv[8], d[8];
             operands(u, dy, xv);
             weighed(u, dy, d);
@@ -769,8 +848,8 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
             }
             word_pack<Td, NW>(d, w);
             for (int k = 0; k < p.n_dxs; ++k)
-                store8<Td, ALIGNED>(static_cast<char *>(p.dx[k]) + r64 * p.dx_stride[k] + static_cast<long long>(col) * Elem<Td>::bytes,
-                                    w, col, p.ne0, col + 8 <= p.ne0, on, t.prev(), t.next(u, p.ne0));
+                store8<Td, ALIGNED>(static_cast<char *>(p.dx[k]) + r64 * p.dx_stride[k] + t.col(u) * Elem<Td>::bytes, w, t.col(u), ne0,
+                                    t.have[u] == 8, on, t.prev, t.next(u, ne0));
         }
     }
     copy_wait(0);
@@ -794,12 +873,12 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
                 const int unit = c / 8, at = (unit / t.bx * 8 + c % 8) * t.bx + unit % t.bx;
                 float s = 0.0f;
                 for (int y = 0; y < t.by; ++y) s += sums[y * width + at];
-                if (static_cast<unsigned long long>(c) < p.ne0) row[c] = s;
+                if (static_cast<unsigned>(c) < ne0) row[c] = s;
             }
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (t.col(u) >= p.ne0) continue;
+                if (!t.have[u]) continue;
                 const float(&v)[8] = which == 0 ? sw[u] : which == 1 ? ss[u] : sb[u];
                 *reinterpret_cast<float4 *>(row + t.col(u)) = make_float4(v[0], v[1], v[2], v[3]);
                 *reinterpret_cast<float4 *>(row + t.col(u) + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -813,8 +892,8 @@ template <int Td>
 __device__ __forceinline__ void grad_elem(const NormGradParams &p, size_t row, size_t i, float mean, float rstd, float &dy,
                                           float &g, float &x) {
     const long long at = static_cast<long long>(i);
-    dy = load_elem<Td, false>(p.dy.base + static_cast<long long>(row) * p.dy.stride, at);
-    const float h = p.h.base ? load_elem<Td, false>(p.h.base + static_cast<long long>(row) * p.h.stride, at)
+    dy = load_elem<Td, false>(p.dy.base + static_cast<long long>(row) * p.dy.wide, at);
+    const float h = p.h.base ? load_elem<Td, false>(p.h.base + static_cast<long long>(row) * p.h.wide, at)
                              : decode_elem(p.kept, row, i);
     g = p.weight ? dy * load_elem<Td, false>(p.weight, at) : dy;
     x = (h - mean) * rstd;
@@ -860,7 +939,7 @@ __global__ void __launch_bounds__(256) ar_norm_grad_any_kernel(const __grid_cons
             if (!p.rms) d -= p.row_sums[row] * p.inv_n;
             d *= rstd;
             if (p.dsum.base)
-                d += load_elem<Td, false>(p.dsum.base + static_cast<long long>(row) * p.dsum.stride, static_cast<long long>(i));
+                d += load_elem<Td, false>(p.dsum.base + static_cast<long long>(row) * p.dsum.wide, static_cast<long long>(i));
             s[0] += dy * x;
             s[1] += dy;
             s[2] += d;

@@ -192,12 +192,28 @@ int vecs_of(size_t es, bool aligned) { return static_cast<int>(es) / 2 + (aligne
 
 using NormFn = void (*)(tps::NormParams);
 
-template <int Td, bool ALIGNED>
-NormFn pick_forward(const RowShape &s) {
-    if (s.warp) return s.U == 1 ? tps::ar_norm_kernel<Td, ALIGNED, 1, true> : tps::ar_norm_kernel<Td, ALIGNED, 2, true>;
-    return s.U == 1   ? tps::ar_norm_kernel<Td, ALIGNED, 1, false>
-           : s.U == 2 ? tps::ar_norm_kernel<Td, ALIGNED, 2, false>
-                      : tps::ar_norm_kernel<Td, ALIGNED, 4, false>;
+// How the forward pass lays a row over threads; U = 0: too long.
+RowShape forward_shape(size_t ne0, size_t ne1, size_t es, bool aligned) {
+    const size_t cols = aligned ? 32 / es : 8, units = (ne0 + cols - 1) / cols;
+    RowShape s{};
+    s.cluster = 1;
+    s.threads = tps::kNormThreads;
+    auto share = [&] { return (units + s.cluster - 1) / s.cluster; };
+    if (units <= 128) {
+        s.warp = true;
+        s.threads = 128;
+        s.bx = 32;
+        while (s.bx > 4 && static_cast<size_t>(s.bx) / 2 >= units) s.bx /= 2;
+    } else {
+        // few rows: the blocks that would be idle share them
+        while (s.cluster < tps::kRowBlocks && ne1 * s.cluster * 2 <= kSMs && share() >= 128) s.cluster *= 2;
+        while (s.cluster < tps::kRowBlocks && share() * cols * es > 16 * 1024) s.cluster *= 2;
+        s.bx = static_cast<int>(s.threads);
+    }
+    s.U = static_cast<int>((share() + s.bx - 1) / s.bx);
+    s.smem = static_cast<size_t>(s.threads) * s.U * cols * es;
+    if (s.smem > ring_bytes(1)) s.U = 0;
+    return s;
 }
 
 using GradFn = void (*)(tps::NormGradParams);
@@ -221,7 +237,9 @@ Fn pick_rows(int dtype, bool aligned, const RowShape &s) {
 
 template <int Td, bool ALIGNED>
 struct Forward {
-    static NormFn of(const RowShape &s) { return pick_forward<Td, ALIGNED>(s); }
+    static NormFn of(const RowShape &s) {
+        return s.warp ? tps::ar_norm_kernel<Td, ALIGNED, true> : tps::ar_norm_kernel<Td, ALIGNED, false>;
+    }
 };
 template <int Td, bool ALIGNED>
 struct Backward {
@@ -231,13 +249,16 @@ struct Backward {
 // A tensor's rows and where they end; `rows` of them, one where the stride is 0.
 tps::RowSource source_of(const void *p, long long stride, size_t rows, size_t row) {
     const char *base = static_cast<const char *>(p);
-    return tps::RowSource{base, stride, base ? base + (rows - 1) * static_cast<size_t>(stride) + row : nullptr};
+    return tps::RowSource{base, base ? base + (rows - 1) * static_cast<size_t>(stride) + row : nullptr, stride,
+                          static_cast<unsigned>(stride), stride >= 64};
 }
 
 // Whether every row of every buffer starts on a vector boundary (32 bytes for f32, else 16).
 struct Alignment {
     uintptr_t bits = 0;
+    bool narrow = true;  // row numbers and strides of 32 bits
     void add(const void *p, long long stride, size_t rows) {
+        if (p && rows > 1 && (stride > 0xFFFFFFFFll || rows > 0xFFFFFFFFull)) narrow = false;
         bits |= reinterpret_cast<uintptr_t>(p) | (rows > 1 ? static_cast<uintptr_t>(stride) : 0);
     }
     bool holds(size_t es) const { return bits % (es == 4 ? 32 : 16) == 0; }
@@ -372,26 +393,30 @@ int ar_reduce_norm(const void *const *srcs, void *const *dsts, int n_dsts, const
     for (int k = 0; k < p.n_sums; ++k) al.add(p.sum[k], p.sum_stride[k], x.ne1);
     al.add(x.residual, x.res_stride, x.ne1);
     if (x.residual) p.source[p.n_sources++] = source_of(x.residual, x.res_stride, x.ne1, packed);
-    for (const void *row : {p.weight, p.shift, p.bias}) al.add(row, 0, 1);
     const size_t es = dtype_bytes(dst_dtype);
-    const bool aligned = al.holds(es);
-    const RowShape s = row_shape(L->ne0, L->ne1, vecs_of(es, aligned) * (p.n_sources ? p.n_sources : 1), 4);
-    if (s.U == 0) {
+    const bool aligned = al.bits % 32 == 0;
+    const RowShape s = forward_shape(L->ne0, L->ne1, es, aligned);
+    if (s.U == 0 || !al.narrow) {
         const NormFn any = by_type<NormFn>(dst_dtype, tps::ar_norm_any_kernel<tps::kF32>, tps::ar_norm_any_kernel<tps::kF16>,
                                            tps::ar_norm_any_kernel<tps::kBF16>);
         const size_t blocks = L->ne1 < 65535 ? L->ne1 : 65535;
         return launched(tps::launch_dependent(any, dim3(static_cast<unsigned>(blocks)), static_cast<unsigned>(kAnyThreads), 0,
                                               stream, c.pdl, p));
     }
+    Alignment rows;
+    for (const void *row : {p.weight, p.shift, p.bias}) rows.add(row, 0, 1);
+    p.rows_aligned = rows.bits % 16 == 0;
+    p.apart = 1;
+    for (int k = 0; k < p.n_sources; ++k) p.apart &= p.source[k].apart;
     p.bx = s.bx;
-    p.cluster = s.cluster;
-    p.stages = s.stages;
-    p.vecs = s.vecs;
+    p.units = s.U;
+    while (1 << p.cluster_bits < s.cluster) ++p.cluster_bits;
     const NormFn fn = pick_rows<NormFn, Forward>(dst_dtype, aligned, s);
     st = allow_ring(fn, s);
     if (st != AR_OK) return st;
-    return launched(tps::launch_clustered(fn, dim3(static_cast<unsigned>(row_grid(s, L->ne1))), static_cast<unsigned>(s.cluster),
-                                          s.threads, s.smem, stream, c.pdl, p));
+    const size_t turn = s.warp ? s.threads / s.bx : 1, most = (1u << 30) / s.cluster, groups = (L->ne1 + turn - 1) / turn;
+    return launched(tps::launch_clustered(fn, dim3(static_cast<unsigned>((groups < most ? groups : most) * s.cluster)),
+                                          static_cast<unsigned>(s.cluster), s.threads, s.smem, stream, c.pdl, p));
 }
 
 int ar_reduce_norm_grad_workspace(const ar_layout *L, int n_sums, size_t *bytes) {
@@ -495,7 +520,7 @@ int ar_reduce_norm_grad(const void *dy, const void *h, const ar_checkpoint *ck, 
         const bool aligned = al.holds(es);
         const int v = vecs_of(es, aligned);
         const RowShape s = row_shape(L->ne0, L->ne1, v + (h ? v : 1) + (L->residual ? v : 0), 2);
-        if (s.U) {
+        if (s.U && al.narrow) {
             const size_t grid = row_grid(s, L->ne1);
             blocks = grid / s.cluster;
             place(static_cast<float *>(ws));
