@@ -3,7 +3,7 @@
 // element is rounded once, and the same inputs give the same codes everywhere.
 #pragma once
 
-#include "ar_kernels.cuh"
+#include "ar_pairs.cuh"
 
 namespace tps {
 
@@ -55,6 +55,48 @@ __device__ __forceinline__ void decode2(int format, uint32_t v, float &lo, float
     } else {
         lo = static_cast<float>(static_cast<int8_t>(v & 0xFFu));
         hi = static_cast<float>(static_cast<int8_t>((v >> 8) & 0xFFu));
+    }
+}
+
+// Codes of 2 N values times 2^-e, four to a word.  int8: adding 1.5 * 2^23 rounds to a whole number, ties to even,
+// in the low bits.
+template <int N>
+__device__ __forceinline__ void encode_pairs(int format, const pair_t (&v)[N], pair_t inv, uint32_t (&w)[N / 2]) {
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+        const pair_t a = mul2(v[k], inv), b = mul2(v[k + 1], inv);
+        if (format == kE4M3) {
+            const float2 f = halves(a), g = halves(b);
+            w[k / 2] = encode2(kE4M3, f.x, f.y) | encode2(kE4M3, g.x, g.y) << 16;
+        } else {
+            const pair_t magic = both(12582912.0f);
+            const float2 f = halves(add2(a, magic)), g = halves(add2(b, magic));
+            const uint32_t lo = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x0040);
+            const uint32_t hi = __byte_perm(__float_as_uint(g.x), __float_as_uint(g.y), 0x0040);
+            w[k / 2] = __byte_perm(lo, hi, 0x5410);
+        }
+    }
+}
+// What they stand for.  int8: the byte plus 128 in the low bits of 2^23.
+template <int N>
+__device__ __forceinline__ void decode_pairs(int format, const uint32_t (&w)[N / 2], float scale, pair_t (&v)[N]) {
+    const pair_t s = both(scale);
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+        float a, b, c, d;
+        if (format == kE4M3) {
+            decode2(kE4M3, w[k / 2], a, b);
+            decode2(kE4M3, w[k / 2] >> 16, c, d);
+            v[k] = mul2(make_pair(a, b), s);
+            v[k + 1] = mul2(make_pair(c, d), s);
+        } else {
+            const uint32_t x = w[k / 2] ^ 0x80808080u;
+            const pair_t bias = both(-8388736.0f);
+            v[k] = mul2(add2(make_pair(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7440)),
+                                       __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7441))), bias), s);
+            v[k + 1] = mul2(add2(make_pair(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7442)),
+                                           __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7443))), bias), s);
+        }
     }
 }
 

@@ -53,6 +53,7 @@ struct NormGradParams {
     float *part[3];  // [row block][part_ld] partial column sums of dweight, dshift, dbias; nullptr: not wanted
     unsigned long long part_ld;
     int bx, cluster, stages, vecs;
+    int apart, rows_aligned;  // as in NormParams
     // rows of any length
     float *row_sums;  // [2][ne1]: sum g and sum g x of each row
     unsigned rows_per_block;
@@ -274,8 +275,11 @@ __device__ __forceinline__ void copy_wait(int ahead) {
         asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
+// 32-bit words of a unit: 32 bytes from 32-byte boundaries, else eight columns.
 template <int T, bool ALIGNED>
-constexpr int kUnitVecs = kWords8<T> / 4 + (ALIGNED ? 0 : 1);  // 16-byte vectors of a unit in the ring
+constexpr int kUnitWords = ALIGNED ? 8 : kWords8<T>;
+template <int T, bool ALIGNED>
+constexpr int kUnitVecs = kUnitWords<T, ALIGNED> / 4 + (ALIGNED ? 0 : 1);  // its 16-byte vectors in the ring
 
 // Copy the vectors of the unit at `at` to `to`, `step` bytes apart; `inner`: those around it lie inside the tensor.
 template <int T, bool ALIGNED>
@@ -286,7 +290,8 @@ __device__ __forceinline__ void unit_copy(unsigned to, unsigned step, const char
     if (inner || (from >= s.base && from + 16 * V <= s.end)) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (v < V - 1 || ALIGNED || off) copy_async(to + v * step, from + 16 * v, 16);
+            if (v < V - 1 || ALIGNED || off)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + v * step), "l"(from + 16 * v) : "memory");
         return;
     }
     // next to the tensor's ends
@@ -316,61 +321,32 @@ __device__ __forceinline__ uint4 read_shared(unsigned at) {
     return q;
 }
 
-// The words of the unit that unit_copy brought from an address whose low bits are `low`.
+// The columns of the unit that unit_copy brought from an address whose low bits are `low`.
 template <int T, bool ALIGNED>
-__device__ __forceinline__ void unit_read(unsigned from, unsigned step, unsigned low, uint32_t (&w)[kWords8<T>]) {
-    constexpr int NW = kWords8<T>;
+__device__ __forceinline__ void unit_read(unsigned from, unsigned step, unsigned low, pair_t (&v)[kCols<T, kUnitWords<T, ALIGNED>> / 2]) {
+    constexpr int W = kUnitWords<T, ALIGNED>;
+    uint32_t w[W + (ALIGNED ? 0 : 4)];
+#pragma unroll
+    for (int k = 0; k < W + (ALIGNED ? 0 : 4); k += 4) {
+        const uint4 q = read_shared(from + k / 4 * step);
+        w[k] = q.x, w[k + 1] = q.y, w[k + 2] = q.z, w[k + 3] = q.w;
+    }
     if constexpr (ALIGNED) {
-#pragma unroll
-        for (int k = 0; k < NW; k += 4) {
-            const uint4 q = read_shared(from + k / 4 * step);
-            w[k] = q.x, w[k + 1] = q.y, w[k + 2] = q.z, w[k + 3] = q.w;
-        }
+        widen_pairs<T, W>(w, v);
     } else {
-        uint32_t s[NW + 4];
-#pragma unroll
-        for (int k = 0; k < NW + 4; k += 4) {
-            const uint4 q = read_shared(from + k / 4 * step);
-            s[k] = q.x, s[k + 1] = q.y, s[k + 2] = q.z, s[k + 3] = q.w;
-        }
-        shift_words<NW>(s, low & 15, w);
+        uint32_t o[W];
+        shift_words<W>(w, low & 15, o);
+        widen_pairs<T, W>(o, v);
     }
 }
 
-// Set the elements from `n` (0..8) on to zero.
-template <int T>
-__device__ __forceinline__ void keep_first(uint32_t (&w)[kWords8<T>], int n) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (k >= n) {
-            if constexpr (T == kF32)
-                w[k] = 0u;
-            else
-                w[k / 2] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-        }
-}
-
-// The words of eight elements of a row that stays for the whole launch.
-template <int T, bool ALIGNED>
-__device__ __forceinline__ void row_words(const void *row, unsigned long long col, unsigned long long ne0, uint32_t (&w)[kWords8<T>]) {
-    if (!row || col >= ne0) {
-#pragma unroll
-        for (int k = 0; k < kWords8<T>; ++k) w[k] = 0u;
-        return;
-    }
-    Raw8<T, ALIGNED> raw;
-    const char *at = static_cast<const char *>(row) + col * Elem<T>::bytes;
-    load8<T, ALIGNED>(at, col, ne0, col + 8 <= ne0, raw);
-    raw8_words<T, ALIGNED>(raw, at, w);
-}
-
-// Which columns a thread holds: units of eight, bx apart, in the bx lanes of a warp (WARP: 1 / bx of the block's
+// Which columns a thread holds: units of C, bx apart, in the bx lanes of a warp (WARP: 1 / bx of the block's
 // threads to a row) or in the blocks of a cluster.
-template <int U, bool WARP>
+template <int C, int U, bool WARP>
 struct RowThread {
     int bx, by, tx, ty, cluster;
     unsigned rank, col0;  // of unit 0
-    int have[U];          // columns of each unit inside the row, 0..8
+    int have[U];          // columns of each unit inside the row, 0..C
     bool prev;            // for store8: the lane before holds the columns before
     size_t group, groups;
     __device__ __forceinline__ RowThread(int p_bx, int p_cluster, unsigned ne0) {
@@ -381,23 +357,16 @@ struct RowThread {
         ty = WARP ? t / bx : 0;
         cluster = WARP ? 1 : p_cluster;
         rank = cluster == 1 ? 0u : cluster_rank();
-        col0 = (rank * static_cast<unsigned>(bx) * U + static_cast<unsigned>(tx)) * 8u;
+        col0 = (rank * static_cast<unsigned>(bx) * U + static_cast<unsigned>(tx)) * C;
         prev = tx > 0 && threadIdx.x % 32 > 0;
         group = blockIdx.x / static_cast<unsigned>(cluster);
         groups = gridDim.x / static_cast<unsigned>(cluster);
 #pragma unroll
-        for (int u = 0; u < U; ++u) have[u] = col(u) >= ne0 ? 0 : ne0 - col(u) >= 8 ? 8 : static_cast<int>(ne0 - col(u));
+        for (int u = 0; u < U; ++u) have[u] = col(u) >= ne0 ? 0 : ne0 - col(u) >= C ? C : static_cast<int>(ne0 - col(u));
     }
-    __device__ __forceinline__ unsigned col(int u) const { return col0 + static_cast<unsigned>(u * bx) * 8u; }
-    // For store8: the lane after holds the columns after.
-    __device__ __forceinline__ bool next(int u, unsigned ne0) const {
-        return tx + 1 < bx && threadIdx.x % 32 < 31 && col(u) + 16 <= ne0;
-    }
+    __device__ __forceinline__ unsigned col(int u) const { return col0 + static_cast<unsigned>(u * bx) * C; }
+    __device__ __forceinline__ bool lane_next() const { return tx + 1 < bx && threadIdx.x % 32 < 31; }
 };
-
-// 32-bit words of a unit: 32 bytes from 32-byte boundaries, else eight columns.
-template <int T, bool ALIGNED>
-constexpr int kUnitWords = ALIGNED ? 8 : kWords8<T>;
 
 // A unit as loaded: its own words, or the aligned vectors around it with the bytes to shift by.
 template <int T, bool ALIGNED>
@@ -508,13 +477,7 @@ __device__ __forceinline__ void unit_encode(const CodeRows &c, unsigned row, uns
     const unsigned byte = scale_byte(c.format, top);
     const pair_t inv = both(scale_inverse(byte));
     uint32_t w[N / 2] = {};
-    if (byte != 255u) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const float2 f = halves(mul2(v[k], inv));
-            w[k / 2] |= encode2(c.format, f.x, f.y) << (16 * (k & 1));
-        }
-    }
+    if (byte != 255u) encode_pairs(c.format, v, inv, w);
     uint8_t *at = c.codes + row * static_cast<unsigned long long>(c.code_row) + col;
     if (have == 2 * N) {
         if constexpr (N == 8)
@@ -682,58 +645,51 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<Td, ALIGNED, WARP>) 
     }
 }
 
-// The values of eight codes and their scale byte.
-__device__ __forceinline__ void decode8(int format, uint2 c, unsigned byte, float (&v)[8]) {
-    const float scale = scale_value(byte);
-#pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-        decode2(format, (k < 4 ? c.x : c.y) >> (8 * (k & 3)), v[k], v[k + 1]);
-        v[k] *= scale;
-        v[k + 1] *= scale;
-    }
-}
-
 // The backward pass in one pass over the rows: persistent blocks, dy, the kept sum and dsum of `stages` rows in the
-// ring.  The row's two sums are formed from one reading of the ring, the results from a second; a thread adds up its
-// columns over its block's rows in registers.
+// ring.  dy and x stay in registers while the row's two sums are taken; a thread adds up its columns, 16 at most,
+// over its block's rows in registers.
 template <int Td, bool ALIGNED, int U, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_norm_grad_kernel(const __grid_constant__ NormGradParams p) {
-    constexpr int NW = kWords8<Td>, V = kUnitVecs<Td, ALIGNED>;
+    constexpr int W = kUnitWords<Td, ALIGNED>, C = kCols<Td, W>, N = C / 2, V = kUnitVecs<Td, ALIGNED>;
     extern __shared__ uint4 ring[];
     __shared__ RowRoom room[WARP ? 1 : 2];
     pdl_launch_dependents();
-    const unsigned ne0 = static_cast<unsigned>(p.ne0);
-    const RowThread<U, WARP> t(p.bx, p.cluster, ne0);
-    const unsigned step = blockDim.x * 16u * U;
+    const unsigned ne0 = static_cast<unsigned>(p.ne0), ne1 = static_cast<unsigned>(p.ne1);
+    const RowThread<C, U, WARP> t(p.bx, p.cluster, ne0);
+    const unsigned hop = blockDim.x * 16u, step = hop * U;  // from a unit's vector to the next unit's, and to its own next
     const unsigned mine = static_cast<unsigned>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16u;
     const unsigned stage_bytes = step * static_cast<unsigned>(p.vecs);
     const unsigned at_h = V * step, at_dsum = at_h + (p.kept.codes ? 1u : V) * step;
     pdl_wait();
     if (!WARP && t.cluster > 1) cluster_barrier();
-    uint32_t weight[U][NW];
-    float sw[U][8] = {}, ss[U][8] = {}, sb[U][8] = {};
+    pair_t weight[U][N], sw[U][N], ss[U][N], sb[U][N];
 #pragma unroll
-    for (int u = 0; u < U; ++u) row_words<Td, ALIGNED>(p.weight, t.col(u), p.ne0, weight[u]);
-    auto issue = [&](size_t row, int stage) {
-        if (row < p.ne1) {
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) weight[u][k] = both(1.0f), sw[u][k] = ss[u][k] = sb[u][k] = 0;
+        if (p.weight && t.have[u]) {
+            uint32_t w[W];
+            row_unit<Td, W>(p.weight, t.col(u), t.have[u], p.rows_aligned, w);
+            widen_pairs<Td, W>(w, weight[u]);
+        }
+    }
+    auto issue = [&](unsigned row, int stage) {
+        if (row < ne1) {
             const unsigned to = mine + static_cast<unsigned>(stage) * stage_bytes;
-            const long long r64 = static_cast<long long>(row);
-            const bool between = row > 0 && row + 1 < p.ne1;
+            const bool inner = p.apart && row > 0 && row + 1 < ne1;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (!t.have[u]) continue;
-                const unsigned slot = to + u * (blockDim.x * 16u);
-                const unsigned at = t.col(u) * Elem<Td>::bytes;
-                unit_copy<Td, ALIGNED>(slot, step, p.dy.row(static_cast<unsigned>(row)) + at, p.dy, between && p.dy.apart);
-                if (p.kept.codes) {
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(slot + at_h),
-                                 "l"(p.kept.codes + r64 * p.kept.code_row + t.col(u)), "r"(t.have[u])
+                const unsigned slot = to + u * hop, at = t.col(u) * Elem<Td>::bytes;
+                unit_copy<Td, ALIGNED>(slot, step, p.dy.row(row) + at, p.dy, inner);
+                if (p.kept.codes)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(slot + at_h),
+                                 "l"(p.kept.codes + row * static_cast<unsigned long long>(p.kept.code_row) + t.col(u)), "n"(C == 16 ? 16 : 8),
+                                 "r"(t.have[u])
                                  : "memory");
-                } else {
-                    unit_copy<Td, ALIGNED>(slot + at_h, step, p.h.row(static_cast<unsigned>(row)) + at, p.h, between && p.h.apart);
-                }
-                if (p.dsum.base) unit_copy<Td, ALIGNED>(slot + at_dsum, step, p.dsum.row(static_cast<unsigned>(row)) + at, p.dsum,
-                                                            between && p.dsum.apart);
+                else
+                    unit_copy<Td, ALIGNED>(slot + at_h, step, p.h.row(row) + at, p.h, inner);
+                if (p.dsum.base) unit_copy<Td, ALIGNED>(slot + at_dsum, step, p.dsum.row(row) + at, p.dsum, inner);
             }
         }
         copy_commit();
@@ -741,29 +697,28 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
     // what is read straight into registers, a row ahead
     float next_mean = 0.0f, next_rstd = 0.0f;
     unsigned next_scale[U] = {};
-    auto fetch = [&](size_t row) {
-        if (row >= p.ne1) return;
+    auto fetch = [&](unsigned row) {
+        if (row >= ne1) return;
         next_mean = p.rms ? 0.0f : p.mean[row];
         next_rstd = p.rstd[row];
         if (p.kept.codes) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (t.have[u])
-                    next_scale[u] = p.kept.scales[static_cast<long long>(row) * p.kept.scale_row + static_cast<long long>(t.col(u) / kCodeBlock)];
+                if (t.have[u]) next_scale[u] = p.kept.scales[row * static_cast<unsigned long long>(p.kept.scale_row) + t.col(u) / kCodeBlock];
         }
     };
-    const size_t turn = t.groups * t.by;
-    size_t ahead = t.group * t.by + t.ty;
+    const unsigned turn = static_cast<unsigned>(t.groups) * t.by;
+    unsigned ahead = static_cast<unsigned>(t.group) * t.by + t.ty;
     int put = 0, get = 0, parity = 0;
     fetch(ahead);
     for (int s = 0; s + 1 < p.stages; ++s, ahead += turn) issue(ahead, put++);
-    for (size_t row0 = t.group * t.by; row0 < p.ne1; row0 += turn, ahead += turn, parity ^= 1) {
+    for (unsigned row0 = static_cast<unsigned>(t.group) * t.by; row0 < ne1; row0 += turn, ahead += turn, parity ^= 1) {
         issue(ahead, put);
         if (++put == p.stages) put = 0;
-        const size_t row = row0 + t.ty;
-        const bool in_row = row < p.ne1;
-        const long long r64 = static_cast<long long>(row);
-        const float mean = next_mean, rstd = next_rstd;
+        const unsigned row = row0 + t.ty;
+        const bool in_row = row < ne1;
+        const pair_t minus_mean = both(-next_mean);
+        const float rstd = next_rstd;
         unsigned scale[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) scale[u] = next_scale[u];
@@ -772,84 +727,70 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
         const unsigned from = mine + static_cast<unsigned>(get) * stage_bytes;
         if (++get == p.stages) get = 0;
         auto low = [&](const RowSource &s, int u) {
-            return static_cast<unsigned>(reinterpret_cast<uintptr_t>(s.base)) + static_cast<unsigned>(row) * static_cast<unsigned>(s.stride) +
-                   t.col(u) * Elem<Td>::bytes;
+            return static_cast<unsigned>(reinterpret_cast<uintptr_t>(s.base)) + row * s.stride + t.col(u) * Elem<Td>::bytes;
         };
-        // dy and x of unit u, dy = 0 and x finite outside of the row
-        auto operands = [&](int u, float (&dy)[8], float (&xv)[8]) {
-            const unsigned slot = from + u * (blockDim.x * 16u);
-            const int n = in_row ? t.have[u] : 0;
-            const bool whole = n == 8;
-            uint32_t w[NW];
-            unit_read<Td, ALIGNED>(slot, step, low(p.dy, u), w);
-            if (!whole) keep_first<Td>(w, n);
-            widen8<Td>(w, dy);
-            if (p.kept.codes) {
-                uint2 c;
-                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(c.x), "=r"(c.y) : "r"(slot + at_h) : "memory");
-                decode8(p.kept.format, c, scale[u], xv);
-            } else {
-                unit_read<Td, ALIGNED>(slot + at_h, step, low(p.h, u), w);
-                widen8<Td>(w, xv);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) xv[k] = (xv[k] - mean) * rstd;
-            if (!whole) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) xv[k] = k < n ? xv[k] : 0.0f;
-            }
-        };
-        auto weighed = [&](int u, const float (&dy)[8], float (&g)[8]) {
-            if (p.weight) {
-                float f[8];
-                widen8<Td>(weight[u], f);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) g[k] = dy[k] * f[k];
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) g[k] = dy[k];
-            }
-        };
-        float a = 0.0f, b = 0.0f;
+        pair_t dy[U][N], x[U][N], a2 = 0, b2 = 0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float dy[8], xv[8], g[8];
-            operands(u, dy, xv);
-            weighed(u, dy, g);
-            a += add8(g);
+            const unsigned slot = from + u * hop;
+            unit_read<Td, ALIGNED>(slot, step, low(p.dy, u), dy[u]);
+            if (p.kept.codes) {
+                uint32_t c[N / 2];
+                if constexpr (C == 16) {
+                    const uint4 q = read_shared(slot + at_h);
+                    c[0] = q.x, c[1] = q.y, c[N / 2 - 2] = q.z, c[N / 2 - 1] = q.w;
+                } else {
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(c[0]), "=r"(c[1]) : "r"(slot + at_h) : "memory");
+                }
+                decode_pairs(p.kept.format, c, scale_value(scale[u]), x[u]);
+            } else {
+                unit_read<Td, ALIGNED>(slot + at_h, step, low(p.h, u), x[u]);
+            }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) b = fmaf(g[k], xv[k], b);
+            for (int k = 0; k < N; ++k) x[u][k] = mul2(add2(x[u][k], minus_mean), both(rstd));
+            if (!in_row || t.have[u] < C) {
+                first_pairs(dy[u], in_row ? t.have[u] : 0);
+                first_pairs(x[u], in_row ? t.have[u] : 0);
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const pair_t g = mul2(dy[u][k], weight[u][k]);
+                a2 = add2(a2, g);
+                b2 = fma2(g, x[u][k], b2);
+            }
         }
+        const float2 af = halves(a2), bf = halves(b2);
+        float a = af.x + af.y, b = bf.x + bf.y;
         row_sum<WARP, true>(a, b, t.bx, t.cluster, t.rank, room[WARP ? 0 : parity]);
-        const float c1 = p.rms ? 0.0f : a * p.inv_n, c2 = b * p.inv_n;
+        // rstd (g - a / n - x b / n)
+        const pair_t k0 = both(rstd), k1 = both(p.rms ? 0.0f : -(a * p.inv_n) * rstd), k2 = both(-(b * p.inv_n) * rstd);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool on = in_row && t.have[u];
-            float dy[8], xv[8], d[8];
-            operands(u, dy, xv);
-            weighed(u, dy, d);
+            pair_t d[N];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                d[k] = (d[k] - c1 - xv[k] * c2) * rstd;
-                sw[u][k] += dy[k] * xv[k];
-                ss[u][k] += dy[k];
+            for (int k = 0; k < N; ++k) {
+                const pair_t g = mul2(dy[u][k], weight[u][k]);
+                d[k] = fma2(x[u][k], k2, fma2(g, k0, k1));
+                sw[u][k] = fma2(dy[u][k], x[u][k], sw[u][k]);
+                ss[u][k] = add2(ss[u][k], dy[u][k]);
             }
-            uint32_t w[NW];
             if (p.dsum.base) {
-                float f[8];
-                unit_read<Td, ALIGNED>(from + at_dsum + u * (blockDim.x * 16u), step, low(p.dsum, u), w);
-                widen8<Td>(w, f);
+                pair_t f[N];
+                unit_read<Td, ALIGNED>(from + at_dsum + u * hop, step, low(p.dsum, u), f);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) d[k] += f[k];
+                for (int k = 0; k < N; ++k) d[k] = add2(d[k], f[k]);
             }
             if (on) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) sb[u][k] += d[k];  // columns behind the row's end are not looked at
+                for (int k = 0; k < N; ++k) sb[u][k] = add2(sb[u][k], d[k]);  // columns behind the row's end are not looked at
             }
-            word_pack<Td, NW>(d, w);
+            uint32_t w[W];
+            round_pairs<Td, W>(d, w);
             for (int k = 0; k < p.n_dxs; ++k)
-                store8<Td, ALIGNED>(static_cast<char *>(p.dx[k]) + r64 * p.dx_stride[k] + t.col(u) * Elem<Td>::bytes, w, t.col(u), ne0,
-                                    t.have[u] == 8, on, t.prev, t.next(u, ne0));
+                unit_store<Td, ALIGNED>(static_cast<char *>(p.dx[k]) + static_cast<unsigned long long>(row) * static_cast<unsigned>(p.dx_stride[k]) +
+                                            t.col(u) * Elem<Td>::bytes,
+                                        w, t.col(u), ne0, on ? t.have[u] : 0, t.prev, t.lane_next());
         }
     }
     copy_wait(0);
@@ -864,13 +805,16 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    sums[((t.ty * U + u) * 8 + k) * t.bx + t.tx] = which == 0 ? sw[u][k] : which == 1 ? ss[u][k] : sb[u][k];
+                for (int k = 0; k < N; ++k) {
+                    const float2 f = halves(which == 0 ? sw[u][k] : which == 1 ? ss[u][k] : sb[u][k]);
+                    sums[((t.ty * U + u) * C + 2 * k) * t.bx + t.tx] = f.x;
+                    sums[((t.ty * U + u) * C + 2 * k + 1) * t.bx + t.tx] = f.y;
+                }
             __syncthreads();
-            const int width = t.bx * U * 8;
+            const int width = t.bx * U * C;
             for (int c = threadIdx.x; c < width; c += blockDim.x) {
-                // column c of the block: unit c / 8, held by lane unit % bx as its unit / bx-th
-                const int unit = c / 8, at = (unit / t.bx * 8 + c % 8) * t.bx + unit % t.bx;
+                // column c of the block: unit c / C, held by lane unit % bx as its unit / bx-th
+                const int unit = c / C, at = (unit / t.bx * C + c % C) * t.bx + unit % t.bx;
                 float s = 0.0f;
                 for (int y = 0; y < t.by; ++y) s += sums[y * width + at];
                 if (static_cast<unsigned>(c) < ne0) row[c] = s;
@@ -879,9 +823,12 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (!t.have[u]) continue;
-                const float(&v)[8] = which == 0 ? sw[u] : which == 1 ? ss[u] : sb[u];
-                *reinterpret_cast<float4 *>(row + t.col(u)) = make_float4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<float4 *>(row + t.col(u) + 4) = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+                for (int k = 0; k < N; k += 2) {
+                    const pair_t(&v)[N] = which == 0 ? sw[u] : which == 1 ? ss[u] : sb[u];
+                    const float2 f = halves(v[k]), g = halves(v[k + 1]);
+                    *reinterpret_cast<float4 *>(row + t.col(u) + 2 * k) = make_float4(f.x, f.y, g.x, g.y);
+                }
             }
         }
     }
@@ -990,27 +937,35 @@ static __global__ void __launch_bounds__(256) ar_norm_column_sum_kernel(const __
 // ---- checkpoints ----------------------------------------------------------------
 
 struct PackParams {
-    void *tensor;
-    long long stride;
+    RowSource tensor;
     unsigned long long ne0, ne1;
+    unsigned per_row;
     CodeRows kept;
 };
 
-// A warp to a block of 32 elements, the blocks of all rows in turn.
-template <int Td>
+// The row of a unit; 64-bit divisions only where they are needed.
+__device__ __forceinline__ unsigned unit_row(size_t at, unsigned per_row) {
+    return at >> 32 ? static_cast<unsigned>(at / per_row) : static_cast<unsigned>(at) / per_row;
+}
+
+// A unit of columns to a thread, the rows' units one after another; `per_row` of them (a whole number of blocks).
+template <int Td, bool ALIGNED>
 __global__ void __launch_bounds__(256) ar_checkpoint_pack_kernel(const __grid_constant__ PackParams p) {
+    constexpr int C = kCols<Td, kUnitWords<Td, ALIGNED>>;
     pdl_launch_dependents();
+    const size_t at = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    const unsigned row = unit_row(at, p.per_row), col = static_cast<unsigned>(at - static_cast<size_t>(row) * p.per_row) * C;
+    const unsigned ne0 = static_cast<unsigned>(p.ne0), ne1 = static_cast<unsigned>(p.ne1);
+    const int have = row >= ne1 || col >= ne0 ? 0 : ne0 - col >= C ? C : static_cast<int>(ne0 - col);
     pdl_wait();
-    const size_t per_row = (p.ne0 + 31) / 32, total = per_row * p.ne1;
-    const size_t step = static_cast<size_t>(gridDim.x) * (blockDim.x / 32);
-    for (size_t b = static_cast<size_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32; b < total; b += step) {
-        const size_t row = b / per_row, i = b % per_row * 32 + threadIdx.x % 32;
-        const bool inside = i < p.ne0;
-        const float x = inside ? load_elem<Td, false>(static_cast<const char *>(p.tensor) + static_cast<long long>(row) * p.stride,
-                                                      static_cast<long long>(i))
-                               : 0.0f;
-        encode_block(p.kept, row, i, x, inside);
+    pair_t v[C / 2] = {};
+    if (have) {
+        Unit<Td, ALIGNED> r;
+        unit_load<Td, ALIGNED>(r, p.tensor.row(row) + col * Elem<Td>::bytes, p.tensor, p.tensor.apart && row > 0 && row + 1 < ne1, have);
+        unit_pairs<Td, ALIGNED>(r, v);
+        if (have < C) first_pairs(v, have);
     }
+    unit_encode(p.kept, row, col, have, v);
 }
 
 // At most T's largest finite value in magnitude; NaN stays.
@@ -1020,17 +975,60 @@ __device__ __forceinline__ float saturated(float x) {
     return x > most ? most : x < -most ? -most : x;
 }
 
-template <int Td>
+template <int Td, bool ALIGNED>
 __global__ void __launch_bounds__(256) ar_checkpoint_unpack_kernel(const __grid_constant__ PackParams p) {
+    constexpr int W = kUnitWords<Td, ALIGNED>, C = kCols<Td, W>, N = C / 2;
+    pdl_launch_dependents();
+    const size_t at = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    const unsigned row = unit_row(at, p.per_row), unit = static_cast<unsigned>(at - static_cast<size_t>(row) * p.per_row);
+    const unsigned ne0 = static_cast<unsigned>(p.ne0), ne1 = static_cast<unsigned>(p.ne1), col = unit * C;
+    const int have = row >= ne1 || col >= ne0 ? 0 : ne0 - col >= C ? C : static_cast<int>(ne0 - col);
+    pdl_wait();
+    uint32_t c[N / 2] = {}, w[W];
+    unsigned scale = 0;
+    if (have) {
+        const uint8_t *from = p.kept.codes + row * static_cast<unsigned long long>(p.kept.code_row) + col;
+        scale = p.kept.scales[row * static_cast<unsigned long long>(p.kept.scale_row) + col / kCodeBlock];
+        if (have == C) {
+            if constexpr (C == 16) {
+                load_words<16, false>(from, reinterpret_cast<uint32_t(&)[4]>(c));
+            } else {
+                const uint2 q = *reinterpret_cast<const uint2 *>(from);
+                c[0] = q.x, c[1] = q.y;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < C; ++k)
+                if (k < have) c[k / 4] |= static_cast<uint32_t>(from[k]) << (8 * (k & 3));
+        }
+    }
+    pair_t v[N];
+    decode_pairs(p.kept.format, c, scale_value(scale), v);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float2 f = halves(v[k]);
+        v[k] = make_pair(saturated<Td>(f.x), saturated<Td>(f.y));
+    }
+    round_pairs<Td, W>(v, w);
+    const unsigned prev = threadIdx.x % 32 > 0 && unit > 0, next = threadIdx.x % 32 < 31;
+    unit_store<Td, ALIGNED>(const_cast<char *>(p.tensor.row(row)) + col * Elem<Td>::bytes, w, col, ne0, have, prev, next);
+}
+
+// The same for rows and strides past 32 bits: a warp to a block of 32 elements.
+template <int Td>
+__global__ void __launch_bounds__(256) ar_checkpoint_any_kernel(const __grid_constant__ PackParams p, bool pack) {
     pdl_launch_dependents();
     pdl_wait();
     const size_t per_row = (p.ne0 + 31) / 32, total = per_row * p.ne1;
     const size_t step = static_cast<size_t>(gridDim.x) * (blockDim.x / 32);
     for (size_t b = static_cast<size_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32; b < total; b += step) {
         const size_t row = b / per_row, i = b % per_row * 32 + threadIdx.x % 32;
-        if (i < p.ne0)
-            store_elem<Td>(static_cast<char *>(p.tensor) + static_cast<long long>(row) * p.stride, static_cast<long long>(i),
-                           saturated<Td>(decode_elem(p.kept, row, i)));
+        char *at = const_cast<char *>(p.tensor.base) + static_cast<long long>(row) * p.tensor.wide;
+        const bool inside = i < p.ne0;
+        if (pack)
+            encode_block(p.kept, row, i, inside ? load_elem<Td, false>(at, static_cast<long long>(i)) : 0.0f, inside);
+        else if (inside)
+            store_elem<Td>(at, static_cast<long long>(i), saturated<Td>(decode_elem(p.kept, row, i)));
     }
 }
 

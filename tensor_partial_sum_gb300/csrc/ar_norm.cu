@@ -64,35 +64,6 @@ tps::CodeRows code_rows(const ar_checkpoint *c) {
                          static_cast<uint8_t *>(c->scales), static_cast<long long>(scale_stride(*c)), c->format};
 }
 
-using PackFn = void (*)(tps::PackParams);
-
-int run_checkpoint(const ar_checkpoint *ck, const void *tensor, int64_t row_bytes, int dtype, cudaStream_t stream,
-                   bool pack) {
-    std::lock_guard<std::mutex> lock(tps::context_mutex());
-    tps::CallContext c;
-    if (!tps::current_context(&c)) return AR_ERR_NOT_INITIALIZED;
-    int st = ar_check_checkpoint(ck, tensor, row_bytes, c.max_elems, dtype);
-    if (st != AR_OK || ck->ne0 * ck->ne1 == 0) return st;
-    st = tps::check_launch_device(c);
-    if (st != AR_OK) return st;
-    tps::PackParams p;
-    memset(&p, 0, sizeof p);
-    p.tensor = const_cast<void *>(tensor);
-    p.stride = row_bytes ? row_bytes : static_cast<int64_t>(ck->ne0 * dtype_bytes(dtype));
-    p.ne0 = ck->ne0;
-    p.ne1 = ck->ne1;
-    p.kept = code_rows(ck);
-    const PackFn fn = pack ? by_type<PackFn>(dtype, tps::ar_checkpoint_pack_kernel<tps::kF32>,
-                                             tps::ar_checkpoint_pack_kernel<tps::kF16>,
-                                             tps::ar_checkpoint_pack_kernel<tps::kBF16>)
-                           : by_type<PackFn>(dtype, tps::ar_checkpoint_unpack_kernel<tps::kF32>,
-                                             tps::ar_checkpoint_unpack_kernel<tps::kF16>,
-                                             tps::ar_checkpoint_unpack_kernel<tps::kBF16>);
-    const size_t blocks = (scale_row(*ck) * ck->ne1 + 7) / 8;
-    return launched(tps::launch_dependent(fn, dim3(static_cast<unsigned>(blocks < 65535 ? blocks : 65535)), 256u, 0, stream,
-                                          c.pdl, p));
-}
-
 // ---- norm ------------------------------------------------------------------------
 
 int check_norm(const ar_norm *n, size_t es) {
@@ -124,13 +95,13 @@ struct RowShape {
 constexpr size_t ring_bytes(size_t n) { return 227 * 1024 / n - 3 * 1024; }
 constexpr size_t kSMs = 152;
 
-// `most_u`: the most units that the kernel holds; vecs: 16-byte vectors of a unit and row.
-RowShape row_shape(size_t ne0, size_t ne1, int vecs, int most_u) {
-    const size_t units = (ne0 + 7) / 8;
+// `cols`: columns of a unit; vecs: its 16-byte vectors in a row of the ring; `most_u`: the most units of a thread.
+RowShape row_shape(size_t ne0, size_t ne1, size_t cols, int vecs, int most_u) {
+    const size_t units = (ne0 + cols - 1) / cols;
     RowShape s{};
     s.cluster = 1;
     s.vecs = vecs;
-    if (units <= 64) {
+    if (units <= 32 * static_cast<size_t>(most_u)) {
         s.warp = true;
         s.threads = 256;
         s.U = units <= 32 ? 1 : 2;
@@ -146,7 +117,7 @@ RowShape row_shape(size_t ne0, size_t ne1, int vecs, int most_u) {
         if (!fits(1)) return s;
         // few rows: the blocks that would be idle share them
         while (s.cluster < tps::kRowBlocks && ne1 * s.cluster * 2 <= kSMs && share() >= 128) s.cluster *= 2;
-        s.U = share() <= 128 ? 1 : share() <= 1024 ? 2 : 4;
+        s.U = share() <= 128 ? 1 : most_u;
         s.threads = static_cast<unsigned>(((share() + s.U - 1) / s.U + 31) / 32 * 32);
         s.bx = static_cast<int>(s.threads);
     }
@@ -176,8 +147,8 @@ size_t any_rows(size_t ne1) {
 }
 size_t any_blocks(size_t ne1) { return (ne1 + any_rows(ne1) - 1) / any_rows(ne1); }
 size_t ring_blocks(size_t ne0, size_t ne1) {
-    // 512 threads of at most two units on an SM
-    const size_t units = (ne0 + 7) / 8, most = kSMs * (units <= 64 ? 2 : (1024 + units - 1) / units);
+    // 512 threads of at most 16 columns on an SM
+    const size_t most = kSMs * (ne0 <= 512 ? 2 : (8192 + ne0 - 1) / ne0);
     return ne1 < most ? ne1 : most;
 }
 size_t part_ld(size_t ne0) { return (ne0 + 7) / 8 * 8; }
@@ -187,8 +158,6 @@ int allow_ring(Fn fn, const RowShape &s) {
     if (s.smem <= 44 * 1024) return AR_OK;  // 48 KB with what the kernel declares itself
     return launched(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ring_bytes(1))));
 }
-
-int vecs_of(size_t es, bool aligned) { return static_cast<int>(es) / 2 + (aligned ? 0 : 1); }
 
 using NormFn = void (*)(tps::NormParams);
 
@@ -220,8 +189,11 @@ using GradFn = void (*)(tps::NormGradParams);
 
 template <int Td, bool ALIGNED>
 GradFn pick_backward(const RowShape &s) {
-    if (s.warp) return s.U == 1 ? tps::ar_norm_grad_kernel<Td, ALIGNED, 1, true> : tps::ar_norm_grad_kernel<Td, ALIGNED, 2, true>;
-    return s.U == 1 ? tps::ar_norm_grad_kernel<Td, ALIGNED, 1, false> : tps::ar_norm_grad_kernel<Td, ALIGNED, 2, false>;
+    if (s.U == 1) return s.warp ? tps::ar_norm_grad_kernel<Td, ALIGNED, 1, true> : tps::ar_norm_grad_kernel<Td, ALIGNED, 1, false>;
+    if constexpr (ALIGNED && Td != tps::kF32)
+        return nullptr;  // one unit is 16 columns
+    else
+        return s.warp ? tps::ar_norm_grad_kernel<Td, ALIGNED, 2, true> : tps::ar_norm_grad_kernel<Td, ALIGNED, 2, false>;
 }
 
 template <typename Fn, template <int, bool> class Pick>
@@ -253,7 +225,7 @@ tps::RowSource source_of(const void *p, long long stride, size_t rows, size_t ro
                           static_cast<unsigned>(stride), stride >= 64};
 }
 
-// Whether every row of every buffer starts on a vector boundary (32 bytes for f32, else 16).
+// What the row starts of a call's buffers have in common.
 struct Alignment {
     uintptr_t bits = 0;
     bool narrow = true;  // row numbers and strides of 32 bits
@@ -261,8 +233,53 @@ struct Alignment {
         if (p && rows > 1 && (stride > 0xFFFFFFFFll || rows > 0xFFFFFFFFull)) narrow = false;
         bits |= reinterpret_cast<uintptr_t>(p) | (rows > 1 ? static_cast<uintptr_t>(stride) : 0);
     }
-    bool holds(size_t es) const { return bits % (es == 4 ? 32 : 16) == 0; }
 };
+
+// ---- checkpoint calls ---------------------------------------------------------------
+
+using PackFn = void (*)(tps::PackParams);
+using PackAnyFn = void (*)(tps::PackParams, bool);
+
+template <bool ALIGNED>
+PackFn pick_pack(int dtype, bool pack) {
+    return pack ? by_type<PackFn>(dtype, tps::ar_checkpoint_pack_kernel<tps::kF32, ALIGNED>,
+                                  tps::ar_checkpoint_pack_kernel<tps::kF16, ALIGNED>,
+                                  tps::ar_checkpoint_pack_kernel<tps::kBF16, ALIGNED>)
+                : by_type<PackFn>(dtype, tps::ar_checkpoint_unpack_kernel<tps::kF32, ALIGNED>,
+                                  tps::ar_checkpoint_unpack_kernel<tps::kF16, ALIGNED>,
+                                  tps::ar_checkpoint_unpack_kernel<tps::kBF16, ALIGNED>);
+}
+
+int run_checkpoint(const ar_checkpoint *ck, const void *tensor, int64_t row_bytes, int dtype, cudaStream_t stream,
+                   bool pack) {
+    std::lock_guard<std::mutex> lock(tps::context_mutex());
+    tps::CallContext c;
+    if (!tps::current_context(&c)) return AR_ERR_NOT_INITIALIZED;
+    int st = ar_check_checkpoint(ck, tensor, row_bytes, c.max_elems, dtype);
+    if (st != AR_OK || ck->ne0 * ck->ne1 == 0) return st;
+    st = tps::check_launch_device(c);
+    if (st != AR_OK) return st;
+    const size_t es = dtype_bytes(dtype), row = ck->ne0 * es;
+    tps::PackParams p;
+    memset(&p, 0, sizeof p);
+    Alignment al;
+    al.add(tensor, row_bytes ? row_bytes : static_cast<int64_t>(row), ck->ne1);
+    p.tensor = source_of(tensor, row_bytes ? row_bytes : static_cast<int64_t>(row), ck->ne1, row);
+    p.ne0 = ck->ne0;
+    p.ne1 = ck->ne1;
+    p.kept = code_rows(ck);
+    const bool aligned = al.bits % 32 == 0;
+    const size_t cols = aligned ? 32 / es : 8, lanes = AR_CHECKPOINT_BLOCK / cols;
+    const size_t per_row = ((ck->ne0 + cols - 1) / cols + lanes - 1) / lanes * lanes, blocks = (per_row * ck->ne1 + 255) / 256;
+    p.per_row = static_cast<unsigned>(per_row);
+    if (!al.narrow || ck->ne0 > 0x7FFFFFFF || blocks > 0x7FFFFFFF) {
+        const PackAnyFn any = by_type<PackAnyFn>(dtype, tps::ar_checkpoint_any_kernel<tps::kF32>, tps::ar_checkpoint_any_kernel<tps::kF16>,
+                                                 tps::ar_checkpoint_any_kernel<tps::kBF16>);
+        return launched(tps::launch_dependent(any, dim3(static_cast<unsigned>(kSMs * 8)), 256u, 0, stream, c.pdl, p, pack));
+    }
+    return launched(tps::launch_dependent(aligned ? pick_pack<true>(dtype, pack) : pick_pack<false>(dtype, pack),
+                                          dim3(static_cast<unsigned>(blocks)), 256u, 0, stream, c.pdl, p));
+}
 
 }  // namespace
 
@@ -517,9 +534,12 @@ int ar_reduce_norm_grad(const void *dy, const void *h, const ar_checkpoint *ck, 
         p.ne0 = L->ne0;
         p.ne1 = L->ne1;
         p.weight = norm->weight;
-        const bool aligned = al.holds(es);
-        const int v = vecs_of(es, aligned);
-        const RowShape s = row_shape(L->ne0, L->ne1, v + (h ? v : 1) + (L->residual ? v : 0), 2);
+        const bool aligned = al.bits % 32 == 0;
+        const size_t cols = aligned ? 32 / es : 8;
+        const int v = aligned ? 2 : static_cast<int>(es) / 2 + 1;
+        const RowShape s = row_shape(L->ne0, L->ne1, cols, v + (h ? v : 1) + (L->residual ? v : 0), cols == 16 ? 1 : 2);
+        p.rows_aligned = reinterpret_cast<uintptr_t>(norm->weight) % 16 == 0;
+        p.apart = p.dy.apart && (!h || p.h.apart) && (!L->residual || p.dsum.apart);
         if (s.U && al.narrow) {
             const size_t grid = row_grid(s, L->ne1);
             blocks = grid / s.cluster;
