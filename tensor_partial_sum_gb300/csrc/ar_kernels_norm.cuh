@@ -3,6 +3,7 @@
 
 #include "ar_codes.cuh"
 #include "ar_kernels_ex.cuh"
+#include "ar_umma.cuh"
 #include "ar_pairs.cuh"
 #include "ar_rows8.cuh"
 
@@ -54,6 +55,7 @@ struct NormGradParams {
     unsigned long long part_ld;
     int bx, cluster, stages, vecs;
     int apart, rows_aligned;  // as in NormParams
+    unsigned *status;         // a wait that runs out sets bit 1
     // rows of any length
     float *row_sums;  // [2][ne1]: sum g and sum g x of each row
     unsigned rows_per_block;
@@ -185,14 +187,6 @@ constexpr int kRowBlocks = 8;   // most blocks of a cluster along a row
 constexpr int kRowThreads = 512;   // of the backward pass, at most
 constexpr int kNormThreads = 128;  // of the forward pass
 
-__device__ __forceinline__ unsigned cluster_rank() {
-    unsigned r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ void store_remote(const float *mine, unsigned rank, float v) {
     const unsigned at = static_cast<unsigned>(__cvta_generic_to_shared(mine));
     unsigned there;
@@ -240,7 +234,7 @@ __device__ __forceinline__ void row_sum(float &a, float &b, int bx, int cluster,
                 store_remote(&room.v[at].x, static_cast<unsigned>(lane), a);
                 store_remote(&room.v[at].y, static_cast<unsigned>(lane), b);
             }
-            cluster_barrier();
+            cluster_sync();
             a = b = 0.0f;
             for (int k = lane; k < cluster * warps; k += 32) a += room.v[k].x, b += room.v[k].y;
             lanes();
@@ -440,6 +434,19 @@ __device__ __forceinline__ void row_unit(const void *row, unsigned col, int have
     }
 }
 
+// The first `have` elements of W words, one by one.
+template <int T, int W>
+__device__ __forceinline__ void element_store(char *at, int have, const uint32_t (&w)[W]) {
+#pragma unroll
+    for (int k = 0; k < kCols<T, W>; ++k)
+        if (k < have) {
+            if constexpr (T == kF32)
+                *reinterpret_cast<uint32_t *>(at + 4 * k) = w[k];
+            else
+                *reinterpret_cast<unsigned short *>(at + 2 * k) = static_cast<unsigned short>(w[k / 2] >> (16 * (k & 1)));
+        }
+}
+
 // Store a unit at `at`; see store8 for units off 16-byte boundaries.  The whole warp calls.
 template <int T, bool ALIGNED>
 __device__ __forceinline__ void unit_store(char *at, const uint32_t (&w)[kUnitWords<T, ALIGNED>], unsigned col, unsigned ne0, int have,
@@ -450,14 +457,7 @@ __device__ __forceinline__ void unit_store(char *at, const uint32_t (&w)[kUnitWo
     } else if (have == kCols<T, W>) {
         store_words<4 * W>(at, w);
     } else {
-#pragma unroll
-        for (int k = 0; k < kCols<T, W>; ++k)
-            if (k < have) {
-                if constexpr (T == kF32)
-                    *reinterpret_cast<uint32_t *>(at + 4 * k) = w[k];
-                else
-                    *reinterpret_cast<unsigned short *>(at + 2 * k) = static_cast<unsigned short>(w[k / 2] >> (16 * (k & 1)));
-            }
+        element_store<T, W>(at, have, w);
     }
 }
 
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<Td, ALIGNED, WARP>) 
     const bool prev = tx > 0 && threadIdx.x % 32 > 0, lane_next = tx + 1 < bx && threadIdx.x % 32 < 31;
     uint4 *const mine = held + threadIdx.x;
     pdl_wait();
-    if (!WARP && cluster > 1) cluster_barrier();  // every block of the cluster runs before one writes to another
+    if (!WARP && cluster > 1) cluster_sync();  // every block of the cluster runs before one writes to another
     for (unsigned row0 = group * by; row0 < ne1; row0 += groups * by) {
         const unsigned row = row0 + static_cast<unsigned>(ty);
         const bool in_row = row < ne1, inner = p.apart && row > 0 && row + 1 < ne1;
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
     const unsigned stage_bytes = step * static_cast<unsigned>(p.vecs);
     const unsigned at_h = V * step, at_dsum = at_h + (p.kept.codes ? 1u : V) * step;
     pdl_wait();
-    if (!WARP && t.cluster > 1) cluster_barrier();
+    if (!WARP && t.cluster > 1) cluster_sync();
     pair_t weight[U][N], sw[U][N], ss[U][N], sb[U][N];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -834,6 +834,204 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
     }
 }
 
+// The same for rows on 32-byte boundaries that take a block or more: the copy engine brings a row's share of dy, of the
+// kept sum and of dsum (cp.async copies held the loads to 3 TB/s: 4096 rows of 4096 floats took 92 us without the
+// sums).  A thread holds U 16-byte vectors, 16 columns, blockDim.x vectors apart, so that neither shared memory nor stores
+// have bank conflicts or gaps.
+template <int Td>
+__global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __grid_constant__ NormGradParams p) {
+    constexpr int W = 4, C = kCols<Td, W>, N = C / 2, U = 16 / C;
+    extern __shared__ uint4 ring[];
+    __shared__ RowRoom room[2];
+    __shared__ unsigned long long full[4];
+    __shared__ volatile unsigned lost;
+    pdl_launch_dependents();
+    const unsigned ne0 = static_cast<unsigned>(p.ne0), ne1 = static_cast<unsigned>(p.ne1), T = blockDim.x;
+    const RowThread<C, U, false> t(0, p.cluster, ne0);
+    // a stage: dy, the kept sum (or its codes), dsum; this block's share of a row each
+    const unsigned share = T * U * 16u, at_h = share, code_bytes = T * U * C, at_dsum = at_h + (p.kept.codes ? code_bytes : share);
+    const unsigned stage_bytes = at_dsum + (p.dsum.base ? share : 0u);
+    const unsigned base = static_cast<unsigned>(__cvta_generic_to_shared(ring)), first_col = t.rank * T * U * C;
+    if (threadIdx.x == 0) {
+        lost = 0;
+        for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    pdl_wait();
+    if (t.cluster > 1) cluster_sync();
+    pair_t weight[U][N], sw[U][N], ss[U][N], sb[U][N];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) weight[u][k] = both(1.0f), sw[u][k] = ss[u][k] = sb[u][k] = 0;
+        if (p.weight && t.have[u]) {
+            uint32_t w[W];
+            row_unit<Td, W>(p.weight, t.col(u), t.have[u], p.rows_aligned, w);
+            widen_pairs<Td, W>(w, weight[u]);
+        }
+    }
+    // The bytes of a share that are copied: whole vectors up to the row's end, in the last row those inside the tensor.
+    auto vectors = [&](unsigned bytes_before, unsigned row_bytes, bool last, unsigned most) {
+        const unsigned end = last ? row_bytes / 16 * 16 : (row_bytes + 15) / 16 * 16;
+        return end <= bytes_before ? 0u : end - bytes_before < most ? end - bytes_before : most;
+    };
+    auto issue = [&](unsigned row, int stage) {  // one thread
+        constexpr unsigned es = Elem<Td>::bytes;
+        const bool last = row + 1 == ne1;
+        const unsigned n = vectors(first_col * es, ne0 * es, last, share);
+        const unsigned nc = p.kept.codes ? vectors(first_col, ne0, last, code_bytes) : n;
+        char *to = reinterpret_cast<char *>(ring) + static_cast<unsigned>(stage) * stage_bytes;
+        mbar_expect_tx(&full[stage], n + nc + (p.dsum.base ? n : 0u));
+        if (n) bulk_load(to, p.dy.row(row) + first_col * es, n, &full[stage]);
+        if (nc)
+            bulk_load(to + at_h,
+                      p.kept.codes ? reinterpret_cast<const char *>(p.kept.codes) + row * static_cast<unsigned long long>(p.kept.code_row) + first_col
+                                   : p.h.row(row) + first_col * es,
+                      nc, &full[stage]);
+        if (n && p.dsum.base) bulk_load(to + at_dsum, p.dsum.row(row) + first_col * es, n, &full[stage]);
+    };
+    // what is read straight into registers, a row ahead
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    unsigned next_scale[U] = {};
+    auto fetch = [&](unsigned row) {
+        if (row >= ne1) return;
+        next_mean = p.rms ? 0.0f : p.mean[row];
+        next_rstd = p.rstd[row];
+        if (p.kept.codes) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (t.have[u]) next_scale[u] = p.kept.scales[row * static_cast<unsigned long long>(p.kept.scale_row) + t.col(u) / kCodeBlock];
+        }
+    };
+    const unsigned turn = static_cast<unsigned>(t.groups);
+    fetch(static_cast<unsigned>(t.group));
+    if (threadIdx.x == 0)
+        for (int s = 0; s < p.stages; ++s) {
+            const unsigned row = static_cast<unsigned>(t.group) + s * turn;
+            if (row < ne1) issue(row, s);
+        }
+    int stage = 0;
+    unsigned phase = 0, parity = 0;
+    for (unsigned row = static_cast<unsigned>(t.group); row < ne1; row += turn, parity ^= 1) {
+        const pair_t minus_mean = both(-next_mean);
+        const float rstd = next_rstd;
+        const bool last = row + 1 == ne1;
+        unsigned scale[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) scale[u] = next_scale[u];
+        fetch(row + turn);
+        if (!mbar_wait_bounded(smem_u32(&full[stage]), phase, &lost) && !lost) {
+            lost = 1;
+            atomicOr(p.status, 2u);
+        }
+        const unsigned from = base + static_cast<unsigned>(stage) * stage_bytes;
+        // vector u of a tensor's share; the last row's last columns, which are not copied, straight from the tensor
+        auto read = [&](unsigned at, const RowSource &s, int u, pair_t(&v)[N]) {
+            uint32_t w[W];
+            if (last && t.have[u] && t.have[u] < C) {
+                element_words<Td, W>(s.row(row) + t.col(u) * Elem<Td>::bytes, t.have[u], w);
+            } else {
+                const uint4 q = read_shared(from + at + (u * T + threadIdx.x) * 16u);
+                w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+            }
+            widen_pairs<Td, W>(w, v);
+        };
+        pair_t dy[U][N], x[U][N], a2 = 0, b2 = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            read(0, p.dy, u, dy[u]);
+            if (p.kept.codes) {
+                uint32_t c[N / 2] = {};
+                const unsigned at = from + at_h + (u * T + threadIdx.x) * C;
+                if (last && t.have[u] && (ne0 - t.col(u)) < 16) {
+                    const uint8_t *codes = p.kept.codes + row * static_cast<unsigned long long>(p.kept.code_row) + t.col(u);
+#pragma unroll
+                    for (int k = 0; k < C; ++k)
+                        if (k < t.have[u]) c[k / 4] |= static_cast<uint32_t>(codes[k]) << (8 * (k & 3));
+                } else if constexpr (C == 8) {
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(c[0]), "=r"(c[N / 2 - 1]) : "r"(at) : "memory");
+                } else {
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(c[0]) : "r"(at) : "memory");
+                }
+                decode_pairs(p.kept.format, c, scale_value(scale[u]), x[u]);
+            } else {
+                read(at_h, p.h, u, x[u]);
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) x[u][k] = mul2(add2(x[u][k], minus_mean), both(rstd));
+            if (t.have[u] < C) {
+                first_pairs(dy[u], t.have[u]);
+                first_pairs(x[u], t.have[u]);
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const pair_t g = mul2(dy[u][k], weight[u][k]);
+                a2 = add2(a2, g);
+                b2 = fma2(g, x[u][k], b2);
+            }
+        }
+        const float2 af = halves(a2), bf = halves(b2);
+        float a = af.x + af.y, b = bf.x + bf.y;
+        row_sum<false, true>(a, b, 0, t.cluster, t.rank, room[parity]);
+        // rstd (g - a / n - x b / n)
+        const pair_t k0 = both(rstd), k1 = both(p.rms ? 0.0f : -(a * p.inv_n) * rstd), k2 = both(-(b * p.inv_n) * rstd);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            pair_t d[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const pair_t g = mul2(dy[u][k], weight[u][k]);
+                d[k] = fma2(x[u][k], k2, fma2(g, k0, k1));
+                sw[u][k] = fma2(dy[u][k], x[u][k], sw[u][k]);
+                ss[u][k] = add2(ss[u][k], dy[u][k]);
+            }
+            if (p.dsum.base) {
+                pair_t f[N];
+                read(at_dsum, p.dsum, u, f);
+#pragma unroll
+                for (int k = 0; k < N; ++k) d[k] = add2(d[k], f[k]);
+            }
+            if (!t.have[u]) continue;
+#pragma unroll
+            for (int k = 0; k < N; ++k) sb[u][k] = add2(sb[u][k], d[k]);  // columns behind the row's end are not looked at
+            uint32_t w[W];
+            round_pairs<Td, W>(d, w);
+            for (int k = 0; k < p.n_dxs; ++k) {
+                char *to = static_cast<char *>(p.dx[k]) + static_cast<unsigned long long>(row) * static_cast<unsigned>(p.dx_stride[k]) +
+                           t.col(u) * Elem<Td>::bytes;
+                if (t.have[u] == C)
+                    store_words<16>(to, w);
+                else
+                    element_store<Td, W>(to, t.have[u], w);
+            }
+        }
+        __syncthreads();  // the stage has been read
+        if (threadIdx.x == 0) {
+            const unsigned next = row + static_cast<unsigned>(p.stages) * turn;
+            if (next < ne1 && next > row) issue(next, stage);
+        }
+        if (++stage == p.stages) stage = 0, phase ^= 1;
+    }
+    if (lost && threadIdx.x == 0)  // a copy that came too late must not find another block's shared memory
+        for (int s = 0; s < p.stages; ++s) mbar_wait(&full[s], phase, kUmmaTimeoutNs);
+#pragma unroll
+    for (int which = 0; which < 3; ++which) {
+        if (!p.part[which]) continue;
+        float *row = p.part[which] + t.group * p.part_ld;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!t.have[u]) continue;
+#pragma unroll
+            for (int k = 0; k < N; k += 2) {
+                const pair_t(&v)[N] = which == 0 ? sw[u] : which == 1 ? ss[u] : sb[u];
+                const float2 f = halves(v[k]), g = halves(v[k + 1]);
+                *reinterpret_cast<float4 *>(row + t.col(u) + 2 * k) = make_float4(f.x, f.y, g.x, g.y);
+            }
+        }
+    }
+}
+
 // dy, g = dy * weight and x of one element of the backward pass.
 template <int Td>
 __device__ __forceinline__ void grad_elem(const NormGradParams &p, size_t row, size_t i, float mean, float rstd, float &dy,
@@ -905,8 +1103,8 @@ __global__ void __launch_bounds__(256) ar_norm_grad_any_kernel(const __grid_cons
     }
 }
 
-// out[i] = sum over the row blocks of part[block][i]; blockIdx.y picks the sum.  32 columns and eight groups of
-// row blocks to a block; the groups are added in order.
+// out[i] = sum over the row blocks of part[block][i]; blockIdx.y picks the sum.  64 columns, four to a lane, and 32
+// groups of row blocks to a block; the groups are added in order.
 struct NormColumnSums {
     const float *part[3];
     float *out[3];
@@ -914,23 +1112,29 @@ struct NormColumnSums {
     unsigned blocks;
 };
 
-static __global__ void __launch_bounds__(256) ar_norm_column_sum_kernel(const __grid_constant__ NormColumnSums p) {
-    __shared__ float sums[8][32];
+static __global__ void __launch_bounds__(512) ar_norm_column_sum_kernel(const __grid_constant__ NormColumnSums p) {
+    __shared__ float4 sums[32][17];
     pdl_launch_dependents();
-    pdl_wait();
     const float *part = p.part[blockIdx.y];
-    const int c = threadIdx.x % 32, g = threadIdx.x / 32;
-    const size_t i = static_cast<size_t>(blockIdx.x) * 32 + c;
-    float s = 0.0f;
+    const int c = threadIdx.x % 16, g = threadIdx.x / 16;
+    const size_t i = (static_cast<size_t>(blockIdx.x) * 16 + c) * 4;
+    pdl_wait();
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (i < p.ne0) {
-#pragma unroll 8
-        for (unsigned b = g; b < p.blocks; b += 8) s += part[b * p.ld + i];
+#pragma unroll 10
+        for (unsigned b = g; b < p.blocks; b += 32) {
+            const float4 f = *reinterpret_cast<const float4 *>(part + b * p.ld + i);
+            s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
+        }
     }
     sums[g][c] = s;
     __syncthreads();
-    if (g == 0 && i < p.ne0) {
-        for (int q = 1; q < 8; ++q) s += sums[q][c];
-        p.out[blockIdx.y][i] = s;
+    if (threadIdx.x < 64) {
+        const size_t out = static_cast<size_t>(blockIdx.x) * 64 + threadIdx.x;
+        float t = 0.0f;
+#pragma unroll 8
+        for (int q = 0; q < 32; ++q) t += reinterpret_cast<const float *>(&sums[q][0])[threadIdx.x];
+        if (out < p.ne0) p.out[blockIdx.y][out] = t;
     }
 }
 

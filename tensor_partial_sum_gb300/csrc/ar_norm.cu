@@ -132,6 +132,32 @@ RowShape row_shape(size_t ne0, size_t ne1, size_t cols, int vecs, int most_u) {
     return s;
 }
 
+// The same for rows that the copy engine brings: 16 columns a thread, `bytes` of a column in a row of the ring.  U = 0:
+// too short or too long.
+RowShape copied_shape(size_t ne0, size_t ne1, size_t es, size_t bytes) {
+    RowShape s{};
+    if (ne0 <= 512) return s;
+    s.cluster = 1;
+    const size_t vectors = (ne0 * es + 15) / 16, units = 16 * es / 16;  // a thread's vectors
+    auto share = [&] { return (vectors + s.cluster - 1) / s.cluster; };
+    auto threads = [&] { return ((share() + units - 1) / units + 31) / 32 * 32; };
+    auto fits = [&](size_t rows) { return threads() <= tps::kRowThreads && threads() * 16 * bytes * rows <= ring_bytes(1); };
+    while (s.cluster < tps::kRowBlocks && !fits(2)) s.cluster *= 2;
+    if (!fits(2)) return s;
+    while (s.cluster < tps::kRowBlocks && ne1 * s.cluster * 2 <= kSMs && threads() >= 64) s.cluster *= 2;
+    s.threads = static_cast<unsigned>(threads());
+    s.U = static_cast<int>(units);
+    s.bx = static_cast<int>(s.threads);
+    const size_t row = s.threads * 16 * bytes;
+    s.resident = static_cast<int>(tps::kRowThreads / s.threads);
+    if (s.resident > 8) s.resident = 8;
+    while (s.resident > 1 && row * 2 > ring_bytes(s.resident)) --s.resident;
+    const size_t rows = ring_bytes(s.resident) / row;
+    s.stages = static_cast<int>(rows > 4 ? 4 : rows);
+    s.smem = row * s.stages;
+    return s;
+}
+
 // Blocks of a launch over ne1 rows, whole clusters.
 size_t row_grid(const RowShape &s, size_t ne1) {
     const size_t turn = s.warp ? s.threads / s.bx : 1;
@@ -151,7 +177,7 @@ size_t ring_blocks(size_t ne0, size_t ne1) {
     const size_t most = kSMs * (ne0 <= 512 ? 2 : (8192 + ne0 - 1) / ne0);
     return ne1 < most ? ne1 : most;
 }
-size_t part_ld(size_t ne0) { return (ne0 + 7) / 8 * 8; }
+size_t part_ld(size_t n) { return (n + 7) / 8 * 8; }
 
 template <typename Fn>
 int allow_ring(Fn fn, const RowShape &s) {
@@ -228,9 +254,9 @@ tps::RowSource source_of(const void *p, long long stride, size_t rows, size_t ro
 // What the row starts of a call's buffers have in common.
 struct Alignment {
     uintptr_t bits = 0;
-    bool narrow = true;  // row numbers and strides of 32 bits
+    bool narrow = true;  // strides of 32 bits, and row numbers that stay below them a grid further on
     void add(const void *p, long long stride, size_t rows) {
-        if (p && rows > 1 && (stride > 0xFFFFFFFFll || rows > 0xFFFFFFFFull)) narrow = false;
+        if (p && rows > 1 && (stride > 0xFFFFFFFFll || rows > 0x3FFFFFFFull)) narrow = false;
         bits |= reinterpret_cast<uintptr_t>(p) | (rows > 1 ? static_cast<uintptr_t>(stride) : 0);
     }
 };
@@ -440,7 +466,7 @@ int ar_reduce_norm_grad_workspace(const ar_layout *L, int n_sums, size_t *bytes)
     if (!L || !bytes || n_sums < 0 || n_sums > 3) return AR_ERR_INVALID_ARG;
     if (L->ne0 > SIZE_MAX / 16 || (L->ne0 && L->ne1 > SIZE_MAX / L->ne0 / 16)) return AR_ERR_TOO_LARGE;
     // which path a call takes depends on its pointers: room for the larger
-    const size_t any = 2 * L->ne1 + static_cast<size_t>(n_sums) * any_blocks(L->ne1) * part_ld(L->ne0);
+    const size_t any = part_ld(2 * L->ne1) + static_cast<size_t>(n_sums) * any_blocks(L->ne1) * part_ld(L->ne0);
     const size_t ring = static_cast<size_t>(n_sums) * ring_blocks(L->ne0, L->ne1) * part_ld(L->ne0);
     *bytes = L->ne0 ? (any > ring ? any : ring) * sizeof(float) : 0;
     return AR_OK;
@@ -537,7 +563,12 @@ int ar_reduce_norm_grad(const void *dy, const void *h, const ar_checkpoint *ck, 
         const bool aligned = al.bits % 32 == 0;
         const size_t cols = aligned ? 32 / es : 8;
         const int v = aligned ? 2 : static_cast<int>(es) / 2 + 1;
-        const RowShape s = row_shape(L->ne0, L->ne1, cols, v + (h ? v : 1) + (L->residual ? v : 0), cols == 16 ? 1 : 2);
+        p.status = c.dev_status;
+        // whole vectors of a row that is broadcast could reach behind its end
+        const bool copied = aligned && !(L->residual && L->residual_row_bytes == 0 && L->ne1 > 1 && packed % 16);
+        const RowShape rows = copied ? copied_shape(L->ne0, L->ne1, es, es + (h ? es : 1) + (L->residual ? es : 0)) : RowShape{};
+        const RowShape s =
+            rows.U ? rows : row_shape(L->ne0, L->ne1, cols, v + (h ? v : 1) + (L->residual ? v : 0), cols == 16 ? 1 : 2);
         p.rows_aligned = reinterpret_cast<uintptr_t>(norm->weight) % 16 == 0;
         p.apart = p.dy.apart && (!h || p.h.apart) && (!L->residual || p.dsum.apart);
         if (s.U && al.narrow) {
@@ -548,7 +579,10 @@ int ar_reduce_norm_grad(const void *dy, const void *h, const ar_checkpoint *ck, 
             p.cluster = s.cluster;
             p.stages = s.stages;
             p.vecs = s.vecs;
-            const GradFn fn = pick_rows<GradFn, Backward>(dst_dtype, aligned, s);
+            const GradFn fn = rows.U ? by_type<GradFn>(dst_dtype, tps::ar_norm_grad_rows_kernel<tps::kF32>,
+                                                       tps::ar_norm_grad_rows_kernel<tps::kF16>,
+                                                       tps::ar_norm_grad_rows_kernel<tps::kBF16>)
+                                     : pick_rows<GradFn, Backward>(dst_dtype, aligned, s);
             st = allow_ring(fn, s);
             if (st != AR_OK) return st;
             st = launched(tps::launch_clustered(fn, dim3(static_cast<unsigned>(grid)), static_cast<unsigned>(s.cluster), s.threads,
@@ -556,7 +590,7 @@ int ar_reduce_norm_grad(const void *dy, const void *h, const ar_checkpoint *ck, 
         } else {
             blocks = any_blocks(L->ne1);
             p.row_sums = static_cast<float *>(ws);
-            place(p.row_sums + 2 * L->ne1);
+            place(p.row_sums + part_ld(2 * L->ne1));  // on a 16-byte boundary
             p.rows_per_block = static_cast<unsigned>(any_rows(L->ne1));
             const GradFn stats = by_type<GradFn>(dst_dtype, tps::ar_norm_row_sums_kernel<tps::kF32>,
                                                  tps::ar_norm_row_sums_kernel<tps::kF16>, tps::ar_norm_row_sums_kernel<tps::kBF16>);
@@ -581,8 +615,8 @@ int ar_reduce_norm_grad(const void *dy, const void *h, const ar_checkpoint *ck, 
     s.ld = p.part_ld;
     s.blocks = static_cast<unsigned>(blocks);
     return launched(tps::launch_dependent(tps::ar_norm_column_sum_kernel,
-                                          dim3(static_cast<unsigned>((L->ne0 + 31) / 32), static_cast<unsigned>(n_sums)),
-                                          256u, 0, stream, c.pdl, s));
+                                          dim3(static_cast<unsigned>((L->ne0 + 63) / 64), static_cast<unsigned>(n_sums)),
+                                          512u, 0, stream, c.pdl, s));
 }
 
 }  // extern "C"
