@@ -1,6 +1,8 @@
 // Device code of ar_reduce_norm and ar_reduce_norm_grad.
 #pragma once
 
+
+
 #include "ar_codes.cuh"
 #include "ar_kernels_ex.cuh"
 #include "ar_umma.cuh"
@@ -838,7 +840,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
 // kept sum and of dsum (cp.async copies held the loads to 3 TB/s: 4096 rows of 4096 floats took 92 us without the
 // sums).  A thread holds U 16-byte vectors, 16 columns, blockDim.x vectors apart, so that neither shared memory nor stores
 // have bank conflicts or gaps.
-template <int Td>
+template <int Td, bool BIAS>
 __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __grid_constant__ NormGradParams p) {
     constexpr int W = 4, C = kCols<Td, W>, N = C / 2, U = 16 / C;
     extern __shared__ uint4 ring[];
@@ -851,7 +853,8 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
     // a stage: dy, the kept sum (or its codes), dsum; this block's share of a row each
     const unsigned share = T * U * 16u, at_h = share, code_bytes = T * U * C, at_dsum = at_h + (p.kept.codes ? code_bytes : share);
     const unsigned stage_bytes = at_dsum + (p.dsum.base ? share : 0u);
-    const unsigned base = static_cast<unsigned>(__cvta_generic_to_shared(ring)), first_col = t.rank * T * U * C;
+    const unsigned base = static_cast<unsigned>(__cvta_generic_to_shared(ring)), first_col = t.rank * T * U * C, hop = T * 16u;
+    const bool inside = t.have[U - 1] == C;  // all of this thread's columns are inside the row
     if (threadIdx.x == 0) {
         lost = 0;
         for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
@@ -860,11 +863,11 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
     __syncthreads();
     pdl_wait();
     if (t.cluster > 1) cluster_sync();
-    pair_t weight[U][N], sw[U][N], ss[U][N], sb[U][N];
+    pair_t weight[U][N], sw[U][N], ss[U][N], sb[BIAS ? U : 1][N];  // BIAS: dbias is wanted
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) weight[u][k] = both(1.0f), sw[u][k] = ss[u][k] = sb[u][k] = 0;
+        for (int k = 0; k < N; ++k) weight[u][k] = both(1.0f), sw[u][k] = ss[u][k] = sb[BIAS ? u : 0][k] = 0;
         if (p.weight && t.have[u]) {
             uint32_t w[W];
             row_unit<Td, W>(p.weight, t.col(u), t.have[u], p.rows_aligned, w);
@@ -925,87 +928,104 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
             lost = 1;
             atomicOr(p.status, 2u);
         }
-        const unsigned from = base + static_cast<unsigned>(stage) * stage_bytes;
-        // vector u of a tensor's share; the last row's last columns, which are not copied, straight from the tensor
-        auto read = [&](unsigned at, const RowSource &s, int u, pair_t(&v)[N]) {
+        const unsigned from = base + static_cast<unsigned>(stage) * stage_bytes + threadIdx.x * 16u;
+        pair_t dy[U][N], x[U][N], a2 = 0, b2 = 0;
+        float a = 0.0f, b = 0.0f;
+        // EDGE: some columns lie behind the row's end, or in the tensor's last vector, which is not copied
+        auto half = [&](const bool edge, unsigned at, const RowSource &s, int u, pair_t(&v)[N]) {
             uint32_t w[W];
-            if (last && t.have[u] && t.have[u] < C) {
+            if (edge && last && t.have[u] && t.have[u] < C) {
                 element_words<Td, W>(s.row(row) + t.col(u) * Elem<Td>::bytes, t.have[u], w);
             } else {
-                const uint4 q = read_shared(from + at + (u * T + threadIdx.x) * 16u);
+                const uint4 q = read_shared(from + at + u * hop);
                 w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
             }
             widen_pairs<Td, W>(w, v);
         };
-        pair_t dy[U][N], x[U][N], a2 = 0, b2 = 0;
+        auto sums = [&](const bool edge) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            read(0, p.dy, u, dy[u]);
-            if (p.kept.codes) {
-                uint32_t c[N / 2] = {};
-                const unsigned at = from + at_h + (u * T + threadIdx.x) * C;
-                if (last && t.have[u] && (ne0 - t.col(u)) < 16) {
-                    const uint8_t *codes = p.kept.codes + row * static_cast<unsigned long long>(p.kept.code_row) + t.col(u);
+            for (int u = 0; u < U; ++u) {
+                half(edge, 0, p.dy, u, dy[u]);
+                if (p.kept.codes) {
+                    uint32_t c[N / 2] = {};
+                    const unsigned at = from + at_h - threadIdx.x * (16u - C) + u * (T * C);
+                    if (edge && last && t.have[u] && (ne0 - t.col(u)) < 16) {
+                        const uint8_t *codes = p.kept.codes + row * static_cast<unsigned long long>(p.kept.code_row) + t.col(u);
 #pragma unroll
-                    for (int k = 0; k < C; ++k)
-                        if (k < t.have[u]) c[k / 4] |= static_cast<uint32_t>(codes[k]) << (8 * (k & 3));
-                } else if constexpr (C == 8) {
-                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(c[0]), "=r"(c[N / 2 - 1]) : "r"(at) : "memory");
+                        for (int k = 0; k < C; ++k)
+                            if (k < t.have[u]) c[k / 4] |= static_cast<uint32_t>(codes[k]) << (8 * (k & 3));
+                    } else if constexpr (C == 8) {
+                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(c[0]), "=r"(c[N / 2 - 1]) : "r"(at) : "memory");
+                    } else {
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(c[0]) : "r"(at) : "memory");
+                    }
+                    decode_pairs(p.kept.format, c, scale_value(scale[u]), x[u]);
                 } else {
-                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(c[0]) : "r"(at) : "memory");
+                    half(edge, at_h, p.h, u, x[u]);
                 }
-                decode_pairs(p.kept.format, c, scale_value(scale[u]), x[u]);
-            } else {
-                read(at_h, p.h, u, x[u]);
+#pragma unroll
+                for (int k = 0; k < N; ++k) x[u][k] = mul2(add2(x[u][k], minus_mean), both(rstd));
+                if (edge && t.have[u] < C) {
+                    first_pairs(dy[u], t.have[u]);
+                    first_pairs(x[u], t.have[u]);
+                }
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const pair_t g = mul2(dy[u][k], weight[u][k]);
+                    a2 = add2(a2, g);
+                    b2 = fma2(g, x[u][k], b2);
+                }
             }
+            const float2 af = halves(a2), bf = halves(b2);
+            a = af.x + af.y, b = bf.x + bf.y;
+        };
+        auto results = [&](const bool edge) {
+            // rstd (g - a / n - x b / n)
+            const pair_t k0 = both(rstd), k1 = both(p.rms ? 0.0f : -(a * p.inv_n) * rstd), k2 = both(-(b * p.inv_n) * rstd);
+            uint32_t w[U][W];
 #pragma unroll
-            for (int k = 0; k < N; ++k) x[u][k] = mul2(add2(x[u][k], minus_mean), both(rstd));
-            if (t.have[u] < C) {
-                first_pairs(dy[u], t.have[u]);
-                first_pairs(x[u], t.have[u]);
+            for (int u = 0; u < U; ++u) {
+                pair_t d[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const pair_t g = mul2(dy[u][k], weight[u][k]);
+                    d[k] = fma2(x[u][k], k2, fma2(g, k0, k1));
+                    sw[u][k] = fma2(dy[u][k], x[u][k], sw[u][k]);
+                    ss[u][k] = add2(ss[u][k], dy[u][k]);
+                }
+                if (p.dsum.base) {
+                    pair_t f[N];
+                    half(edge, at_dsum, p.dsum, u, f);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) d[k] = add2(d[k], f[k]);
+                }
+                if constexpr (BIAS) {  // columns behind the row's end are not looked at
+#pragma unroll
+                    for (int k = 0; k < N; ++k) sb[u][k] = add2(sb[u][k], d[k]);
+                }
+                round_pairs<Td, W>(d, w[u]);
             }
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const pair_t g = mul2(dy[u][k], weight[u][k]);
-                a2 = add2(a2, g);
-                b2 = fma2(g, x[u][k], b2);
-            }
-        }
-        const float2 af = halves(a2), bf = halves(b2);
-        float a = af.x + af.y, b = bf.x + bf.y;
-        row_sum<false, true>(a, b, 0, t.cluster, t.rank, room[parity]);
-        // rstd (g - a / n - x b / n)
-        const pair_t k0 = both(rstd), k1 = both(p.rms ? 0.0f : -(a * p.inv_n) * rstd), k2 = both(-(b * p.inv_n) * rstd);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            pair_t d[N];
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const pair_t g = mul2(dy[u][k], weight[u][k]);
-                d[k] = fma2(x[u][k], k2, fma2(g, k0, k1));
-                sw[u][k] = fma2(dy[u][k], x[u][k], sw[u][k]);
-                ss[u][k] = add2(ss[u][k], dy[u][k]);
-            }
-            if (p.dsum.base) {
-                pair_t f[N];
-                read(at_dsum, p.dsum, u, f);
-#pragma unroll
-                for (int k = 0; k < N; ++k) d[k] = add2(d[k], f[k]);
-            }
-            if (!t.have[u]) continue;
-#pragma unroll
-            for (int k = 0; k < N; ++k) sb[u][k] = add2(sb[u][k], d[k]);  // columns behind the row's end are not looked at
-            uint32_t w[W];
-            round_pairs<Td, W>(d, w);
             for (int k = 0; k < p.n_dxs; ++k) {
                 char *to = static_cast<char *>(p.dx[k]) + static_cast<unsigned long long>(row) * static_cast<unsigned>(p.dx_stride[k]) +
-                           t.col(u) * Elem<Td>::bytes;
-                if (t.have[u] == C)
-                    store_words<16>(to, w);
-                else
-                    element_store<Td, W>(to, t.have[u], w);
+                           t.col(0) * Elem<Td>::bytes;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (!edge || t.have[u] == C)
+                        store_words<16>(to + u * hop, w[u]);
+                    else
+                        element_store<Td, W>(to + u * hop, t.have[u], w[u]);
+                }
             }
-        }
+        };
+        if (inside && !last)
+            sums(false);
+        else
+            sums(true);
+        row_sum<false, true>(a, b, 0, t.cluster, t.rank, room[parity]);
+        if (inside && !last)
+            results(false);
+        else
+            results(true);
         __syncthreads();  // the stage has been read
         if (threadIdx.x == 0) {
             const unsigned next = row + static_cast<unsigned>(p.stages) * turn;
@@ -1017,14 +1037,14 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
         for (int s = 0; s < p.stages; ++s) mbar_wait(&full[s], phase, kUmmaTimeoutNs);
 #pragma unroll
     for (int which = 0; which < 3; ++which) {
-        if (!p.part[which]) continue;
+        if (!p.part[which] || (which == 2 && !BIAS)) continue;
         float *row = p.part[which] + t.group * p.part_ld;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (!t.have[u]) continue;
 #pragma unroll
             for (int k = 0; k < N; k += 2) {
-                const pair_t(&v)[N] = which == 0 ? sw[u] : which == 1 ? ss[u] : sb[u];
+                const pair_t(&v)[N] = which == 0 ? sw[u] : which == 1 ? ss[u] : sb[BIAS ? u : 0];
                 const float2 f = halves(v[k]), g = halves(v[k + 1]);
                 *reinterpret_cast<float4 *>(row + t.col(u) + 2 * k) = make_float4(f.x, f.y, g.x, g.y);
             }

@@ -222,6 +222,12 @@ GradFn pick_backward(const RowShape &s) {
         return s.warp ? tps::ar_norm_grad_kernel<Td, ALIGNED, 2, true> : tps::ar_norm_grad_kernel<Td, ALIGNED, 2, false>;
 }
 
+template <bool BIAS>
+GradFn pick_copied(int dtype) {
+    return by_type<GradFn>(dtype, tps::ar_norm_grad_rows_kernel<tps::kF32, BIAS>, tps::ar_norm_grad_rows_kernel<tps::kF16, BIAS>,
+                           tps::ar_norm_grad_rows_kernel<tps::kBF16, BIAS>);
+}
+
 template <typename Fn, template <int, bool> class Pick>
 Fn pick_rows(int dtype, bool aligned, const RowShape &s) {
     if (aligned)
@@ -579,9 +585,7 @@ int ar_reduce_norm_grad(const void *dy, const void *h, const ar_checkpoint *ck, 
             p.cluster = s.cluster;
             p.stages = s.stages;
             p.vecs = s.vecs;
-            const GradFn fn = rows.U ? by_type<GradFn>(dst_dtype, tps::ar_norm_grad_rows_kernel<tps::kF32>,
-                                                       tps::ar_norm_grad_rows_kernel<tps::kF16>,
-                                                       tps::ar_norm_grad_rows_kernel<tps::kBF16>)
+            const GradFn fn = rows.U ? (dbias ? pick_copied<true>(dst_dtype) : pick_copied<false>(dst_dtype))
                                      : pick_rows<GradFn, Backward>(dst_dtype, aligned, s);
             st = allow_ring(fn, s);
             if (st != AR_OK) return st;
