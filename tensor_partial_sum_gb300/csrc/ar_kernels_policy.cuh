@@ -1,8 +1,9 @@
 // Device code of ar_policy_loss.
 //
 // The means need counts before the first gradient can be written, so the mask is read once for them and the
-// tokens once for the rest: zero the counts, count, compute, join the blocks' sums.  Counts are integers, whose
-// order of adding does not matter; floats are added in a fixed order.
+// tokens once for the rest.  Few tokens: one block does both.  Many: a launch counts (behind one that zeroes the
+// counts of the sequences, where those are wanted), the next computes, and its last block joins the blocks' sums.
+// Counts are integers, whose order of adding does not matter; floats are added in a fixed order.
 #pragma once
 
 #include <climits>
@@ -18,12 +19,13 @@ namespace tps {
 constexpr int kPolicyThreads = 256;
 constexpr int kPolicyEach = 8;  // adjacent tokens of a thread
 constexpr int kPolicyChunk = kPolicyThreads * kPolicyEach;
+constexpr int kPolicySmallThreads = 1024;  // of the one block that few tokens take
+constexpr int kPolicySmall = 2 * kPolicySmallThreads * kPolicyEach;  // tokens, at most
 
 struct PolicyCounts {
-    unsigned ticket;
-    unsigned tokens;     // counted tokens
-    unsigned sequences;  // sequences that have some
-    unsigned pad;
+    unsigned ticket;     // blocks that are done
+    unsigned sequences;  // sequences that have counted tokens
+    unsigned pad[2];
 };
 
 struct PolicyParams {
@@ -39,8 +41,9 @@ struct PolicyParams {
     float *totals, *dnll;
     PolicyCounts *counts;
     unsigned *per_sequence;  // counted tokens of each sequence (the mean over sequences)
+    unsigned *per_block;     // counted tokens of each block of the counting launch (the mean over tokens)
     double *part;            // [block][4]: gain, kl, clipped, counted
-    unsigned blocks;
+    unsigned blocks, count_blocks;
 };
 
 // How many of the sequences + 1 offsets are <= t, found by a warp, 32 probes at a time.  Stays within 0 ..
@@ -103,22 +106,92 @@ static __global__ void __launch_bounds__(256) ar_policy_zero_kernel(const __grid
     pdl_wait();
     const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i == 0) *p.counts = PolicyCounts{};
-    if (p.mean == 2 && i < p.sequences) p.per_sequence[i] = 0u;
+    if (i < p.sequences) p.per_sequence[i] = 0u;
 }
 
-template <int N>
+// The sum of n over the block, in every thread.  `room`: a word for each warp.
 __device__ __forceinline__ unsigned block_count(unsigned n, unsigned *room) {
     n = __reduce_add_sync(~0u, n);
+    __syncthreads();
     if (threadIdx.x % 32 == 0) room[threadIdx.x / 32] = n;
     __syncthreads();
     unsigned s = 0;
-#pragma unroll
-    for (int k = 0; k < N / 32; ++k) s += room[k];
-    __syncthreads();
+    for (unsigned k = 0; k < blockDim.x / 32; ++k) s += room[k];
     return s;
 }
 
-// Counted tokens, of each sequence where the mean is over sequences.
+// Bit k: token t0 + k counts as far as the mask and the array's end say.
+__device__ __forceinline__ unsigned mask_bits(const PolicyParams &p, unsigned long long t0, unsigned long long end) {
+    if (t0 >= end) return 0u;
+    unsigned bits = end - t0 >= 8 ? 0xFFu : (1u << (end - t0)) - 1u;
+    if (!p.mask) return bits;
+    if (p.vec && bits == 0xFFu) {
+        const uint2 m = *reinterpret_cast<const uint2 *>(p.mask + t0);
+        bits = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) bits |= static_cast<unsigned>(((k < 4 ? m.x : m.y) >> (8 * (k & 3)) & 0xFFu) != 0) << k;
+        return bits;
+    }
+    unsigned some = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) some |= static_cast<unsigned>((bits >> k & 1u) && p.mask[t0 + k] != 0) << k;
+    return some;
+}
+// Bit k: token t0 + k lies between the first and the last offset.
+__device__ __forceinline__ unsigned between_bits(unsigned long long t0, long long first, long long last) {
+    const long long t = static_cast<long long>(t0);
+    if (t >= first && t + 8 <= last) return 0xFFu;
+    unsigned bits = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bits |= static_cast<unsigned>(t + k >= first && t + k < last) << k;
+    return bits;
+}
+
+// Adds up the counted tokens of each sequence among eight tokens.
+__device__ __forceinline__ void count_sequences(const PolicyParams &p, unsigned long long t0, unsigned bits, const unsigned *bounds) {
+    SequenceWalk w;
+    w.seek(p, static_cast<long long>(t0), bounds[0], bounds[1]);
+    if (w.next >= static_cast<long long>(t0) + 8) {
+        if (bits && w.inside(p)) atomicAdd(p.per_sequence + w.upto - 1, __popc(bits));
+        return;
+    }
+    unsigned here = 0, at = w.upto;
+    for (int k = 0; k < 8; ++k) {
+        w.advance(p, static_cast<long long>(t0 + k));
+        if (w.upto != at) {
+            if (here) atomicAdd(p.per_sequence + at - 1, here);
+            here = 0;
+            at = w.upto;
+        }
+        here += w.inside(p) && (bits >> k & 1u);
+    }
+    if (here) atomicAdd(p.per_sequence + at - 1, here);
+}
+
+// Sequences with counted tokens, in every thread of the block.
+__device__ __forceinline__ unsigned counted_sequences(const PolicyParams &p, unsigned *room) {
+    unsigned some = 0;
+    for (unsigned s = threadIdx.x; s < p.sequences; s += blockDim.x) some += __ldcg(p.per_sequence + s) > 0;
+    return block_count(some, room);
+}
+
+// Counted tokens of each block, and the ticket of the launch behind this one.
+static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_count_tokens_kernel(const __grid_constant__ PolicyParams p) {
+    __shared__ unsigned room[kPolicyThreads / 32];
+    pdl_launch_dependents();
+    pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.counts = PolicyCounts{};
+    const long long first = p.sequences ? p.offsets[0] : 0, last = p.sequences ? p.offsets[p.sequences] : 0;
+    unsigned n = 0;
+#pragma unroll 4
+    for (unsigned long long t = (static_cast<unsigned long long>(blockIdx.x) * kPolicyThreads + threadIdx.x) * 8; t < p.tokens;
+         t += static_cast<unsigned long long>(gridDim.x) * kPolicyThreads * 8)
+        n += __popc(mask_bits(p, t, p.tokens) & between_bits(t, first, last));
+    n = block_count(n, room);
+    if (threadIdx.x == 0) p.per_block[blockIdx.x] = n;
+}
+
+// Counted tokens of each sequence; the last block counts the sequences that have some.
 static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_count_kernel(const __grid_constant__ PolicyParams p) {
     __shared__ unsigned bounds[2], room[kPolicyThreads / 32];
     __shared__ bool last_block;
@@ -126,40 +199,18 @@ static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_count_kernel(
     pdl_wait();
     const unsigned long long first = static_cast<unsigned long long>(blockIdx.x) * kPolicyChunk;
     const unsigned long long end = first + kPolicyChunk < p.tokens ? first + kPolicyChunk : p.tokens;
-    unsigned counted = 0;
-    chunk_bounds(p, first, end - 1, bounds);
     const unsigned long long t0 = first + threadIdx.x * kPolicyEach;
-    if (p.sequences && t0 < end) {
-        SequenceWalk w;
-        w.seek(p, static_cast<long long>(t0), bounds[0], bounds[1]);
-        unsigned here = 0, at = w.upto;
-        for (int k = 0; k < kPolicyEach && t0 + k < end; ++k) {
-            w.advance(p, static_cast<long long>(t0 + k));
-            if (p.mean == 2 && w.upto != at) {
-                if (here) atomicAdd(p.per_sequence + at - 1, here);
-                counted += here;
-                here = 0;
-                at = w.upto;
-            }
-            here += w.inside(p) && (!p.mask || p.mask[t0 + k]);
-        }
-        counted += here;
-        if (p.mean == 2 && here) atomicAdd(p.per_sequence + at - 1, here);
-    }
-    counted = block_count<kPolicyThreads>(counted, room);
-    if (threadIdx.x == 0) {
-        if (counted) atomicAdd(&p.counts->tokens, counted);
-        __threadfence();
-        last_block = atomicAdd(&p.counts->ticket, 1u) == gridDim.x - 1;
-    }
-    if (p.mean != 2) return;
+    const unsigned bits = mask_bits(p, t0, end);
+    chunk_bounds(p, first, end - 1, bounds);
+    if (p.sequences && bits) count_sequences(p, t0, bits, bounds);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last_block = atomicAdd(&p.counts->ticket, 1u) == gridDim.x - 1;
     __syncthreads();
     if (!last_block) return;
     __threadfence();
-    unsigned some = 0;
-    for (unsigned s = threadIdx.x; s < p.sequences; s += blockDim.x) some += __ldcg(p.per_sequence + s) > 0;
-    some = block_count<kPolicyThreads>(some, room);
-    if (threadIdx.x == 0) p.counts->sequences = some;
+    const unsigned some = counted_sequences(p, room);
+    if (threadIdx.x == 0) p.counts->sequences = some, p.counts->ticket = 0u;  // the ticket of the launch behind this one
 }
 
 // exp(d) - d - 1 and its derivative exp(d) - 1.  Near zero the first is d^2 / 2 + d^3 / 6 + ..., of which the
@@ -227,38 +278,22 @@ __device__ __forceinline__ void tokens8(const float *a, unsigned long long t, un
     }
 }
 
-static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_kernel(const __grid_constant__ PolicyParams p) {
-    __shared__ unsigned bounds[2];
-    __shared__ float room[4][kPolicyThreads / 32];
-    pdl_launch_dependents();
-    pdl_wait();
-    const unsigned long long first = static_cast<unsigned long long>(blockIdx.x) * kPolicyChunk;
-    const unsigned long long end = first + kPolicyChunk < p.tokens ? first + kPolicyChunk : p.tokens;
-    const unsigned long long t0 = first + threadIdx.x * kPolicyEach;
-    const bool mine = t0 < end;
-    float nll[8], old_nll[8], ref_nll[8], adv[8], out[8];
-    unsigned counts = 0;
-    if (mine) {
-        tokens8(p.nll, t0, end, p.vec, nll);
-        if (p.old_nll) tokens8(p.old_nll, t0, end, p.vec, old_nll);
-        if (p.ref_nll) tokens8(p.ref_nll, t0, end, p.vec, ref_nll);
-        if (p.token_adv) tokens8(p.adv, t0, end, p.vec, adv);
-        if (!p.mask) {
-            counts = 0xFFu;
-        } else if (p.vec && t0 + 8 <= end) {
-            const uint2 m = *reinterpret_cast<const uint2 *>(p.mask + t0);
+// The eight tokens from t0 on: their sums, and their gradients.  `n`: what the mean divides by; `bits`: which tokens
+// the mask leaves; `bounds`: the chunk's, where sequences matter.
+__device__ __forceinline__ void policy_tokens(const PolicyParams &p, unsigned long long t0, unsigned long long end, unsigned bits,
+                                              const float (&nll)[8], const float (&old_nll)[8], const float (&ref_nll)[8],
+                                              const float (&adv)[8], unsigned n, const unsigned *bounds, long long first, long long last,
+                                              PolicySums &s) {
+    const float base = static_cast<float>(p.scale / (n ? n : 1u)), beta = static_cast<float>(p.kl_weight);
+    float out[8];
+    if (p.token_adv && p.mean != 2) {
+        bits &= between_bits(t0, first, last);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) counts |= static_cast<unsigned>(((k < 4 ? m.x : m.y) >> (8 * (k & 3)) & 0xFFu) != 0) << k;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) counts |= static_cast<unsigned>(t0 + k < end && p.mask[t0 + k] != 0) << k;
+        for (int k = 0; k < 8; ++k) {
+            out[k] = 0.0f;
+            if (bits >> k & 1u) out[k] = policy_token(p, nll[k], old_nll[k], ref_nll[k], adv[k], 1.0f, beta, s) * base;
         }
-    }
-    chunk_bounds(p, first, end - 1, bounds);
-    PolicySums s;
-    if (mine) {
-        const unsigned n = p.mean == 0 ? 1u : p.mean == 1 ? p.counts->tokens : p.counts->sequences;
-        const float base = static_cast<float>(p.scale / (n ? n : 1u)), beta = static_cast<float>(p.kl_weight);
+    } else {
         SequenceWalk w;
         unsigned at = ~0u;
         float a = 0.0f, weight = 1.0f;
@@ -266,65 +301,167 @@ static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_kernel(const 
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             out[k] = 0.0f;
-            if (!((counts >> k) & 1u) || t0 + k >= end || !p.sequences) continue;
+            if (!(bits >> k & 1u) || !p.sequences) continue;
             w.advance(p, static_cast<long long>(t0 + k));
             if (!w.inside(p)) continue;
             if (w.upto != at) {
                 at = w.upto;
                 if (!p.token_adv) a = p.adv[at - 1];
-                if (p.mean == 2) weight = 1.0f / static_cast<float>(p.per_sequence[at - 1]);
+                if (p.mean == 2) weight = 1.0f / static_cast<float>(__ldcg(p.per_sequence + at - 1));
             }
             out[k] = policy_token(p, nll[k], old_nll[k], ref_nll[k], p.token_adv ? adv[k] : a, weight, beta, s) * (base * weight);
         }
-        if (p.dnll) {
-            if (p.vec && t0 + 8 <= end) {
-                *reinterpret_cast<float4 *>(p.dnll + t0) = make_float4(out[0], out[1], out[2], out[3]);
-                *reinterpret_cast<float4 *>(p.dnll + t0 + 4) = make_float4(out[4], out[5], out[6], out[7]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (t0 + k < end) p.dnll[t0 + k] = out[k];
-            }
-        }
     }
-    float v[4] = {s.gain, s.kl, static_cast<float>(s.clipped), static_cast<float>(s.counted)};  // counts: at most 2048
+    if (!p.dnll) return;
+    if (p.vec && t0 + 8 <= end) {
+        __stcs(reinterpret_cast<float4 *>(p.dnll + t0), make_float4(out[0], out[1], out[2], out[3]));
+        __stcs(reinterpret_cast<float4 *>(p.dnll + t0 + 4), make_float4(out[4], out[5], out[6], out[7]));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (t0 + k < end) p.dnll[t0 + k] = out[k];
+    }
+}
+
+// The block's sums in 64 bits, in threads 0 .. 3.  `room`: [4][warps].
+__device__ __forceinline__ double policy_block_sums(const PolicySums &s, float *room) {
+    const unsigned warps = blockDim.x / 32;
+    float v[4] = {s.gain, s.kl, static_cast<float>(s.clipped), static_cast<float>(s.counted)};  // counts: at most 16384
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) v[k] += __shfl_xor_sync(~0u, v[k], m);
-        if (threadIdx.x % 32 == 0) room[k][threadIdx.x / 32] = v[k];
+        if (threadIdx.x % 32 == 0) room[k * warps + threadIdx.x / 32] = v[k];
     }
     __syncthreads();
-    if (threadIdx.x < 4) {
-        double sum = 0.0;
-        for (int q = 0; q < kPolicyThreads / 32; ++q) sum += room[threadIdx.x][q];
-        p.part[blockIdx.x * 4ull + threadIdx.x] = sum;
-    }
+    double sum = 0.0;
+    if (threadIdx.x < 4)
+        for (unsigned q = 0; q < warps; ++q) sum += room[threadIdx.x * warps + q];
+    return sum;
 }
 
-// The blocks' sums in a fixed order, and the totals.
-static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_join_kernel(const __grid_constant__ PolicyParams p) {
-    __shared__ double room[kPolicyThreads];
-    pdl_launch_dependents();
-    pdl_wait();
+// The totals from all sums; `some`: sequences with counted tokens.
+__device__ __forceinline__ void policy_totals(const PolicyParams &p, double gain_sum, double kl_sum, double clipped, double tokens,
+                                              unsigned some) {
+    const double counted = tokens > 0.0 ? tokens : 1.0;
+    const double n = p.mean == 1 ? counted : p.mean == 2 && some ? some : 1u;
+    const double gain = 0.0 - p.scale * gain_sum / n, kl = p.scale * kl_sum / n;
+    p.totals[0] = static_cast<float>(p.kl_weight == 0.0 ? gain : gain + p.kl_weight * kl);
+    p.totals[1] = static_cast<float>(gain);
+    p.totals[2] = static_cast<float>(kl);
+    p.totals[3] = static_cast<float>(clipped / counted);
+}
+
+// The blocks' sums in a fixed order, by kPolicyThreads threads.
+__device__ __forceinline__ void policy_join(const PolicyParams &p, unsigned some, double *room) {
     const int which = threadIdx.x % 4;
     double s = 0.0;
-    for (unsigned b = threadIdx.x / 4; b < p.blocks; b += kPolicyThreads / 4) s += p.part[b * 4ull + which];
+#pragma unroll 8
+    for (unsigned b = threadIdx.x / 4; b < p.blocks; b += kPolicyThreads / 4) s += __ldcg(p.part + b * 4ull + which);
     room[threadIdx.x] = s;
     for (int n = kPolicyThreads / 2; n >= 4; n >>= 1) {
         __syncthreads();
         if (threadIdx.x < n) room[threadIdx.x] += room[threadIdx.x + n];
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        const double counted = room[3] > 0.0 ? room[3] : 1.0;
-        const unsigned some = p.mean == 2 && p.blocks ? p.counts->sequences : 1u;
-        const double n = p.mean == 1 ? counted : some ? some : 1u;
-        const double gain = 0.0 - p.scale * room[0] / n, kl = p.scale * room[1] / n;
-        p.totals[0] = static_cast<float>(p.kl_weight == 0.0 ? gain : gain + p.kl_weight * kl);
-        p.totals[1] = static_cast<float>(gain);
-        p.totals[2] = static_cast<float>(kl);
-        p.totals[3] = static_cast<float>(room[2] / counted);
+    if (threadIdx.x == 0) policy_totals(p, room[0], room[1], room[2], room[3], some);
+}
+
+// A chunk of the tokens to a block.  Behind a counting launch (JOIN) the last block joins the blocks' sums.
+template <bool JOIN>
+__global__ void __launch_bounds__(kPolicyThreads) ar_policy_kernel(const __grid_constant__ PolicyParams p) {
+    __shared__ unsigned bounds[2], counts[kPolicyThreads / 32];
+    __shared__ float room[4 * kPolicyThreads / 32];
+    __shared__ double joined[kPolicyThreads];
+    __shared__ bool last_block;
+    pdl_launch_dependents();
+    pdl_wait();
+    const unsigned long long first = static_cast<unsigned long long>(blockIdx.x) * kPolicyChunk;
+    const unsigned long long end = first + kPolicyChunk < p.tokens ? first + kPolicyChunk : p.tokens;
+    const unsigned long long t0 = first + threadIdx.x * kPolicyEach;
+    float nll[8], old_nll[8], ref_nll[8], adv[8];
+    const unsigned bits = mask_bits(p, t0, end);
+    if (t0 < end) {
+        tokens8(p.nll, t0, end, p.vec, nll);
+        if (p.old_nll) tokens8(p.old_nll, t0, end, p.vec, old_nll);
+        if (p.ref_nll) tokens8(p.ref_nll, t0, end, p.vec, ref_nll);
+        if (p.token_adv) tokens8(p.adv, t0, end, p.vec, adv);
+    }
+    long long from = 0, to = 0;
+    if (p.sequences) from = p.offsets[0], to = p.offsets[p.sequences];
+    unsigned n = 1, some = 1;
+    if (p.mean == 1) {
+        n = 0;
+        for (unsigned b = threadIdx.x; b < p.count_blocks; b += kPolicyThreads) n += p.per_block[b];
+        n = block_count(n, counts);
+    } else if (p.mean == 2) {
+        n = some = p.counts->sequences;
+    }
+    if (!(p.token_adv && p.mean != 2)) chunk_bounds(p, first, end - 1, bounds);
+    PolicySums s;
+    if (t0 < end) policy_tokens(p, t0, end, bits, nll, old_nll, ref_nll, adv, n, bounds, from, to, s);
+    const double sum = policy_block_sums(s, room);
+    if (threadIdx.x < 4) __stcg(p.part + blockIdx.x * 4ull + threadIdx.x, sum);
+    if constexpr (JOIN) {
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) last_block = atomicAdd(&p.counts->ticket, 1u) == gridDim.x - 1;
+        __syncthreads();
+        if (!last_block) return;
+        __threadfence();
+        policy_join(p, some, joined);
+    }
+}
+
+static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_join_kernel(const __grid_constant__ PolicyParams p) {
+    __shared__ double joined[kPolicyThreads];
+    pdl_launch_dependents();
+    pdl_wait();
+    policy_join(p, 1u, joined);
+}
+
+// Few tokens: everything in one block.
+static __global__ void __launch_bounds__(kPolicySmallThreads) ar_policy_small_kernel(const __grid_constant__ PolicyParams p) {
+    __shared__ unsigned bounds[2], counts[32];
+    __shared__ float room[4 * 32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const unsigned chunk = blockDim.x * kPolicyEach;
+    const bool walk = p.sequences && p.tokens && !(p.token_adv && p.mean != 2);
+    long long from = 0, to = 0;
+    if (p.sequences) from = p.offsets[0], to = p.offsets[p.sequences];
+    if (walk) chunk_bounds(p, 0, p.tokens - 1, bounds);
+    unsigned n = 1, some = 1;
+    if (p.mean == 1) {
+        n = 0;
+        for (unsigned t0 = threadIdx.x * kPolicyEach; t0 < p.tokens; t0 += chunk)
+            n += __popc(mask_bits(p, t0, p.tokens) & between_bits(t0, from, to));
+        n = block_count(n, counts);
+    } else if (p.mean == 2) {
+        for (unsigned q = threadIdx.x; q < p.sequences; q += blockDim.x) p.per_sequence[q] = 0u;
+        __threadfence();
+        __syncthreads();
+        for (unsigned t0 = threadIdx.x * kPolicyEach; t0 < p.tokens; t0 += chunk) {
+            const unsigned bits = mask_bits(p, t0, p.tokens);
+            if (p.sequences && bits) count_sequences(p, t0, bits, bounds);
+        }
+        __threadfence();
+        __syncthreads();
+        n = some = counted_sequences(p, counts);
+    }
+    PolicySums s;
+    for (unsigned t0 = threadIdx.x * kPolicyEach; t0 < p.tokens; t0 += chunk) {
+        float nll[8], old_nll[8], ref_nll[8], adv[8];
+        tokens8(p.nll, t0, p.tokens, p.vec, nll);
+        if (p.old_nll) tokens8(p.old_nll, t0, p.tokens, p.vec, old_nll);
+        if (p.ref_nll) tokens8(p.ref_nll, t0, p.tokens, p.vec, ref_nll);
+        if (p.token_adv) tokens8(p.adv, t0, p.tokens, p.vec, adv);
+        policy_tokens(p, t0, p.tokens, mask_bits(p, t0, p.tokens), nll, old_nll, ref_nll, adv, n, bounds, from, to, s);
+    }
+    double sum = policy_block_sums(s, room);
+    if (threadIdx.x < 32) {
+        const double kl = __shfl_sync(~0u, sum, 1), clipped = __shfl_sync(~0u, sum, 2), counted = __shfl_sync(~0u, sum, 3);
+        if (threadIdx.x == 0) policy_totals(p, sum, kl, clipped, counted, some);
     }
 }
 

@@ -11,17 +11,21 @@ using tps::launched;
 
 namespace {
 
-// A call's workspace: the counts, those of each sequence, and the blocks' sums.
+// A call's workspace: the counts, those of each sequence or counting block, and the blocks' sums.
 struct Plan {
-    size_t blocks, per_sequence, part, bytes;
+    size_t blocks, count_blocks, counts, part, bytes;
+    bool small;
 };
 
 Plan plan_of(const ar_policy *p) {
     Plan w;
-    w.blocks = (p->tokens + tps::kPolicyChunk - 1) / tps::kPolicyChunk;
-    w.per_sequence = sizeof(tps::PolicyCounts);
-    const size_t counts = p->mean == AR_POLICY_SEQUENCES ? p->sequences * sizeof(unsigned) : 0;
-    w.part = (w.per_sequence + counts + 15) / 16 * 16;
+    w.small = p->tokens <= tps::kPolicySmall;
+    w.blocks = w.small ? 0 : (p->tokens + tps::kPolicyChunk - 1) / tps::kPolicyChunk;
+    // four chunks to a thread of the counting launch, and no more blocks than every later block sums quickly
+    w.count_blocks = (w.blocks + 3) / 4 < 1024 ? (w.blocks + 3) / 4 : 1024;
+    w.counts = sizeof(tps::PolicyCounts);
+    const size_t counts = p->mean == AR_POLICY_SEQUENCES ? p->sequences : p->mean == AR_POLICY_TOKENS ? w.count_blocks : 0;
+    w.part = (w.counts + counts * sizeof(unsigned) + 15) / 16 * 16;
     w.bytes = w.part + w.blocks * 4 * sizeof(double);
     return w;
 }
@@ -115,23 +119,29 @@ int ar_policy_loss(const ar_policy *a, float *totals, float *dnll, void *ws, siz
     p.dnll = dnll;
     char *base = static_cast<char *>(ws);
     p.counts = reinterpret_cast<tps::PolicyCounts *>(base);
-    p.per_sequence = reinterpret_cast<unsigned *>(base + w.per_sequence);
+    p.per_sequence = p.per_block = reinterpret_cast<unsigned *>(base + w.counts);
     p.part = reinterpret_cast<double *>(base + w.part);
     p.blocks = static_cast<unsigned>(w.blocks);
-    const unsigned threads = tps::kPolicyThreads;
-    auto go = [&](void (*fn)(tps::PolicyParams), size_t blocks) {
+    p.count_blocks = static_cast<unsigned>(w.count_blocks);
+    auto go = [&](void (*fn)(tps::PolicyParams), size_t blocks, unsigned threads = tps::kPolicyThreads) {
         return launched(tps::launch_dependent(fn, dim3(static_cast<unsigned>(blocks)), threads, 0, stream, c.pdl, p));
     };
-    if (a->mean != AR_POLICY_SUM && w.blocks) {
-        st = go(tps::ar_policy_zero_kernel, a->mean == AR_POLICY_SEQUENCES ? S / threads + 1 : 1);
+    if (w.small) {
+        const size_t threads = (T / tps::kPolicyEach + 32) / 32 * 32;
+        return go(tps::ar_policy_small_kernel, 1, threads < tps::kPolicySmallThreads ? static_cast<unsigned>(threads < 64 ? 64 : threads)
+                                                                                      : static_cast<unsigned>(tps::kPolicySmallThreads));
+    }
+    if (a->mean == AR_POLICY_SUM) {
+        st = go(tps::ar_policy_kernel<false>, w.blocks);
+        return st == AR_OK ? go(tps::ar_policy_join_kernel, 1) : st;
+    }
+    if (a->mean == AR_POLICY_TOKENS) {
+        st = go(tps::ar_policy_count_tokens_kernel, w.count_blocks);
+    } else {
+        st = go(tps::ar_policy_zero_kernel, S / tps::kPolicyThreads + 1);
         if (st == AR_OK) st = go(tps::ar_policy_count_kernel, w.blocks);
-        if (st != AR_OK) return st;
     }
-    if (w.blocks) {
-        st = go(tps::ar_policy_kernel, w.blocks);
-        if (st != AR_OK) return st;
-    }
-    return go(tps::ar_policy_join_kernel, 1);
+    return st == AR_OK ? go(tps::ar_policy_kernel<true>, w.blocks) : st;
 }
 
 }  // extern "C"
