@@ -28,6 +28,13 @@ struct PolicyCounts {
     unsigned pad[2];
 };
 
+// A 64-bit number as floats: rounded, what that leaves rounded, and the sign of what is left then.  Each float
+// operation in place of 64-bit ones counts: this GPU has two of those a cycle and SM (with them the kernel was
+// bound by them, at 75 us for four million tokens).
+struct PolicyLimit {
+    float x, rest, sign;
+};
+
 struct PolicyParams {
     unsigned tokens;
     unsigned sequences;
@@ -35,8 +42,8 @@ struct PolicyParams {
     const float *nll, *old_nll, *ref_nll, *adv;
     const uint8_t *mask;
     int token_adv, mean, vec;  // vec: every array of tokens starts on a 16-byte boundary
-    double log_high, log_low;  // log(1 + clip_high), log(1 - clip_low)
-    float limit_high, limit_low;
+    PolicyLimit high, low;  // log(1 + clip_high), log(1 - clip_low)
+    float limit_high, limit_low, beta;
     double kl_weight, scale;
     float *totals, *dnll;
     PolicyCounts *counts;
@@ -234,15 +241,13 @@ __device__ __forceinline__ void kl_terms(float d, float &kl, float &slope) {
     }
 }
 
-// Whether old - nll lies above (below) a 64-bit limit.  The rounded difference decides unless it is the rounded
-// limit itself, because rounding keeps the order.
-__device__ __forceinline__ bool above(float x, float old_nll, float nll, double limit) {
-    const float l = static_cast<float>(limit);
-    return x > l || (x == l && static_cast<double>(old_nll) - static_cast<double>(nll) > limit);
-}
-__device__ __forceinline__ bool below(float x, float old_nll, float nll, double limit) {
-    const float l = static_cast<float>(limit);
-    return x < l || (x == l && static_cast<double>(old_nll) - static_cast<double>(nll) < limit);
+// Where x = a - b, rounded, lies next to a 64-bit limit: > 0 above, < 0 below.  x decides unless it is the rounded
+// limit itself, because rounding keeps the order; then what rounding took from a - b, which is a float, decides.
+__device__ __forceinline__ float side(float x, float a, float b, const PolicyLimit &l) {
+    if (x != l.x) return x > l.x ? 1.0f : x < l.x ? -1.0f : 0.0f;
+    const float z = __fsub_rn(x, a);
+    const float e = __fsub_rn(__fsub_rn(a, __fsub_rn(x, z)), __fadd_rn(b, z));
+    return e > l.rest ? 1.0f : e < l.rest ? -1.0f : -l.sign;
 }
 
 struct PolicySums {
@@ -254,8 +259,8 @@ struct PolicySums {
 __device__ __forceinline__ float policy_token(const PolicyParams &p, float nll, float old_nll, float ref_nll, float adv,
                                               float weight, float beta, PolicySums &s) {
     const float x = p.old_nll ? old_nll - nll : 0.0f;
-    const bool clipped = p.old_nll && ((adv > 0.0f && above(x, old_nll, nll, p.log_high)) ||
-                                       (adv < 0.0f && below(x, old_nll, nll, p.log_low)));
+    const bool clipped = p.old_nll && ((adv > 0.0f && side(x, old_nll, nll, p.high) > 0.0f) ||
+                                       (adv < 0.0f && side(x, old_nll, nll, p.low) < 0.0f));
     const float slope = clipped || adv == 0.0f ? 0.0f : expf(x) * adv;
     const float gain = clipped ? (adv > 0.0f ? p.limit_high : p.limit_low) * adv : slope;
     float kl = 0.0f, dkl = 0.0f;
@@ -278,13 +283,13 @@ __device__ __forceinline__ void tokens8(const float *a, unsigned long long t, un
     }
 }
 
-// The eight tokens from t0 on: their sums, and their gradients.  `n`: what the mean divides by; `bits`: which tokens
+// The eight tokens from t0 on: their sums, and their gradients.  `base`: scale over what the mean divides by; `bits`: which tokens
 // the mask leaves; `bounds`: the chunk's, where sequences matter.
 __device__ __forceinline__ void policy_tokens(const PolicyParams &p, unsigned long long t0, unsigned long long end, unsigned bits,
                                               const float (&nll)[8], const float (&old_nll)[8], const float (&ref_nll)[8],
-                                              const float (&adv)[8], unsigned n, const unsigned *bounds, long long first, long long last,
+                                              const float (&adv)[8], float base, const unsigned *bounds, long long first, long long last,
                                               PolicySums &s) {
-    const float base = static_cast<float>(p.scale / (n ? n : 1u)), beta = static_cast<float>(p.kl_weight);
+    const float beta = p.beta;
     float out[8];
     if (p.token_adv && p.mean != 2) {
         bits &= between_bits(t0, first, last);
@@ -326,7 +331,7 @@ __device__ __forceinline__ void policy_tokens(const PolicyParams &p, unsigned lo
 // The block's sums in 64 bits, in threads 0 .. 3.  `room`: [4][warps].
 __device__ __forceinline__ double policy_block_sums(const PolicySums &s, float *room) {
     const unsigned warps = blockDim.x / 32;
-    float v[4] = {s.gain, s.kl, static_cast<float>(s.clipped), static_cast<float>(s.counted)};  // counts: at most 16384
+    float v[4] = {s.gain, s.kl, static_cast<float>(s.clipped), static_cast<float>(s.counted)};  // counts: below 2^24
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -367,26 +372,15 @@ __device__ __forceinline__ void policy_join(const PolicyParams &p, unsigned some
     if (threadIdx.x == 0) policy_totals(p, room[0], room[1], room[2], room[3], some);
 }
 
-// A chunk of the tokens to a block.  Behind a counting launch (JOIN) the last block joins the blocks' sums.
+// The chunks of the tokens in turn.  Behind a counting launch (JOIN) the last block joins the blocks' sums.
 template <bool JOIN>
-__global__ void __launch_bounds__(kPolicyThreads) ar_policy_kernel(const __grid_constant__ PolicyParams p) {
+__global__ void __launch_bounds__(kPolicyThreads, 4) ar_policy_kernel(const __grid_constant__ PolicyParams p) {
     __shared__ unsigned bounds[2], counts[kPolicyThreads / 32];
-    __shared__ float room[4 * kPolicyThreads / 32];
+    __shared__ float room[4 * kPolicyThreads / 32], shared_base;
     __shared__ double joined[kPolicyThreads];
     __shared__ bool last_block;
     pdl_launch_dependents();
     pdl_wait();
-    const unsigned long long first = static_cast<unsigned long long>(blockIdx.x) * kPolicyChunk;
-    const unsigned long long end = first + kPolicyChunk < p.tokens ? first + kPolicyChunk : p.tokens;
-    const unsigned long long t0 = first + threadIdx.x * kPolicyEach;
-    float nll[8], old_nll[8], ref_nll[8], adv[8];
-    const unsigned bits = mask_bits(p, t0, end);
-    if (t0 < end) {
-        tokens8(p.nll, t0, end, p.vec, nll);
-        if (p.old_nll) tokens8(p.old_nll, t0, end, p.vec, old_nll);
-        if (p.ref_nll) tokens8(p.ref_nll, t0, end, p.vec, ref_nll);
-        if (p.token_adv) tokens8(p.adv, t0, end, p.vec, adv);
-    }
     long long from = 0, to = 0;
     if (p.sequences) from = p.offsets[0], to = p.offsets[p.sequences];
     unsigned n = 1, some = 1;
@@ -397,9 +391,29 @@ __global__ void __launch_bounds__(kPolicyThreads) ar_policy_kernel(const __grid_
     } else if (p.mean == 2) {
         n = some = p.counts->sequences;
     }
-    if (!(p.token_adv && p.mean != 2)) chunk_bounds(p, first, end - 1, bounds);
+    if (threadIdx.x == 0) shared_base = static_cast<float>(p.scale / (n ? n : 1u));
+    __syncthreads();
+    const float base = shared_base;
+    const bool walk = !(p.token_adv && p.mean != 2);
     PolicySums s;
-    if (t0 < end) policy_tokens(p, t0, end, bits, nll, old_nll, ref_nll, adv, n, bounds, from, to, s);
+    for (unsigned long long first = static_cast<unsigned long long>(blockIdx.x) * kPolicyChunk; first < p.tokens;
+         first += static_cast<unsigned long long>(gridDim.x) * kPolicyChunk) {
+        const unsigned long long end = first + kPolicyChunk < p.tokens ? first + kPolicyChunk : p.tokens;
+        const unsigned long long t0 = first + threadIdx.x * kPolicyEach;
+        float nll[8], old_nll[8], ref_nll[8], adv[8];
+        const unsigned bits = mask_bits(p, t0, end);
+        if (t0 < end) {
+            tokens8(p.nll, t0, end, p.vec, nll);
+            if (p.old_nll) tokens8(p.old_nll, t0, end, p.vec, old_nll);
+            if (p.ref_nll) tokens8(p.ref_nll, t0, end, p.vec, ref_nll);
+            if (p.token_adv) tokens8(p.adv, t0, end, p.vec, adv);
+        }
+        if (walk) {
+            __syncthreads();  // the bounds of the chunk before have been read
+            chunk_bounds(p, first, end - 1, bounds);
+        }
+        if (t0 < end) policy_tokens(p, t0, end, bits, nll, old_nll, ref_nll, adv, base, bounds, from, to, s);
+    }
     const double sum = policy_block_sums(s, room);
     if (threadIdx.x < 4) __stcg(p.part + blockIdx.x * 4ull + threadIdx.x, sum);
     if constexpr (JOIN) {
@@ -423,7 +437,7 @@ static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_join_kernel(c
 // Few tokens: everything in one block.
 static __global__ void __launch_bounds__(kPolicySmallThreads) ar_policy_small_kernel(const __grid_constant__ PolicyParams p) {
     __shared__ unsigned bounds[2], counts[32];
-    __shared__ float room[4 * 32];
+    __shared__ float room[4 * 32], shared_base;
     pdl_launch_dependents();
     pdl_wait();
     const unsigned chunk = blockDim.x * kPolicyEach;
@@ -449,6 +463,9 @@ static __global__ void __launch_bounds__(kPolicySmallThreads) ar_policy_small_ke
         __syncthreads();
         n = some = counted_sequences(p, counts);
     }
+    if (threadIdx.x == 0) shared_base = static_cast<float>(p.scale / (n ? n : 1u));
+    __syncthreads();
+    const float base = shared_base;
     PolicySums s;
     for (unsigned t0 = threadIdx.x * kPolicyEach; t0 < p.tokens; t0 += chunk) {
         float nll[8], old_nll[8], ref_nll[8], adv[8];
@@ -456,7 +473,7 @@ static __global__ void __launch_bounds__(kPolicySmallThreads) ar_policy_small_ke
         if (p.old_nll) tokens8(p.old_nll, t0, p.tokens, p.vec, old_nll);
         if (p.ref_nll) tokens8(p.ref_nll, t0, p.tokens, p.vec, ref_nll);
         if (p.token_adv) tokens8(p.adv, t0, p.tokens, p.vec, adv);
-        policy_tokens(p, t0, p.tokens, mask_bits(p, t0, p.tokens), nll, old_nll, ref_nll, adv, n, bounds, from, to, s);
+        policy_tokens(p, t0, p.tokens, mask_bits(p, t0, p.tokens), nll, old_nll, ref_nll, adv, base, bounds, from, to, s);
     }
     double sum = policy_block_sums(s, room);
     if (threadIdx.x < 32) {

@@ -11,18 +11,21 @@ using tps::launched;
 
 namespace {
 
+constexpr size_t kMostBlocks = 608;  // four on each of 152 SMs
+
 // A call's workspace: the counts, those of each sequence or counting block, and the blocks' sums.
 struct Plan {
-    size_t blocks, count_blocks, counts, part, bytes;
+    size_t chunks, blocks, count_blocks, counts, part, bytes;
     bool small;
 };
 
 Plan plan_of(const ar_policy *p) {
     Plan w;
     w.small = p->tokens <= tps::kPolicySmall;
-    w.blocks = w.small ? 0 : (p->tokens + tps::kPolicyChunk - 1) / tps::kPolicyChunk;
+    w.chunks = w.small ? 0 : (p->tokens + tps::kPolicyChunk - 1) / tps::kPolicyChunk;
+    w.blocks = w.chunks < kMostBlocks ? w.chunks : kMostBlocks;
     // four chunks to a thread of the counting launch, and no more blocks than every later block sums quickly
-    w.count_blocks = (w.blocks + 3) / 4 < 1024 ? (w.blocks + 3) / 4 : 1024;
+    w.count_blocks = (w.chunks + 3) / 4 < kMostBlocks ? (w.chunks + 3) / 4 : kMostBlocks;
     w.counts = sizeof(tps::PolicyCounts);
     const size_t counts = p->mean == AR_POLICY_SEQUENCES ? p->sequences : p->mean == AR_POLICY_TOKENS ? w.count_blocks : 0;
     w.part = (w.counts + counts * sizeof(unsigned) + 15) / 16 * 16;
@@ -35,6 +38,16 @@ int check_sizes(const ar_policy *p) {
     if (p->mean != AR_POLICY_SUM && p->mean != AR_POLICY_TOKENS && p->mean != AR_POLICY_SEQUENCES) return AR_ERR_INVALID_ARG;
     if (p->tokens > 0xFFFFFFFFull || p->sequences >= (1ull << 31)) return AR_ERR_TOO_LARGE;
     return AR_OK;
+}
+
+tps::PolicyLimit limit_of(double v) {
+    tps::PolicyLimit l{static_cast<float>(v), 0.0f, 0.0f};
+    if (std::isfinite(v)) {
+        l.rest = static_cast<float>(v - l.x);
+        const double left = v - l.x - l.rest;
+        l.sign = left > 0.0 ? 1.0f : left < 0.0 ? -1.0f : 0.0f;
+    }
+    return l;
 }
 
 template <typename T>
@@ -109,10 +122,11 @@ int ar_policy_loss(const ar_policy *a, float *totals, float *dnll, void *ws, siz
                      reinterpret_cast<uintptr_t>(dnll);
     if (a->token_advantages) bits |= reinterpret_cast<uintptr_t>(a->advantages);
     p.vec = bits % 16 == 0;
-    p.log_high = std::log1p(a->clip_high);
-    p.log_low = std::log1p(-a->clip_low);
+    p.high = limit_of(std::log1p(a->clip_high));
+    p.low = limit_of(std::log1p(-a->clip_low));
     p.limit_high = static_cast<float>(1.0 + a->clip_high);
     p.limit_low = static_cast<float>(1.0 - a->clip_low);
+    p.beta = static_cast<float>(a->kl_weight);
     p.kl_weight = a->kl_weight;
     p.scale = a->scale;
     p.totals = totals;
@@ -139,7 +153,7 @@ int ar_policy_loss(const ar_policy *a, float *totals, float *dnll, void *ws, siz
         st = go(tps::ar_policy_count_tokens_kernel, w.count_blocks);
     } else {
         st = go(tps::ar_policy_zero_kernel, S / tps::kPolicyThreads + 1);
-        if (st == AR_OK) st = go(tps::ar_policy_count_kernel, w.blocks);
+        if (st == AR_OK) st = go(tps::ar_policy_count_kernel, w.chunks);
     }
     return st == AR_OK ? go(tps::ar_policy_kernel<true>, w.blocks) : st;
 }
