@@ -69,43 +69,57 @@ __device__ __forceinline__ unsigned offsets_upto_warp(const PolicyParams &p, lon
     }
     return lo;
 }
-// The same for one thread between lo and hi, which bound it.
-__device__ __forceinline__ unsigned offsets_upto(const PolicyParams &p, long long t, unsigned lo, unsigned hi) {
-    while (lo < hi) {
-        const unsigned mid = lo + (hi - lo) / 2;
-        if (p.offsets[mid] <= t)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo;
-}
+// The offsets that lie inside a chunk of tokens: `lo` of all are <= its first token, `hi` <= its last.  Few of them
+// are held in shared memory.
+constexpr unsigned kHeldOffsets = 512;
+struct ChunkOffsets {
+    unsigned lo, hi;
+    long long held[kHeldOffsets];
+};
 
 // Walks a thread's tokens through the sequences.  `upto` is the number of offsets <= the token, so the token's
 // sequence is upto - 1, none for 0 and sequences + 1.
 struct SequenceWalk {
-    unsigned upto, most;
-    long long next;  // the offset that ends this sequence
-    __device__ __forceinline__ void seek(const PolicyParams &p, long long t, unsigned lo, unsigned hi) {
-        most = hi;
-        upto = offsets_upto(p, t, lo, hi);
-        next = upto < hi ? p.offsets[upto] : LLONG_MAX;  // the chunk ends before the offset behind `hi`
+    unsigned upto, lo, hi;
+    const long long *at;  // offsets lo, lo + 1, ...
+    long long next;       // the offset that ends this sequence
+    __device__ __forceinline__ SequenceWalk(const PolicyParams &p, const ChunkOffsets &c) {
+        upto = lo = c.lo;
+        hi = c.hi;
+        at = hi > lo && hi - lo <= kHeldOffsets ? c.held : p.offsets + lo;
     }
-    __device__ __forceinline__ void advance(const PolicyParams &p, long long t) {
-        if (t >= next) seek(p, t, upto, most);
+    // The first token at or behind the last one sought.
+    __device__ __forceinline__ void seek(long long t) {
+        unsigned a = upto, b = hi;
+        while (a < b) {
+            const unsigned mid = a + (b - a) / 2;
+            if (at[mid - lo] <= t)
+                a = mid + 1;
+            else
+                b = mid;
+        }
+        upto = a;
+        next = upto < hi ? at[upto - lo] : LLONG_MAX;  // the chunk ends before the offset behind `hi`
+    }
+    __device__ __forceinline__ void advance(long long t) {
+        if (t >= next) seek(t);
     }
     __device__ __forceinline__ bool inside(const PolicyParams &p) const { return upto > 0 && upto <= p.sequences; }
 };
 
-// The bounds of a chunk's offsets: those of its first and its last token.  `room`: 2 words.
-__device__ __forceinline__ void chunk_bounds(const PolicyParams &p, unsigned long long first, unsigned long long last,
-                                             unsigned *room) {
+// The whole block finds the offsets inside its chunk.
+__device__ __forceinline__ void chunk_offsets(const PolicyParams &p, unsigned long long first, unsigned long long last,
+                                              ChunkOffsets &c) {
     const int warp = threadIdx.x / 32;
     if (warp < 2) {
         const unsigned n = p.sequences ? offsets_upto_warp(p, static_cast<long long>(warp ? last : first)) : 0;
-        if (threadIdx.x % 32 == 0) room[warp] = n;
+        if (threadIdx.x % 32 == 0) (warp ? c.hi : c.lo) = n;
     }
     __syncthreads();
+    if (c.hi > c.lo && c.hi - c.lo <= kHeldOffsets) {
+        for (unsigned k = threadIdx.x; k < c.hi - c.lo; k += blockDim.x) c.held[k] = p.offsets[c.lo + k];
+        __syncthreads();
+    }
 }
 
 static __global__ void __launch_bounds__(256) ar_policy_zero_kernel(const __grid_constant__ PolicyParams p) {
@@ -154,17 +168,26 @@ __device__ __forceinline__ unsigned between_bits(unsigned long long t0, long lon
     return bits;
 }
 
-// Adds up the counted tokens of each sequence among eight tokens.
-__device__ __forceinline__ void count_sequences(const PolicyParams &p, unsigned long long t0, unsigned bits, const unsigned *bounds) {
-    SequenceWalk w;
-    w.seek(p, static_cast<long long>(t0), bounds[0], bounds[1]);
-    if (w.next >= static_cast<long long>(t0) + 8) {
-        if (bits && w.inside(p)) atomicAdd(p.per_sequence + w.upto - 1, __popc(bits));
+// Adds up the counted tokens of each sequence; the whole block calls, each thread with eight tokens.
+__device__ __forceinline__ void count_sequences(const PolicyParams &p, unsigned long long t0, unsigned bits, const ChunkOffsets &c,
+                                                unsigned *room) {
+    if (c.lo == c.hi) {  // one sequence
+        const unsigned n = block_count(__popc(bits), room);
+        if (threadIdx.x == 0 && n && c.lo > 0 && c.lo <= p.sequences) atomicAdd(p.per_sequence + c.lo - 1, n);
+        return;
+    }
+    SequenceWalk w(p, c);
+    w.seek(static_cast<long long>(t0));
+    const unsigned lane0 = __shfl_sync(~0u, w.upto, 0);  // every lane takes part, whatever it finds below
+    const bool same = w.next >= static_cast<long long>(t0) + 8 && w.upto == lane0;
+    if (__all_sync(~0u, same)) {  // one sequence for the warp
+        const unsigned n = __reduce_add_sync(~0u, __popc(bits));
+        if (threadIdx.x % 32 == 0 && n && w.inside(p)) atomicAdd(p.per_sequence + w.upto - 1, n);
         return;
     }
     unsigned here = 0, at = w.upto;
     for (int k = 0; k < 8; ++k) {
-        w.advance(p, static_cast<long long>(t0 + k));
+        w.advance(static_cast<long long>(t0 + k));
         if (w.upto != at) {
             if (here) atomicAdd(p.per_sequence + at - 1, here);
             here = 0;
@@ -200,7 +223,8 @@ static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_count_tokens_
 
 // Counted tokens of each sequence; the last block counts the sequences that have some.
 static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_count_kernel(const __grid_constant__ PolicyParams p) {
-    __shared__ unsigned bounds[2], room[kPolicyThreads / 32];
+    __shared__ ChunkOffsets inner;
+    __shared__ unsigned room[kPolicyThreads / 32];
     __shared__ bool last_block;
     pdl_launch_dependents();
     pdl_wait();
@@ -208,8 +232,8 @@ static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_count_kernel(
     const unsigned long long end = first + kPolicyChunk < p.tokens ? first + kPolicyChunk : p.tokens;
     const unsigned long long t0 = first + threadIdx.x * kPolicyEach;
     const unsigned bits = mask_bits(p, t0, end);
-    chunk_bounds(p, first, end - 1, bounds);
-    if (p.sequences && bits) count_sequences(p, t0, bits, bounds);
+    chunk_offsets(p, first, end - 1, inner);
+    if (p.sequences) count_sequences(p, t0, bits, inner, room);
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) last_block = atomicAdd(&p.counts->ticket, 1u) == gridDim.x - 1;
@@ -223,31 +247,29 @@ static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_count_kernel(
 // exp(d) - d - 1 and its derivative exp(d) - 1.  Near zero the first is d^2 / 2 + d^3 / 6 + ..., of which the
 // difference would leave nothing: nine terms are off by less than 2^-27 of it up to |d| = 1/2.
 __device__ __forceinline__ void kl_terms(float d, float &kl, float &slope) {
-    if (fabsf(d) < 0.5f) {
-        float s = 1.0f / 3628800.0f;
-        s = fmaf(s, d, 1.0f / 362880.0f);
-        s = fmaf(s, d, 1.0f / 40320.0f);
-        s = fmaf(s, d, 1.0f / 5040.0f);
-        s = fmaf(s, d, 1.0f / 720.0f);
-        s = fmaf(s, d, 1.0f / 120.0f);
-        s = fmaf(s, d, 1.0f / 24.0f);
-        s = fmaf(s, d, 1.0f / 6.0f);
-        s = fmaf(s, d, 0.5f);
-        kl = s * d * d;
-        slope = kl + d;
-    } else {
-        slope = expf(d) - 1.0f;
-        kl = slope - d;
-    }
+    float s = 1.0f / 3628800.0f;
+    s = fmaf(s, d, 1.0f / 362880.0f);
+    s = fmaf(s, d, 1.0f / 40320.0f);
+    s = fmaf(s, d, 1.0f / 5040.0f);
+    s = fmaf(s, d, 1.0f / 720.0f);
+    s = fmaf(s, d, 1.0f / 120.0f);
+    s = fmaf(s, d, 1.0f / 24.0f);
+    s = fmaf(s, d, 1.0f / 6.0f);
+    s = fmaf(s, d, 0.5f);
+    const float near = s * d * d, far = expf(d) - 1.0f;
+    const bool small = fabsf(d) < 0.5f;
+    kl = small ? near : far - d;
+    slope = small ? near + d : far;
 }
 
-// Where x = a - b, rounded, lies next to a 64-bit limit: > 0 above, < 0 below.  x decides unless it is the rounded
-// limit itself, because rounding keeps the order; then what rounding took from a - b, which is a float, decides.
-__device__ __forceinline__ float side(float x, float a, float b, const PolicyLimit &l) {
-    if (x != l.x) return x > l.x ? 1.0f : x < l.x ? -1.0f : 0.0f;
+// Whether a - b, which rounds to x, lies above (sign 1) or below (sign -1) a 64-bit limit.  x decides unless it is the
+// rounded limit itself, because rounding keeps the order; then what rounding took from a - b, which is a float, decides.
+__device__ __forceinline__ bool beyond(float x, float a, float b, const PolicyLimit &l, float sign) {
+    if (x != l.x) return sign > 0.0f ? x > l.x : x < l.x;
     const float z = __fsub_rn(x, a);
     const float e = __fsub_rn(__fsub_rn(a, __fsub_rn(x, z)), __fadd_rn(b, z));
-    return e > l.rest ? 1.0f : e < l.rest ? -1.0f : -l.sign;
+    const float at = e > l.rest ? 1.0f : e < l.rest ? -1.0f : -l.sign;
+    return at * sign > 0.0f;
 }
 
 struct PolicySums {
@@ -259,8 +281,8 @@ struct PolicySums {
 __device__ __forceinline__ float policy_token(const PolicyParams &p, float nll, float old_nll, float ref_nll, float adv,
                                               float weight, float beta, PolicySums &s) {
     const float x = p.old_nll ? old_nll - nll : 0.0f;
-    const bool clipped = p.old_nll && ((adv > 0.0f && side(x, old_nll, nll, p.high) > 0.0f) ||
-                                       (adv < 0.0f && side(x, old_nll, nll, p.low) < 0.0f));
+    const PolicyLimit limit = adv > 0.0f ? p.high : p.low;
+    const bool clipped = p.old_nll && adv != 0.0f && beyond(x, old_nll, nll, limit, adv);
     const float slope = clipped || adv == 0.0f ? 0.0f : expf(x) * adv;
     const float gain = clipped ? (adv > 0.0f ? p.limit_high : p.limit_low) * adv : slope;
     float kl = 0.0f, dkl = 0.0f;
@@ -284,10 +306,10 @@ __device__ __forceinline__ void tokens8(const float *a, unsigned long long t, un
 }
 
 // The eight tokens from t0 on: their sums, and their gradients.  `base`: scale over what the mean divides by; `bits`: which tokens
-// the mask leaves; `bounds`: the chunk's, where sequences matter.
+// the mask leaves; `c`: the chunk's offsets, where sequences matter.
 __device__ __forceinline__ void policy_tokens(const PolicyParams &p, unsigned long long t0, unsigned long long end, unsigned bits,
                                               const float (&nll)[8], const float (&old_nll)[8], const float (&ref_nll)[8],
-                                              const float (&adv)[8], float base, const unsigned *bounds, long long first, long long last,
+                                              const float (&adv)[8], float base, const ChunkOffsets &c, long long first, long long last,
                                               PolicySums &s) {
     const float beta = p.beta;
     float out[8];
@@ -299,15 +321,15 @@ __device__ __forceinline__ void policy_tokens(const PolicyParams &p, unsigned lo
             if (bits >> k & 1u) out[k] = policy_token(p, nll[k], old_nll[k], ref_nll[k], adv[k], 1.0f, beta, s) * base;
         }
     } else {
-        SequenceWalk w;
+        SequenceWalk w(p, c);
         unsigned at = ~0u;
         float a = 0.0f, weight = 1.0f;
-        if (p.sequences) w.seek(p, static_cast<long long>(t0), bounds[0], bounds[1]);
+        w.seek(static_cast<long long>(t0));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             out[k] = 0.0f;
             if (!(bits >> k & 1u) || !p.sequences) continue;
-            w.advance(p, static_cast<long long>(t0 + k));
+            w.advance(static_cast<long long>(t0 + k));
             if (!w.inside(p)) continue;
             if (w.upto != at) {
                 at = w.upto;
@@ -375,7 +397,8 @@ __device__ __forceinline__ void policy_join(const PolicyParams &p, unsigned some
 // The chunks of the tokens in turn.  Behind a counting launch (JOIN) the last block joins the blocks' sums.
 template <bool JOIN>
 __global__ void __launch_bounds__(kPolicyThreads, 4) ar_policy_kernel(const __grid_constant__ PolicyParams p) {
-    __shared__ unsigned bounds[2], counts[kPolicyThreads / 32];
+    __shared__ ChunkOffsets inner;
+    __shared__ unsigned counts[kPolicyThreads / 32];
     __shared__ float room[4 * kPolicyThreads / 32], shared_base;
     __shared__ double joined[kPolicyThreads];
     __shared__ bool last_block;
@@ -409,10 +432,10 @@ __global__ void __launch_bounds__(kPolicyThreads, 4) ar_policy_kernel(const __gr
             if (p.token_adv) tokens8(p.adv, t0, end, p.vec, adv);
         }
         if (walk) {
-            __syncthreads();  // the bounds of the chunk before have been read
-            chunk_bounds(p, first, end - 1, bounds);
+            __syncthreads();  // the offsets of the chunk before have been read
+            chunk_offsets(p, first, end - 1, inner);
         }
-        if (t0 < end) policy_tokens(p, t0, end, bits, nll, old_nll, ref_nll, adv, base, bounds, from, to, s);
+        if (t0 < end) policy_tokens(p, t0, end, bits, nll, old_nll, ref_nll, adv, base, inner, from, to, s);
     }
     const double sum = policy_block_sums(s, room);
     if (threadIdx.x < 4) __stcg(p.part + blockIdx.x * 4ull + threadIdx.x, sum);
@@ -436,7 +459,8 @@ static __global__ void __launch_bounds__(kPolicyThreads) ar_policy_join_kernel(c
 
 // Few tokens: everything in one block.
 static __global__ void __launch_bounds__(kPolicySmallThreads) ar_policy_small_kernel(const __grid_constant__ PolicyParams p) {
-    __shared__ unsigned bounds[2], counts[32];
+    __shared__ ChunkOffsets inner;
+    __shared__ unsigned counts[32];
     __shared__ float room[4 * 32], shared_base;
     pdl_launch_dependents();
     pdl_wait();
@@ -444,7 +468,7 @@ static __global__ void __launch_bounds__(kPolicySmallThreads) ar_policy_small_ke
     const bool walk = p.sequences && p.tokens && !(p.token_adv && p.mean != 2);
     long long from = 0, to = 0;
     if (p.sequences) from = p.offsets[0], to = p.offsets[p.sequences];
-    if (walk) chunk_bounds(p, 0, p.tokens - 1, bounds);
+    if (walk) chunk_offsets(p, 0, p.tokens - 1, inner);
     unsigned n = 1, some = 1;
     if (p.mean == 1) {
         n = 0;
@@ -455,10 +479,11 @@ static __global__ void __launch_bounds__(kPolicySmallThreads) ar_policy_small_ke
         for (unsigned q = threadIdx.x; q < p.sequences; q += blockDim.x) p.per_sequence[q] = 0u;
         __threadfence();
         __syncthreads();
-        for (unsigned t0 = threadIdx.x * kPolicyEach; t0 < p.tokens; t0 += chunk) {
-            const unsigned bits = mask_bits(p, t0, p.tokens);
-            if (p.sequences && bits) count_sequences(p, t0, bits, bounds);
-        }
+        if (p.sequences)
+            for (unsigned first = 0; first < p.tokens; first += chunk) {
+                const unsigned t0 = first + threadIdx.x * kPolicyEach;
+                count_sequences(p, t0, mask_bits(p, t0, p.tokens), inner, counts);
+            }
         __threadfence();
         __syncthreads();
         n = some = counted_sequences(p, counts);
@@ -473,7 +498,7 @@ static __global__ void __launch_bounds__(kPolicySmallThreads) ar_policy_small_ke
         if (p.old_nll) tokens8(p.old_nll, t0, p.tokens, p.vec, old_nll);
         if (p.ref_nll) tokens8(p.ref_nll, t0, p.tokens, p.vec, ref_nll);
         if (p.token_adv) tokens8(p.adv, t0, p.tokens, p.vec, adv);
-        policy_tokens(p, t0, p.tokens, mask_bits(p, t0, p.tokens), nll, old_nll, ref_nll, adv, base, bounds, from, to, s);
+        policy_tokens(p, t0, p.tokens, mask_bits(p, t0, p.tokens), nll, old_nll, ref_nll, adv, base, inner, from, to, s);
     }
     double sum = policy_block_sums(s, room);
     if (threadIdx.x < 32) {
