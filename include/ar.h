@@ -193,8 +193,8 @@ typedef enum {
     AR_Q_HOST_CHUNK_BYTES = 9,  /* ar_reduce_host pipeline chunk, bytes per buffer (default 4 MiB;
                                    at most 64 chunks per call) */
     AR_Q_DEVICE_STATUS = 10,    /* device-side status word (bit 0: a bounded wait of the TMA
-                                   variant ran out; bit 1: one of ar_vocab_loss or
-                                   ar_vocab_loss_grad, after two seconds - the call's results are
+                                   variant ran out; bit 1: one of ar_vocab_loss,
+                                   ar_vocab_loss_grad or ar_reduce_norm_grad, after two seconds - the call's results are
                                    then unspecified and the context stays usable); reading it
                                    synchronises with the device; set it to 0 to clear it */
     AR_Q_TMA_DROP_TILE = 11     /* test hook for failure detection, -1 (default) = off: TMA

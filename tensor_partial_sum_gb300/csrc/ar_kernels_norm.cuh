@@ -126,6 +126,17 @@ __device__ __forceinline__ float rounded(float x) {
     return wire1<kF32, T>(x);
 }
 
+// A sum of many terms that may cancel, with what its additions lose.
+struct LongSum {
+    float sum = 0.0f, lost = 0.0f;
+    __device__ __forceinline__ void add(float v) {
+        const float t = __fadd_rn(sum, v);
+        lost += fabsf(sum) >= fabsf(v) ? __fadd_rn(__fsub_rn(sum, t), v) : __fadd_rn(__fsub_rn(v, t), sum);
+        sum = t;
+    }
+    __device__ __forceinline__ float value() const { return lost == lost ? sum + lost : sum; }
+};
+
 // The mean m + off; an infinite m has no difference to anything.
 __device__ __forceinline__ float norm_mean(float m, float off) { return off == off ? m + off : m; }
 // 1 / sqrt(variance + eps) from the mean square about a value that is `off` away from the mean.  Not with fmaxf,
@@ -136,8 +147,9 @@ __device__ __forceinline__ float norm_rstd(float square, float off, float eps) {
 }
 
 // A row of any length to a block, element by element: the sum is formed three times (for the mean, the squares,
-// the results).  Squares are taken about the rounded mean m, and sum (h - m) corrects both what rounding the mean left
-// and the squares: a row far from zero loses nothing to its offset.
+// the results).  Squares are taken about m, the mean rounded to T: for 16-bit rows h - m is then exact (against the
+// unrounded mean, all elements of one exponent are rounded alike, which left the mean 2e-6 off). sum (h - m) corrects
+// both the mean and the squares: a row far from zero loses nothing to its offset.
 template <int Td>
 __global__ void __launch_bounds__(512) ar_norm_any_kernel(const __grid_constant__ NormParams p) {
     __shared__ float room[64];
@@ -147,16 +159,20 @@ __global__ void __launch_bounds__(512) ar_norm_any_kernel(const __grid_constant_
     for (size_t row = blockIdx.x; row < x.ne1; row += gridDim.x) {
         float m = 0.0f, a = 0.0f, b = 0.0f;
         if (!p.rms) {
-            for (size_t i = threadIdx.x; i < x.ne0; i += blockDim.x) a += rounded<Td>(norm_fold<Td>(p, row, i));
+            LongSum s;
+            for (size_t i = threadIdx.x; i < x.ne0; i += blockDim.x) s.add(rounded<Td>(norm_fold<Td>(p, row, i)));
+            a = s.value();
             block_sum2(a, b, room);
-            m = a * p.inv_n;
+            m = rounded<Td>(a * p.inv_n);
         }
-        a = b = 0.0f;
+        LongSum s;
+        b = 0.0f;
         for (size_t i = threadIdx.x; i < x.ne0; i += blockDim.x) {
             const float d = rounded<Td>(norm_fold<Td>(p, row, i)) - m;
-            a += d;
+            s.add(d);
             b += d * d;
         }
+        a = s.value();
         block_sum2(a, b, room);
         const float off = p.rms ? 0.0f : a * p.inv_n;
         const float rstd = norm_rstd(b * p.inv_n, off, p.eps);
@@ -242,10 +258,6 @@ __device__ __forceinline__ void row_sum(float &a, float &b, int bx, int cluster,
             lanes();
         }
     }
-}
-
-__device__ __forceinline__ float add8(const float (&v)[8]) {
-    return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 }
 
 // ---- rows through shared memory -----------------------------------------------------
@@ -594,7 +606,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<Td, ALIGNED, WARP>) 
         };
         if (!p.rms) {
             row_sum<WARP, false>(a, b, bx, cluster, rank, room[0]);
-            m = a * p.inv_n;
+            m = rounded<Td>(a * p.inv_n);
         }
         a = b = 0.0f;
         col = col0;
