@@ -121,7 +121,7 @@ RowShape row_shape(size_t ne0, size_t ne1, size_t cols, int vecs, int most_u) {
         s.threads = static_cast<unsigned>(((share() + s.U - 1) / s.U + 31) / 32 * 32);
         s.bx = static_cast<int>(s.threads);
     }
-    // rows ahead before blocks: two rows at least, four at most
+    // two rows in the ring at least, if blocks have to go for it; four at most
     const size_t row = static_cast<size_t>(s.threads) * s.U * 16 * vecs;
     s.resident = static_cast<int>(tps::kRowThreads / s.threads);
     while (s.resident > 1 && row * 2 > ring_bytes(s.resident)) --s.resident;
@@ -579,8 +579,10 @@ int ar_reduce_norm_grad(const void *dy, const void *h, const ar_checkpoint *ck, 
         p.rows_aligned = reinterpret_cast<uintptr_t>(norm->weight) % 16 == 0;
         p.apart = p.dy.apart && (!h || p.h.apart) && (!L->residual || p.dsum.apart);
         if (s.U && al.narrow) {
-            const size_t grid = row_grid(s, L->ne1);
-            blocks = grid / s.cluster;
+            // no more blocks than the workspace has rows of partial sums for
+            const size_t most = ring_blocks(L->ne0, L->ne1), groups = row_grid(s, L->ne1) / s.cluster;
+            blocks = groups < most ? groups : most;
+            const size_t grid = blocks * s.cluster;
             place(static_cast<float *>(ws));
             p.bx = s.bx;
             p.cluster = s.cluster;
