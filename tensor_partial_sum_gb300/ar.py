@@ -500,10 +500,12 @@ def _layout_buffers(srcs, dsts, layout, dcode, call):
     dst = _layout_pointers(dsts, layout.dst_row_bytes or None, row, ne1, "destination", call)
     res = layout._residual_obj if hasattr(layout, "_residual_obj") else None
     if res is not None and row * ne1:
-        reach = _reach(res)
         n = row if layout.residual_row_bytes == 0 else (ne1 - 1) * layout.residual_row_bytes + row
-        if reach is not None and reach < n:
-            raise ValueError(f"{call}: the residual reaches {reach} bytes, its rows span {n}")
+        # a contiguous tensor of enough bytes needs no look at its storage
+        if not (getattr(res, "is_cuda", False) and res.nbytes >= n and res.is_contiguous()):
+            reach = _reach(res)
+            if reach is not None and reach < n:
+                raise ValueError(f"{call}: the residual reaches {reach} bytes, its rows span {n}")
     return src, dst
 
 
