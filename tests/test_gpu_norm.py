@@ -147,8 +147,9 @@ def test_very_long_rows(ne0, dst):
 
 @pytest.mark.parametrize("dst,wire", PAIRS)
 @pytest.mark.parametrize("R", [1, 2, 5])
-def test_type_pairs(dst, wire, R):
-    forward(R, 1029, 5, dst, wire, n_dsts=2, bias=True, residual="full")
+@pytest.mark.parametrize("ne0", [1029, 96, 2112])
+def test_type_pairs(dst, wire, R, ne0):
+    forward(R, ne0, 5, dst, wire, n_dsts=2, bias=True, residual="full")
 
 
 @pytest.mark.parametrize("dst", TYPES)
@@ -172,8 +173,21 @@ def test_many_ranks_and_destinations(dst, R):
 
 
 @pytest.mark.parametrize("inactive", [(0,), (1, 2)])
-def test_inactive_ranks(inactive):
-    forward(3, 260, 6, "bf16", "bf16", inactive=inactive, bias=True, residual="row")
+@pytest.mark.parametrize("ne0", [260, 2048])
+def test_inactive_ranks(inactive, ne0):
+    forward(3, ne0, 6, "bf16", "bf16", inactive=inactive, bias=True, residual="row")
+
+
+@pytest.mark.parametrize("ne0", [96, 2048])
+def test_no_active_rank_normalises_the_residual(ne0):
+    """The norm of a tensor that is there already, and of nothing at all."""
+    tps.ar_init(2, 5 * ne0)
+    x, y = normal((5, ne0), 4), torch.empty((5, ne0), device="cuda")
+    for res in (x, None):
+        lay = tps.make_layout(ne0, 5, residual=res, inactive=(0, 1))
+        tps.ar_reduce_norm([None, None], [y], lay, tps.make_norm(EPS), "f32", "f32")
+        want, _, _, slack = norm_forward((x if res is x else torch.zeros_like(x)).double(), None, None, EPS, False)
+        close(y, want, slack, torch.float32, "y")
 
 
 @pytest.mark.parametrize("pads,lead", [((0,), 0), ((3,), 1)])

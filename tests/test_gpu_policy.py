@@ -66,7 +66,7 @@ def run(nll, offsets, adv, old=None, ref=None, mask=None, low=0.2, high=0.28, be
 
 
 @pytest.mark.parametrize("T,S", [(1, 1), (2, 1), (7, 3), (8, 8), (31, 1), (300, 5), (2047, 9), (2048, 1), (2049, 40), (5000, 5000),
-                                 (8191, 3), (8193, 700), (40_000, 17), (300_000, 11), (70_001, 9000)])
+                                 (8191, 3), (8193, 700), (40_000, 17), (300_000, 11), (70_001, 9000), (60_001, 50_000)])
 @pytest.mark.parametrize("mean", ["sum", "tokens", "sequences"])
 @pytest.mark.parametrize("token", [False, True])
 def test_sizes(T, S, mean, token):
