@@ -286,7 +286,7 @@ __device__ __forceinline__ float policy_token(const PolicyParams &p, float nll, 
                                               float weight, float beta, PolicySums &s) {
     const float x = p.old_nll ? old_nll - nll : 0.0f;
     const PolicyLimit limit = adv > 0.0f ? p.high : p.low;
-    const bool clipped = p.old_nll && adv != 0.0f && beyond(x, old_nll, nll, limit, adv);
+    const bool clipped = p.old_nll && (adv > 0.0f || adv < 0.0f) && beyond(x, old_nll, nll, limit, adv);
     const float slope = clipped || adv == 0.0f ? 0.0f : expf(x) * adv;
     const float gain = clipped ? (adv > 0.0f ? p.limit_high : p.limit_low) * adv : slope;
     float kl = 0.0f, dkl = 0.0f;

@@ -177,6 +177,19 @@ def test_overflow_stays_where_it_is():
     assert g[7] == -math.inf and totals[0] == math.inf and torch.isfinite(torch.cat([g[:7], g[8:]])).all()
 
 
+@pytest.mark.parametrize("T", [120, 30_000])
+def test_numbers_that_are_none_stay_with_their_tokens(T):
+    """A NaN in a counted token makes its gradient NaN, wherever it stands, and the totals."""
+    tps.ar_init(1, T)
+    for which in range(4):
+        nll, offsets, adv, old, ref, _ = inputs(T, 3, 19, False, token=True)
+        (nll, adv, old, ref)[which][50] = np.nan
+        t = [torch.from_numpy(x).cuda() for x in (nll, offsets, adv, old, ref)]
+        totals, g = torch.empty(4, device="cuda"), torch.empty(T, device="cuda")
+        tps.ar_policy_loss(*t[:3], totals, g, old_nll=t[3], ref_nll=t[4], kl_weight=0.1, token_advantages=True)
+        assert g[50].isnan() and totals[0].isnan() and int(g.isnan().sum()) == 1, which
+
+
 def test_offsets_out_of_order_touch_nothing_else():
     """Offsets that break the rule give unspecified numbers, but no token outside of the arrays is touched."""
     T = 5000
