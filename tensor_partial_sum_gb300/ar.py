@@ -808,6 +808,14 @@ def make_norm(eps=1e-5, weight=None, shift=None, bias=None, kind="layer") -> ArN
     return n
 
 
+def _row_address(x, n, dtype, name, call):
+    """Address of a device row that _typed_row accepts, None for None."""
+    if x is None or type(x) is int:
+        return x
+    _typed_row(x, n, dtype, name, call)
+    return x.data_ptr()
+
+
 def _norm_rows(norm, ne0, dcode, call):
     for x, name in zip(getattr(norm, "_rows", ()), ("the weight", "the shift", "the bias")):
         if x is not None:
@@ -825,12 +833,8 @@ def _norm_kept(layout, dcode, sums, sum_row_bytes, mean, rstd, checkpoint, call)
         k.sums = k._pointers
         if rows is not None:
             k.sum_row_bytes = rows
-    if mean is not None:
-        _typed_row(mean, ne1, AR_F32, "mean", call)
-        k.mean = _ptr(mean)
-    if rstd is not None:
-        _typed_row(rstd, ne1, AR_F32, "rstd", call)
-        k.rstd = _ptr(rstd)
+    k.mean = _row_address(mean, ne1, AR_F32, "mean", call)
+    k.rstd = _row_address(rstd, ne1, AR_F32, "rstd", call)
     if checkpoint is not None:
         k.checkpoint = ctypes.pointer(checkpoint)
     return k
@@ -883,16 +887,15 @@ def ar_reduce_norm_grad(dy, kept, dxs, layout: ArLayout, norm: ArNorm, mean, rst
     src, dst = _layout_buffers([dy] if saved else [dy, kept], dxs, layout, dcode, call)
     ne0, ne1 = layout.ne0, layout.ne1
     _norm_rows(norm, ne0, dcode, call)
-    n_sums = 0
-    for x, n, name in ((mean, ne1, "mean"), (rstd, ne1, "rstd"), (dweight, ne0, "dweight"), (dshift, ne0, "dshift"),
-                       (dbias, ne0, "dbias")):
-        if x is not None:
-            _typed_row(x, n, AR_F32, name, call)
-            n_sums += name[0] == "d"
+    mean, rstd = _row_address(mean, ne1, AR_F32, "mean", call), _row_address(rstd, ne1, AR_F32, "rstd", call)
+    dweight = _row_address(dweight, ne0, AR_F32, "dweight", call)
+    dshift = _row_address(dshift, ne0, AR_F32, "dshift", call)
+    dbias = _row_address(dbias, ne0, AR_F32, "dbias", call)
+    n_sums = (dweight is not None) + (dshift is not None) + (dbias is not None)
     ws, ws_bytes = _workspace(ar_reduce_norm_grad_workspace(layout, n_sums), workspace, stream, dy, call)
     _check(lib().ar_reduce_norm_grad(_ptr(dy), None if saved else _ptr(kept), ctypes.byref(kept) if saved else None,
-                                     _ptr(mean), _ptr(rstd), dst, len(dxs), ctypes.byref(layout), ctypes.byref(norm),
-                                     _ptr(dweight), _ptr(dshift), _ptr(dbias), _ptr(ws), ws_bytes, dcode,
+                                     mean, rstd, dst, len(dxs), ctypes.byref(layout), ctypes.byref(norm),
+                                     dweight, dshift, dbias, _ptr(ws), ws_bytes, dcode,
                                      _stream(stream)), call)
 
 
