@@ -588,7 +588,10 @@ typedef struct {
  *   dst[d][row][i] = T_dst((h - mean) * rstd * weight[i] + shift[i])
  * What is normalised is the sum as it is stored, so that the backward pass sees
  * the same h.  Statistics are float sums in a fixed order: the same call gives
- * the same bits.  Rows whose squares leave the float range do not keep the formula.
+ * the same bits.  A row's sum is carried with what its additions lose, so that the
+ * mean of float rows is off by its own last bit, next to zero too, and that of 16-bit
+ * rows by a few roundings of the mean magnitude at most.
+ * Rows whose squares leave the float range do not keep the formula.
  * Layout, in-place and overlap rules as for ar_reduce_ex, for the sums as for
  * the destinations: a sum may be exactly a source or exactly the residual
  * (h = h + allreduce(partials) in place); outputs may not overlap one another, nor the rows

@@ -102,6 +102,25 @@ __device__ __forceinline__ void block_sum2(float &a, float &b, float *room) {
     }
 }
 
+// One such sum over the block, the same in every thread.
+__device__ __forceinline__ void block_long_sum(LongSum &s, float *room) {
+    auto lanes = [&] {
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) {
+            const float a = __shfl_xor_sync(~0u, s.sum, k), b = __shfl_xor_sync(~0u, s.lost, k);
+            s.join(a, b);
+        }
+    };
+    lanes();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+    __syncthreads();
+    if (lane == 0) room[warp] = s.sum, room[32 + warp] = s.lost;
+    __syncthreads();
+    s.sum = lane < warps ? room[lane] : 0.0f;
+    s.lost = lane < warps ? room[32 + lane] : 0.0f;
+    lanes();
+}
+
 // The sum h of one element before its rounding to T_dst.
 template <int Td>
 __device__ __forceinline__ float norm_fold(const NormParams &p, size_t row, size_t i) {
@@ -137,17 +156,16 @@ __device__ __forceinline__ float rounded(float x) {
     return wire1<kF32, T>(x);
 }
 
-// A sum of many terms that may cancel, with what its additions lose.
-struct LongSum {
-    float sum = 0.0f, lost = 0.0f;
-    __device__ __forceinline__ void add(float v) {
-        const float t = __fadd_rn(sum, v);
-        lost += fabsf(sum) >= fabsf(v) ? __fadd_rn(__fsub_rn(sum, t), v) : __fadd_rn(__fsub_rn(v, t), sum);
-        sum = t;
-    }
-    __device__ __forceinline__ float value() const { return lost == lost ? sum + lost : sum; }
-};
-
+// The first mean m, rounded to T: 16-bit elements' differences to it are exact, and floats' differences from values far
+// from zero.  The row's mean is off by what m leaves of the sum; summing the differences again would not tell how much of it,
+// because m's last bits lie below those of floats, and elements of one exponent are all rounded the same way.
+template <int T>
+__device__ __forceinline__ float first_mean(const LongSum &s, float inv_n) {
+    return rounded<T>(s.sum * inv_n);
+}
+__device__ __forceinline__ float mean_rest(const LongSum &s, float m, float n, float inv_n) {
+    return (fmaf(-n, m, s.sum) + s.lost) * inv_n;
+}
 // The mean m + off; an infinite m has no difference to anything.
 __device__ __forceinline__ float norm_mean(float m, float off) { return off == off ? m + off : m; }
 // 1 / sqrt(variance + eps) from the mean square about a value that is `off` away from the mean.  Not with fmaxf,
@@ -158,9 +176,7 @@ __device__ __forceinline__ float norm_rstd(float square, float off, float eps) {
 }
 
 // A row of any length to a block, element by element: the sum is formed three times (for the mean, the squares,
-// the results).  Squares are taken about m, the mean rounded to T: for 16-bit rows h - m is then exact (against the
-// unrounded mean, all elements of one exponent are rounded alike, which left the mean 2e-6 off). sum (h - m) corrects
-// both the mean and the squares: a row far from zero loses nothing to its offset.
+// the results).  Squares are taken about m: a row far from zero loses nothing to its offset.
 template <int Td>
 __global__ void __launch_bounds__(512) ar_norm_any_kernel(const __grid_constant__ NormParams p) {
     __shared__ float room[64];
@@ -168,24 +184,20 @@ __global__ void __launch_bounds__(512) ar_norm_any_kernel(const __grid_constant_
     pdl_wait();
     const ArExParams &x = p.ex;
     for (size_t row = blockIdx.x; row < x.ne1; row += gridDim.x) {
-        float m = 0.0f, a = 0.0f, b = 0.0f;
+        float m = 0.0f, off = 0.0f, b = 0.0f, unused = 0.0f;
         if (!p.rms) {
             LongSum s;
             for (size_t i = threadIdx.x; i < x.ne0; i += blockDim.x) s.add(rounded<Td>(norm_fold<Td>(p, row, i)));
-            a = s.value();
-            block_sum2(a, b, room);
-            m = rounded<Td>(a * p.inv_n);
+            block_long_sum(s, room);
+            m = first_mean<Td>(s, p.inv_n);
+            // in 64 bits: not every length is a float
+            off = static_cast<float>((static_cast<double>(s.sum) + s.lost) / static_cast<double>(x.ne0) - m);
         }
-        LongSum s;
-        b = 0.0f;
         for (size_t i = threadIdx.x; i < x.ne0; i += blockDim.x) {
             const float d = rounded<Td>(norm_fold<Td>(p, row, i)) - m;
-            s.add(d);
             b += d * d;
         }
-        a = s.value();
-        block_sum2(a, b, room);
-        const float off = p.rms ? 0.0f : a * p.inv_n;
+        block_sum2(b, unused, room);
         const float rstd = norm_rstd(b * p.inv_n, off, p.eps);
         if (threadIdx.x == 0) {
             if (p.mean) p.mean[row] = norm_mean(m, off);
@@ -230,21 +242,32 @@ struct RowRoom {
 };
 
 // The sums of a (and b) over a row, the same in all its threads and in a fixed order: over the `bx` lanes of a warp
-// (WARP), over the block, or over the blocks of a cluster, which write into each other's shared memory.
-template <bool WARP, bool BOTH>
+// (WARP), over the block, or over the blocks of a cluster, which write into each other's shared memory.  LONG: a is a sum and
+// b what its additions lost.
+enum RowSum { kOne, kBoth, kLong };
+template <bool WARP, RowSum KIND>
 __device__ __forceinline__ void row_sum(float &a, float &b, int bx, int cluster, unsigned rank, RowRoom &room) {
-    if constexpr (WARP) {
-        for (int k = bx / 2; k > 0; k >>= 1) {
-            a += __shfl_xor_sync(~0u, a, k);
-            if constexpr (BOTH) b += __shfl_xor_sync(~0u, b, k);
+    auto join = [&](float c, float d) {
+        if constexpr (KIND == kLong) {
+            LongSum s;
+            s.sum = a, s.lost = b;
+            s.join(c, d);
+            a = s.sum, b = s.lost;
+        } else {
+            a += c;
+            if constexpr (KIND == kBoth) b += d;
         }
+    };
+    auto lane_at = [&](int k) {
+        const float c = __shfl_xor_sync(~0u, a, k), d = KIND == kOne ? 0.0f : __shfl_xor_sync(~0u, b, k);
+        join(c, d);
+    };
+    if constexpr (WARP) {
+        for (int k = bx / 2; k > 0; k >>= 1) lane_at(k);
     } else {
         auto lanes = [&] {
-#pragma unroll
-            for (int k = 16; k > 0; k >>= 1) {
-                a += __shfl_xor_sync(~0u, a, k);
-                if constexpr (BOTH) b += __shfl_xor_sync(~0u, b, k);
-            }
+#pragma unroll KIND == kLong ? 1 : 5
+            for (int k = 16; k > 0; k >>= 1) lane_at(k);
         };
         lanes();
         const int lane = threadIdx.x % 32, warps = static_cast<int>(blockDim.x) / 32, warp = threadIdx.x / 32;
@@ -254,18 +277,17 @@ __device__ __forceinline__ void row_sum(float &a, float &b, int bx, int cluster,
             a = room.v[0].x, b = room.v[0].y;
             for (int k = 1; k < warps; ++k) {
                 const float2 q = room.v[k];
-                a += q.x;
-                if constexpr (BOTH) b += q.y;
+                join(q.x, q.y);
             }
         } else {
             const int at = static_cast<int>(rank) * warps + warp;
             if (lane < cluster) {
                 store_remote(&room.v[at].x, static_cast<unsigned>(lane), a);
-                store_remote(&room.v[at].y, static_cast<unsigned>(lane), b);
+                if constexpr (KIND != kOne) store_remote(&room.v[at].y, static_cast<unsigned>(lane), b);
             }
             cluster_sync();
             a = b = 0.0f;
-            for (int k = lane; k < cluster * warps; k += 32) a += room.v[k].x, b += room.v[k].y;
+            for (int k = lane; k < cluster * warps; k += 32) join(room.v[k].x, room.v[k].y);
             lanes();
         }
     }
@@ -558,7 +580,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<Td, ALIGNED, WARP>) 
                                         col * Elem<Td>::bytes,
                                     w, col, ne0, have, prev, lane_next);
         };
-        float m = 0.0f, a = 0.0f, b = 0.0f;
+        LongSum total;
         unsigned col = col0;
         for (int u = 0; u < units; ++u, col += hop) {
             const int have = inside(col);
@@ -605,7 +627,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<Td, ALIGNED, WARP>) 
             for (int s = 0; s < p.n_sums; ++s) put(p.sum[s], p.sum_stride[s], col, have, h);
             widen_pairs<Td, W>(h, acc);
             if (p.kept.codes) unit_encode(p.kept, row, col, have, acc);
-            a += sum_pairs(acc);
+            if (!p.rms) add_columns<Td>(acc, total);
         }
         auto take = [&](int u, pair_t(&v)[N]) {
             uint32_t h[W];
@@ -616,11 +638,12 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<Td, ALIGNED, WARP>) 
             }
             widen_pairs<Td, W>(h, v);
         };
+        float m = 0.0f, off = 0.0f, square = 0.0f, unused = 0.0f;
         if (!p.rms) {
-            row_sum<WARP, false>(a, b, bx, cluster, rank, room[0]);
-            m = rounded<Td>(a * p.inv_n);
+            row_sum<WARP, kLong>(total.sum, total.lost, bx, cluster, rank, room[0]);
+            m = first_mean<Td>(total, p.inv_n);
+            off = mean_rest(total, m, static_cast<float>(ne0), p.inv_n);  // ne0 is below 2^24 here
         }
-        a = b = 0.0f;
         col = col0;
         const pair_t minus_m = both(-m);
         for (int u = 0; u < units; ++u, col += hop) {
@@ -630,15 +653,13 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<Td, ALIGNED, WARP>) 
             for (int k = 0; k < N; ++k) v[k] = add2(v[k], minus_m);
             const int have = inside(col);
             if (have < C) first_pairs(v, have);
-            a += sum_pairs(v);
 #pragma unroll
             for (int k = 0; k < N; ++k) q = fma2(v[k], v[k], q);
             const float2 f = halves(q);
-            b += f.x + f.y;
+            square += f.x + f.y;
         }
-        row_sum<WARP, true>(a, b, bx, cluster, rank, room[WARP ? 0 : 1]);
-        const float off = p.rms ? 0.0f : a * p.inv_n;
-        const float rstd = norm_rstd(b * p.inv_n, off, p.eps);
+        row_sum<WARP, kOne>(square, unused, bx, cluster, rank, room[WARP ? 0 : 1]);
+        const float rstd = norm_rstd(square * p.inv_n, off, p.eps);
         if (in_row && col0 == 0) {
             if (p.mean) p.mean[row] = norm_mean(m, off);
             if (p.rstd) p.rstd[row] = rstd;
@@ -787,7 +808,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
         }
         const float2 af = halves(a2), bf = halves(b2);
         float a = af.x + af.y, b = bf.x + bf.y;
-        row_sum<WARP, true>(a, b, t.bx, t.cluster, t.rank, room[WARP ? 0 : parity]);
+        row_sum<WARP, kBoth>(a, b, t.bx, t.cluster, t.rank, room[WARP ? 0 : parity]);
         // rstd (g - a / n - x b / n)
         const pair_t k0 = both(rstd), k1 = both(p.rms ? 0.0f : -(a * p.inv_n) * rstd), k2 = both(-(b * p.inv_n) * rstd);
 #pragma unroll
@@ -1046,7 +1067,7 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
             sums(false);
         else
             sums(true);
-        row_sum<false, true>(a, b, 0, t.cluster, t.rank, room[parity]);
+        row_sum<false, kBoth>(a, b, 0, t.cluster, t.rank, room[parity]);
         if (inside && !last)
             results(false);
         else

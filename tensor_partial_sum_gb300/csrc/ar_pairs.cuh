@@ -25,6 +25,11 @@ __device__ __forceinline__ pair_t add2(pair_t a, pair_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ pair_t sub2(pair_t a, pair_t b) {
+    pair_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) {
     pair_t d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -80,18 +85,65 @@ __device__ __forceinline__ void wire_pairs(int wire, pair_t (&v)[N]) {
     if (wire == kF16) through([](float &a, float &b) { wire2<T, kF16>(a, b); });
     if (wire == kBF16) through([](float &a, float &b) { wire2<T, kBF16>(a, b); });
 }
-// Their sum, in pairs of pairs.
-template <int N>
-__device__ __forceinline__ float sum_pairs(const pair_t (&v)[N]) {
-    pair_t s[N];
+// a + b, and in `lost` what its rounding left off of it (Knuth's two-sum: exact unless it overflows).
+__device__ __forceinline__ float exact_add(float a, float b, float &lost) {
+    const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
+    lost = __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z));
+    return s;
+}
+// Sums of many terms that may cancel, with what their additions lose.  No bits get lost but those below the losses'
+// own sum.
+struct LongSum {
+    float sum = 0.0f, lost = 0.0f;
+    __device__ __forceinline__ void add(float v) {
+        float e;
+        sum = exact_add(sum, v, e);
+        lost += e;
+    }
+    __device__ __forceinline__ void join(float other_sum, float other_lost) {  // the same bits whichever of the two is *this
+        float e;
+        sum = exact_add(sum, other_sum, e);
+        lost = (lost + other_lost) + e;
+    }
+};
+struct PairSum {
+    pair_t sum = 0, lost = 0;
+    __device__ __forceinline__ void add(pair_t v) {
+        const pair_t s = add2(sum, v), z = sub2(s, sum);
+        lost = add2(lost, add2(sub2(sum, sub2(s, z)), sub2(v, z)));
+        sum = s;
+    }
+    __device__ __forceinline__ LongSum joined() const {
+        const float2 s = halves(sum), l = halves(lost);
+        LongSum t;
+        t.sum = s.x, t.lost = l.x;
+        t.join(s.y, l.y);
+        return t;
+    }
+};
+// The sum of 2 N columns of type T added to `total`.  Floats keep what every addition loses.  16-bit elements are added
+// plainly first: with their 8 or 11 bits in a float's 24, few of those additions lose anything, and none more than 2^-24
+// of the columns' magnitudes at each of its levels (keeping it took 20% of the forward pass of bf16 [4096, 4096]).
+template <int T, int N>
+__device__ __forceinline__ void add_columns(const pair_t (&v)[N], LongSum &total) {
+    if constexpr (T == kF32) {
+        PairSum s;
+        s.sum = v[0];
 #pragma unroll
-    for (int k = 0; k < N; ++k) s[k] = v[k];
+        for (int k = 1; k < N; ++k) s.add(v[k]);
+        const LongSum j = s.joined();
+        total.join(j.sum, j.lost);
+    } else {
+        pair_t s[N];
 #pragma unroll
-    for (int n = N / 2; n > 0; n /= 2)
+        for (int k = 0; k < N; ++k) s[k] = v[k];
 #pragma unroll
-        for (int k = 0; k < n; ++k) s[k] = add2(s[k], s[k + n]);
-    const float2 f = halves(s[0]);
-    return f.x + f.y;
+        for (int n = N / 2; n > 0; n /= 2)
+#pragma unroll
+            for (int k = 0; k < n; ++k) s[k] = add2(s[k], s[k + n]);
+        const float2 f = halves(s[0]);
+        total.add(f.x + f.y);
+    }
 }
 // Set the columns from `n` on to +0.
 template <int N>
