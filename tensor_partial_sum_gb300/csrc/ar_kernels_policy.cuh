@@ -469,7 +469,7 @@ static __global__ void __launch_bounds__(kPolicySmallThreads) ar_policy_small_ke
     pdl_launch_dependents();
     pdl_wait();
     const unsigned chunk = blockDim.x * kPolicyEach;
-    const bool walk = p.sequences && p.tokens && !(p.token_adv && p.mean != 2);
+    const bool walk = p.tokens && !(p.token_adv && p.mean != 2);  // no sequences: the chunk holds no offsets
     long long from = 0, to = 0;
     if (p.sequences) from = p.offsets[0], to = p.offsets[p.sequences];
     if (walk) chunk_offsets(p, 0, p.tokens - 1, inner);
