@@ -1218,6 +1218,12 @@ __device__ __forceinline__ unsigned unit_row(size_t at, unsigned per_row) {
     return at >> 32 ? static_cast<unsigned>(at / per_row) : static_cast<unsigned>(at) / per_row;
 }
 
+// Where a column of a row starts; a flattened tensor's row may have 2^31 - 1 of them.
+template <int T>
+__device__ __forceinline__ size_t col_bytes(unsigned col) {
+    return static_cast<size_t>(col) * Elem<T>::bytes;
+}
+
 // A unit of columns to a thread, the rows' units one after another; `per_row` of them (a whole number of blocks).
 template <int Td, bool ALIGNED>
 __global__ void __launch_bounds__(256) ar_checkpoint_pack_kernel(const __grid_constant__ PackParams p) {
@@ -1231,7 +1237,7 @@ __global__ void __launch_bounds__(256) ar_checkpoint_pack_kernel(const __grid_co
     pair_t v[C / 2] = {};
     if (have) {
         Unit<Td, ALIGNED> r;
-        unit_load<Td, ALIGNED>(r, p.tensor.row(row) + col * Elem<Td>::bytes, p.tensor, p.tensor.apart && row > 0 && row + 1 < ne1, have);
+        unit_load<Td, ALIGNED>(r, p.tensor.row(row) + col_bytes<Td>(col), p.tensor, p.tensor.apart && row > 0 && row + 1 < ne1, have);
         unit_pairs<Td, ALIGNED>(r, v);
         if (have < C) first_pairs(v, have);
     }
@@ -1281,7 +1287,7 @@ __global__ void __launch_bounds__(256) ar_checkpoint_unpack_kernel(const __grid_
     }
     round_pairs<Td, W>(v, w);
     const unsigned prev = threadIdx.x % 32 > 0 && unit > 0, next = threadIdx.x % 32 < 31;
-    unit_store<Td, ALIGNED>(const_cast<char *>(p.tensor.row(row)) + col * Elem<Td>::bytes, w, col, ne0, have, prev, next);
+    unit_store<Td, ALIGNED>(const_cast<char *>(p.tensor.row(row)) + col_bytes<Td>(col), w, col, ne0, have, prev, next);
 }
 
 // The same for rows and strides past 32 bits: a warp to a block of 32 elements.
