@@ -201,7 +201,9 @@ typedef enum {
                                    launches never load tile n, so the CTA that owns it waits
                                    for data that never comes until its bound (100 ms) runs out,
                                    reports through AR_Q_DEVICE_STATUS and returns; the results of
-                                   such a launch are unspecified and the context stays usable */
+                                   such a launch are unspecified and the context stays usable.
+                                   ar_reduce_norm_grad, where it brings rows by bulk copies, never
+                                   loads row n, with the same bound on all of its waits */
 } ar_key;
 
 /* Read one context value into *value.  AR_ERR_NOT_INITIALIZED before init. */

@@ -473,7 +473,7 @@ std::mutex &context_mutex() { return g_mu; }
 bool current_context(CallContext *out) {
     if (!g_ctx.ready) return false;
     *out = CallContext{g_ctx.R,        g_ctx.max_elems,         g_ctx.device,    g_ctx.sm_count,
-                       g_ctx.pdl != 0, g_ctx.fault_inject != 0, g_ctx.dev_status};
+                       g_ctx.pdl != 0, g_ctx.fault_inject != 0, g_ctx.dev_status, g_ctx.tma_drop_tile};
     return true;
 }
 

@@ -21,6 +21,7 @@ struct CallContext {
     bool pdl;
     bool fault_inject;
     unsigned *dev_status;
+    int64_t drop_tile;  // test hook (AR_Q_TMA_DROP_TILE), -1 = off
 };
 
 // Guards the context; a call holds it from its checks to its last launch.

@@ -69,6 +69,8 @@ struct NormGradParams {
     int bx, cluster, stages, vecs;
     int apart, rows_aligned;  // as in NormParams
     unsigned *status;         // a wait that runs out sets bit 1
+    unsigned long long timeout_ns;  // bound of every wait
+    unsigned long long drop_row;    // test hook: this row's copies are never issued (~0 = none)
     // rows of any length
     float *row_sums;  // [2][ne1]: sum g and sum g x of each row
     unsigned rows_per_block;
@@ -893,6 +895,7 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
     __shared__ RowRoom room[2];
     __shared__ unsigned long long full[4];
     __shared__ volatile unsigned lost;
+    __shared__ unsigned issued;  // rows whose copies were issued, for thread 0
     pdl_launch_dependents();
     const unsigned ne0 = static_cast<unsigned>(p.ne0), ne1 = static_cast<unsigned>(p.ne1), T = blockDim.x;
     const RowThread<C, U, false> t(0, p.cluster, ne0);
@@ -902,7 +905,7 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
     const unsigned base = static_cast<unsigned>(__cvta_generic_to_shared(ring)), first_col = t.rank * T * U * C, hop = T * 16u;
     const bool inside = t.have[U - 1] == C;  // all of this thread's columns are inside the row
     if (threadIdx.x == 0) {
-        lost = 0;
+        lost = issued = 0;
         for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -930,6 +933,8 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
         const bool last = row + 1 == ne1;
         const unsigned n = vectors(first_col * es, ne0 * es, last, share);
         const unsigned nc = p.kept.codes ? vectors(first_col, ne0, last, code_bytes) : n;
+        ++issued;
+        if (row == p.drop_row) return;
         char *to = reinterpret_cast<char *>(ring) + static_cast<unsigned>(stage) * stage_bytes;
         mbar_expect_tx(&full[stage], n + nc + (p.dsum.base ? n : 0u));
         if (n) bulk_load(to, p.dy.row(row) + first_col * es, n, &full[stage]);
@@ -962,6 +967,7 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
         }
     int stage = 0;
     unsigned phase = 0, parity = 0;
+    bool gone = false;  // a copy came too late: nothing is waited for or issued any more
     for (unsigned row = static_cast<unsigned>(t.group); row < ne1; row += turn, parity ^= 1) {
         const pair_t minus_mean = both(-next_mean);
         const float rstd = next_rstd;
@@ -970,7 +976,7 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
 #pragma unroll
         for (int u = 0; u < U; ++u) scale[u] = next_scale[u];
         fetch(row + turn);
-        if (!mbar_wait_bounded(smem_u32(&full[stage]), phase, &lost) && !lost) {
+        if (!gone && !mbar_wait_bounded(smem_u32(&full[stage]), phase, &lost, p.timeout_ns) && !lost) {
             lost = 1;
             atomicOr(p.status, 2u);
         }
@@ -1073,14 +1079,20 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
         else
             results(true);
         __syncthreads();  // the stage has been read
-        if (threadIdx.x == 0) {
+        gone = lost;
+        if (threadIdx.x == 0 && !gone) {
             const unsigned next = row + static_cast<unsigned>(p.stages) * turn;
             if (next < ne1 && next > row) issue(next, stage);
         }
         if (++stage == p.stages) stage = 0, phase ^= 1;
     }
-    if (lost && threadIdx.x == 0)  // a copy that came too late must not find another block's shared memory
-        for (int s = 0; s < p.stages; ++s) mbar_wait(&full[s], phase, kUmmaTimeoutNs);
+    if (gone && threadIdx.x == 0) {
+        // a copy that comes too late must not find another block's shared memory: the last row of every stage is waited for,
+        // at its own parity
+        const unsigned stages = static_cast<unsigned>(p.stages);
+        for (unsigned k = issued > stages ? issued - stages : 0u; k < issued; ++k)
+            mbar_wait(&full[k % stages], k / stages & 1u, p.timeout_ns);
+    }
 #pragma unroll
     for (int which = 0; which < 3; ++which) {
         if (!p.part[which] || (which == 2 && !BIAS)) continue;

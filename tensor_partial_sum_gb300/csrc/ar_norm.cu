@@ -571,6 +571,8 @@ int ar_reduce_norm_grad(const void *dy, const void *h, const ar_checkpoint *ck, 
         const size_t cols = aligned ? 32 / es : 8;
         const int v = aligned ? 2 : static_cast<int>(es) / 2 + 1;
         p.status = c.dev_status;
+        p.timeout_ns = c.drop_tile < 0 ? tps::kUmmaTimeoutNs : 100ull * 1000 * 1000;
+        p.drop_row = c.drop_tile < 0 ? ~0ull : static_cast<unsigned long long>(c.drop_tile);
         // whole vectors of a row that is broadcast could reach behind its end
         const bool copied = aligned && !(L->residual && L->residual_row_bytes == 0 && L->ne1 > 1 && packed % 16);
         const RowShape rows = copied ? copied_shape(L->ne0, L->ne1, es, es + (h ? es : 1) + (L->residual ? es : 0)) : RowShape{};

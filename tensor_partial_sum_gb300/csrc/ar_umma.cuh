@@ -44,17 +44,19 @@ __device__ __forceinline__ bool mbar_try(unsigned addr, unsigned parity) {
         : "memory");
     return done != 0;
 }
-// Wait for the phase of the given parity; false when kUmmaTimeoutNs ran out or another warp gave up.
+// Wait for the phase of the given parity; false when the limit ran out or another warp gave up.
 // The clock and the flag are read only once the first try has failed: the threads that feed the
 // tensor cores have a few hundred cycles for a block of K.
-__device__ __forceinline__ bool mbar_wait_slow(unsigned addr, unsigned parity, const volatile unsigned *abort_flag) {
-    const unsigned long long deadline = global_ns() + kUmmaTimeoutNs;
+__device__ __forceinline__ bool mbar_wait_slow(unsigned addr, unsigned parity, const volatile unsigned *abort_flag,
+                                               unsigned long long limit_ns) {
+    const unsigned long long deadline = global_ns() + limit_ns;
     while (!mbar_try(addr, parity))
         if (*abort_flag || global_ns() > deadline) return false;
     return true;
 }
-__device__ __forceinline__ bool mbar_wait_bounded(unsigned addr, unsigned parity, const volatile unsigned *abort_flag) {
-    return mbar_try(addr, parity) || mbar_wait_slow(addr, parity, abort_flag);
+__device__ __forceinline__ bool mbar_wait_bounded(unsigned addr, unsigned parity, const volatile unsigned *abort_flag,
+                                                  unsigned long long limit_ns = kUmmaTimeoutNs) {
+    return mbar_try(addr, parity) || mbar_wait_slow(addr, parity, abort_flag, limit_ns);
 }
 __device__ __forceinline__ void mbar_arrive_cluster(unsigned cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
