@@ -23,7 +23,7 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ar_kernels.cuh", "ar_kernels_
                                                    "ar_dispatch.h", "ar_context.h", "ar_philox.cuh",
                                                    "ar_kernels_dropout.cuh", "ar_kernels_vocab.cuh", "ar_vocab_plan.h",
                                                    "ar_umma.cuh", "ar_buffers.h", "ar_rows8.cuh", "ar_pairs.cuh",
-                                                   "ar_codes.cuh", "ar_kernels_norm.cuh",
+                                                   "ar_codes.cuh", "ar_kernels_norm.cuh", "ar_norm_plan.h",
                                                    "ar_kernels_policy.cuh")] + [os.path.join(INCLUDE, "ar.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")

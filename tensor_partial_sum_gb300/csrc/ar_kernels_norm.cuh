@@ -12,10 +12,9 @@
 // partial column sums take through L2.
 #pragma once
 
-
-
 #include "ar_codes.cuh"
 #include "ar_kernels_ex.cuh"
+#include "ar_norm_plan.h"
 #include "ar_umma.cuh"
 #include "ar_pairs.cuh"
 #include "ar_rows8.cuh"
@@ -225,10 +224,6 @@ __global__ void __launch_bounds__(512) ar_norm_any_kernel(const __grid_constant_
 }
 
 // ---- rows in registers ------------------------------------------------------------
-
-constexpr int kRowBlocks = 8;   // most blocks of a cluster along a row
-constexpr int kRowThreads = 512;   // of the backward pass, at most
-constexpr int kNormThreads = 128;  // of the forward pass
 
 __device__ __forceinline__ void store_remote(const float *mine, unsigned rank, float v) {
     const unsigned at = static_cast<unsigned>(__cvta_generic_to_shared(mine));
