@@ -105,6 +105,7 @@ struct LongSum {
         sum = exact_add(sum, other_sum, e);
         lost = (lost + other_lost) + e;
     }
+    __device__ __forceinline__ float value() const { return lost == lost ? sum + lost : sum; }  // an infinite sum loses NaN
 };
 struct PairSum {
     pair_t sum = 0, lost = 0;

@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import tensor_partial_sum_gb300 as tps
-from tests.norm_ref import norm_backward, norm_forward
+from tests.gpu_util import TORCH_DTYPE
+from tests.norm_ref import HALF_STEP, norm_backward, norm_forward
 from tests.test_gpu_norm import EPS, backward, close, forward, normal
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +80,41 @@ def test_strides_past_32_bits(ne0):
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 def test_backward(dst, keep, kind):
     backward(131_080, 70, dst, kind, n_dxs=2, dsum=True, keep=keep)
+
+
+# ---- long sums ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dst,ne0", LONG + [("f32", 30_000_001), ("bf16", 30_000_001)])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_long_rows_keep_their_variance(dst, ne0, kind):
+    """1 / standard deviation to a few roundings, however many squares are added: each square is rounded twice, its
+    sum's losses are added up, and the mean square, its distance from the mean's square, eps and the root follow."""
+    x = (normal((2, ne0), 7, False) + torch.tensor([[0.0], [1.5]], device="cuda")).to(TORCH_DTYPE[dst])
+    tps.ar_init(1, 2 * ne0)
+    y, mean, rstd = torch.empty_like(x), torch.empty(2, device="cuda"), torch.empty(2, device="cuda")
+    tps.ar_reduce_norm([x], [y], tps.make_layout(ne0, 2), tps.make_norm(EPS, kind=kind), dst, dst, mean=mean, rstd=rstd)
+    h = x.double()
+    d = h - h.mean(1, keepdim=True) if kind == "layer" else h
+    want = 1 / torch.sqrt((d * d).mean(1) + EPS)
+    assert ((rstd.double() - want).abs() <= 8 * 2.0 ** -24 * want).all(), ((rstd.double() - want).abs() / want / 2.0 ** -24).tolist()
+
+
+@pytest.mark.parametrize("ne0", [1_000_003, 30_000_001])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_long_rows_keep_their_gradient(kind, ne0):
+    """dy of one sign, so that g - mean(g) cancels: off by roundings of g, x and the means, not by their number."""
+    tps.ar_init(1, 2 * ne0)
+    dy, h = 1 + normal((2, ne0), 8, False) * 2.0 ** -4, normal((2, ne0), 9, False)
+    x = h.double()
+    mean = x.mean(1) if kind == "layer" else torch.zeros(2, dtype=torch.float64, device="cuda")
+    rstd = 1 / torch.sqrt(((x - mean[:, None]) ** 2).mean(1) + EPS)
+    mean, rstd = mean.float(), rstd.float()
+    dx = torch.empty_like(dy)
+    tps.ar_reduce_norm_grad(dy, h, [dx], tps.make_layout(ne0, 2), tps.make_norm(EPS, kind=kind), mean, rstd, "f32")
+    want, _ = norm_backward(dy.double(), x, mean.double(), rstd.double(), None, None, kind == "rms")["dx"]
+    xs = ((x - mean.double()[:, None]) * rstd.double()[:, None]).abs()
+    g = dy.double().abs()
+    size = rstd.double()[:, None] * (g + g.mean(1, keepdim=True) + xs * (g * xs).mean(1, keepdim=True))
+    err = (dx.double() - want).abs()
+    bound = 8 * HALF_STEP[torch.float32] * (size + want.abs())
+    assert (err <= bound).all(), f"worst {(err / bound).max().item():.2f} times the bound"
