@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
     __shared__ RowRoom room[2];
     __shared__ unsigned long long full[4];
     __shared__ volatile unsigned lost;
-    __shared__ unsigned issued;  // rows whose copies were issued, for thread 0
+    __shared__ unsigned stop;  // the row behind which nothing was issued any more, for thread 0
     pdl_launch_dependents();
     const unsigned ne0 = static_cast<unsigned>(p.ne0), ne1 = static_cast<unsigned>(p.ne1), T = blockDim.x;
     const RowThread<C, U, false> t(0, p.cluster, ne0);
@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
     const unsigned base = static_cast<unsigned>(__cvta_generic_to_shared(ring)), first_col = t.rank * T * U * C, hop = T * 16u;
     const bool inside = t.have[U - 1] == C;  // all of this thread's columns are inside the row
     if (threadIdx.x == 0) {
-        lost = issued = 0;
+        lost = 0, stop = ~0u;
         for (int s = 0; s < p.stages; ++s) mbar_init(&full[s], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -910,7 +910,6 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
         const bool last = row + 1 == ne1;
         const unsigned n = vectors(first_col * es, ne0 * es, last, share);
         const unsigned nc = p.kept.codes ? vectors(first_col, ne0, last, code_bytes) : n;
-        ++issued;
         if (row == p.drop_row) return;
         char *to = reinterpret_cast<char *>(ring) + static_cast<unsigned>(stage) * stage_bytes;
         mbar_expect_tx(&full[stage], n + nc + (p.dsum.base ? n : 0u));
@@ -944,7 +943,6 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
         }
     int stage = 0;
     unsigned phase = 0, parity = 0;
-    bool gone = false;  // a copy came too late: nothing is waited for or issued any more
     for (unsigned row = static_cast<unsigned>(t.group); row < ne1; row += turn, parity ^= 1) {
         const pair_t minus_mean = both(-next_mean);
         const float rstd = next_rstd;
@@ -953,7 +951,9 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
 #pragma unroll
         for (int u = 0; u < U; ++u) scale[u] = next_scale[u];
         fetch(row + turn);
-        if (!gone && !mbar_wait_bounded(smem_u32(&full[stage]), phase, &lost, p.timeout_ns) && !lost) {
+        // Behind a copy that came too late nothing is issued any more, and no row waits longer than the first try.
+        const unsigned bar = smem_u32(&full[stage]);
+        if (!mbar_try(bar, phase, 20000u) && !lost && !mbar_wait_slow(bar, phase, &lost, p.timeout_ns) && !lost) {
             lost = 1;
             atomicOr(p.status, 2u);
         }
@@ -1051,22 +1051,26 @@ __global__ void __launch_bounds__(kRowThreads) ar_norm_grad_rows_kernel(const __
         else
             sums(true);
         row_sum<false, kBoth>(a, b, 0, t.cluster, t.rank, room[parity]);
+        const bool gone = lost;  // the whole block has waited; read later it cost 3% of the rows from codes
         if (inside && !last)
             results(false);
         else
             results(true);
         __syncthreads();  // the stage has been read
-        gone = lost;
-        if (threadIdx.x == 0 && !gone) {
+        if (threadIdx.x == 0) {
             const unsigned next = row + static_cast<unsigned>(p.stages) * turn;
-            if (next < ne1 && next > row) issue(next, stage);
+            if (gone)
+                stop = stop < row ? stop : row;
+            else if (next < ne1 && next > row)
+                issue(next, stage);
         }
         if (++stage == p.stages) stage = 0, phase ^= 1;
     }
-    if (gone && threadIdx.x == 0) {
+    if (lost && threadIdx.x == 0) {
         // a copy that comes too late must not find another block's shared memory: the last row of every stage is waited for,
-        // at its own parity
-        const unsigned stages = static_cast<unsigned>(p.stages);
+        // at its own parity.  Every row in front of `stop` was followed by the issue of another, if there was one.
+        const unsigned stages = static_cast<unsigned>(p.stages), first = static_cast<unsigned>(t.group);
+        const unsigned rows = (ne1 - 1 - first) / turn + 1, some = (stop - first) / turn + stages, issued = some < rows ? some : rows;
         for (unsigned k = issued > stages ? issued - stages : 0u; k < issued; ++k)
             mbar_wait(&full[k % stages], k / stages & 1u, p.timeout_ns);
     }

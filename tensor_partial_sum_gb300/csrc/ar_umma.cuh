@@ -44,6 +44,16 @@ __device__ __forceinline__ bool mbar_try(unsigned addr, unsigned parity) {
         : "memory");
     return done != 0;
 }
+// The same, at most about `ns` nanoseconds long.
+__device__ __forceinline__ bool mbar_try(unsigned addr, unsigned parity, unsigned ns) {
+    unsigned done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(addr), "r"(parity), "r"(ns)
+        : "memory");
+    return done != 0;
+}
 // Wait for the phase of the given parity; false when the limit ran out or another warp gave up.
 // The clock and the flag are read only once the first try has failed: the threads that feed the
 // tensor cores have a few hundred cycles for a block of K.
@@ -54,9 +64,8 @@ __device__ __forceinline__ bool mbar_wait_slow(unsigned addr, unsigned parity, c
         if (*abort_flag || global_ns() > deadline) return false;
     return true;
 }
-__device__ __forceinline__ bool mbar_wait_bounded(unsigned addr, unsigned parity, const volatile unsigned *abort_flag,
-                                                  unsigned long long limit_ns = kUmmaTimeoutNs) {
-    return mbar_try(addr, parity) || mbar_wait_slow(addr, parity, abort_flag, limit_ns);
+__device__ __forceinline__ bool mbar_wait_bounded(unsigned addr, unsigned parity, const volatile unsigned *abort_flag) {
+    return mbar_try(addr, parity) || mbar_wait_slow(addr, parity, abort_flag, kUmmaTimeoutNs);
 }
 __device__ __forceinline__ void mbar_arrive_cluster(unsigned cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
