@@ -215,7 +215,7 @@ __device__ __forceinline__ void store_remote(const float *mine, unsigned rank, f
 }
 
 // Where the warps of a row's blocks leave their parts of sums.  Two rooms in turn need one barrier a sum: the next
-// write to a room comes behind the barrier of the other.
+// write to a room comes behind the barrier of the other.  (The forward pass takes each of them once.)
 struct RowRoom {
     float2 v[kRowBlocks * kRowThreads / 32];
 };
@@ -518,13 +518,13 @@ __device__ __forceinline__ void unit_encode(const CodeRows &c, unsigned row, uns
     if (col % kCodeBlock == 0) c.scales[row * static_cast<unsigned long long>(c.scale_row) + col / kCodeBlock] = static_cast<uint8_t>(byte);
 }
 
-// Blocks on an SM: 72 registers a thread, 80 where a unit has 16 columns, 96 where it is shifted into place in rows
-// that share a block.  Seven where they fit: 2048 rows are then two waves of blocks (37 us; six: 2.25 waves, 43 us).
+// Blocks on an SM at least.  The kernel takes 60 registers a thread (eight blocks), 74 where a unit has 16 columns, 72 to 86
+// where it is shifted into place.
 template <int Td, bool ALIGNED, bool WARP>
 constexpr int kNormBlocks = ALIGNED ? (WARP || Td != kF32 ? 6 : 7) : (WARP ? 5 : 7);
 
 // The forward pass: bx lanes of a warp, a block or a cluster's blocks to a row, each thread with `units` units one
-// after another.  128 threads a block: with 256 or 512 a row's phases overlap less with other rows' (f32 [2048, 4096]: 42 and 47 us
+// after another; every block takes one turn of rows (a loop over them that ran once took 12 registers more).  128 threads a block: with 256 or 512 a row's phases overlap less with other rows' (f32 [2048, 4096]: 42 and 47 us
 // against 37).  The sum h of a thread's columns waits in shared memory for the row's statistics, where only the
 // thread itself reads it: no barrier, few registers, and enough blocks on an SM that their phases overlap.
 template <int Td, bool ALIGNED, bool WARP>
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<Td, ALIGNED, WARP>) 
     const unsigned rank = cluster == 1 ? 0u : cluster_rank();
     const unsigned ne0 = static_cast<unsigned>(x.ne0), ne1 = static_cast<unsigned>(x.ne1);
     const unsigned col0 = (rank * static_cast<unsigned>(bx * units) + static_cast<unsigned>(tx)) * C, hop = static_cast<unsigned>(bx) * C;
-    const unsigned group = blockIdx.x >> (WARP ? 0 : p.cluster_bits), groups = gridDim.x >> (WARP ? 0 : p.cluster_bits);
+    const unsigned group = blockIdx.x >> (WARP ? 0 : p.cluster_bits);
     const int ranks = p.n_sources - (x.residual != nullptr);
     // every sum starts from -0, which changes no operand; an inactive rank adds +0, which turns a -0 into +0
     const pair_t start = both(x.inactive ? 0.0f : -0.0f);
@@ -549,125 +549,123 @@ __global__ void __launch_bounds__(kNormThreads, kNormBlocks<Td, ALIGNED, WARP>) 
     uint4 *const mine = held + threadIdx.x;
     pdl_wait();
     if (!WARP && cluster > 1) cluster_sync();  // every block of the cluster runs before one writes to another
-    for (unsigned row0 = group * by; row0 < ne1; row0 += groups * by) {
-        const unsigned row = row0 + static_cast<unsigned>(ty);
-        const bool in_row = row < ne1, inner = p.apart && row > 0 && row + 1 < ne1;
-        // how many columns of the unit at `col` are inside the row
-        auto inside = [&](unsigned col) { return !in_row || col >= ne0 ? 0 : ne0 - col >= C ? C : static_cast<int>(ne0 - col); };
-        auto put = [&](void *base, long long stride, unsigned col, int have, const uint32_t(&w)[W]) {
-            unit_store<Td, ALIGNED>(static_cast<char *>(base) + static_cast<unsigned long long>(row) * static_cast<unsigned>(stride) +
-                                        col * Elem<Td>::bytes,
-                                    w, col, ne0, have, prev, lane_next);
-        };
-        LongSum total;
-        unsigned col = col0;
-        for (int u = 0; u < units; ++u, col += hop) {
-            const int have = inside(col);
-            const unsigned at = col * Elem<Td>::bytes;
-            pair_t acc[N];
+    const unsigned row = group * by + static_cast<unsigned>(ty);
+    const bool in_row = row < ne1, inner = p.apart && row > 0 && row + 1 < ne1;
+    // how many columns of the unit at `col` are inside the row
+    auto inside = [&](unsigned col) { return !in_row || col >= ne0 ? 0 : ne0 - col >= C ? C : static_cast<int>(ne0 - col); };
+    auto put = [&](void *base, long long stride, unsigned col, int have, const uint32_t(&w)[W]) {
+        unit_store<Td, ALIGNED>(static_cast<char *>(base) + static_cast<unsigned long long>(row) * static_cast<unsigned>(stride) +
+                                    col * Elem<Td>::bytes,
+                                w, col, ne0, have, prev, lane_next);
+    };
+    LongSum total;
+    unsigned col = col0;
+    for (int u = 0; u < units; ++u, col += hop) {
+        const int have = inside(col);
+        const unsigned at = col * Elem<Td>::bytes;
+        pair_t acc[N];
 #pragma unroll
-            for (int k = 0; k < N; ++k) acc[k] = start;
-            if (have) {
-                Unit<Td, ALIGNED> res;
-                pair_t v[N];
-                if (x.residual) unit_load<Td, ALIGNED>(res, p.source[ranks].row(row) + at, p.source[ranks], inner, have);
-                for (int s0 = 0; s0 < ranks; s0 += RB) {
-                    Unit<Td, ALIGNED> in[RB];
+        for (int k = 0; k < N; ++k) acc[k] = start;
+        if (have) {
+            Unit<Td, ALIGNED> res;
+            pair_t v[N];
+            if (x.residual) unit_load<Td, ALIGNED>(res, p.source[ranks].row(row) + at, p.source[ranks], inner, have);
+            for (int s0 = 0; s0 < ranks; s0 += RB) {
+                Unit<Td, ALIGNED> in[RB];
 #pragma unroll
-                    for (int j = 0; j < RB; ++j)
-                        if (s0 + j < ranks) unit_load<Td, ALIGNED>(in[j], p.source[s0 + j].row(row) + at, p.source[s0 + j], inner, have);
+                for (int j = 0; j < RB; ++j)
+                    if (s0 + j < ranks) unit_load<Td, ALIGNED>(in[j], p.source[s0 + j].row(row) + at, p.source[s0 + j], inner, have);
 #pragma unroll
-                    for (int j = 0; j < RB; ++j) {
-                        if (s0 + j >= ranks) break;
-                        unit_pairs<Td, ALIGNED>(in[j], v);
-                        wire_pairs<Td>(p.wire, v);
-#pragma unroll
-                        for (int k = 0; k < N; ++k) acc[k] = add2(acc[k], v[k]);
-                    }
-                }
-                if (p.bias) {
-                    uint32_t w[W];
-                    row_unit<Td, W>(p.bias, col, have, p.rows_aligned, w);
-                    widen_pairs<Td, W>(w, v);
-#pragma unroll
-                    for (int k = 0; k < N; ++k) acc[k] = add2(acc[k], v[k]);
-                }
-                if (x.residual) {
-                    unit_pairs<Td, ALIGNED>(res, v);
+                for (int j = 0; j < RB; ++j) {
+                    if (s0 + j >= ranks) break;
+                    unit_pairs<Td, ALIGNED>(in[j], v);
+                    wire_pairs<Td>(p.wire, v);
 #pragma unroll
                     for (int k = 0; k < N; ++k) acc[k] = add2(acc[k], v[k]);
                 }
             }
-            if (have < C) first_pairs(acc, have);  // nothing behind the row's end, where the sums look
-            uint32_t h[W];
-            round_pairs<Td, W>(acc, h);
+            if (p.bias) {
+                uint32_t w[W];
+                row_unit<Td, W>(p.bias, col, have, p.rows_aligned, w);
+                widen_pairs<Td, W>(w, v);
 #pragma unroll
-            for (int k = 0; k < W; k += 4) mine[(u * (W / 4) + k / 4) * T] = make_uint4(h[k], h[k + 1], h[k + 2], h[k + 3]);
-            for (int s = 0; s < p.n_sums; ++s) put(p.sum[s], p.sum_stride[s], col, have, h);
-            widen_pairs<Td, W>(h, acc);
-            if (p.kept.codes) unit_encode(p.kept, row, col, have, acc);
-            if (!p.rms) add_columns<Td>(acc, total);
-        }
-        auto take = [&](int u, pair_t(&v)[N]) {
-            uint32_t h[W];
-#pragma unroll
-            for (int k = 0; k < W; k += 4) {
-                const uint4 q = mine[(u * (W / 4) + k / 4) * T];
-                h[k] = q.x, h[k + 1] = q.y, h[k + 2] = q.z, h[k + 3] = q.w;
+                for (int k = 0; k < N; ++k) acc[k] = add2(acc[k], v[k]);
             }
-            widen_pairs<Td, W>(h, v);
-        };
-        float m = 0.0f, off = 0.0f, square = 0.0f, unused = 0.0f;
-        if (!p.rms) {
-            row_sum<WARP, kLong>(total.sum, total.lost, bx, cluster, rank, room[0]);
-            m = first_mean<Td>(total, p.inv_n);
-            off = mean_rest(total, m, static_cast<float>(ne0), p.inv_n);  // ne0 is below 2^24 here
-        }
-        col = col0;
-        const pair_t minus_m = both(-m);
-        for (int u = 0; u < units; ++u, col += hop) {
-            pair_t v[N], q = 0;
-            take(u, v);
+            if (x.residual) {
+                unit_pairs<Td, ALIGNED>(res, v);
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = add2(v[k], minus_m);
-            const int have = inside(col);
-            if (have < C) first_pairs(v, have);
-#pragma unroll
-            for (int k = 0; k < N; ++k) q = fma2(v[k], v[k], q);
-            const float2 f = halves(q);
-            square += f.x + f.y;
-        }
-        row_sum<WARP, kOne>(square, unused, bx, cluster, rank, room[WARP ? 0 : 1]);
-        const float rstd = norm_rstd(square * p.inv_n, off, p.eps);
-        if (in_row && col0 == 0) {
-            if (p.mean) p.mean[row] = norm_mean(m, off);
-            if (p.rstd) p.rstd[row] = rstd;
-        }
-        // ((h - m) - off) rstd
-        const pair_t scale = both(rstd), rest = both(-off * rstd);
-        col = col0;
-        for (int u = 0; u < units; ++u, col += hop) {
-            const int have = inside(col);
-            pair_t v[N], f[N];
-            uint32_t w[W], g[W];
-            if (p.weight) row_unit<Td, W>(p.weight, col, have, p.rows_aligned, w);
-            if (p.shift) row_unit<Td, W>(p.shift, col, have, p.rows_aligned, g);
-            take(u, v);
-#pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = fma2(add2(v[k], minus_m), scale, rest);
-            if (p.weight) {
-                widen_pairs<Td, W>(w, f);
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[k] = mul2(v[k], f[k]);
+                for (int k = 0; k < N; ++k) acc[k] = add2(acc[k], v[k]);
             }
-            if (p.shift) {
-                widen_pairs<Td, W>(g, f);
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[k] = add2(v[k], f[k]);
-            }
-            round_pairs<Td, W>(v, w);
-            for (int d = 0; d < x.n_dsts; ++d) put(x.dst[d], x.dst_stride[d], col, have, w);
         }
+        if (have < C) first_pairs(acc, have);  // nothing behind the row's end, where the sums look
+        uint32_t h[W];
+        round_pairs<Td, W>(acc, h);
+#pragma unroll
+        for (int k = 0; k < W; k += 4) mine[(u * (W / 4) + k / 4) * T] = make_uint4(h[k], h[k + 1], h[k + 2], h[k + 3]);
+        for (int s = 0; s < p.n_sums; ++s) put(p.sum[s], p.sum_stride[s], col, have, h);
+        widen_pairs<Td, W>(h, acc);
+        if (p.kept.codes) unit_encode(p.kept, row, col, have, acc);
+        if (!p.rms) add_columns<Td>(acc, total);
+    }
+    auto take = [&](int u, pair_t(&v)[N]) {
+        uint32_t h[W];
+#pragma unroll
+        for (int k = 0; k < W; k += 4) {
+            const uint4 q = mine[(u * (W / 4) + k / 4) * T];
+            h[k] = q.x, h[k + 1] = q.y, h[k + 2] = q.z, h[k + 3] = q.w;
+        }
+        widen_pairs<Td, W>(h, v);
+    };
+    float m = 0.0f, off = 0.0f, square = 0.0f, unused = 0.0f;
+    if (!p.rms) {
+        row_sum<WARP, kLong>(total.sum, total.lost, bx, cluster, rank, room[0]);
+        m = first_mean<Td>(total, p.inv_n);
+        off = mean_rest(total, m, static_cast<float>(ne0), p.inv_n);  // ne0 is below 2^24 here
+    }
+    col = col0;
+    const pair_t minus_m = both(-m);
+    for (int u = 0; u < units; ++u, col += hop) {
+        pair_t v[N], q = 0;
+        take(u, v);
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = add2(v[k], minus_m);
+        const int have = inside(col);
+        if (have < C) first_pairs(v, have);
+#pragma unroll
+        for (int k = 0; k < N; ++k) q = fma2(v[k], v[k], q);
+        const float2 f = halves(q);
+        square += f.x + f.y;
+    }
+    row_sum<WARP, kOne>(square, unused, bx, cluster, rank, room[WARP ? 0 : 1]);
+    const float rstd = norm_rstd(square * p.inv_n, off, p.eps);
+    if (in_row && col0 == 0) {
+        if (p.mean) p.mean[row] = norm_mean(m, off);
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+    // ((h - m) - off) rstd
+    const pair_t scale = both(rstd), rest = both(-off * rstd);
+    col = col0;
+    for (int u = 0; u < units; ++u, col += hop) {
+        const int have = inside(col);
+        pair_t v[N], f[N];
+        uint32_t w[W], g[W];
+        if (p.weight) row_unit<Td, W>(p.weight, col, have, p.rows_aligned, w);
+        if (p.shift) row_unit<Td, W>(p.shift, col, have, p.rows_aligned, g);
+        take(u, v);
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = fma2(add2(v[k], minus_m), scale, rest);
+        if (p.weight) {
+            widen_pairs<Td, W>(w, f);
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = mul2(v[k], f[k]);
+        }
+        if (p.shift) {
+            widen_pairs<Td, W>(g, f);
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = add2(v[k], f[k]);
+        }
+        round_pairs<Td, W>(v, w);
+        for (int d = 0; d < x.n_dsts; ++d) put(x.dst[d], x.dst_stride[d], col, have, w);
     }
 }
 

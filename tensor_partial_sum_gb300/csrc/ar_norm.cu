@@ -312,7 +312,8 @@ int ar_reduce_norm(const void *const *srcs, void *const *dsts, int n_dsts, const
     const size_t es = dtype_bytes(dst_dtype);
     const bool aligned = al.bits % 32 == 0;
     const RowShape s = forward_shape(L->ne0, L->ne1, es, aligned);
-    if (s.U == 0 || !al.narrow) {
+    const size_t grid = s.U ? forward_grid(s, L->ne1) : 0;
+    if (s.U == 0 || !al.narrow || grid > 0x7FFFFFFF) {
         const NormFn any = by_type<NormFn>(dst_dtype, tps::ar_norm_any_kernel<tps::kF32>, tps::ar_norm_any_kernel<tps::kF16>,
                                            tps::ar_norm_any_kernel<tps::kBF16>);
         const size_t blocks = L->ne1 < 65535 ? L->ne1 : 65535;
@@ -330,9 +331,8 @@ int ar_reduce_norm(const void *const *srcs, void *const *dsts, int n_dsts, const
     const NormFn fn = pick_rows<NormFn, Forward>(dst_dtype, aligned, s);
     st = allow_ring(fn, s);
     if (st != AR_OK) return st;
-    const size_t turn = s.warp ? s.threads / s.bx : 1, most = (1u << 30) / s.cluster, groups = (L->ne1 + turn - 1) / turn;
-    return launched(tps::launch_clustered(fn, dim3(static_cast<unsigned>((groups < most ? groups : most) * s.cluster)),
-                                          static_cast<unsigned>(s.cluster), s.threads, s.smem, stream, c.pdl, p));
+    return launched(tps::launch_clustered(fn, dim3(static_cast<unsigned>(grid)), static_cast<unsigned>(s.cluster), s.threads, s.smem,
+                                          stream, c.pdl, p));
 }
 
 int ar_reduce_norm_grad_workspace(const ar_layout *L, int n_sums, size_t *bytes) {

@@ -136,6 +136,12 @@ inline RowShape forward_shape(size_t ne0, size_t ne1, size_t es, bool aligned) {
     return s;
 }
 
+// Its blocks: every block takes one turn of rows.
+inline size_t forward_grid(const RowShape &s, size_t ne1) {
+    const size_t turn = s.warp ? s.threads / s.bx : 1;
+    return (ne1 + turn - 1) / turn * s.cluster;
+}
+
 // What the row starts of a call's buffers have in common.
 struct Alignment {
     uintptr_t bits = 0;

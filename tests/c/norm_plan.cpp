@@ -2,7 +2,7 @@
 // rows start on 32-byte boundaries, 16-byte vectors of a unit and row in the ring (v, for the backward pass: of dy, the
 // kept sum and dsum together), bytes of a column in a row of the ring, whether strides fit 32 bits.  Prints
 //   forward: U bx cluster threads warp smem; ring: U bx cluster threads warp smem stages blocks;
-//   copied: U cluster threads smem stages blocks; rows of partial sums; pack: vectors per_row blocks.
+//   copied: U cluster threads smem stages blocks; rows of partial sums; pack: vectors per_row blocks; forward: blocks.
 #include <cstdio>
 
 #include "ar_norm_plan.h"
@@ -25,7 +25,7 @@ int main() {
         al.bits = aligned ? 0 : es;
         al.narrow = narrow;
         const PackShape p = pack_shape(ne0, ne1, es, al);
-        printf("%d %zu %zu\n", p.vectors, p.per_row, p.blocks);
+        printf("%d %zu %zu %zu\n", p.vectors, p.per_row, p.blocks, f.U ? forward_grid(f, ne1) : 0);
     }
     return 0;
 }

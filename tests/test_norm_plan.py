@@ -13,7 +13,7 @@ from tests.test_gpu_norm_any import LONG
 HERE = os.path.dirname(os.path.abspath(__file__))
 ES = {"f32": 4, "f16": 2, "bf16": 2}
 FIELDS = ("f_U f_bx f_cluster f_threads f_warp f_smem r_U r_bx r_cluster r_threads r_warp r_smem r_stages r_blocks "
-          "c_U c_cluster c_threads c_smem c_stages c_blocks parts vectors per_row pack_blocks").split()
+          "c_U c_cluster c_threads c_smem c_stages c_blocks parts vectors per_row pack_blocks f_blocks").split()
 MOST_SMEM = 224 * 1024  # next to 2 KB and a few words of a kernel's own: 227 KB are possible
 
 
@@ -79,6 +79,9 @@ def test_every_column_has_a_thread_and_every_launch_fits(plans):
             assert p["f_smem"] == p["f_threads"] * p["f_U"] * cols * es <= MOST_SMEM, c
             # a block of 32 columns with one scale lies in adjacent lanes of a warp
             assert p["f_bx"] * cols % 32 == 0, c
+            # every block takes one turn of rows
+            turn = p["f_threads"] // p["f_bx"] if p["f_warp"] else 1
+            assert p["f_blocks"] % p["f_cluster"] == 0 and p["f_blocks"] // p["f_cluster"] * turn >= c[1], c
         if p["r_U"]:
             assert p["r_bx"] * p["r_U"] * cols * p["r_cluster"] >= ne0 and p["r_threads"] <= 512, c
             assert p["r_smem"] <= MOST_SMEM and 1 <= p["r_stages"] <= 4, c
