@@ -16,7 +16,7 @@
 
 #include <cuda_runtime.h>
 
-#include "ar_kernels.cuh"
+#include "ar_pairs.cuh"
 
 namespace tps {
 
@@ -405,6 +405,7 @@ __global__ void __launch_bounds__(kPolicyThreads, 4) ar_policy_kernel(const __gr
     __shared__ unsigned counts[kPolicyThreads / 32];
     __shared__ float room[4 * kPolicyThreads / 32], shared_base;
     __shared__ double joined[kPolicyThreads];
+    __shared__ float4 long_sums[kPolicyThreads];
     __shared__ bool last_block;
     pdl_launch_dependents();
     pdl_wait();
@@ -422,6 +423,10 @@ __global__ void __launch_bounds__(kPolicyThreads, 4) ar_policy_kernel(const __gr
     __syncthreads();
     const float base = shared_base;
     const bool walk = !(p.token_adv && p.mean != 2);
+    // A thread's tokens are added in two steps, those of a chunk and then the chunks, with what that loses: plain sums of equal
+    // terms left the totals of 2^28 tokens 1.7e-5 off.  Between chunks the long sums wait in shared memory (in registers they
+    // spilled).
+    long_sums[threadIdx.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     PolicySums s;
     for (unsigned long long first = static_cast<unsigned long long>(blockIdx.x) * kPolicyChunk; first < p.tokens;
          first += static_cast<unsigned long long>(gridDim.x) * kPolicyChunk) {
@@ -440,6 +445,19 @@ __global__ void __launch_bounds__(kPolicyThreads, 4) ar_policy_kernel(const __gr
             chunk_offsets(p, first, end - 1, inner);
         }
         if (t0 < end) policy_tokens(p, t0, end, bits, nll, old_nll, ref_nll, adv, base, inner, from, to, s);
+        const float4 q = long_sums[threadIdx.x];
+        LongSum gain, kl;
+        gain.sum = q.x, gain.lost = q.y, kl.sum = q.z, kl.lost = q.w;
+        gain.add(s.gain);
+        kl.add(s.kl);
+        long_sums[threadIdx.x] = make_float4(gain.sum, gain.lost, kl.sum, kl.lost);
+        s.gain = s.kl = 0.0f;
+    }
+    {
+        const float4 q = long_sums[threadIdx.x];
+        LongSum gain, kl;
+        gain.sum = q.x, gain.lost = q.y, kl.sum = q.z, kl.lost = q.w;
+        s.gain = gain.value(), s.kl = kl.value();
     }
     const double sum = policy_block_sums(s, room);
     if (threadIdx.x < 4) __stcg(p.part + blockIdx.x * 4ull + threadIdx.x, sum);
