@@ -479,6 +479,9 @@ def make_layout(ne0, ne1, src_row_bytes=None, dst_row_bytes=None, residual=None,
         L.src_row_bytes = _i64s(src_row_bytes)
     if dst_row_bytes is not None:
         L.dst_row_bytes = _i64s(dst_row_bytes)
+    # how many strides there are, for the binding's check
+    L._strides = (AR_MAX_RANKS if src_row_bytes is None else len(src_row_bytes),
+                  AR_MAX_RANKS if dst_row_bytes is None else len(dst_row_bytes))
     L.residual = _ptr(residual)
     L._residual_obj = residual  # kept for the binding's reach check
     if residual is not None and residual_row_bytes is None:
@@ -491,11 +494,20 @@ def make_layout(ne0, ne1, src_row_bytes=None, dst_row_bytes=None, residual=None,
     return L
 
 
+def _too_few(call, srcs, dsts, strides):
+    """More tensors than the layout has strides; more than AR_MAX_RANKS is the library's to refuse."""
+    for what, n, have in (("source", srcs, strides[0]), ("destination", dsts, strides[1])):
+        if n > have < AR_MAX_RANKS:
+            raise ValueError(f"{call}: {n} {what} tensors, the layout has {have} {what} strides")
+
+
 def _layout_buffers(srcs, dsts, layout, dcode, call):
     """Checked, packed addresses of the sources and destinations of an
     ar_layout call, whose residual is checked too."""
     ne0, ne1 = layout.ne0, layout.ne1
     row = ne0 * ESIZE[dcode]
+    if hasattr(layout, "_strides") and (len(srcs) > layout._strides[0] or len(dsts) > layout._strides[1]):
+        _too_few(call, len(srcs), len(dsts), layout._strides)
     src = _layout_pointers(srcs, layout.src_row_bytes or None, row, ne1, "source", call)
     dst = _layout_pointers(dsts, layout.dst_row_bytes or None, row, ne1, "destination", call)
     res = layout._residual_obj if hasattr(layout, "_residual_obj") else None
@@ -828,6 +840,8 @@ def _norm_kept(layout, dcode, sums, sum_row_bytes, mean, rstd, checkpoint, call)
     k = ArNormKept()
     if sums:
         rows = None if sum_row_bytes is None else _i64s(sum_row_bytes)
+        if rows is not None and len(rows) < len(sums):
+            raise ValueError(f"{call}: {len(sums)} sums, {len(rows)} strides")
         k.n_sums = len(sums)
         k._pointers = _layout_pointers(sums, rows, ne0 * ESIZE[dcode], ne1, "sum", call)
         k.sums = k._pointers
