@@ -29,7 +29,7 @@ __device__ __forceinline__ unsigned scale_byte(int format, uint32_t amax_bits) {
                                   : static_cast<int>((amax_bits + 0x01FFFFu) >> 23) - 6;
     return e > 0 ? static_cast<unsigned>(e) : 0u;
 }
-// 2^-e for the scale byte of finite elements, at most 248.
+// 2^-e for the scale byte of finite elements, at most 249 (int8, next to the largest floats).
 __device__ __forceinline__ float scale_inverse(unsigned byte) { return __uint_as_float((254u - byte) << 23); }
 // 2^e, NaN for 255 and the subnormal 2^-127 for 0.
 __device__ __forceinline__ float scale_value(unsigned byte) {

@@ -2,12 +2,12 @@
 //
 // All are bound by memory where there are enough rows.  Measured on a GB300 in a graph of calls over input sets larger than
 // L2, against the bytes that a call cannot do without at the copy rate of 6.78 TB/s:
-//   forward, R = 2 f32 [n, 4096], two destinations, sum kept, bias, weight, shift, residual: 2048 rows 37.3 us (79%),
-//   16384 rows 253 us (94%); R = 2 bf16 [4096, 4096], one destination 34.1 us (73%);
-//   backward, f32 [n, 4096] to two, dsum: 2048 rows with three column sums 35.5 us (70%), 4096 rows without sums
-//   55.6 us (89%);
-//   forward and backward by an e4m3 checkpoint, R = 4 bf16 [4096, 8192] to four: 181 us (88%);
-//   checkpoint written and read, f32 [2048, 4096]: 15.6 us (80%), bf16 [4096, 8192]: 33.7 us (89%).
+//   forward, R = 2 f32 [n, 4096], two destinations, sum kept, bias, weight, shift, residual: 2048 rows 38.4 us (77%),
+//   16384 rows 244 us (97%); R = 2 bf16 [4096, 4096], one destination 34.8 us (71%);
+//   backward, f32 [n, 4096] to two, dsum: 2048 rows with three column sums 36.0 us (69%), 4096 rows without sums
+//   55.5 us (89%);
+//   forward and backward by an e4m3 checkpoint, R = 4 bf16 [4096, 8192] to four: 183 us (87%);
+//   checkpoint written and read, f32 [2048, 4096]: 15.7 us (79%), bf16 [4096, 8192]: 33.8 us (89%).
 // What is lost at 2048 rows is the start and end of each wave of blocks, and of the backward pass the 4 to 7 us that
 // partial column sums take through L2.
 #pragma once
@@ -524,8 +524,8 @@ template <int Td, bool ALIGNED, bool WARP>
 constexpr int kNormBlocks = ALIGNED ? (WARP || Td != kF32 ? 6 : 7) : (WARP ? 5 : 7);
 
 // The forward pass: bx lanes of a warp, a block or a cluster's blocks to a row, each thread with `units` units one
-// after another; every block takes one turn of rows (a loop over them that ran once took 12 registers more).  128 threads a block: with 256 or 512 a row's phases overlap less with other rows' (f32 [2048, 4096]: 42 and 47 us
-// against 37).  The sum h of a thread's columns waits in shared memory for the row's statistics, where only the
+// after another; every block takes one turn of rows (a loop over them that ran once took 12 registers more).
+// 128 threads a block: with 256 or 512 a row's phases overlap less with other rows' (f32 [2048, 4096]: 42 and 47 us against 37).  The sum h of a thread's columns waits in shared memory for the row's statistics, where only the
 // thread itself reads it: no barrier, few registers, and enough blocks on an SM that their phases overlap.
 template <int Td, bool ALIGNED, bool WARP>
 __global__ void __launch_bounds__(kNormThreads, kNormBlocks<Td, ALIGNED, WARP>) ar_norm_kernel(const __grid_constant__ NormParams p) {
@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(WARP ? 256 : kRowThreads, WARP ? 2 : 1) ar_nor
 
 // The same for rows on 32-byte boundaries that take a block or more: the copy engine brings a row's share of dy, of the
 // kept sum and of dsum (cp.async copies held the loads to 3 TB/s, whatever their depth: 4096 rows of 4096 floats took 92 us
-// without the sums; this takes 55.6).  Blocks of a cluster that add their column sums before writing them: no gain with two,
+// without the sums; this takes 55.5).  Blocks of a cluster that add their column sums before writing them: no gain with two,
 // and with four not all blocks are resident (73 us).  A thread holds U 16-byte vectors, 16 columns, blockDim.x vectors apart, so that neither shared memory nor stores
 // have bank conflicts or gaps.
 template <int Td, bool BIAS>

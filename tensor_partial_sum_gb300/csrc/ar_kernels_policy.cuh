@@ -5,8 +5,8 @@
 // counts of the sequences, where those are wanted), the next computes, and its last block joins the blocks' sums.
 // Counts are integers, whose order of adding does not matter; floats are added in a fixed order.
 //
-// Measured on a GB300 in a graph: 300 tokens 7.4 us (one block: four rounds of dependent loads, an exponential, a sum);
-// 262143 tokens in 257 sequences 18.9 us (three launches); four million tokens with an advantage each 32.8 us, 28 of them
+// Measured on a GB300 in a graph: 300 tokens 7.3 us (one block: four rounds of dependent loads, an exponential, a sum);
+// 262143 tokens in 257 sequences 19.2 us (three launches); four million tokens with an advantage each 33.2 us, 28 of them
 // the main launch: 2.7 TB/s, about 100 instructions a token.
 #pragma once
 
