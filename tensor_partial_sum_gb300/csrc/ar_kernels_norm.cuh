@@ -525,8 +525,9 @@ constexpr int kNormBlocks = ALIGNED ? (WARP || Td != kF32 ? 6 : 7) : (WARP ? 5 :
 
 // The forward pass: bx lanes of a warp, a block or a cluster's blocks to a row, each thread with `units` units one
 // after another; every block takes one turn of rows (a loop over them that ran once took 12 registers more).
-// 128 threads a block: with 256 or 512 a row's phases overlap less with other rows' (f32 [2048, 4096]: 42 and 47 us against 37).  The sum h of a thread's columns waits in shared memory for the row's statistics, where only the
-// thread itself reads it: no barrier, few registers, and enough blocks on an SM that their phases overlap.
+// 128 threads a block: with 256 or 512 a row's phases overlap less with other rows' (f32 [2048, 4096]: 42 and 47 us against
+// 37).  The sum h of a thread's columns waits in shared memory for the row's statistics, where only the thread itself reads
+// it: no barrier, few registers, and enough blocks on an SM that their phases overlap.
 template <int Td, bool ALIGNED, bool WARP>
 __global__ void __launch_bounds__(kNormThreads, kNormBlocks<Td, ALIGNED, WARP>) ar_norm_kernel(const __grid_constant__ NormParams p) {
     constexpr int W = kUnitWords<Td, ALIGNED>, C = kCols<Td, W>, N = C / 2, RB = 16 / W;
